@@ -2,7 +2,9 @@
  * dspark.h — C ABI of the DSpark per-round speculative-decoding hot path on GB300
  * (sm_103a): Markov-head draft -> confidence scheduler -> exact verification, with the
  * recurrent-head draft, verification on a flattened target batch, the fixed-cutoff
- * scheduler, the acceptance-overlap diagnostic and sequential temperature scaling.
+ * scheduler, the acceptance-overlap diagnostic and sequential temperature scaling; and the
+ * operators a serving loop needs beside a round: token log probabilities (with their
+ * gradient), the paged key-value cache and attention over it.
  *
  * The method is the one described on the pages about DSpark (Cheng, Yu, Shao et al.,
  * "DSpark: Confidence-Scheduled Speculative Decoding with Semi-Autoregressive
@@ -71,6 +73,9 @@ typedef int dspark_status;
 
 #define DSPARK_F32 0
 #define DSPARK_BF16 1
+/* accepted where an entry point says so (token log probabilities, the paged cache) */
+#define DSPARK_F16 2
+#define DSPARK_E4M3 3
 
 #define DSPARK_EARLY_STOP 0
 #define DSPARK_FULL_SEARCH 1
@@ -425,6 +430,150 @@ DSPARK_API size_t dspark_sts_fit_workspace_size(int N, int gamma, int G, int M);
 DSPARK_API dspark_status dspark_sts_fit(
     int N, int gamma, const float* z, const int32_t* acc_len, const float* grid, int G, int M,
     float* T_out, float* ece_out, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Log probabilities of given tokens, with entropy and the best alternatives.
+ *
+ * For each row n of logits [N,V] that has a token (0 <= tokens[n] < V), with z = x/T:
+ *   lse_out[n]      = ln sum_v exp z_v
+ *   logprob_out[n]  = z_{tokens[n]} - lse_out[n]
+ *   entropy_out[n]  = -sum_v p_v ln p_v, p = softmax(z)   (a masked id adds nothing)
+ *   top_ids_out[n,i], top_logprobs_out[n,i], i < top_k: the ids of the largest logits,
+ *                     largest first, the lower id first among equals, and z - lse.
+ * Rows without a token (verification writes -1 past the emitted tokens) are not read:
+ * their values are NaN and their ids -1.  A logit of -inf masks its id.  A row of which
+ * nothing is left (every logit -inf) has lse -inf, log probabilities -inf and entropy 0;
+ * a row that holds a NaN or +inf has no distribution: values NaN, ids -1.
+ *
+ *   row_stride  elements between rows (>= V); rows need only their type's alignment.
+ *   dtype       DSPARK_F32, DSPARK_BF16 or DSPARK_F16.
+ *   temperature T > 0.
+ *   top_k       0..32 and <= V; 0: top_ids_out and top_logprobs_out may be NULL.
+ * N = 0 does nothing.  Sums are fp32 in a fixed order (deterministic).  No workspace.
+ * Limits: V <= 1048576.
+ * ---------------------------------------------------------------------------------- */
+DSPARK_API dspark_status dspark_token_logprobs(
+    int N, int V, int64_t row_stride, int dtype, const void* logits, const int32_t* tokens, float temperature,
+    int top_k, float* logprob_out, float* entropy_out, float* lse_out, int32_t* top_ids_out,
+    float* top_logprobs_out, void* stream);
+
+/* The gradient of sum_n grad_logprob[n] logprob[n] + grad_entropy[n] entropy[n] for the
+ * logits of dspark_token_logprobs, from its lse_out and entropy_out:
+ *   d/dx_v = (g_l (1[v = token] - p_v) - g_H p_v (ln p_v + entropy)) / T.
+ * grad_out [N,V] has the logits' type and its own row stride; it may be the logits' own
+ * array (same stride).  grad_entropy may be NULL.  Rows without a token and rows of which
+ * nothing is left get zeros, rows without a distribution NaN. */
+DSPARK_API dspark_status dspark_token_logprobs_backward(
+    int N, int V, int64_t row_stride, int64_t grad_stride, int dtype, const void* logits, const int32_t* tokens,
+    float temperature, const float* lse, const float* entropy, const float* grad_logprob,
+    const float* grad_entropy, void* grad_out, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Paged key-value cache.
+ *
+ * One request's context is a list of pages of page_size tokens.  The tables are device
+ * arrays of the caller, shared by every layer:
+ *   page_table [R, max_pages] int32, rows table_stride apart: the pages of request slot r
+ *              in order; entries past its context are -1.
+ *   seq_len    [R] int32 tokens in the slot's context (0: the slot is empty).
+ *   ref_count  [num_pages] int32 slots that hold the page (0: the page is free).
+ * Keys and values of a layer are two pools of num_pages pages.  Entry points that read or
+ * write rows take strides (in elements) between pages, heads and tokens, the same for both
+ * pools, and D contiguous elements a row; rows start on 16-byte boundaries.  Entry points
+ * that move whole pages take `pools`, a host array of n_pools device pointers (each layer's
+ * keys and values), whose pages are page_bytes apart (a multiple of 16).
+ * Every call is asynchronous, allocates nothing, changes the tables in place and can be
+ * captured.  Table entries, lengths and ids that are out of range are reported in the
+ * workspace's status word (dspark_workspace_status) and touch nothing.  Page choices depend
+ * only on the tables (never on timing).  Workspace of all five calls:
+ * dspark_cache_workspace_size().
+ * Limits: R <= 8192, num_pages <= 4194304, max_pages * page_size < 2^31, n_pools <= 512.
+ * ---------------------------------------------------------------------------------- */
+DSPARK_API size_t dspark_cache_workspace_size(int R, int num_pages);
+
+/* Slot dst[f] (empty) becomes a copy of slot src[f]: it holds the same pages, whose counts
+ * grow by one; no page is copied until dspark_cache_reserve has one written.  A pair whose
+ * dst is not empty, appears earlier in dst, or whose src is also a dst is reported and
+ * skipped.  F = 0 does nothing. */
+DSPARK_API dspark_status dspark_cache_fork(
+    int F, int R, int num_pages, int page_size, int max_pages, int64_t table_stride, int32_t* page_table,
+    int32_t* seq_len, int32_t* ref_count, const int32_t* src, const int32_t* dst, void* workspace, size_t ws_bytes,
+    void* stream);
+
+/* Room for n_new[r] more tokens in every slot, before their keys and values are written:
+ * seq_len grows by n_new, and pages are taken for what its last page cannot hold.  If that
+ * last page is partly filled and shared (ref_count > 1), the slot first gets a copy of its
+ * own: copies_out[r] = (old page, new page), else (-1,-1), and the page is copied in every
+ * pool.  Pages are handed out lowest index first, to the slots in order (a copy before the
+ * slot's further pages).  A slot is granted all it asked for (granted_out[r] = n_new[r]) or,
+ * if the slots up to it ask for more pages than are free or its table row is too short,
+ * nothing (granted_out[r] = 0 and the slot is unchanged).  n_pools may be 0. */
+DSPARK_API dspark_status dspark_cache_reserve(
+    int R, int num_pages, int page_size, int max_pages, int64_t table_stride, int32_t* page_table, int32_t* seq_len,
+    int32_t* ref_count, const int32_t* n_new, int32_t* granted_out, int32_t* copies_out, int n_pools,
+    void* const* pools, size_t page_bytes, void* workspace, size_t ws_bytes, void* stream);
+
+/* Writes the keys and values of the last tokens of every slot into one layer's pools: rows
+ * q_start[r] .. q_start[r+1] - 1 of k and v [T,Hkv,D] are the slot's last positions.
+ * granted (NULL: all) skips slots whose entry is 0.  k and v have strides between tokens and
+ * heads.  dtype_in is DSPARK_BF16 or DSPARK_F16; dtype_kv the same, or DSPARK_E4M3: then
+ * element x of head h is stored as x / scale[h], rounded to nearest even and held within
+ * +-448 (k_scale, v_scale [Hkv] > 0; they must be NULL otherwise).  T = 0 does nothing. */
+DSPARK_API dspark_status dspark_cache_write(
+    int T, int R, int Hkv, int D, int num_pages, int page_size, int max_pages, int dtype_in, int dtype_kv,
+    const void* k, const void* v, int64_t in_stride_token, int64_t in_stride_head, void* k_pool, void* v_pool,
+    int64_t page_stride, int64_t head_stride, int64_t token_stride, const int32_t* page_table, int64_t table_stride,
+    const int32_t* seq_len, const int32_t* q_start, const int32_t* granted, const float* k_scale,
+    const float* v_scale, void* workspace, size_t ws_bytes, void* stream);
+
+/* Slot r keeps its first new_len[r] tokens (a longer new_len changes nothing, a negative one
+ * is reported and counts as 0); pages past them leave the slot, and are free once no slot
+ * holds them.  After verification: new_len = old length + 1 + n_acc.  0 frees the slot. */
+DSPARK_API dspark_status dspark_cache_truncate(
+    int R, int num_pages, int page_size, int max_pages, int64_t table_stride, int32_t* page_table, int32_t* seq_len,
+    int32_t* ref_count, const int32_t* new_len, void* workspace, size_t ws_bytes, void* stream);
+
+/* Moves the pages in use to the lowest indexes: with U pages in use, the i-th used page at or
+ * past U (ascending) moves to the i-th free page below U, in every pool; tables and counts
+ * follow.  n_moves_out [1]: pages moved.  n_pools may be 0. */
+DSPARK_API dspark_status dspark_cache_compact(
+    int R, int num_pages, int page_size, int max_pages, int64_t table_stride, int32_t* page_table,
+    const int32_t* seq_len, int32_t* ref_count, int32_t* n_moves_out, int n_pools, void* const* pools,
+    size_t page_bytes, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Attention of each request's last tokens over its paged cache (one new token, or the
+ * verified block of a speculative round).
+ *
+ * Request r has queries t = q_start[r] .. q_start[r+1] - 1 (nq of them), the last nq
+ * positions of its context: query number i sits at position P = seq_len[r] - nq + i and
+ * sees positions j with max(0, P - window + 1) <= j <= P (window = 0: from 0).  Query head h
+ * reads cache head h / (Hq / Hkv):
+ *   s_j = scale * (q . k_j) * k_scale[head],  w = softmax(s),
+ *   out[t,h,:] = v_scale[head] * sum_j w_j v_j,  lse_out[t,h] = ln sum_j exp s_j.
+ * A query that sees nothing gets out 0 and lse -inf.  What a query does not see has no
+ * influence on it, NaN and infinities included.
+ *
+ *   q        [T,Hq,D] with strides between tokens and heads; DSPARK_BF16 or DSPARK_F16.
+ *   dtype_kv the type of q, or DSPARK_E4M3 with k_scale, v_scale [Hkv] (NULL otherwise).
+ *   max_q    an upper bound of every nq, 1..128; a request with more, or one whose queries
+ *            do not lie within [0,T), is reported and its rows are not written.
+ *   out      [T,Hq,D] of q's type, contiguous; lse_out [T,Hq] fp32 or NULL.
+ * Scores, softmax statistics and sums are fp32; the weights are rounded to q's type (16-bit
+ * floats, with an e4m3 cache to fp16) for the product with v.  Deterministic.
+ * Queries that belong to no request (before q_start[0], past q_start[R]) are not written.
+ * Limits: D a multiple of 16, 16..256; Hq a multiple of Hkv, Hq / Hkv <= 64; R <= 8192;
+ * max_pages * page_size < 2^31.
+ * Workspace: dspark_paged_attention_workspace_size() (0 for unsupported sizes).
+ * ---------------------------------------------------------------------------------- */
+DSPARK_API size_t dspark_paged_attention_workspace_size(int T, int R, int Hq, int Hkv, int D, int max_q);
+
+DSPARK_API dspark_status dspark_paged_attention(
+    int T, int R, int Hq, int Hkv, int D, int num_pages, int page_size, int max_pages, int max_q, int dtype_q,
+    int dtype_kv, const void* q, int64_t q_stride_token, int64_t q_stride_head, const void* k_pool,
+    const void* v_pool, int64_t page_stride, int64_t head_stride, int64_t token_stride, const int32_t* page_table,
+    int64_t table_stride, const int32_t* seq_len, const int32_t* q_start, float scale, const float* k_scale,
+    const float* v_scale, int window, void* out, float* lse_out, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -14,9 +14,11 @@ import torch
 
 from . import build as _build
 
-F32, BF16 = 0, 1
+F32, BF16, F16, E4M3 = 0, 1, 2, 3
 EARLY_STOP, FULL_SEARCH, CAPACITY_K, FIXED = 0, 1, 2, 3
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
+_LOGIT_DT = {**_DT, torch.float16: F16}
+_CACHE_DT = {torch.bfloat16: BF16, torch.float16: F16, torch.float8_e4m3fn: E4M3}
 
 
 class DSparkError(RuntimeError):
@@ -76,6 +78,30 @@ def _load_library():
     lib.dspark_sts_fit_workspace_size.argtypes = [i32] * 4
     lib.dspark_sts_fit.argtypes = [i32, i32, P, P, P, i32, i32, P, P, P, sz, P]
     lib.dspark_sts_fit.restype = i32
+    i64 = ctypes.c_int64
+    lib.dspark_token_logprobs.argtypes = [i32, i32, i64, i32, P, P, f32, i32] + [P] * 6
+    lib.dspark_token_logprobs.restype = i32
+    lib.dspark_token_logprobs_backward.argtypes = [i32, i32, i64, i64, i32, P, P, f32] + [P] * 6
+    lib.dspark_token_logprobs_backward.restype = i32
+    tables = [i32] * 4 + [i64] + [P] * 3
+    lib.dspark_cache_workspace_size.argtypes = [i32, i32]
+    lib.dspark_cache_workspace_size.restype = sz
+    lib.dspark_cache_fork.argtypes = [i32] + tables + [P, P, P, sz, P]
+    lib.dspark_cache_fork.restype = i32
+    lib.dspark_cache_reserve.argtypes = tables + [P, P, P, i32, P, sz, P, sz, P]
+    lib.dspark_cache_reserve.restype = i32
+    lib.dspark_cache_write.argtypes = ([i32] * 9 + [P, P, i64, i64, P, P, i64, i64, i64, P, i64] + [P] * 5
+                                       + [P, sz, P])
+    lib.dspark_cache_write.restype = i32
+    lib.dspark_cache_truncate.argtypes = tables + [P, P, sz, P]
+    lib.dspark_cache_truncate.restype = i32
+    lib.dspark_cache_compact.argtypes = tables + [P, i32, P, sz, P, sz, P]
+    lib.dspark_cache_compact.restype = i32
+    lib.dspark_paged_attention_workspace_size.argtypes = [i32] * 6
+    lib.dspark_paged_attention_workspace_size.restype = sz
+    lib.dspark_paged_attention.argtypes = ([i32] * 11 + [P, i64, i64, P, P, i64, i64, i64, P, i64, P, P, f32, P, P,
+                                           i32, P, P, P, sz, P])
+    lib.dspark_paged_attention.restype = i32
     for fn in ("dspark_markov_draft", "dspark_schedule", "dspark_verify", "dspark_workspace_status"):
         getattr(lib, fn).restype = i32
     return lib
@@ -602,3 +628,349 @@ class Round:
     def status(self) -> int:
         codes = [device_status(ws) for ws in (self.ws_draft, self.ws_sched, self.ws_verify)]
         return max(codes)
+
+
+# ------------------------------------------------------------- token log probabilities
+
+def _rows(t, name):
+    """A 2-D CUDA tensor whose rows are contiguous (any row stride)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise DSparkError(f"{name} must be a CUDA tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise DSparkError(f"{name} must be 2-D with contiguous rows")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise DSparkError(f"the rows of {name} overlap")
+    return t
+
+
+def _row_stride(t):
+    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+
+
+def _stride(t, i):
+    """The stride of dimension i (0 where it has one entry, whose stride means nothing)."""
+    return t.stride(i) if t.shape[i] > 1 else 0
+
+
+def _vector(t, name, n, dtype):
+    _cuda(t, name, dtype)
+    if t.numel() != n:
+        raise DSparkError(f"{name} must hold {n} values, got {t.numel()}")
+    return t
+
+
+def token_logprobs(logits, tokens, temperature=1.0, top_k=0, out=None, stream=None):
+    """Log probability of each row's token, the row's entropy and log-normaliser, and its
+    ``top_k`` best alternatives (dspark_token_logprobs).  logits [N,V] float32, bfloat16 or
+    float16 with any row stride; tokens [N] int32, rows with an id outside [0,V) (verification
+    writes -1) are skipped and hold NaN / -1.  Returns dict logprob, entropy, lse [N] and, with
+    top_k, top_ids, top_logprobs [N,top_k]."""
+    _rows(logits, "logits")
+    N, V = logits.shape
+    if logits.dtype not in _LOGIT_DT:
+        raise DSparkError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    _vector(tokens, "tokens", N, torch.int32)
+    top_k = int(top_k)
+    if out is None:
+        f = dict(dtype=torch.float32, device=logits.device)
+        out = dict(logprob=torch.empty(N, **f), entropy=torch.empty(N, **f), lse=torch.empty(N, **f))
+        if top_k > 0:
+            out["top_ids"] = torch.empty((N, top_k), dtype=torch.int32, device=logits.device)
+            out["top_logprobs"] = torch.empty((N, top_k), **f)
+    else:
+        for k in ("logprob", "entropy", "lse"):
+            _vector(out[k], k, N, torch.float32)
+        if top_k > 0:
+            _vector(out["top_ids"], "top_ids", N * top_k, torch.int32)
+            _vector(out["top_logprobs"], "top_logprobs", N * top_k, torch.float32)
+    st = lib.dspark_token_logprobs(N, V, _row_stride(logits), _LOGIT_DT[logits.dtype], _p(logits), _p(tokens),
+                                   float(temperature), top_k, _p(out["logprob"]), _p(out["entropy"]),
+                                   _p(out["lse"]), _p(out.get("top_ids")), _p(out.get("top_logprobs")),
+                                   _stream(stream))
+    _check(st, "dspark_token_logprobs")
+    return out
+
+
+def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad_entropy=None, temperature=1.0, out=None,
+                            stream=None):
+    """The gradient of sum(grad_logprob * logprob + grad_entropy * entropy) for ``logits``
+    (dspark_token_logprobs_backward), from token_logprobs' lse and entropy.  ``out`` [N,V] of the
+    logits' type may be the logits themselves."""
+    _rows(logits, "logits")
+    N, V = logits.shape
+    if logits.dtype not in _LOGIT_DT:
+        raise DSparkError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    _vector(tokens, "tokens", N, torch.int32)
+    for t, n in ((lse, "lse"), (entropy, "entropy"), (grad_logprob, "grad_logprob")):
+        _vector(t, n, N, torch.float32)
+    if grad_entropy is not None:
+        _vector(grad_entropy, "grad_entropy", N, torch.float32)
+    if out is None:
+        out = torch.empty((N, V), dtype=logits.dtype, device=logits.device)
+    elif _rows(out, "out").shape != logits.shape or out.dtype != logits.dtype:
+        raise DSparkError("out must have the logits' shape and type")
+    st = lib.dspark_token_logprobs_backward(N, V, _row_stride(logits), _row_stride(out), _LOGIT_DT[logits.dtype],
+                                            _p(logits), _p(tokens), float(temperature), _p(lse), _p(entropy),
+                                            _p(grad_logprob), _p(grad_entropy), _p(out), _stream(stream))
+    _check(st, "dspark_token_logprobs_backward")
+    return out
+
+
+# ------------------------------------------------------------------------- paged cache
+
+def cache_workspace_size(R, num_pages) -> int:
+    return int(lib.dspark_cache_workspace_size(R, num_pages))
+
+
+class CachePools:
+    """The pools whose pages move together (every layer's keys and values), as the pointer
+    list that dspark_cache_reserve and dspark_cache_compact take.  Keeps the tensors alive."""
+
+    def __init__(self, pools):
+        self.tensors = list(pools)
+        self.page_bytes, self.num_pages = 0, None
+        for i, t in enumerate(self.tensors):
+            _cuda(t, f"pools[{i}]")
+            if t.dim() < 2 or t.shape != self.tensors[0].shape or t.element_size() != self.tensors[0].element_size():
+                raise DSparkError("pools must share one shape [num_pages, ...] and element size")
+        if self.tensors:
+            t = self.tensors[0]
+            self.num_pages = t.shape[0]
+            self.page_bytes = t.numel() // max(1, t.shape[0]) * t.element_size()
+        self.array = (ctypes.c_void_p * max(1, len(self.tensors)))(*[t.data_ptr() for t in self.tensors])
+
+
+def cache_pools(pools) -> CachePools:
+    return CachePools(pools)
+
+
+def _tables(page_table, seq_len, ref_count, page_size):
+    """The leading arguments of the calls that change the tables."""
+    _rows(page_table, "page_table")
+    R, width = page_table.shape
+    if page_table.dtype != torch.int32:
+        raise DSparkError(f"page_table must be torch.int32, got {page_table.dtype}")
+    _vector(seq_len, "seq_len", R, torch.int32)
+    _cuda(ref_count, "ref_count", torch.int32)
+    return (R, ref_count.numel(), int(page_size), width, _row_stride(page_table), _p(page_table), _p(seq_len),
+            _p(ref_count))
+
+
+def _cache_ws(ws, R, num_pages, device):
+    return workspace(cache_workspace_size(R, num_pages), device) if ws is None else ws
+
+
+def _page_pools(pools, num_pages):
+    pools = pools if isinstance(pools, CachePools) else CachePools(pools or [])
+    if pools.num_pages not in (None, num_pages):
+        raise DSparkError(f"the pools have {pools.num_pages} pages, ref_count {num_pages}")
+    return pools
+
+
+def cache_fork(page_table, seq_len, ref_count, src, dst, page_size, ws=None, stream=None):
+    """Empty slots ``dst`` become copies of slots ``src`` that share their pages
+    (dspark_cache_fork).  src, dst [F] int32."""
+    t = _tables(page_table, seq_len, ref_count, page_size)
+    F = src.numel()
+    _vector(src, "src", F, torch.int32)
+    _vector(dst, "dst", F, torch.int32)
+    ws = _cache_ws(ws, t[0], t[1], page_table.device)
+    _check(lib.dspark_cache_fork(F, *t, _p(src), _p(dst), _p(ws), ws.numel(), _stream(stream)), "dspark_cache_fork")
+
+
+def cache_reserve(page_table, seq_len, ref_count, n_new, page_size, pools, out=None, ws=None, stream=None):
+    """Room for ``n_new`` [R] int32 more tokens in every slot, with a copy of each partly filled
+    shared page about to be written (dspark_cache_reserve).  ``pools``: cache_pools(...), a list
+    of pools, or None to change the tables only.  Returns dict granted [R], copies [R,2]."""
+    t = _tables(page_table, seq_len, ref_count, page_size)
+    R = t[0]
+    _vector(n_new, "n_new", R, torch.int32)
+    if out is None:
+        out = dict(granted=torch.empty(R, dtype=torch.int32, device=page_table.device),
+                   copies=torch.empty((R, 2), dtype=torch.int32, device=page_table.device))
+    else:
+        _vector(out["granted"], "granted", R, torch.int32)
+        _vector(out["copies"], "copies", 2 * R, torch.int32)
+    pools = _page_pools(pools, t[1])
+    ws = _cache_ws(ws, R, t[1], page_table.device)
+    _check(lib.dspark_cache_reserve(*t, _p(n_new), _p(out["granted"]), _p(out["copies"]), len(pools.tensors),
+                                    pools.array, pools.page_bytes, _p(ws), ws.numel(), _stream(stream)),
+           "dspark_cache_reserve")
+    return out
+
+
+def _pool_args(k_pool, v_pool, k_scale, v_scale):
+    """(num_pages, Hkv, page_size, D, type code) of two pools [num_pages, Hkv, page_size, D] with
+    contiguous rows and the same strides."""
+    for t, n in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise DSparkError(f"{n} must be a CUDA tensor")
+        if t.dim() != 4 or t.stride(3) != 1:
+            raise DSparkError(f"{n} must be [num_pages, Hkv, page_size, D] with contiguous rows")
+    if k_pool.dtype not in _CACHE_DT or k_pool.dtype != v_pool.dtype:
+        raise DSparkError("the pools must share a type: bfloat16, float16 or float8_e4m3fn")
+    if k_pool.shape != v_pool.shape or any(_stride(k_pool, i) != _stride(v_pool, i) for i in range(3)):
+        raise DSparkError("the pools must share their shape and strides")
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t is not None:
+            _vector(t, n, k_pool.shape[1], torch.float32)
+    return (*k_pool.shape, _CACHE_DT[k_pool.dtype])
+
+
+def _token_rows(t, name, H, D):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise DSparkError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or t.shape[1:] != (H, D) or (D > 1 and t.stride(2) != 1):
+        raise DSparkError(f"{name} must be [T, {H}, {D}] with contiguous rows")
+    return t
+
+
+def _lookup(page_table, seq_len, q_start):
+    _rows(page_table, "page_table")
+    if page_table.dtype != torch.int32:
+        raise DSparkError(f"page_table must be torch.int32, got {page_table.dtype}")
+    R = page_table.shape[0]
+    _vector(seq_len, "seq_len", R, torch.int32)
+    _vector(q_start, "q_start", R + 1, torch.int32)
+    return R
+
+
+def cache_write(k, v, k_pool, v_pool, page_table, seq_len, q_start, granted=None, k_scale=None, v_scale=None, ws=None,
+                stream=None):
+    """Writes the keys and values k, v [T,Hkv,D] of every slot's last tokens (rows q_start[r] ..
+    q_start[r+1]-1) into one layer's pools [num_pages,Hkv,page_size,D] (dspark_cache_write), after
+    cache_reserve made room.  Pools of float8_e4m3fn hold x / scale[head]."""
+    num_pages, H, page_size, D, kv = _pool_args(k_pool, v_pool, k_scale, v_scale)
+    _token_rows(k, "k", H, D)
+    _token_rows(v, "v", H, D)
+    if k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float16):
+        raise DSparkError("k and v must share a type: bfloat16 or float16")
+    if k.shape != v.shape or any(_stride(k, i) != _stride(v, i) for i in range(2)):
+        raise DSparkError("k and v must share their shape and strides")
+    R = _lookup(page_table, seq_len, q_start)
+    if granted is not None:
+        _vector(granted, "granted", R, torch.int32)
+    if ws is None:
+        ws = workspace(256, k_pool.device)
+    _check(lib.dspark_cache_write(k.shape[0], R, H, D, num_pages, page_size, page_table.shape[1],
+                                  _CACHE_DT[k.dtype], kv, _p(k), _p(v), _stride(k, 0), _stride(k, 1), _p(k_pool),
+                                  _p(v_pool), _stride(k_pool, 0), _stride(k_pool, 1), _stride(k_pool, 2), _p(page_table),
+                                  _row_stride(page_table), _p(seq_len), _p(q_start), _p(granted), _p(k_scale),
+                                  _p(v_scale), _p(ws), ws.numel(), _stream(stream)), "dspark_cache_write")
+
+
+def cache_truncate(page_table, seq_len, ref_count, new_len, page_size, ws=None, stream=None):
+    """Every slot keeps its first ``new_len`` [R] int32 tokens; pages past them are released
+    (dspark_cache_truncate).  0 frees the slot."""
+    t = _tables(page_table, seq_len, ref_count, page_size)
+    _vector(new_len, "new_len", t[0], torch.int32)
+    ws = _cache_ws(ws, t[0], t[1], page_table.device)
+    _check(lib.dspark_cache_truncate(*t, _p(new_len), _p(ws), ws.numel(), _stream(stream)), "dspark_cache_truncate")
+
+
+def cache_compact(page_table, seq_len, ref_count, page_size, pools, out=None, ws=None, stream=None):
+    """Moves the used pages to the lowest indexes, in the tables and in every pool
+    (dspark_cache_compact).  Returns the number of pages moved, [1] int32."""
+    t = _tables(page_table, seq_len, ref_count, page_size)
+    if out is None:
+        out = torch.empty(1, dtype=torch.int32, device=page_table.device)
+    else:
+        _vector(out, "out", 1, torch.int32)
+    pools = _page_pools(pools, t[1])
+    ws = _cache_ws(ws, t[0], t[1], page_table.device)
+    _check(lib.dspark_cache_compact(*t, _p(out), len(pools.tensors), pools.array, pools.page_bytes, _p(ws),
+                                    ws.numel(), _stream(stream)), "dspark_cache_compact")
+    return out
+
+
+def paged_attention_workspace_size(T, R, Hq, Hkv, D, max_q) -> int:
+    return int(lib.dspark_paged_attention_workspace_size(T, R, Hq, Hkv, D, max_q))
+
+
+def paged_attention(q, k_pool, v_pool, page_table, seq_len, q_start, max_q, scale, k_scale=None, v_scale=None,
+                    window=0, out=None, ws=None, stream=None):
+    """Attention of every slot's last tokens over its paged context (dspark_paged_attention).
+    q [T,Hq,D] bfloat16 or float16, rows q_start[r] .. q_start[r+1]-1 for slot r, at most
+    ``max_q`` a slot.  Returns dict out [T,Hq,D], lse [T,Hq] float32."""
+    num_pages, H, page_size, D, kv = _pool_args(k_pool, v_pool, k_scale, v_scale)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise DSparkError("q must be a CUDA tensor [T, Hq, D]")
+    T, Hq = q.shape[0], q.shape[1]
+    _token_rows(q, "q", Hq, D)
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise DSparkError(f"q must be bfloat16 or float16, got {q.dtype}")
+    R = _lookup(page_table, seq_len, q_start)
+    if out is None:
+        out = dict(out=torch.empty((T, Hq, D), dtype=q.dtype, device=q.device),
+                   lse=torch.empty((T, Hq), dtype=torch.float32, device=q.device))
+    else:
+        _vector(out["out"], "out", T * Hq * D, q.dtype)
+        if out.get("lse") is not None:
+            _vector(out["lse"], "lse", T * Hq, torch.float32)
+    if ws is None:
+        ws = workspace(paged_attention_workspace_size(T, R, Hq, H, D, max_q), q.device)
+    st = lib.dspark_paged_attention(T, R, Hq, H, D, num_pages, page_size, page_table.shape[1], int(max_q),
+                                    _CACHE_DT[q.dtype], kv, _p(q), q.stride(0), q.stride(1), _p(k_pool), _p(v_pool),
+                                    _stride(k_pool, 0), _stride(k_pool, 1), _stride(k_pool, 2), _p(page_table),
+                                    _row_stride(page_table), _p(seq_len), _p(q_start), float(scale), _p(k_scale),
+                                    _p(v_scale), int(window), _p(out["out"]), _p(out.get("lse")), _p(ws),
+                                    ws.numel(), _stream(stream))
+    _check(st, "dspark_paged_attention")
+    return out
+
+
+class PagedCache:
+    """A paged key-value cache: the tables of ``slots`` requests over ``num_pages`` pages, and
+    the pools [layers, num_pages, Hkv, page_size, D] of keys and values.  Methods launch kernels
+    only (buffers are made once), so a serving step over it can be captured as a CUDA graph."""
+
+    def __init__(self, slots, num_pages, page_size, max_pages, layers, Hkv, D, dtype=torch.bfloat16, device="cuda",
+                 k_scale=None, v_scale=None):
+        i32 = dict(dtype=torch.int32, device=device)
+        self.page_size = page_size
+        self.page_table = torch.full((slots, max_pages), -1, **i32)
+        self.seq_len = torch.zeros(slots, **i32)
+        self.ref_count = torch.zeros(num_pages, **i32)
+        self.k = torch.zeros((layers, num_pages, Hkv, page_size, D), dtype=dtype, device=device)
+        self.v = torch.zeros_like(self.k)
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.pools = cache_pools([*self.k.unbind(0), *self.v.unbind(0)])
+        self.plan = dict(granted=torch.empty(slots, **i32), copies=torch.empty((slots, 2), **i32))
+        self.moves = torch.empty(1, **i32)
+        self.ws = workspace(cache_workspace_size(slots, num_pages), device)
+        self._attention_ws = {}
+
+    def fork(self, src, dst, stream=None):
+        cache_fork(self.page_table, self.seq_len, self.ref_count, src, dst, self.page_size, ws=self.ws, stream=stream)
+
+    def reserve(self, n_new, stream=None):
+        return cache_reserve(self.page_table, self.seq_len, self.ref_count, n_new, self.page_size, self.pools,
+                             out=self.plan, ws=self.ws, stream=stream)
+
+    def write(self, layer, k, v, q_start, stream=None):
+        cache_write(k, v, self.k[layer], self.v[layer], self.page_table, self.seq_len, q_start,
+                    granted=self.plan["granted"], k_scale=self.k_scale, v_scale=self.v_scale, ws=self.ws,
+                    stream=stream)
+
+    def attend(self, layer, q, q_start, max_q, scale, window=0, out=None, stream=None):
+        """Each (T, Hq, max_q) keeps a workspace of its own, made on its first call."""
+        T, Hq, D = q.shape
+        key = (T, Hq, max_q)
+        if key not in self._attention_ws:
+            n = paged_attention_workspace_size(T, self.seq_len.numel(), Hq, self.k.shape[2], D, max_q)
+            self._attention_ws[key] = workspace(n, q.device)
+        return paged_attention(q, self.k[layer], self.v[layer], self.page_table, self.seq_len, q_start, max_q, scale,
+                               k_scale=self.k_scale, v_scale=self.v_scale, window=window, out=out,
+                               ws=self._attention_ws[key], stream=stream)
+
+    def truncate(self, new_len, stream=None):
+        cache_truncate(self.page_table, self.seq_len, self.ref_count, new_len, self.page_size, ws=self.ws,
+                       stream=stream)
+
+    def compact(self, stream=None):
+        return cache_compact(self.page_table, self.seq_len, self.ref_count, self.page_size, self.pools,
+                             out=self.moves, ws=self.ws, stream=stream)
+
+    def status(self) -> int:
+        """The worst device status of the cache's workspaces (0 OK, 1 bad device data)."""
+        return max(device_status(w) for w in (self.ws, *self._attention_ws.values()))
