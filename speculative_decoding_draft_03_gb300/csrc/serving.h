@@ -92,7 +92,7 @@ struct CacheWriteArgs {
 cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t s);
 
 struct AttentionArgs {
-  int T, R, Hq, Hkv, D, num_pages, page_size, max_pages, max_q, dtype_q, dtype_kv;
+  int T, R, Hq, Hkv, G, D, num_pages, page_size, max_pages, max_q, dtype_q, dtype_kv;  // G = Hq / Hkv
   const void* q;
   int64_t q_stride_token, q_stride_head;
   const void* k_pool;

@@ -340,8 +340,8 @@ dspark_status dspark_paged_attention(int T, int R, int Hq, int Hkv, int D, int n
   CHECK_ALIGN(out, 16);
   CHECK(check_strided(q, q_stride_token, q_stride_head, "q"));
   dspark::AttentionArgs a = {};
-  a.T = T; a.R = R; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.num_pages = num_pages; a.page_size = page_size;
-  a.max_pages = max_pages; a.max_q = max_q; a.dtype_q = dtype_q; a.dtype_kv = dtype_kv; a.q = q;
+  a.T = T; a.R = R; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.D = D; a.num_pages = num_pages;
+  a.page_size = page_size; a.max_pages = max_pages; a.max_q = max_q; a.dtype_q = dtype_q; a.dtype_kv = dtype_kv; a.q = q;
   a.q_stride_token = q_stride_token; a.q_stride_head = q_stride_head; a.k_pool = k_pool; a.v_pool = v_pool;
   a.page_stride = page_stride; a.head_stride = head_stride; a.token_stride = token_stride;
   a.page_table = page_table; a.table_stride = table_stride; a.seq_len = seq_len; a.q_start = q_start;
