@@ -630,34 +630,55 @@ class Round:
         return max(codes)
 
 
-# ------------------------------------------------------------- token log probabilities
+# The calls below take a few microseconds of GPU time at serving's small sizes, so their
+# marshalling is kept short: one look at each tensor, plain integers for pointers, and the
+# current stream as the raw handle.
 
-def _rows(t, name):
-    """A 2-D CUDA tensor whose rows are contiguous (any row stride)."""
+_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream_of is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream_of(_current_device())
+
+
+def _ptr(t, name, dtype, n=None):
+    """The address of a contiguous CUDA tensor of `dtype` (and n elements)."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous()
+            or (n is not None and t.numel() != n)):
+        _cuda(t, name, dtype)
+        raise DSparkError(f"{name} must hold {n} values, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _opt(t, name, dtype, n=None):
+    return None if t is None else _ptr(t, name, dtype, n)
+
+
+def _rows(t, name, dtype=None):
+    """(address, rows, columns, row stride) of a 2-D CUDA tensor with contiguous rows."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise DSparkError(f"{name} must be a CUDA tensor")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise DSparkError(f"{name} must be 2-D with contiguous rows")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise DSparkError(f"the rows of {name} overlap")
-    return t
+    if dtype is not None and t.dtype is not dtype:
+        raise DSparkError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise DSparkError(f"{name} must be 2-D")
+    n, m = t.shape
+    rs, cs = t.stride()
+    if m > 1 and cs != 1:
+        raise DSparkError(f"the rows of {name} must be contiguous")
+    if n <= 1 or rs < m:
+        if n > 1:
+            raise DSparkError(f"the rows of {name} overlap")
+        rs = m  # the stride of one row means nothing
+    return t.data_ptr(), n, m, rs
 
 
-def _row_stride(t):
-    return max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
-
-
-def _stride(t, i):
-    """The stride of dimension i (0 where it has one entry, whose stride means nothing)."""
-    return t.stride(i) if t.shape[i] > 1 else 0
-
-
-def _vector(t, name, n, dtype):
-    _cuda(t, name, dtype)
-    if t.numel() != n:
-        raise DSparkError(f"{name} must hold {n} values, got {t.numel()}")
-    return t
-
+# ------------------------------------------------------------- token log probabilities
 
 def token_logprobs(logits, tokens, temperature=1.0, top_k=0, out=None, stream=None):
     """Log probability of each row's token, the row's entropy and log-normaliser, and its
@@ -665,29 +686,24 @@ def token_logprobs(logits, tokens, temperature=1.0, top_k=0, out=None, stream=No
     float16 with any row stride; tokens [N] int32, rows with an id outside [0,V) (verification
     writes -1) are skipped and hold NaN / -1.  Returns dict logprob, entropy, lse [N] and, with
     top_k, top_ids, top_logprobs [N,top_k]."""
-    _rows(logits, "logits")
-    N, V = logits.shape
-    if logits.dtype not in _LOGIT_DT:
+    x, N, V, rs = _rows(logits, "logits")
+    dt = _LOGIT_DT.get(logits.dtype)
+    if dt is None:
         raise DSparkError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
-    _vector(tokens, "tokens", N, torch.int32)
-    top_k = int(top_k)
     if out is None:
         f = dict(dtype=torch.float32, device=logits.device)
         out = dict(logprob=torch.empty(N, **f), entropy=torch.empty(N, **f), lse=torch.empty(N, **f))
         if top_k > 0:
             out["top_ids"] = torch.empty((N, top_k), dtype=torch.int32, device=logits.device)
             out["top_logprobs"] = torch.empty((N, top_k), **f)
-    else:
-        for k in ("logprob", "entropy", "lse"):
-            _vector(out[k], k, N, torch.float32)
-        if top_k > 0:
-            _vector(out["top_ids"], "top_ids", N * top_k, torch.int32)
-            _vector(out["top_logprobs"], "top_logprobs", N * top_k, torch.float32)
-    st = lib.dspark_token_logprobs(N, V, _row_stride(logits), _LOGIT_DT[logits.dtype], _p(logits), _p(tokens),
-                                   float(temperature), top_k, _p(out["logprob"]), _p(out["entropy"]),
-                                   _p(out["lse"]), _p(out.get("top_ids")), _p(out.get("top_logprobs")),
-                                   _stream(stream))
-    _check(st, "dspark_token_logprobs")
+    f32 = torch.float32
+    st = lib.dspark_token_logprobs(
+        N, V, rs, dt, x, _ptr(tokens, "tokens", torch.int32, N), temperature, top_k,
+        _ptr(out["logprob"], "logprob", f32, N), _ptr(out["entropy"], "entropy", f32, N), _ptr(out["lse"], "lse", f32, N),
+        _ptr(out["top_ids"], "top_ids", torch.int32, N * top_k) if top_k > 0 else None,
+        _ptr(out["top_logprobs"], "top_logprobs", f32, N * top_k) if top_k > 0 else None, _raw_stream(stream))
+    if st:
+        _check(st, "dspark_token_logprobs")
     return out
 
 
@@ -696,23 +712,22 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad_ent
     """The gradient of sum(grad_logprob * logprob + grad_entropy * entropy) for ``logits``
     (dspark_token_logprobs_backward), from token_logprobs' lse and entropy.  ``out`` [N,V] of the
     logits' type may be the logits themselves."""
-    _rows(logits, "logits")
-    N, V = logits.shape
-    if logits.dtype not in _LOGIT_DT:
+    x, N, V, rs = _rows(logits, "logits")
+    dt = _LOGIT_DT.get(logits.dtype)
+    if dt is None:
         raise DSparkError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
-    _vector(tokens, "tokens", N, torch.int32)
-    for t, n in ((lse, "lse"), (entropy, "entropy"), (grad_logprob, "grad_logprob")):
-        _vector(t, n, N, torch.float32)
-    if grad_entropy is not None:
-        _vector(grad_entropy, "grad_entropy", N, torch.float32)
     if out is None:
         out = torch.empty((N, V), dtype=logits.dtype, device=logits.device)
-    elif _rows(out, "out").shape != logits.shape or out.dtype != logits.dtype:
-        raise DSparkError("out must have the logits' shape and type")
-    st = lib.dspark_token_logprobs_backward(N, V, _row_stride(logits), _row_stride(out), _LOGIT_DT[logits.dtype],
-                                            _p(logits), _p(tokens), float(temperature), _p(lse), _p(entropy),
-                                            _p(grad_logprob), _p(grad_entropy), _p(out), _stream(stream))
-    _check(st, "dspark_token_logprobs_backward")
+    y, n, v, gs = _rows(out, "out", logits.dtype)
+    if n != N or v != V:
+        raise DSparkError("out must have the logits' shape")
+    f32 = torch.float32
+    st = lib.dspark_token_logprobs_backward(
+        N, V, rs, gs, dt, x, _ptr(tokens, "tokens", torch.int32, N), temperature, _ptr(lse, "lse", f32, N),
+        _ptr(entropy, "entropy", f32, N), _ptr(grad_logprob, "grad_logprob", f32, N),
+        _opt(grad_entropy, "grad_entropy", f32, N), y, _raw_stream(stream))
+    if st:
+        _check(st, "dspark_token_logprobs_backward")
     return out
 
 
@@ -728,7 +743,7 @@ class CachePools:
 
     def __init__(self, pools):
         self.tensors = list(pools)
-        self.page_bytes, self.num_pages = 0, None
+        self.n, self.page_bytes, self.num_pages = len(self.tensors), 0, None
         for i, t in enumerate(self.tensors):
             _cuda(t, f"pools[{i}]")
             if t.dim() < 2 or t.shape != self.tensors[0].shape or t.element_size() != self.tensors[0].element_size():
@@ -737,7 +752,7 @@ class CachePools:
             t = self.tensors[0]
             self.num_pages = t.shape[0]
             self.page_bytes = t.numel() // max(1, t.shape[0]) * t.element_size()
-        self.array = (ctypes.c_void_p * max(1, len(self.tensors)))(*[t.data_ptr() for t in self.tensors])
+        self.array = (ctypes.c_void_p * max(1, self.n))(*[t.data_ptr() for t in self.tensors])
 
 
 def cache_pools(pools) -> CachePools:
@@ -746,23 +761,19 @@ def cache_pools(pools) -> CachePools:
 
 def _tables(page_table, seq_len, ref_count, page_size):
     """The leading arguments of the calls that change the tables."""
-    _rows(page_table, "page_table")
-    R, width = page_table.shape
-    if page_table.dtype != torch.int32:
-        raise DSparkError(f"page_table must be torch.int32, got {page_table.dtype}")
-    _vector(seq_len, "seq_len", R, torch.int32)
-    _cuda(ref_count, "ref_count", torch.int32)
-    return (R, ref_count.numel(), int(page_size), width, _row_stride(page_table), _p(page_table), _p(seq_len),
-            _p(ref_count))
+    table, R, width, stride = _rows(page_table, "page_table", torch.int32)
+    return (R, ref_count.numel(), page_size, width, stride, table, _ptr(seq_len, "seq_len", torch.int32, R),
+            _ptr(ref_count, "ref_count", torch.int32))
 
 
-def _cache_ws(ws, R, num_pages, device):
-    return workspace(cache_workspace_size(R, num_pages), device) if ws is None else ws
+def _cache_ws(ws, t, like):
+    return workspace(cache_workspace_size(t[0], t[1]), like.device) if ws is None else ws
 
 
 def _page_pools(pools, num_pages):
-    pools = pools if isinstance(pools, CachePools) else CachePools(pools or [])
-    if pools.num_pages not in (None, num_pages):
+    if not isinstance(pools, CachePools):
+        pools = CachePools(pools or [])
+    if pools.n and pools.num_pages != num_pages:
         raise DSparkError(f"the pools have {pools.num_pages} pages, ref_count {num_pages}")
     return pools
 
@@ -772,10 +783,11 @@ def cache_fork(page_table, seq_len, ref_count, src, dst, page_size, ws=None, str
     (dspark_cache_fork).  src, dst [F] int32."""
     t = _tables(page_table, seq_len, ref_count, page_size)
     F = src.numel()
-    _vector(src, "src", F, torch.int32)
-    _vector(dst, "dst", F, torch.int32)
-    ws = _cache_ws(ws, t[0], t[1], page_table.device)
-    _check(lib.dspark_cache_fork(F, *t, _p(src), _p(dst), _p(ws), ws.numel(), _stream(stream)), "dspark_cache_fork")
+    ws = _cache_ws(ws, t, page_table)
+    st = lib.dspark_cache_fork(F, *t, _ptr(src, "src", torch.int32, F), _ptr(dst, "dst", torch.int32, F), ws.data_ptr(),
+                               ws.numel(), _raw_stream(stream))
+    if st:
+        _check(st, "dspark_cache_fork")
 
 
 def cache_reserve(page_table, seq_len, ref_count, n_new, page_size, pools, out=None, ws=None, stream=None):
@@ -784,55 +796,53 @@ def cache_reserve(page_table, seq_len, ref_count, n_new, page_size, pools, out=N
     of pools, or None to change the tables only.  Returns dict granted [R], copies [R,2]."""
     t = _tables(page_table, seq_len, ref_count, page_size)
     R = t[0]
-    _vector(n_new, "n_new", R, torch.int32)
     if out is None:
         out = dict(granted=torch.empty(R, dtype=torch.int32, device=page_table.device),
                    copies=torch.empty((R, 2), dtype=torch.int32, device=page_table.device))
-    else:
-        _vector(out["granted"], "granted", R, torch.int32)
-        _vector(out["copies"], "copies", 2 * R, torch.int32)
     pools = _page_pools(pools, t[1])
-    ws = _cache_ws(ws, R, t[1], page_table.device)
-    _check(lib.dspark_cache_reserve(*t, _p(n_new), _p(out["granted"]), _p(out["copies"]), len(pools.tensors),
-                                    pools.array, pools.page_bytes, _p(ws), ws.numel(), _stream(stream)),
-           "dspark_cache_reserve")
+    ws = _cache_ws(ws, t, page_table)
+    i32 = torch.int32
+    st = lib.dspark_cache_reserve(*t, _ptr(n_new, "n_new", i32, R), _ptr(out["granted"], "granted", i32, R),
+                                  _ptr(out["copies"], "copies", i32, 2 * R), pools.n, pools.array, pools.page_bytes,
+                                  ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    if st:
+        _check(st, "dspark_cache_reserve")
     return out
 
 
-def _pool_args(k_pool, v_pool, k_scale, v_scale):
-    """(num_pages, Hkv, page_size, D, type code) of two pools [num_pages, Hkv, page_size, D] with
+def _strides(t, shape):
+    """The leading strides (0 where a dimension has one entry, whose stride means nothing)."""
+    return [s if n > 1 else 0 for s, n in zip(t.stride(), shape)][:-1]
+
+
+def _pool_args(k_pool, v_pool):
+    """(shape, strides, type code, addresses) of two pools [num_pages, Hkv, page_size, D] with
     contiguous rows and the same strides."""
-    for t, n in ((k_pool, "k_pool"), (v_pool, "v_pool")):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise DSparkError(f"{n} must be a CUDA tensor")
-        if t.dim() != 4 or t.stride(3) != 1:
-            raise DSparkError(f"{n} must be [num_pages, Hkv, page_size, D] with contiguous rows")
-    if k_pool.dtype not in _CACHE_DT or k_pool.dtype != v_pool.dtype:
+    if not isinstance(k_pool, torch.Tensor) or not isinstance(v_pool, torch.Tensor) or not (k_pool.is_cuda and v_pool.is_cuda):
+        raise DSparkError("k_pool and v_pool must be CUDA tensors")
+    shape, kv = k_pool.shape, _CACHE_DT.get(k_pool.dtype)
+    if kv is None or v_pool.dtype is not k_pool.dtype:
         raise DSparkError("the pools must share a type: bfloat16, float16 or float8_e4m3fn")
-    if k_pool.shape != v_pool.shape or any(_stride(k_pool, i) != _stride(v_pool, i) for i in range(3)):
-        raise DSparkError("the pools must share their shape and strides")
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t is not None:
-            _vector(t, n, k_pool.shape[1], torch.float32)
-    return (*k_pool.shape, _CACHE_DT[k_pool.dtype])
+    if len(shape) != 4 or v_pool.shape != shape or k_pool.stride(3) != 1 or v_pool.stride(3) != 1:
+        raise DSparkError("the pools must share a shape [num_pages, Hkv, page_size, D] with contiguous rows")
+    strides = _strides(k_pool, shape)
+    if v_pool.stride() != k_pool.stride() and _strides(v_pool, shape) != strides:
+        raise DSparkError("the pools must share their strides")
+    return shape, strides, kv, k_pool.data_ptr(), v_pool.data_ptr()
 
 
 def _token_rows(t, name, H, D):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise DSparkError(f"{name} must be a CUDA tensor")
-    if t.dim() != 3 or t.shape[1:] != (H, D) or (D > 1 and t.stride(2) != 1):
-        raise DSparkError(f"{name} must be [T, {H}, {D}] with contiguous rows")
-    return t
-
-
-def _lookup(page_table, seq_len, q_start):
-    _rows(page_table, "page_table")
-    if page_table.dtype != torch.int32:
-        raise DSparkError(f"page_table must be torch.int32, got {page_table.dtype}")
-    R = page_table.shape[0]
-    _vector(seq_len, "seq_len", R, torch.int32)
-    _vector(q_start, "q_start", R + 1, torch.int32)
-    return R
+    """(address, tokens, token stride, head stride) of a CUDA tensor [T,H,D] of 16-bit floats
+    with contiguous rows (H, D None: any)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
+        raise DSparkError(f"{name} must be a CUDA tensor [T, heads, D]")
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float16:
+        raise DSparkError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    T, h, d = t.shape
+    st, sh, sd = t.stride()
+    if (H is not None and h != H) or d != D or sd != 1:
+        raise DSparkError(f"{name} must be [T, {'heads' if H is None else H}, {D}] with contiguous rows")
+    return t.data_ptr(), T, h, st if T > 1 else 0, sh if h > 1 else 0
 
 
 def cache_write(k, v, k_pool, v_pool, page_table, seq_len, q_start, granted=None, k_scale=None, v_scale=None, ws=None,
@@ -840,32 +850,33 @@ def cache_write(k, v, k_pool, v_pool, page_table, seq_len, q_start, granted=None
     """Writes the keys and values k, v [T,Hkv,D] of every slot's last tokens (rows q_start[r] ..
     q_start[r+1]-1) into one layer's pools [num_pages,Hkv,page_size,D] (dspark_cache_write), after
     cache_reserve made room.  Pools of float8_e4m3fn hold x / scale[head]."""
-    num_pages, H, page_size, D, kv = _pool_args(k_pool, v_pool, k_scale, v_scale)
-    _token_rows(k, "k", H, D)
-    _token_rows(v, "v", H, D)
-    if k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float16):
-        raise DSparkError("k and v must share a type: bfloat16 or float16")
-    if k.shape != v.shape or any(_stride(k, i) != _stride(v, i) for i in range(2)):
-        raise DSparkError("k and v must share their shape and strides")
-    R = _lookup(page_table, seq_len, q_start)
-    if granted is not None:
-        _vector(granted, "granted", R, torch.int32)
+    (P, H, ps, D), strides, kv, kp, vp = _pool_args(k_pool, v_pool)
+    ka = _token_rows(k, "k", H, D)
+    va = _token_rows(v, "v", H, D)
+    if k.dtype is not v.dtype or ka[1:] != va[1:]:
+        raise DSparkError("k and v must share their type, shape and strides")
+    table, R, width, ts = _rows(page_table, "page_table", torch.int32)
     if ws is None:
         ws = workspace(256, k_pool.device)
-    _check(lib.dspark_cache_write(k.shape[0], R, H, D, num_pages, page_size, page_table.shape[1],
-                                  _CACHE_DT[k.dtype], kv, _p(k), _p(v), _stride(k, 0), _stride(k, 1), _p(k_pool),
-                                  _p(v_pool), _stride(k_pool, 0), _stride(k_pool, 1), _stride(k_pool, 2), _p(page_table),
-                                  _row_stride(page_table), _p(seq_len), _p(q_start), _p(granted), _p(k_scale),
-                                  _p(v_scale), _p(ws), ws.numel(), _stream(stream)), "dspark_cache_write")
+    i32, f32 = torch.int32, torch.float32
+    st = lib.dspark_cache_write(ka[1], R, H, D, P, ps, width, _CACHE_DT[k.dtype], kv, ka[0], va[0], ka[3], ka[4], kp, vp,
+                                *strides, table, ts, _ptr(seq_len, "seq_len", i32, R),
+                                _ptr(q_start, "q_start", i32, R + 1), _opt(granted, "granted", i32, R),
+                                _opt(k_scale, "k_scale", f32, H), _opt(v_scale, "v_scale", f32, H), ws.data_ptr(),
+                                ws.numel(), _raw_stream(stream))
+    if st:
+        _check(st, "dspark_cache_write")
 
 
 def cache_truncate(page_table, seq_len, ref_count, new_len, page_size, ws=None, stream=None):
     """Every slot keeps its first ``new_len`` [R] int32 tokens; pages past them are released
     (dspark_cache_truncate).  0 frees the slot."""
     t = _tables(page_table, seq_len, ref_count, page_size)
-    _vector(new_len, "new_len", t[0], torch.int32)
-    ws = _cache_ws(ws, t[0], t[1], page_table.device)
-    _check(lib.dspark_cache_truncate(*t, _p(new_len), _p(ws), ws.numel(), _stream(stream)), "dspark_cache_truncate")
+    ws = _cache_ws(ws, t, page_table)
+    st = lib.dspark_cache_truncate(*t, _ptr(new_len, "new_len", torch.int32, t[0]), ws.data_ptr(), ws.numel(),
+                                   _raw_stream(stream))
+    if st:
+        _check(st, "dspark_cache_truncate")
 
 
 def cache_compact(page_table, seq_len, ref_count, page_size, pools, out=None, ws=None, stream=None):
@@ -874,12 +885,12 @@ def cache_compact(page_table, seq_len, ref_count, page_size, pools, out=None, ws
     t = _tables(page_table, seq_len, ref_count, page_size)
     if out is None:
         out = torch.empty(1, dtype=torch.int32, device=page_table.device)
-    else:
-        _vector(out, "out", 1, torch.int32)
     pools = _page_pools(pools, t[1])
-    ws = _cache_ws(ws, t[0], t[1], page_table.device)
-    _check(lib.dspark_cache_compact(*t, _p(out), len(pools.tensors), pools.array, pools.page_bytes, _p(ws),
-                                    ws.numel(), _stream(stream)), "dspark_cache_compact")
+    ws = _cache_ws(ws, t, page_table)
+    st = lib.dspark_cache_compact(*t, _ptr(out, "out", torch.int32, 1), pools.n, pools.array, pools.page_bytes,
+                                  ws.data_ptr(), ws.numel(), _raw_stream(stream))
+    if st:
+        _check(st, "dspark_cache_compact")
     return out
 
 
@@ -892,30 +903,24 @@ def paged_attention(q, k_pool, v_pool, page_table, seq_len, q_start, max_q, scal
     """Attention of every slot's last tokens over its paged context (dspark_paged_attention).
     q [T,Hq,D] bfloat16 or float16, rows q_start[r] .. q_start[r+1]-1 for slot r, at most
     ``max_q`` a slot.  Returns dict out [T,Hq,D], lse [T,Hq] float32."""
-    num_pages, H, page_size, D, kv = _pool_args(k_pool, v_pool, k_scale, v_scale)
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise DSparkError("q must be a CUDA tensor [T, Hq, D]")
-    T, Hq = q.shape[0], q.shape[1]
-    _token_rows(q, "q", Hq, D)
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise DSparkError(f"q must be bfloat16 or float16, got {q.dtype}")
-    R = _lookup(page_table, seq_len, q_start)
+    (P, H, ps, D), strides, kv, kp, vp = _pool_args(k_pool, v_pool)
+    qa, T, Hq, q_token, q_head = _token_rows(q, "q", None, D)
+    table, R, width, ts = _rows(page_table, "page_table", torch.int32)
     if out is None:
         out = dict(out=torch.empty((T, Hq, D), dtype=q.dtype, device=q.device),
                    lse=torch.empty((T, Hq), dtype=torch.float32, device=q.device))
-    else:
-        _vector(out["out"], "out", T * Hq * D, q.dtype)
-        if out.get("lse") is not None:
-            _vector(out["lse"], "lse", T * Hq, torch.float32)
     if ws is None:
         ws = workspace(paged_attention_workspace_size(T, R, Hq, H, D, max_q), q.device)
-    st = lib.dspark_paged_attention(T, R, Hq, H, D, num_pages, page_size, page_table.shape[1], int(max_q),
-                                    _CACHE_DT[q.dtype], kv, _p(q), q.stride(0), q.stride(1), _p(k_pool), _p(v_pool),
-                                    _stride(k_pool, 0), _stride(k_pool, 1), _stride(k_pool, 2), _p(page_table),
-                                    _row_stride(page_table), _p(seq_len), _p(q_start), float(scale), _p(k_scale),
-                                    _p(v_scale), int(window), _p(out["out"]), _p(out.get("lse")), _p(ws),
-                                    ws.numel(), _stream(stream))
-    _check(st, "dspark_paged_attention")
+    i32, f32 = torch.int32, torch.float32
+    st = lib.dspark_paged_attention(T, R, Hq, H, D, P, ps, width, max_q, _CACHE_DT[q.dtype], kv, qa, q_token, q_head, kp,
+                                    vp, *strides, table, ts, _ptr(seq_len, "seq_len", i32, R),
+                                    _ptr(q_start, "q_start", i32, R + 1), scale, _opt(k_scale, "k_scale", f32, H),
+                                    _opt(v_scale, "v_scale", f32, H), window,
+                                    _ptr(out["out"], "out", q.dtype, T * Hq * D),
+                                    _opt(out.get("lse"), "lse", f32, T * Hq), ws.data_ptr(), ws.numel(),
+                                    _raw_stream(stream))
+    if st:
+        _check(st, "dspark_paged_attention")
     return out
 
 

@@ -406,18 +406,10 @@ __global__ void __launch_bounds__(256) cache_write_kernel(CacheWriteArgs a) {
   }
 }
 
-int sm_count() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
-}
-
-template <typename F>
-cudaError_t allow_smem(F* kernel, size_t bytes) {
-  return bytes <= 48 * 1024 ? cudaSuccess
-                            : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
+// The planning kernels' shared memory grows with the pool and the slots; the limit that fits
+// the largest of both is set once.
+constexpr size_t kPlanSmem = 4 * (size_t)kMaxSlots + kMaxSlots + 8 * (size_t)(kMaxPages / 32 / 8);
+static_assert(kPlanSmem <= 227 * 1024, "the plan must fit into shared memory");
 
 }  // namespace
 
@@ -429,7 +421,8 @@ cudaError_t launch_cache_reserve(const CacheTables& t, const int32_t* n_new, int
                                  const PagePools& pools, cudaStream_t s) {
   const int ctas = plan_ctas(t.num_pages), words = slice_words(t.num_pages, ctas);
   const size_t smem = 4 * (size_t)t.R + 8 * (size_t)words + t.R;
-  cudaError_t e = allow_smem(cache_reserve_kernel, smem);
+  static std::atomic<uint64_t> done;
+  cudaError_t e = allow_smem(cache_reserve_kernel, kPlanSmem, done);
   if (e != cudaSuccess) return e;
   e = launch_chained(cache_reserve_kernel, dim3(ctas), dim3(kPlanThreads), smem, s, ctas, t, n_new, granted, copies,
                      words);
@@ -447,7 +440,8 @@ cudaError_t launch_cache_compact(const CacheTables& t, const CompactLists& l, in
                                  cudaStream_t s) {
   const int ctas = plan_ctas(t.num_pages), words = slice_words(t.num_pages, ctas);
   const size_t smem = 8 * (size_t)words;
-  cudaError_t e = allow_smem(compact_plan_kernel, smem);
+  static std::atomic<uint64_t> done;
+  cudaError_t e = allow_smem(compact_plan_kernel, kPlanSmem, done);
   if (e != cudaSuccess) return e;
   e = launch_chained(compact_plan_kernel, dim3(ctas), dim3(kPlanThreads), smem, s, ctas, t, l, n_moves, words);
   if (e != cudaSuccess) return e;

@@ -686,13 +686,6 @@ struct Shape {
   static constexpr int ctas = Q8 ? (DP == 256 ? 1 : 2) : (DP == 64 ? 2 : 1);  // per SM
 };
 
-int sm_count() {
-  int dev = 0, n = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-  return n > 0 ? n : 1;
-}
-
 constexpr int kMaxSms = 160;     // of the largest GB300 part; the scratch is sized without a device
 constexpr int kMaxWorkers = kMaxSms * 2 * 4;
 
@@ -703,7 +696,8 @@ cudaError_t launch(const AttentionArgs& a, void* scratch, cudaStream_t s) {
   using S = Shape<Q8, DP>;
   using C = Cfg<BFQ, Q8, DP, S::TK, S::warps, S::stages>;
   auto* kernel = attention_kernel<BFQ, Q8, DP, S::TK, S::warps, S::stages>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem);
+  static std::atomic<uint64_t> done;
+  cudaError_t e = allow_smem(kernel, C::smem, done);
   if (e != cudaSuccess) return e;
   const int grid = std::min(sm_count(), kMaxSms) * S::ctas, workers = grid * S::warps;
   unsigned char* at = static_cast<unsigned char*>(scratch);
