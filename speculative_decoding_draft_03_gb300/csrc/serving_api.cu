@@ -56,7 +56,7 @@ dspark_status check_logits(int N, int V, int64_t row_stride, int dtype, float te
   if (V > dspark::kMaxLogprobV) return fail(DSPARK_UNSUPPORTED_SHAPE, "V=%d exceeds %d", V, dspark::kMaxLogprobV);
   if (!is_float_type(dtype)) return fail(DSPARK_INVALID_ARG, "bad dtype %d", dtype);
   if (row_stride < V) return fail(DSPARK_INVALID_ARG, "row_stride %lld is below V=%d", (long long)row_stride, V);
-  if (!(temperature > 0.f) || !isfinite(temperature) || !isfinite(1.f / temperature))
+  if (!(temperature > 0.f) || !isfinite(temperature) || !isfinite(1.4426951f / temperature))
     return fail(DSPARK_INVALID_ARG, "temperature must be positive and finite");
   return DSPARK_OK;
 }
