@@ -6,7 +6,7 @@
 // base-2 softmax statistics about a running reference, r ~ max of x c (c = log2(e) / T):
 //   s = sum 2^u, w = sum 2^u u, u = x c - r;  lse = (r + log2 s) ln 2,
 //   entropy = (log2 s - w / s) ln 2,  ln p_v = (x_v c - r - log2 s) ln 2.
-// The best K ids come from the same pass.  Each 512-byte segment of the row leaves its
+// The best K ids come from the same pass.  Each 1 KB segment of the row leaves its
 // largest key in shared memory; the K best elements lie in the K segments with the largest
 // maxima (an element of any other segment has K larger ones before it; among equal maxima the
 // earlier segments), so only those few segments are read again, from the L2 cache.
@@ -25,7 +25,10 @@ namespace cg = cooperative_groups;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLargeLse = 1024.f;  // an lse beyond it is known to 2^-14 at best
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kUnroll = 4;           // 16-byte pieces in flight per thread
+constexpr int kPer = 2;              // 16-byte pieces of a segment per lane: segments of 1 KB
+constexpr int kSegPieces = 32 * kPer;
+constexpr int kSteps = 4;            // segments in flight per warp
+constexpr int kRing = kPer * kSteps * kThreads * 16;  // bytes
 constexpr int kSegs = 32;            // segments that are read again, at most (>= kMaxTopK)
 constexpr int kCand = 256;           // candidates that are ranked by counting, at most
 
@@ -118,6 +121,18 @@ struct Row {
   }
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ float max_of(const float (&x)[N]) {
+  float m = x[0];
+#pragma unroll
+  for (int i = 1; i + 1 < N; i += 2) m = max3(m, x[i], x[i + 1]);
+  return fmaxf(m, x[N - 1]);
+}
 // ------------------------------------------------------------------- statistics of a row
 
 // Softmax statistics about the reference r (in base 2).  r is held at kLowRef or above: a
@@ -199,6 +214,7 @@ struct TopShared {
   int count[2][kWarps];
   int n_segs, n_cand, ties;
   Best warp_best[kWarps];
+  alignas(16) uint32_t floor_buf[32];
 };
 
 // Block-wide sum of `mine`; `turn` alternates the two buffers, so one barrier is enough.
@@ -211,6 +227,34 @@ __device__ __forceinline__ int block_sum(int mine, int (*count)[kWarps], int& tu
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) sum += count[turn][w];
   return sum;
+}
+
+// A key that at least K of the block's per-thread values reach: the K-th largest of each warp's
+// few best (the block's K-th largest itself unless one warp holds more than that of them).  One
+// barrier; `buf` is free again after the caller's next barrier.
+constexpr int kWarpBest = 32 / kWarps;
+__device__ __forceinline__ uint32_t kth_floor(uint32_t v, int K, uint32_t* buf) {
+  static_assert(kWarpBest * kWarps == 32 && kMaxTopK <= 32, "one value per lane");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t mine = 0;
+#pragma unroll
+  for (int i = 0; i < kWarpBest; ++i) {
+    const uint32_t m = __reduce_max_sync(~0u, v);
+    if (lane == i) mine = m;
+    const uint32_t at = __ballot_sync(~0u, v == m);
+    if (lane == __ffs(at) - 1) v = 0;
+  }
+  if (lane < kWarpBest) buf[kWarpBest * warp + lane] = mine;
+  __syncthreads();
+  const uint32_t x = buf[lane];
+  int place = 0;
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    const uint4 w = *reinterpret_cast<const uint4*>(buf + j);
+    place += (w.x > x || (w.x == x && j < lane)) + (w.y > x || (w.y == x && j + 1 < lane)) +
+             (w.z > x || (w.z == x && j + 2 < lane)) + (w.w > x || (w.w == x && j + 3 < lane));
+  }
+  return __shfl_sync(~0u, x, __ffs(__ballot_sync(~0u, place == K - 1)) - 1);
 }
 
 // A key with between K and `most` of the counted keys at or above it, or (ties) the K-th
@@ -236,23 +280,25 @@ __device__ void slice_best(const Row<T>& row, int seg0, int n, const uint32_t* s
   int turn = 0;
   if (threadIdx.x < kMaxTopK) sh.result[threadIdx.x] = {0u, 0x7FFFFFFF};
   if (threadIdx.x == 0) sh.n_segs = sh.n_cand = 0;
+  // the thread's best segment; neighbouring segments (where likely ids gather) go to different
+  // warps
   uint32_t top = 0;
-  for (int i = threadIdx.x; i < n; i += kThreads) top = max(top, seg_key[i]);
-  top = __reduce_max_sync(~0u, top);
-  if (lane == 0) sh.warp_best[warp].key = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = max(top, sh.warp_best[w].key);
+  const int turned = lane * kWarps + warp;
+  for (int i = turned; i < n; i += kThreads) top = max(top, seg_key[i]);
 
   // 1. the segments worth another look
-  uint32_t floor_key = kLowestKey;
+  uint32_t floor_key = max(kth_floor(top, K, sh.floor_buf), kLowestKey);
   int n_at = n;
   if (n > kSegs) {
-    floor_key = bisect(kLowestKey, top + 1, K, kSegs, n_at, [&](uint32_t k) {
+    auto at_least = [&](uint32_t k) {
       int c = 0;
       for (int i = threadIdx.x; i < n; i += kThreads) c += seg_key[i] >= k;
       return block_sum(c, sh.count, turn);
-    });
+    };
+    n_at = at_least(floor_key);
+    if (n_at > kSegs) floor_key = bisect(floor_key, 0xFFFFFFFFu, K, kSegs, n_at, at_least);
+  } else {
+    __syncthreads();
   }
   if (n_at <= kSegs) {
     for (int i = threadIdx.x; i < n; i += kThreads)
@@ -273,51 +319,85 @@ __device__ void slice_best(const Row<T>& row, int seg0, int n, const uint32_t* s
   }
   __syncthreads();
 
-  // 2. their elements, in registers
-  constexpr int kMine = kSegs / kWarps;
+  // 2. their elements, in registers as they are stored
+  constexpr int kMine = kSegs / kWarps * kPer;  // pieces per thread
   const int segs = sh.n_segs;
-  uint32_t key[kMine][VE];
-  int id0[kMine];
+  uint4 raw[kMine];
+  int piece[kMine];  // -1: none
 #pragma unroll
   for (int j = 0; j < kMine; ++j) {
-    const int k = j * kWarps + warp;
-    float x[VE];
+    const int k = j / kPer * kWarps + warp;
+    piece[j] = k < segs ? (seg0 + sh.segs[k]) * kSegPieces + j % kPer * 32 + lane : -1;
+    raw[j] = make_uint4(0, 0, 0, 0);
+    if (k < segs && row.whole(piece[j])) raw[j] = *reinterpret_cast<const uint4*>(row.at + row.first(piece[j]));
+  }
+  // f(key, id) of every element of this thread
+  auto each = [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < VE; ++i) key[j][i] = 0;
-    id0[j] = 0;
-    if (k < segs) {
-      const int piece = (seg0 + sh.segs[k]) * 32 + lane;
-      id0[j] = row.first(piece);
-      if (piece < row.pieces) {
-        row.load(piece, x);
+    for (int j = 0; j < kMine; ++j) {
+      if (piece[j] < 0 || piece[j] >= row.pieces) continue;
+      const int id0 = row.first(piece[j]);
+      if (row.whole(piece[j])) {
+        float x[VE];
+        Piece<T>::unpack(raw[j], x);
 #pragma unroll
+        for (int i = 0; i < VE; ++i) f(key_of(x[i]), id0 + i);
+      } else {
         for (int i = 0; i < VE; ++i)
-          if (id0[j] + i >= 0 && id0[j] + i < row.V) key[j][i] = key_of(x[i]);
+          if (id0 + i >= 0 && id0 + i < row.V) f(key_of(Piece<T>::value(row.at[id0 + i])), id0 + i);
       }
     }
-  }
+  };
 
   // 3. a threshold that leaves few of them
   auto at_least = [&](uint32_t k) {
     int c = 0;
-#pragma unroll
-    for (int j = 0; j < kMine; ++j)
-#pragma unroll
-      for (int i = 0; i < VE; ++i) c += key[j][i] >= k;
+    each([&](uint32_t key, int) { c += key >= k; });
     return block_sum(c, sh.count, turn);
   };
-  int n_el = at_least(floor_key);
-  if (n_el > kCand) floor_key = bisect(floor_key, top + 1, K, kCand, n_el, at_least);
-  if (n_el <= kCand) {
+  float most[kMine], best = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kMine; ++j)
+  for (int j = 0; j < kMine; ++j) {
+    most[j] = -INFINITY;
+    if (piece[j] < 0 || piece[j] >= row.pieces) continue;
+    float x[VE];
+    if (row.whole(piece[j])) Piece<T>::unpack(raw[j], x);
+    else row.load(piece[j], x);
+    most[j] = max_of(x);
+    best = fmaxf(best, most[j]);
+  }
+  floor_key = max(floor_key, kth_floor(key_of(best), K, sh.floor_buf));
+  const float floor = value_of(floor_key);
 #pragma unroll
-      for (int i = 0; i < VE; ++i)
-        if (key[j][i] >= floor_key) sh.cand[atomicAdd(&sh.n_cand, 1)] = {key[j][i], id0[j] + i};
+  for (int j = 0; j < kMine; ++j) {
+    if (piece[j] < 0 || piece[j] >= row.pieces || !(most[j] >= floor)) continue;
+    const int id0 = row.first(piece[j]);
+    float x[VE];
+    if (row.whole(piece[j])) Piece<T>::unpack(raw[j], x);
+    else row.load(piece[j], x);
+#pragma unroll
+    for (int i = 0; i < VE; ++i)
+      if (x[i] >= floor && id0 + i >= 0 && id0 + i < row.V) {
+        const int k = atomicAdd(&sh.n_cand, 1);
+        if (k < kCand) sh.cand[k] = {key_of(x[i]), id0 + i};
+      }
+  }
+  __syncthreads();
+  int n_el = sh.n_cand;
+  if (n_el > kCand) {  // too many: a higher threshold, if ties leave one
+    floor_key = bisect(floor_key, 0xFFFFFFFFu, K, kCand, n_el, at_least);
+    if (threadIdx.x == 0) sh.n_cand = 0;
     __syncthreads();
+    if (n_el <= kCand)
+      each([&](uint32_t key, int id) {
+        if (key >= floor_key) sh.cand[atomicAdd(&sh.n_cand, 1)] = {key, id};
+      });
+    __syncthreads();
+  }
+  if (n_el <= kCand) {
     // 4. each candidate's place is the number of those before it
-    if (threadIdx.x < n_el) {
-      const Best mine = sh.cand[threadIdx.x];
+    for (int k = threadIdx.x; k < n_el; k += kThreads) {
+      const Best mine = sh.cand[k];
       int place = 0;
       for (int i = 0; i < n_el; ++i) place += before(sh.cand[i], mine);
       if (place < K) sh.result[place] = mine;
@@ -329,13 +409,10 @@ __device__ void slice_best(const Row<T>& row, int seg0, int n, const uint32_t* s
   Best last = {0xFFFFFFFFu, -1};
   for (int k = 0; k < K; ++k) {
     Best b = {0u, 0x7FFFFFFF};
-#pragma unroll
-    for (int j = 0; j < kMine; ++j)
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const Best e = {key[j][i], id0[j] + i};
-        if (e.key != 0 && before(last, e) && before(e, b)) b = e;
-      }
+    each([&](uint32_t key, int id) {
+      const Best e = {key, id};
+      if (before(last, e) && before(e, b)) b = e;
+    });
 #pragma unroll
     for (int d = 16; d; d >>= 1) {
       const Best e = {__shfl_xor_sync(~0u, b.key, d), __shfl_xor_sync(~0u, b.id, d)};
@@ -355,11 +432,66 @@ __device__ void slice_best(const Row<T>& row, int seg0, int n, const uint32_t* s
 
 // --------------------------------------------------------------------------- forward
 
-// One cluster per row.  Dynamic shared memory: a key per segment of the slice (top_k > 0).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+// Packed pairs, each half rounded like its scalar operation.
+__device__ __forceinline__ void fma_pair(float& a, float& b, float x0, float x1, float y0, float y1, float z0, float z1) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(a), "=f"(b)
+      : "f"(x0), "f"(x1), "f"(y0), "f"(y1), "f"(z0), "f"(z1));
+}
+
+// A thread's statistics take in one piece.  The reference moves only when the piece passes it
+// by kSlack: any reference is right, and sums of up to 2^kSlack each stay well inside fp32.
+constexpr float kSlack = 16.f;
+struct Running {
+  float r, s0, s1, w0, w1;  // sums over even and odd elements
+};
+template <int N>
+__device__ __forceinline__ void take(Running& st, const float (&x)[N], float most, float c) {
+  const float top = most * c;
+  if (top > st.r + kSlack) {
+    const float d = st.r - top, f = ex2(d), dc = fmaxf(d, -200.f);
+    st.w0 = fmaf(dc, st.s0, st.w0) * f;
+    st.w1 = fmaf(dc, st.s1, st.w1) * f;
+    st.s0 *= f;
+    st.s1 *= f;
+    st.r = top;
+  }
+  float u[N], p[N];
+#pragma unroll
+  for (int i = 0; i < N; i += 2) fma_pair(u[i], u[i + 1], x[i], x[i + 1], c, c, -st.r, -st.r);
+#pragma unroll
+  for (int i = 0; i < N; ++i) p[i] = ex2(u[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) u[i] = fmaxf(u[i], -200.f);  // masked ids: 0 x -inf does not arise
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    add2f(st.s0, st.s1, p[i], p[i + 1]);
+    fma_pair(st.w0, st.w1, p[i], p[i + 1], u[i], u[i + 1], st.w0, st.w1);
+  }
+}
+
+// One cluster per row.  A thread copies the pieces that it will read into a ring of its own,
+// kSteps ahead (the ring holds what registers cannot: 32 KB per CTA in flight, no barriers).
+// Dynamic shared memory: the ring, and a key per segment of the slice (top_k > 0).
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, 4) logprob_kernel(LogprobArgs a, int slice) {
+__global__ void __launch_bounds__(kThreads, 3) logprob_kernel(LogprobArgs a, int slice) {
   constexpr int VE = Piece<T>::n;
-  extern __shared__ uint32_t seg_key[];
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  uint32_t* seg_key = reinterpret_cast<uint32_t*>(dynamic + kRing);
   __shared__ Stats2 part[kWarps];
   __shared__ Softmax slow_part[kWarps];
   __shared__ Stats2 mine;
@@ -383,55 +515,59 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(LogprobArgs a, int
   }
   const Row<T> row(a.logits, n * a.row_stride, a.V);
   const float c = a.inv_temp * kLog2e;
-  const int segs = (row.pieces + 31) / 32, seg0 = min(rank * slice, segs), seg1 = min(seg0 + slice, segs);
+  const int segs = (row.pieces + kSegPieces - 1) / kSegPieces, seg0 = min(rank * slice, segs), seg1 = min(seg0 + slice, segs);
 
-  Stats2 st = {kLowRef, 0.f, 0.f};
-  for (int g0 = seg0 + warp; g0 < seg1; g0 += kWarps * kUnroll) {
-    float x[kUnroll][VE];
-    const int last = g0 + (kUnroll - 1) * kWarps;
-    if (last < seg1 && row.first(g0 * 32) >= 0 && row.first(last * 32 + 32) <= row.V) {
-      uint4 v[kUnroll];
+  // segments [full0, full1) lie wholly in the row; the others (its ends) are read directly
+  const int full0 = row.shift ? 1 : 0, full1 = (a.V + row.shift) / (VE * kSegPieces);
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(dynamic) + threadIdx.x * 16;
+  const char* from = reinterpret_cast<const char*>(row.at - row.shift) + lane * 16;
+  int ahead = seg0 + warp;  // the next segment to copy
+  uint32_t put = 0, get = 0;
+  auto issue = [&]() {
+    if (ahead < seg1 && ahead >= full0 && ahead < full1) {
+      const char* src = from + (size_t)ahead * (kSegPieces * 16);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) v[u] = load_once16(row.at + row.first((g0 + u * kWarps) * 32 + lane));
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) Piece<T>::unpack(v[u], x[u]);
-    } else {
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int piece = (g0 + u * kWarps) * 32 + lane;
-        if (g0 + u * kWarps < seg1 && piece < row.pieces) {
-          row.load(piece, x[u]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < VE; ++i) x[u][i] = -INFINITY;
-        }
-      }
+      for (int u = 0; u < kPer; ++u) copy16(ring + put + u * (kThreads * 16), src + u * 512);
     }
+    ahead += kWarps;
+    put = put + kPer * kThreads * 16 == kRing ? 0 : put + kPer * kThreads * 16;
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kSteps - 1; ++i) issue();
+  Running run = {kLowRef, 0.f, 0.f, 0.f, 0.f};
+  for (int g = seg0 + warp; g < seg1; g += kWarps) {
+    issue();
+    copy_wait<kSteps - 1>();
     float most = -INFINITY;
+    if (g >= full0 && g < full1) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      float m = x[u][0];
-#pragma unroll
-      for (int i = 1; i < VE; ++i) m = fmaxf(m, x[u][i]);
-      most = fmaxf(most, m);
-      if (TOP) {
-        const uint32_t k = __reduce_max_sync(~0u, key_of(m));
-        if (lane == 0 && g0 + u * kWarps < seg1) seg_key[g0 + u * kWarps - seg0] = k;
+      for (int u = 0; u < kPer; ++u) {
+        float x[VE];
+        Piece<T>::unpack(lds16(ring + get + u * (kThreads * 16)), x);
+        const float m = max_of(x);
+        take(run, x, m, c);
+        most = fmaxf(most, m);
       }
+    } else {
+      for (int u = 0; u < kPer; ++u) {
+        const int piece = g * kSegPieces + u * 32 + lane;
+        if (piece >= row.pieces) break;
+        float x[VE];
+        row.load(piece, x);
+        const float m = max_of(x);
+        take(run, x, m, c);
+        most = fmaxf(most, m);
+      }
+      __syncwarp();
     }
-    const float r = fmaxf(st.r, most * c), d = st.r - r, f = ex2(d);
-    st.w = fmaf(fmaxf(d, -200.f), st.s, st.w) * f;
-    st.s *= f;
-    st.r = r;
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        const float e = fmaf(x[u][i], c, -r), p = ex2(e);
-        st.s += p;
-        st.w = fmaf(p, fmaxf(e, -200.f), st.w);
-      }
+    get = get + kPer * kThreads * 16 == kRing ? 0 : get + kPer * kThreads * 16;
+    if (TOP) {
+      const uint32_t k = __reduce_max_sync(~0u, key_of(most));
+      if (lane == 0) seg_key[g - seg0] = k;
+    }
   }
+  Stats2 st = join({run.r, run.s0, run.w0}, {run.r, run.s1, run.w1});
   st = warp_join(st);
   if (lane == 0) part[warp] = st;
   __syncthreads();
@@ -449,11 +585,11 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(LogprobArgs a, int
     for (int r = 1; r < ctas; ++r) st = join(st, *cluster.map_shared_rank(&mine, r));
     if (TOP) {
       const int total = ctas * a.top_k;  // <= 8 * 32 = kCand
-      if (threadIdx.x < total)
-        sh.cand[threadIdx.x] = cluster.map_shared_rank(&sh, threadIdx.x / a.top_k)->result[threadIdx.x % a.top_k];
+      for (int k = threadIdx.x; k < total; k += kThreads)
+        sh.cand[k] = cluster.map_shared_rank(&sh, k / a.top_k)->result[k % a.top_k];
       __syncthreads();
-      if (threadIdx.x < total) {
-        const Best me = sh.cand[threadIdx.x];
+      for (int k = threadIdx.x; k < total; k += kThreads) {
+        const Best me = sh.cand[k];
         int place = 0;
         for (int i = 0; i < total; ++i) place += before(sh.cand[i], me);
         if (me.key != 0 && place < a.top_k) sh.result[place] = me;
@@ -504,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprob_kernel(LogprobArgs a, int
 
 // --------------------------------------------------------------------------- backward
 
-constexpr int kBackPieces = 2;  // 16-byte pieces per thread
+constexpr int kBackPieces = 4;  // 16-byte pieces per thread
 
 // grid: (pieces of a row / (256 x kBackPieces), rows).  `together`: a row's logits and its
 // gradient lie alike on the 16-byte grid.
@@ -576,16 +712,21 @@ __global__ void __launch_bounds__(kThreads) logprob_backward_kernel(LogprobArgs 
     to[v] = Piece<T>::rounded(gradient(none ? 0.f : Piece<T>::value(row.at[v]), v));
 }
 
+constexpr size_t kMaxSmem = kRing + sizeof(uint32_t) * (kMaxLogprobV / 4 / kSegPieces + 2);
+
 template <typename T>
 cudaError_t forward(const LogprobArgs& a, cudaStream_t s) {
-  const int pieces = (a.V + 2 * Piece<T>::n - 2) / Piece<T>::n, segs = (pieces + 31) / 32;  // at most, any shift
+  const int pieces = (a.V + 2 * Piece<T>::n - 2) / Piece<T>::n, segs = (pieces + kSegPieces - 1) / kSegPieces;  // at most, any shift
   // CTAs per row: enough rows keep every SM busy by themselves; few are split over a cluster
   // while a slice keeps its threads in work
   int ctas = 1;
-  while (ctas < 8 && (long long)a.N * ctas < 4ll * sm_count() && segs > ctas * 2 * kWarps) ctas *= 2;
+  while (ctas < 8 && (long long)a.N * ctas < 2ll * sm_count() && segs > ctas * 2 * kWarps) ctas *= 2;
   const int slice = (segs + ctas - 1) / ctas;
-  const size_t smem = a.top_k > 0 ? sizeof(uint32_t) * slice : 0;
+  const size_t smem = kRing + (a.top_k > 0 ? sizeof(uint32_t) * slice : 0);
   auto* kernel = a.top_k > 0 ? logprob_kernel<T, true> : logprob_kernel<T, false>;
+  static std::atomic<uint64_t> done[2];
+  const cudaError_t e = allow_smem(kernel, kMaxSmem, done[a.top_k > 0]);
+  if (e != cudaSuccess) return e;
   return launch_chained(kernel, dim3((unsigned)a.N * ctas), dim3(kThreads), smem, s, ctas, a, slice);
 }
 
