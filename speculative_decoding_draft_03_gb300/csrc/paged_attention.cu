@@ -638,52 +638,96 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_cons
   }
 }
 
-// Joins the parts of the item that starts in worker blockIdx.x's range and goes past it.
+// Joins the parts of the item that starts in worker blockIdx.x's range and goes past it: four
+// of its rows per CTA (blockIdx.y), the parts dealt to groups of threads.
+constexpr int kJoinRows = 4, kJoinThreads = 256;
 template <bool BFQ, int DP>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ AttentionArgs a, Scratch scr) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttentionArgs a, Scratch scr) {
+  constexpr int kQuads = DP / 4;                                      // threads of a row
+  constexpr int kGroups = kJoinThreads / (kJoinRows * kQuads) > 0 ? kJoinThreads / (kJoinRows * kQuads) : 1;
+  constexpr int kSpan = kGroups * kJoinRows * kQuads / kJoinThreads;  // rows' quads per thread (DP = 256: 1)
+  static_assert(kSpan == 1, "one quad of one row per thread");
+  __shared__ float2 half[kJoinThreads / 32];
+  __shared__ float4 sums[kJoinThreads];
   griddep_wait();
   const Share k = scr.share[blockIdx.x];
   if (k.r < 0) return;
-  const long long per = *scr.per, w0 = blockIdx.x, w1 = (k.end - 1) / per;  // workers that hold a part
   const int G = a.G, rb = (k.nq * G + kRows - 1) / kRows, h = k.item / rb, row0 = (k.item - h * rb) * kRows;
-  const int rows = min(kRows, k.nq * G - row0);
-  const float vs = a.v_scale != nullptr ? a.v_scale[h] : 1.f;
-  constexpr int kQuads = DP / 4;  // threads of a row
-  for (int e = threadIdx.x; e < rows * kQuads; e += 128) {
-    const int row = e / kQuads, d = e % kQuads * 4;
-    float m = -INFINITY;
-    for (long long w = w0; w <= w1; ++w) m = fmaxf(m, scr.stats[(w * 2 + (w == w0)) * kRows + row].x);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (long long w = w0; w <= w1; ++w) {
-      const size_t at = (size_t)(w * 2 + (w == w0)) * kRows + row;
-      const float2 st = scr.stats[at];
-      const float f = ex2(st.x - ref);
-      const float4 v = *reinterpret_cast<const float4*>(scr.out + at * DP + d);
-      l = fmaf(f, st.y, l);
+  const int rows = min(kRows, k.nq * G - row0), first = blockIdx.y * kJoinRows;
+  if (first >= rows) return;
+  const int w0 = blockIdx.x, parts = (int)((k.end - 1) / *scr.per) - w0 + 1;  // part p: worker w0 + p
+  // the statistics of a row by 64 threads: maximum and sum
+  const int tid = threadIdx.x, lane = tid & 31, mine = tid >> 6;
+  auto stat = [&](int p, int row) { return scr.stats[((size_t)(w0 + p) * 2 + (p == 0)) * kRows + row]; };
+  float m = -INFINITY, l = 0.f;
+  if (first + mine < rows) {
+    for (int p = tid & 63; p < parts; p += 64) {
+      const float2 st = stat(p, first + mine);
+      const float now = fmaxf(m, st.x);
+      if (now > -INFINITY) l = l * ex2(m - now) + st.y * ex2(st.x - now);
+      else l += st.y;
+      m = now;
+    }
+  }
+  auto merge = [&](float m2, float l2) {
+    const float now = fmaxf(m, m2), ref = now == -INFINITY ? 0.f : now;
+    l = l * ex2(m - ref) + l2 * ex2(m2 - ref);
+    m = now;
+  };
+#pragma unroll
+  for (int d = 16; d; d >>= 1) {
+    const float m2 = __shfl_xor_sync(~0u, m, d), l2 = __shfl_xor_sync(~0u, l, d);
+    merge(m2, l2);
+  }
+  if (lane == 0) half[tid >> 5] = make_float2(m, l);
+  __syncthreads();
+
+  const int group = tid / (kJoinRows * kQuads), row = tid / kQuads % kJoinRows, d = tid % kQuads * 4;
+  const bool there = first + row < rows;
+  m = half[2 * row].x, l = half[2 * row].y;
+  merge(half[2 * row + 1].x, half[2 * row + 1].y);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (there) {
+#pragma unroll 4
+    for (int p = group; p < parts; p += kGroups) {
+      const float f = ex2(stat(p, first + row).x - ref);
+      const float4 v =
+          *reinterpret_cast<const float4*>(scr.out + (((size_t)(w0 + p) * 2 + (p == 0)) * kRows + first + row) * DP + d);
       o.x = fmaf(f, v.x, o.x);
       o.y = fmaf(f, v.y, o.y);
       o.z = fmaf(f, v.z, o.z);
       o.w = fmaf(f, v.w, o.w);
     }
-    const int rr = row0 + row, i = rr / G;
-    const size_t at = (size_t)(k.q0 + i) * a.Hq + h * G + rr - i * G;
-    const float f = l == 0.f ? 0.f : vs / l;
-    if (d < a.D)
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * a.D + d) =
-          make_uint2(Half16<BFQ>::pack(o.x * f, o.y * f), Half16<BFQ>::pack(o.z * f, o.w * f));
-    if (d == 0 && a.lse_out != nullptr) a.lse_out[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
+  if (kGroups > 1) {
+    sums[tid] = o;
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) {
+      const float4 v = sums[tid + g * kJoinRows * kQuads];
+      o.x += v.x, o.y += v.y, o.z += v.z, o.w += v.w;
+    }
+  }
+  if (!there) return;
+  const float vs = a.v_scale != nullptr ? a.v_scale[h] : 1.f;
+  const int rr = row0 + first + row, i = rr / G;
+  const size_t at = (size_t)(k.q0 + i) * a.Hq + h * G + rr - i * G;
+  const float f = l == 0.f ? 0.f : vs / l;
+  if (d < a.D)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at * a.D + d) =
+        make_uint2(Half16<BFQ>::pack(o.x * f, o.y * f), Half16<BFQ>::pack(o.z * f, o.w * f));
+  if (d == 0 && a.lse_out != nullptr) a.lse_out[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // Warps per SM and ring stages: together about 190 KB of copies in flight per SM.
 template <bool Q8, int DP>
 struct Shape {
-  static constexpr int TK = !Q8 && DP == 256 ? 16 : 32;
+  static constexpr int TK = !Q8 && DP >= 128 ? 16 : 32;
   static constexpr int warps = 4;
   static constexpr int stages = 3;
-  static constexpr int ctas = Q8 ? (DP == 256 ? 1 : 2) : (DP == 64 ? 2 : 1);  // per SM
+  static constexpr int ctas = DP == 256 ? 1 : 2;  // per SM
 };
 
 constexpr int kMaxSms = 160;     // of the largest GB300 part; the scratch is sized without a device
@@ -709,7 +753,9 @@ cudaError_t launch(const AttentionArgs& a, void* scratch, cudaStream_t s) {
                                      align256(sizeof(float2) * (size_t)kMaxWorkers * 2 * kRows));
   e = launch_chained(kernel, dim3(grid), dim3(S::warps * 32), C::smem, s, 1, a, scr);
   if (e != cudaSuccess) return e;
-  return launch_chained(join_kernel<BFQ, DP>, dim3(workers), dim3(128), 0, s, 1, a, scr);
+  const int rows = std::min(kRows, a.max_q * a.G);  // of an item, at most
+  return launch_chained(join_kernel<BFQ, DP>, dim3(workers, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, s, 1,
+                        a, scr);
 }
 
 template <bool BFQ, bool Q8>
