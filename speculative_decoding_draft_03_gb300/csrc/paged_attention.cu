@@ -1,21 +1,22 @@
 // paged_attention.cu — attention of each request's last tokens over its paged key-value cache.
 //
 // A pass reads every seen key and value once and does little arithmetic on it (with G query
-// heads per cache head and nq queries, nq G / 1 multiply-adds per element read), so what counts
-// is that all SMs stream the cache all the time, whatever the lengths:
-//   * The work is cut into units of TK tokens of one (request, cache head, 16 query rows) and
-//     the units, in order, are dealt out evenly to the warps of the grid.  A warp works on its
-//     own: its own ring of asynchronous copies, its own running maximum, sum and output; no
+// heads per cache head and nq queries, 2 nq G multiply-adds per element pair read), so what
+// counts is that all SMs stream the cache all the time, whatever the lengths:
+//   * The work is cut into units of TK tokens of one (request, cache head, block of query rows)
+//     and the units, in order, are dealt out evenly to the warps of the grid.  A warp works on
+//     its own: its own ring of asynchronous copies, its own running maximum, sum and output; no
 //     barrier between warps.  The cut follows from the lengths on the device (every CTA sums
 //     them), so the launch does not depend on them and can be captured.
-//   * Query rows (the G heads of a cache head, times the queries) are the 16 rows of the
-//     tensor-core product; both products run as m16n8k16 on 16-bit operands with fp32 sums.
-//     The weights go from the first product's result registers to the second's operands.
+//   * Both products run as m16n8k16 on 16-bit operands with fp32 sums, with the tokens (then the
+//     value columns) as the 16 rows and eight query rows (the G heads of a cache head, times the
+//     queries) as the 8 columns: one new token's few rows waste little, and NB groups of eight
+//     share every key and value read from shared memory.
 //   * A (request, head, rows) item that several warps share leaves partial outputs, which a
 //     second kernel joins in a fixed order; an item of one warp is written at once.
 // Element order inside a product is free as long as both operands agree, and is chosen so that
-// a thread reads 16 contiguous bytes of a key row (d = 32 b + 8 t ..) and the query fragments
-// are 16 contiguous bytes of a query row.
+// a thread reads 16 contiguous bytes of a key row at a time and the query fragments are 16
+// contiguous bytes of a query row.
 #include <algorithm>
 
 #include "serving.cuh"
@@ -40,11 +41,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
   return v;
 }
-__device__ __forceinline__ uint2 lds8(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
 __device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -52,6 +48,12 @@ __device__ __forceinline__ void ldmatrix_t(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(a));
+}
+// Transposes an 8 x 8 matrix of 16-bit elements spread over the warp (row g in lanes 4 g ..).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -107,14 +109,12 @@ __device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t two) {
 // ------------------------------------------------------------------------------- the plan
 
 struct Request {
-  int len, nq, q0, first;  // first: the first position that any of its queries sees
-  int chunks, blocks;      // units of a (head, 16 query rows) item, and such items per head
+  int len, nq, q0, first;  // first: where its units begin, a multiple of TK at or before what it sees
+  int chunks, blocks;      // units of a (head, ROWS query rows) item, and such items per head
 };
 
-constexpr int kRows = 16;
-
 // chunks = 0: nothing to do (no queries, or invalid: reported).
-template <int TK>
+template <int TK, int ROWS>
 __device__ __forceinline__ Request request(const AttentionArgs& a, int r, bool report) {
   Request k;
   k.q0 = a.q_start[r];
@@ -129,9 +129,9 @@ __device__ __forceinline__ Request request(const AttentionArgs& a, int r, bool r
     return k;
   }
   if (k.nq == 0) return k;
-  if (a.window > 0) k.first = max(0, k.len - k.nq - a.window + 1);
+  if (a.window > 0) k.first = max(0, k.len - k.nq - a.window + 1) / TK * TK;
   k.chunks = max(1, (k.len - k.first + TK - 1) / TK);
-  k.blocks = (k.nq * a.G + kRows - 1) / kRows;
+  k.blocks = (k.nq * a.G + ROWS - 1) / ROWS;
   return k;
 }
 
@@ -143,8 +143,8 @@ struct Share {
 
 struct Scratch {
   Share* share;   // [workers] the item that starts in a worker's range and goes past it
-  float2* stats;  // [workers][2][16] (maximum in base 2, sum)
-  float* out;     // [workers][2][16][D]
+  float2* stats;  // [workers][2][rows] (maximum in base 2, sum)
+  float* out;     // [workers][2][rows][D]
   long long* per; // [1] units per worker
 };
 
@@ -153,40 +153,43 @@ constexpr int kMinUnits = 2;
 
 // --------------------------------------------------------------------------- the main kernel
 
-template <bool BF, bool Q8, int DP, int TK, int WARPS, int STAGES>
+// Shared memory of a warp: a ring of units, each the keys, then the values, as panels of 128
+// bytes of every token's row ([panel][TK][128]), whose 16-byte pieces are swapped by the row's
+// number: the reads below (16 bytes per thread, transposing loads) touch every bank once.
+template <bool Q8, int DP, int NB, int TK, int WARPS, int STAGES>
 struct Cfg {
   static constexpr int kBytes = Q8 ? 1 : 2;
-  static constexpr int row = DP * kBytes;          // bytes of a row in shared memory
-  static constexpr int tile = TK * row;            // keys, or values, of a unit
+  static constexpr int row = DP * kBytes;
+  static_assert(row % 128 == 0, "whole panels");
+  static constexpr int panels = row / 128;
+  static constexpr int panel = TK * 128;
+  static constexpr int tile = TK * row;  // keys, or values, of a unit
   static constexpr int stage = 2 * tile;
-  static constexpr int smem = WARPS * STAGES * stage;
-  static constexpr int chunks = row / 16;          // 16-byte pieces of a row
+  static constexpr int chunks = row / 16;  // 16-byte pieces of a row
+  static constexpr bool q_smem = NB * DP > 256;  // the queries' fragments do not fit into registers
+  static constexpr int q_bytes = q_smem ? NB * 8 * DP * 2 : 0;
+  static constexpr int per_warp = STAGES * stage + q_bytes;
+  static constexpr int smem = WARPS * per_warp;
 };
-
-// Where piece c of token row i lies: pieces are swapped within groups of eight so that the
-// reads below (16 bytes per thread for keys, transposing loads for values) touch every bank
-// once.
-template <bool Q8>
-__device__ __forceinline__ int key_piece(int i, int c) {
-  return Q8 ? c ^ ((i & 3) << 1) : c ^ ((i & 1) << 2);
+template <int PANEL>
+__device__ __forceinline__ uint32_t piece_at(int i, int c) {
+  return (uint32_t)((c >> 3) * PANEL + i * 128 + (((c & 7) ^ (i & 7)) << 4));
 }
+// Which element of a value row is row r (0..15) of output tile n: with 16-bit values tile n holds
+// 16 n .., with 8-bit ones (a thread reads piece g of a panel) rows g and g + 8 are neighbours.
 template <bool Q8>
-__device__ __forceinline__ int value_piece(int i, int c) {
-  return Q8 ? c ^ (((i >> 1) & 3) << 1) : c ^ (i & 7);
-}
-// Rows of 64 bytes hold four pieces only.
-template <int CHUNKS>
-__device__ __forceinline__ int held(int piece) {
-  return CHUNKS >= 8 ? piece : piece & (CHUNKS - 1);
+__device__ __forceinline__ int element(int n, int r) {
+  return Q8 ? n / 8 * 128 + 16 * (r & 7) + 2 * (n % 8) + (r >> 3) : 16 * n + r;
 }
 
-template <bool BFQ, bool Q8, int DP, int TK, int WARPS, int STAGES>
-__global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_constant__ AttentionArgs a, Scratch scr) {
-  using C = Cfg<BFQ, Q8, DP, TK, WARPS, STAGES>;
+template <bool BFQ, bool Q8, int DP, int NB, int TK, int WARPS, int STAGES, int CTAS>
+__global__ void __launch_bounds__(WARPS * 32, CTAS) attention_kernel(const __grid_constant__ AttentionArgs a, Scratch scr) {
+  using C = Cfg<Q8, DP, NB, TK, WARPS, STAGES>;
   using H = Half16<BFQ && !Q8>;  // type of the products
-  constexpr int NT = TK / 8;     // key tiles of 8 tokens
-  constexpr int DT = DP / 8;     // output tiles of 8 columns
-  constexpr int DB = DP / 32;    // blocks of 32 elements of a row
+  constexpr int ROWS = 8 * NB;
+  constexpr int MT = TK / 16;    // token tiles of 16
+  constexpr int DT = DP / 16;    // output tiles of 16 elements
+  constexpr int KS = DP / 16;    // steps of 16 elements of a row
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ long long scan[WARPS], start_off[WARPS];
   __shared__ int start_r[WARPS];
@@ -202,7 +205,7 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_cons
             r_hi = min(r_lo + slice, a.R);
   long long mine = 0;
   for (int r = r_lo; r < r_hi; ++r) {
-    const Request k = request<TK>(a, r, blockIdx.x == 0);
+    const Request k = request<TK, ROWS>(a, r, blockIdx.x == 0);
     mine += (long long)a.Hkv * k.blocks * k.chunks;
   }
   long long upto = mine;
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_cons
       long long off = u - (upto - mine);
       int r = r_lo;
       for (;; ++r) {
-        const Request k = request<TK>(a, r, false);
+        const Request k = request<TK, ROWS>(a, r, false);
         const long long n = (long long)a.Hkv * k.blocks * k.chunks;
         if (off < n) break;
         off -= n;
@@ -246,13 +249,13 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_cons
   // ---- the copying side: one unit after the other into a ring of stages
   const unsigned char* k_pool = static_cast<const unsigned char*>(a.k_pool);
   const unsigned char* v_pool = static_cast<const unsigned char*>(a.v_pool);
-  const uint32_t ring = smem_addr(smem) + warp * STAGES * C::stage;
+  const uint32_t ring = smem_addr(smem) + warp * C::per_warp, q_at = ring + STAGES * C::stage;
   struct Cursor {
     Request k;
     int r, item, items, chunk;
   };
   auto open = [&](Cursor& c) {
-    c.k = request<TK>(a, c.r, false);
+    c.k = request<TK, ROWS>(a, c.r, false);
     c.items = a.Hkv * c.k.blocks;
   };
   auto advance = [&](Cursor& c) {
@@ -273,12 +276,14 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_cons
   use.chunk = (int)(start_off[warp] % use.k.chunks);
   Cursor get = use;
 
-  // This lane's token of the unit at `get`: its page, one unit ahead of the copies.
-  int page = 0, pos = 0;
+  // This lane's token of the unit at `get`: its page, looked up one unit ahead of the copies.
+  int page = 0, pos = 0, slot = 0;
   auto look_up = [&]() {
-    pos = get.k.first + get.chunk * TK + (lane % TK);
+    pos = get.k.first + get.chunk * TK + lane % TK;
     page = -1;
-    if (get.r < a.R && pos < get.k.len) page = a.page_table[get.r * a.table_stride + pos / a.page_size];
+    const int nth = pos / a.page_size;
+    slot = pos - nth * a.page_size;
+    if (pos < get.k.len) page = a.page_table[get.r * a.table_stride + nth];
   };
   look_up();
   long long left = u_end - u_begin;  // units still to be copied
@@ -286,17 +291,13 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_cons
   auto issue = [&]() {
     if (left > 0) {
       --left;
-      int64_t from = -1;  // in 16-byte pieces; -1: nothing there, zeros instead
-      if (pos < get.k.len) {
-        if (page >= 0 && page < a.num_pages) {
-          const int h = get.k.blocks == 1 ? get.item : get.item / get.k.blocks;
-          from = ((int64_t)page * a.page_stride + (int64_t)h * a.head_stride + (int64_t)(pos % a.page_size) * a.token_stride) *
-                 C::kBytes / 16;
-        } else {
-          report_bad_input(a.status, kBadPage);
-        }
-      }
+      const int h = get.k.blocks == 1 ? get.item : get.item / get.k.blocks;
       const uint32_t at = ring + put * C::stage;
+      const bool there = pos < get.k.len && page >= 0 && page < a.num_pages;
+      if (pos < get.k.len && !there) report_bad_input(a.status, kBadPage);
+      int64_t from = -1;  // in 16-byte pieces; -1: nothing there, zeros instead
+      if (there)
+        from = ((int64_t)page * a.page_stride + (int64_t)h * a.head_stride + (int64_t)slot * a.token_stride) * C::kBytes / 16;
       constexpr int kPer = C::chunks < 32 ? 32 / C::chunks : 1;  // rows copied at a time
       const int c = lane % C::chunks;
       const bool inside = c * 16 < a.D * C::kBytes;
@@ -306,8 +307,8 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_cons
         const int64_t f = __shfl_sync(~0u, from, i);
         const bool take = f >= 0 && inside;
         const size_t off = take ? (size_t)(f + c) * 16 : 0;
-        copy16(at + i * C::row + held<C::chunks>(key_piece<Q8>(i, c)) * 16, k_pool + off, take);
-        copy16(at + C::tile + i * C::row + held<C::chunks>(value_piece<Q8>(i, c)) * 16, v_pool + off, take);
+        copy16(at + piece_at<C::panel>(i, c), k_pool + off, take);
+        copy16(at + C::tile + piece_at<C::panel>(i, c), v_pool + off, take);
       }
       put = put + 1 == STAGES ? 0 : put + 1;
       if (left > 0) {
@@ -319,38 +320,39 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_cons
   };
   for (int s = 0; s < STAGES - 1; ++s) issue();
 
-  // ---- the computing side
-  float o[DT][4], m[2], l[2];
-  uint32_t qf[DB][2][4];  // query fragments: 32-element block, half of it
-  int last[2], low[2];    // the positions that this thread's rows see: low..last
-  float c_row[2];         // scores in base 2: scale log2(e) (k_scale) (2^e of a scaled fp16 query row)
+  // ---- the computing side.  This thread's query rows are 8 nb + 2 t4 and the next, nb < NB.
+  float o[DT][NB][4], m[NB][2], l[NB][2];
+  uint32_t qf[C::q_smem ? 1 : NB][C::q_smem ? 1 : KS][2];  // query fragments
+  float c_row[Q8 && BFQ ? NB : 1][2];  // scores in base 2: scale log2(e) (k_scale) (2^e of a scaled fp16 query row)
   int stage = 0;
   bool fresh = true;  // the next unit opens an item
   long long item_begin = u_begin - use.chunk;
   for (long long u = u_begin; u < u_end; ++u) {
     const int h = use.k.blocks == 1 ? use.item : use.item / use.k.blocks;
-    const int row0 = (use.item - h * use.k.blocks) * kRows;
+    const int row0 = (use.item - h * use.k.blocks) * ROWS;
     if (fresh) {
       fresh = false;
 #pragma unroll
-      for (int i = 0; i < DT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-      m[0] = m[1] = -INFINITY;
-      l[0] = l[1] = 0.f;
+      for (int n = 0; n < DT; ++n)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) o[n][nb][0] = o[n][nb][1] = o[n][nb][2] = o[n][nb][3] = 0.f;
       const float c = a.scale * kLog2e * (Q8 ? a.k_scale[h] : 1.f);
+      c_row[0][0] = c_row[0][1] = c;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = row0 + g + 8 * j, i = row / G;
+      for (int nb = 0; nb < NB; ++nb) {
+        m[nb][0] = m[nb][1] = -INFINITY;
+        l[nb][0] = l[nb][1] = 0.f;
+        // The order of a row's elements in the steps follows the keys' reads: with 16-bit keys a
+        // thread takes pieces 2 t, 2 t + 1 of 8 elements of each panel, with 8-bit keys those of 16.
+        const int row = row0 + 8 * nb + g, i = row / G;
         const bool there = row < use.k.nq * G;
-        last[j] = there ? use.k.len - use.k.nq + i : -1;
-        low[j] = a.window > 0 ? max(0, last[j] - a.window + 1) : 0;
-        c_row[j] = c;
         const int64_t at = (int64_t)(use.k.q0 + i) * a.q_stride_token + (int64_t)(h * G + row - i * G) * a.q_stride_head;
-        uint4 raw[DB];
+        uint4 raw[KS / 2];
 #pragma unroll
-        for (int b = 0; b < DB; ++b) {
+        for (int b = 0; b < KS / 2; ++b) {
+          const int d = Q8 ? b / 4 * 128 + 32 * t4 + b % 4 * 8 : b / 2 * 64 + 16 * t4 + b % 2 * 8;
           raw[b] = make_uint4(0, 0, 0, 0);
-          if (there && 32 * b + 8 * t4 < a.D)
-            raw[b] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + 32 * b + 8 * t4);
+          if (there && d < a.D) raw[b] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at + d);
         }
         if (Q8 && BFQ) {
           // bf16 queries over an e4m3 cache: fp16 operands, the row scaled by a power of two to
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_cons
           // row's maximum is lost, far under the sums' rounding
           float top = 0.f;
 #pragma unroll
-          for (int b = 0; b < DB; ++b) {
+          for (int b = 0; b < KS / 2; ++b) {
             const uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -368,10 +370,11 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_cons
           top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
           int e2 = 0;
           if (top > 0.f && top < INFINITY) e2 = min(max(ilogbf(top), -126), 126);
-          const float down = ldexpf(1.f, -e2);
-          c_row[j] = c * ldexpf(1.f, e2);
+          const float down = ldexpf(1.f, -e2), up = c * ldexpf(1.f, e2);
+          c_row[Q8 && BFQ ? nb : 0][0] = __shfl_sync(~0u, up, 8 * t4);  // of row 2 t4, held by lanes 4 (2 t4) ..
+          c_row[Q8 && BFQ ? nb : 0][1] = __shfl_sync(~0u, up, 8 * t4 + 4);
 #pragma unroll
-          for (int b = 0; b < DB; ++b) {
+          for (int b = 0; b < KS / 2; ++b) {
             uint32_t w[4] = {raw[b].x, raw[b].y, raw[b].z, raw[b].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -380,11 +383,15 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_cons
           }
         }
 #pragma unroll
-        for (int b = 0; b < DB; ++b) {
-          qf[b][0][j] = raw[b].x;
-          qf[b][0][j + 2] = raw[b].y;
-          qf[b][1][j] = raw[b].z;
-          qf[b][1][j + 2] = raw[b].w;
+        for (int b = 0; b < KS / 2; ++b) {
+          if (C::q_smem) {  // this thread reads back what it wrote
+            sts16(q_at + ((nb * (KS / 2) + b) * 32 + lane) * 16, raw[b]);
+          } else {
+            qf[C::q_smem ? 0 : nb][C::q_smem ? 0 : 2 * b][0] = raw[b].x;
+            qf[C::q_smem ? 0 : nb][C::q_smem ? 0 : 2 * b][1] = raw[b].y;
+            qf[C::q_smem ? 0 : nb][C::q_smem ? 0 : 2 * b + 1][0] = raw[b].z;
+            qf[C::q_smem ? 0 : nb][C::q_smem ? 0 : 2 * b + 1][1] = raw[b].w;
+          }
         }
       }
     }
@@ -394,178 +401,215 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_cons
     __syncwarp();
     const uint32_t keys = ring + stage * C::stage, values = keys + C::tile;
 
-    // scores
-    float s[NT][4];
+    // scores: s[mt][nb] = 16 tokens x 8 rows (tokens g, g + 8; rows 2 t4, 2 t4 + 1)
+    float s[MT][NB][4];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int b = 0; b < DB; ++b) {
+      for (int nb = 0; nb < NB; ++nb) s[i][nb][0] = s[i][nb][1] = s[i][nb][2] = s[i][nb][3] = 0.f;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int i = 8 * j + g;
-        uint32_t x, y, z, w;
-        if (Q8) {
-          const int piece = held<C::chunks>(key_piece<Q8>(i, 2 * b + (t4 >> 1)));
-          const uint2 v = lds8(keys + i * C::row + piece * 16 + (t4 & 1) * 8);
-          x = e4m3_to_half2(v.x);
-          y = e4m3_to_half2(v.x >> 16);
-          z = e4m3_to_half2(v.y);
-          w = e4m3_to_half2(v.y >> 16);
+    for (int b = 0; b < C::chunks / 4; ++b) {  // pieces 2 t, 2 t + 1 of each panel
+      const int c = b / 2 * 8 + 2 * t4 + b % 2;
+      constexpr int kSteps = Q8 ? 4 : 2;  // steps that a piece feeds
+      uint32_t q[NB][kSteps][2];
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        if (C::q_smem) {
+#pragma unroll
+          for (int e = 0; e < kSteps / 2; ++e) {
+            const uint4 v = lds16(q_at + ((nb * (KS / 2) + b * (kSteps / 2) + e) * 32 + lane) * 16);
+            q[nb][2 * e][0] = v.x, q[nb][2 * e][1] = v.y, q[nb][2 * e + 1][0] = v.z, q[nb][2 * e + 1][1] = v.w;
+          }
         } else {
-          const uint4 v = lds16(keys + i * C::row + held<C::chunks>(key_piece<Q8>(i, 4 * b + t4)) * 16);
-          x = v.x, y = v.y, z = v.z, w = v.w;
+#pragma unroll
+          for (int e = 0; e < kSteps; ++e)
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+              q[nb][e][z] = qf[C::q_smem ? 0 : nb][C::q_smem ? 0 : kSteps * b + e][z];
         }
-        H::mma(s[j], qf[b][0], x, y);
-        H::mma(s[j], qf[b][1], z, w);
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const uint4 lo = lds16(keys + piece_at<C::panel>(16 * i + g, c));
+        const uint4 hi = lds16(keys + piece_at<C::panel>(16 * i + 8 + g, c));
+        const uint32_t x[4] = {lo.x, lo.y, lo.z, lo.w}, y[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int e = 0; e < kSteps; ++e) {
+          uint32_t k[4];
+          if (Q8) {
+            k[0] = e4m3_to_half2(x[e]), k[2] = e4m3_to_half2(x[e] >> 16);
+            k[1] = e4m3_to_half2(y[e]), k[3] = e4m3_to_half2(y[e] >> 16);
+          } else {
+            k[0] = x[2 * e % 4], k[2] = x[(2 * e + 1) % 4], k[1] = y[2 * e % 4], k[3] = y[(2 * e + 1) % 4];
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) H::mma(s[i][nb], k, q[nb][e][0], q[nb][e][1]);
+        }
       }
     }
 
     // mask and softmax about the running maximum
     const int p0 = use.k.first + use.chunk * TK;
-    float top[2] = {-INFINITY, -INFINITY};
+    // a unit that not every query sees whole
+    const bool edge = p0 + TK > use.k.len - use.k.nq + 1 || (a.window > 0 && p0 < use.k.len - a.window);
+    float top[NB][2];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int p = p0 + 8 * j + 2 * t4 + (e & 1), row = e >> 1;
-        const bool seen = p >= low[row] && p <= last[row];
-        s[j][e] = seen ? s[j][e] * c_row[row] : -INFINITY;
-        top[row] = fmaxf(top[row], s[j][e]);
+      for (int z = 0; z < 2; ++z) {
+        const float c = c_row[Q8 && BFQ ? nb : 0][z];
+        top[nb][z] = -INFINITY;
+        int last = 0x7FFFFFFF, low = 0;
+        if (edge) {
+          const int row = row0 + 8 * nb + 2 * t4 + z;
+          last = row < use.k.nq * G ? use.k.len - use.k.nq + row / G : -1;
+          if (a.window > 0) low = last - a.window + 1;
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = z; e < 4; e += 2) {
+            const int p = p0 + 16 * i + g + 8 * (e >> 1);
+            s[i][nb][e] = p >= low && p <= last ? s[i][nb][e] * c : -INFINITY;
+            top[nb][z] = fmaxf(top[nb][z], s[i][nb][e]);
+          }
       }
+    bool grows = false;
 #pragma unroll
-    for (int row = 0; row < 2; ++row) {
-      top[row] = fmaxf(top[row], __shfl_xor_sync(~0u, top[row], 1));
-      top[row] = fmaxf(top[row], __shfl_xor_sync(~0u, top[row], 2));
-    }
-    const bool grows = top[0] > m[0] || top[1] > m[1];
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) top[nb][z] = fmaxf(top[nb][z], __shfl_xor_sync(~0u, top[nb][z], d));
+        grows |= top[nb][z] > m[nb][z];
+      }
     if (__any_sync(~0u, grows)) {
 #pragma unroll
-      for (int row = 0; row < 2; ++row) {
-        const float now = fmaxf(m[row], top[row]);
-        const float f = m[row] == -INFINITY ? 0.f : ex2(m[row] - now);
-        m[row] = now;
-        l[row] *= f;
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int i = 0; i < DT; ++i) {
-          o[i][2 * row] *= f;
-          o[i][2 * row + 1] *= f;
+        for (int z = 0; z < 2; ++z) {
+          const float now = fmaxf(m[nb][z], top[nb][z]);
+          const float f = m[nb][z] == -INFINITY ? 0.f : ex2(m[nb][z] - now);
+          m[nb][z] = now;
+          l[nb][z] *= f;
+#pragma unroll
+          for (int n = 0; n < DT; ++n) {
+            o[n][nb][z] *= f;
+            o[n][nb][z + 2] *= f;
+          }
         }
-      }
     }
-    const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[j][e] = ex2(s[j][e] - ref[e >> 1]);
-        l[e >> 1] += s[j][e];
+      for (int z = 0; z < 2; ++z) {
+        const float ref = m[nb][z] == -INFINITY ? 0.f : m[nb][z];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = z; e < 4; e += 2) {
+            s[i][nb][e] = ex2(s[i][nb][e] - ref);
+            l[nb][z] += s[i][nb][e];
+          }
       }
 
-    // Rows that see different positions share this unit's values: a value that is not finite
-    // must not reach the rows that do not see it (0 x NaN).  Such a token is added on its own
-    // to the rows that see it, and its row is cleared for the product.
-    if (use.k.nq > 1 && (p0 + TK > use.k.len - use.k.nq + 1 || (a.window > 0 && p0 < use.k.len - a.window))) {
+    // Rows that see different positions share this unit's values: one that is not finite must not
+    // reach the rows that do not see it (0 x NaN).  Such a token is added on its own to the rows
+    // that see it, and its row is cleared for the product.
+    if (edge && (use.k.nq > 1 || a.window > 0)) {
       uint32_t odd = 0;  // bit i: token i holds a value that is not finite
       for (int i = 0; i < TK; ++i) {
         bool found = false;
-        for (int c = lane; c < C::row / 4; c += 32) {
-          uint32_t w;
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(values + i * C::row + c * 4));
-          if (Q8) {
+        for (int c = lane; c < C::chunks; c += 32) {
+          const uint4 v = lds16(values + piece_at<C::panel>(i, c));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) found |= ((w >> (8 * e)) & 0x7F) == 0x7F;
-          } else {
-            found |= (w & H::kExp) == H::kExp || ((w >> 16) & H::kExp) == H::kExp;
+          for (int e = 0; e < 4; ++e) {
+            if (Q8) {
+#pragma unroll
+              for (int b = 0; b < 4; ++b) found |= ((w[e] >> (8 * b)) & 0x7F) == 0x7F;
+            } else {
+              found |= (w[e] & H::kExp) == H::kExp || ((w[e] >> 16) & H::kExp) == H::kExp;
+            }
           }
         }
         if (__any_sync(~0u, found)) odd |= 1u << i;
       }
       while (odd) {
-        const int i = __ffs(odd) - 1;
+        const int at = __ffs(odd) - 1, p = p0 + at;
         odd &= odd - 1;
-        float w[2];
-        // weight of (row g, token i): held by lane 4 g + (i % 8) / 2
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          if (j == i / 8)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int row = 0; row < 2; ++row) {
-              const float even = __shfl_sync(~0u, s[j][2 * row], (lane & 28) + (i % 8) / 2);
-              const float oddv = __shfl_sync(~0u, s[j][2 * row + 1], (lane & 28) + (i % 8) / 2);
-              w[row] = i & 1 ? oddv : even;
-            }
+          for (int z = 0; z < 2; ++z) {
+            // weight of (token, row 2 t4 + z): held by lane 4 (token % 8) + t4
+            float w = 0.f;
 #pragma unroll
-        for (int n = 0; n < DT; ++n)
+            for (int i = 0; i < MT; ++i)
+              if (i == at / 16) {
+                const float first = __shfl_sync(~0u, s[i][nb][z], (at % 8) * 4 + t4);
+                const float second = __shfl_sync(~0u, s[i][nb][z + 2], (at % 8) * 4 + t4);
+                w = at % 16 < 8 ? first : second;
+              }
+            const int row = row0 + 8 * nb + 2 * t4 + z;
+            const int last = row < use.k.nq * G ? use.k.len - use.k.nq + row / G : -1;
+            const bool sees = p <= last && (a.window == 0 || p > last - a.window);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int d = Q8 ? (2 * t4 + (e & 1)) * (DP / 8) + n : 8 * n + 2 * t4 + (e & 1), row = e >> 1;
-            const int byte = d * C::kBytes;
-            const uint32_t at = values + i * C::row + held<C::chunks>(value_piece<Q8>(i, byte / 16)) * 16 + byte % 16;
-            float v;
-            if (Q8) {
-              uint16_t x;
-              asm volatile("{.reg .b32 t; ld.shared.u8 t, [%1]; cvt.u16.u32 %0, t;}" : "=h"(x) : "r"(at));
-              v = Half16<false>::lo(e4m3_to_half2(x));
-            } else {
-              uint16_t x;
-              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at));
-              v = H::lo(x);
-            }
-            const int p = p0 + i;
-            if (p >= low[row] && p <= last[row]) o[n][e] = fmaf(w[row], v, o[n][e]);
+            for (int n = 0; n < DT; ++n)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const int byte = element<Q8>(n, g + 8 * half) * C::kBytes;
+                const uint32_t from = values + piece_at<C::panel>(at, byte / 16) + byte % 16;
+                uint32_t x;
+                if (Q8) asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(from));
+                else asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(from));
+                const float v = Q8 ? Half16<false>::lo(e4m3_to_half2(x)) : H::lo(x);
+                if (sees) o[n][nb][z + 2 * half] = fmaf(w, v, o[n][nb][z + 2 * half]);
+              }
           }
         __syncwarp();
-        for (int c = lane; c < C::chunks; c += 32) sts16(values + i * C::row + c * 16, make_uint4(0, 0, 0, 0));
+        for (int c = lane; c < C::chunks; c += 32) sts16(values + piece_at<C::panel>(at, c), make_uint4(0, 0, 0, 0));
         __syncwarp();
       }
     }
 
-    // output += weights x values
+    // output (elements x rows) += values x weights
 #pragma unroll
-    for (int k = 0; k < TK / 16; ++k) {
-      const uint32_t p[4] = {H::pack(s[2 * k][0], s[2 * k][1]), H::pack(s[2 * k][2], s[2 * k][3]),
-                             H::pack(s[2 * k + 1][0], s[2 * k + 1][1]), H::pack(s[2 * k + 1][2], s[2 * k + 1][3])};
+    for (int k = 0; k < MT; ++k) {
+      uint32_t p[NB][2];  // weights, transposed: tokens 2 t4 .. (and 8 on), row g
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        p[nb][0] = transpose8(H::pack(s[k][nb][0], s[k][nb][1]));
+        p[nb][1] = transpose8(H::pack(s[k][nb][2], s[k][nb][3]));
+      }
       if (!Q8) {
-        // matrices (tokens 0-7 | 8-15) x (columns 0-7 | 8-15) of 16 columns
-        const int i = 16 * k + (lane & 7) + ((lane >> 3) & 1) * 8;
+        // matrices (tokens 0-7 | 8-15) x (elements 0-7 | 8-15) of a tile of 16 elements
+        const int i = 16 * k + (lane & 7) + (lane >> 4) * 8;
 #pragma unroll
-        for (int n = 0; n < DT; n += 2) {
+        for (int n = 0; n < DT; ++n) {
           uint32_t v[4];
-          ldmatrix_t(v, values + i * C::row + held<C::chunks>(value_piece<Q8>(i, n + (lane >> 4))) * 16);
-          H::mma(o[n], p, v[0], v[1]);
-          H::mma(o[n + 1], p, v[2], v[3]);
+          ldmatrix_t(v, values + piece_at<C::panel>(i, 2 * n + ((lane >> 3) & 1)));
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) H::mma(o[n][nb], v, p[nb][0], p[nb][1]);
         }
       } else {
-        // column n of output tile i is element n DP/8 + i: a thread reads DP/8 contiguous bytes
-        // of four token rows and pairs them up
-        constexpr int kRun = DP / 8;  // bytes
-        constexpr int kStep = kRun < 16 ? kRun : 16;
+        // a thread reads piece g of four token rows of each panel and pairs the bytes up
 #pragma unroll
-        for (int d0 = 0; d0 < kRun; d0 += kStep) {
-          uint32_t w[4][kStep / 4];
+        for (int b = 0; b < C::panels; ++b) {
+          uint32_t w[4][4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int i = 16 * k + 8 * (q >> 1) + 2 * t4 + (q & 1);
-            const int byte = g * kRun + d0;
-            const uint32_t at = values + i * C::row + held<C::chunks>(value_piece<Q8>(i, byte / 16)) * 16 + byte % 16;
-            if (kStep == 16) {
-              const uint4 v = lds16(at);
-              w[q][0] = v.x, w[q][1] = v.y, w[q][2 % (kStep / 4)] = v.z, w[q][3 % (kStep / 4)] = v.w;
-            } else {
-              const uint2 v = lds8(at);
-              w[q][0] = v.x, w[q][1 % (kStep / 4)] = v.y;
-            }
+            const uint4 v = lds16(values + piece_at<C::panel>(16 * k + 8 * (q >> 1) + 2 * t4 + (q & 1), 8 * b + g));
+            w[q][0] = v.x, w[q][1] = v.y, w[q][2] = v.z, w[q][3] = v.w;
           }
 #pragma unroll
-          for (int e = 0; e < kStep / 4; ++e) {
-            // bytes of the two tokens side by side: (r0[0] r1[0] r0[1] r1[1]), (r0[2] ...)
-            const uint32_t a0 = __byte_perm(w[0][e], w[1][e], 0x5140), a1 = __byte_perm(w[0][e], w[1][e], 0x7362);
-            const uint32_t b0 = __byte_perm(w[2][e], w[3][e], 0x5140), b1 = __byte_perm(w[2][e], w[3][e], 0x7362);
-            const int n = d0 + 4 * e;
-            H::mma(o[n], p, e4m3_to_half2(a0), e4m3_to_half2(b0));
-            H::mma(o[n + 1], p, e4m3_to_half2(a0 >> 16), e4m3_to_half2(b0 >> 16));
-            H::mma(o[n + 2], p, e4m3_to_half2(a1), e4m3_to_half2(b1));
-            H::mma(o[n + 3], p, e4m3_to_half2(a1 >> 16), e4m3_to_half2(b1 >> 16));
+          for (int e = 0; e < 8; ++e) {
+            // bytes 2 e, 2 e + 1 of the two tokens side by side: (r0[0] r1[0] r0[1] r1[1])
+            const uint32_t which = e & 1 ? 0x7362 : 0x5140;
+            const uint32_t x = __byte_perm(w[0][e / 2], w[1][e / 2], which), y = __byte_perm(w[2][e / 2], w[3][e / 2], which);
+            const uint32_t v[4] = {e4m3_to_half2(x), e4m3_to_half2(x >> 16), e4m3_to_half2(y), e4m3_to_half2(y >> 16)};
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) H::mma(o[8 * b + e][nb], v, p[nb][0], p[nb][1]);
           }
         }
       }
@@ -577,60 +621,72 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_cons
     if (use.chunk + 1 == use.k.chunks || u + 1 == u_end) {
       const long long item_end = item_begin + use.k.chunks;
 #pragma unroll
-      for (int row = 0; row < 2; ++row) {
-        l[row] += __shfl_xor_sync(~0u, l[row], 1);
-        l[row] += __shfl_xor_sync(~0u, l[row], 2);
-      }
-      if (item_begin >= u_begin && item_end <= u_end) {
-        const float vs = Q8 ? a.v_scale[h] : 1.f;
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int row = 0; row < 2; ++row) {
-          const int rr = row0 + g + 8 * row;
-          if (rr >= use.k.nq * G) continue;
-          const int i = rr / G;
-          const size_t at = (size_t)(use.k.q0 + i) * a.Hq + h * G + rr - i * G;
-          const float f = l[row] == 0.f ? 0.f : vs / l[row];
-          uint16_t* out = static_cast<uint16_t*>(a.out) + at * a.D;
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) l[nb][z] += __shfl_xor_sync(~0u, l[nb][z], d);
+      const bool whole = item_begin >= u_begin && item_end <= u_end;
+      // the worker's part 0 began before its range, part 1 begins in it
+      const int part = item_begin >= u_begin;
+      const size_t base = (size_t)(worker * 2 + part) * ROWS;
+      const float vs = Q8 ? a.v_scale[h] : 1.f;
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int r2 = 8 * nb + 2 * t4;  // this thread's rows r2, r2 + 1
+        if (whole) {
+          const float f0 = l[nb][0] == 0.f ? 0.f : vs / l[nb][0], f1 = l[nb][1] == 0.f ? 0.f : vs / l[nb][1];
           if (!Q8) {
+            // packed by rows, then transposed: row g, elements 2 t4 ..
+            const int rr = row0 + 8 * nb + g, i = rr / G;
+            uint16_t* out = static_cast<uint16_t*>(a.out) + ((size_t)(use.k.q0 + i) * a.Hq + h * G + rr - i * G) * a.D;
 #pragma unroll
-            for (int n = 0; n < DT; ++n)
-              if (8 * n < a.D)
-                *reinterpret_cast<uint32_t*>(out + 8 * n + 2 * t4) =
-                    Half16<BFQ>::pack(o[n][2 * row] * f, o[n][2 * row + 1] * f);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int n = 0; n < DT; n += 2) {
-                const int d = (2 * t4 + e) * (DP / 8) + n;
-                if (d < a.D)
-                  *reinterpret_cast<uint32_t*>(out + d) =
-                      Half16<BFQ>::pack(o[n][2 * row + e] * f, o[n + 1][2 * row + e] * f);
+            for (int n = 0; n < DT; ++n) {
+              const uint32_t x = transpose8(Half16<BFQ>::pack(o[n][nb][0] * f0, o[n][nb][1] * f1));
+              const uint32_t y = transpose8(Half16<BFQ>::pack(o[n][nb][2] * f0, o[n][nb][3] * f1));
+              if (rr < use.k.nq * G && 16 * n < a.D) {
+                *reinterpret_cast<uint32_t*>(out + 16 * n + 2 * t4) = x;
+                *reinterpret_cast<uint32_t*>(out + 16 * n + 8 + 2 * t4) = y;
               }
+            }
           }
-          if (t4 == 0 && a.lse_out != nullptr) a.lse_out[at] = l[row] == 0.f ? -INFINITY : (m[row] + log2f(l[row])) * kLn2;
-        }
-      } else {
-        // the worker's part 0 began before its range, part 1 begins in it
-        const int part = item_begin >= u_begin;
-        const size_t base = (size_t)(worker * 2 + part) * kRows;
 #pragma unroll
-        for (int row = 0; row < 2; ++row) {
-          if (t4 == 0) scr.stats[base + g + 8 * row] = make_float2(m[row], l[row]);
-          float* out = scr.out + (base + g + 8 * row) * DP;
+          for (int z = 0; z < 2; ++z) {
+            const int rr = row0 + r2 + z, i = rr / G;
+            if (rr >= use.k.nq * G) continue;
+            const size_t at = (size_t)(use.k.q0 + i) * a.Hq + h * G + rr - i * G;
+            if (Q8) {
+              uint16_t* out = static_cast<uint16_t*>(a.out) + at * a.D;
+              const float f = z ? f1 : f0;
 #pragma unroll
-          for (int n = 0; n < DT; ++n) {
-            if (!Q8) {
-              *reinterpret_cast<float2*>(out + 8 * n + 2 * t4) = make_float2(o[n][2 * row], o[n][2 * row + 1]);
-            } else {
-              out[(2 * t4) * (DP / 8) + n] = o[n][2 * row];
-              out[(2 * t4 + 1) * (DP / 8) + n] = o[n][2 * row + 1];
+              for (int n = 0; n < DT; ++n) {
+                const int d = element<Q8>(n, g);  // and the next one
+                if (d < a.D)
+                  *reinterpret_cast<uint32_t*>(out + d) = Half16<BFQ>::pack(o[n][nb][z] * f, o[n][nb][z + 2] * f);
+              }
+            }
+            if (g == 0 && a.lse_out != nullptr)
+              a.lse_out[at] = l[nb][z] == 0.f ? -INFINITY : (m[nb][z] + log2f(l[nb][z])) * kLn2;
+          }
+        } else {
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            if (g == 0) scr.stats[base + r2 + z] = make_float2(m[nb][z], l[nb][z]);
+            float* out = scr.out + (base + r2 + z) * DP;
+#pragma unroll
+            for (int n = 0; n < DT; ++n) {
+              if (Q8) {
+                *reinterpret_cast<float2*>(out + element<Q8>(n, g)) = make_float2(o[n][nb][z], o[n][nb][z + 2]);
+              } else {
+                out[element<Q8>(n, g)] = o[n][nb][z];
+                out[element<Q8>(n, g + 8)] = o[n][nb][z + 2];
+              }
             }
           }
         }
-        if (part == 1 && lane == 0)
-          scr.share[worker] = Share{use.r, use.item, use.k.q0, use.k.nq, item_begin, item_end};
       }
+      if (!whole && part == 1 && lane == 0)
+        scr.share[worker] = Share{use.r, use.item, use.k.q0, use.k.nq, item_begin, item_end};
       fresh = true;
       item_begin = item_end;
     }
@@ -641,7 +697,7 @@ __global__ void __launch_bounds__(WARPS * 32) attention_kernel(const __grid_cons
 // Joins the parts of the item that starts in worker blockIdx.x's range and goes past it: four
 // of its rows per CTA (blockIdx.y), the parts dealt to groups of threads.
 constexpr int kJoinRows = 4, kJoinThreads = 256;
-template <bool BFQ, int DP>
+template <bool BFQ, int DP, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttentionArgs a, Scratch scr) {
   constexpr int kQuads = DP / 4;                                      // threads of a row
   constexpr int kGroups = kJoinThreads / (kJoinRows * kQuads) > 0 ? kJoinThreads / (kJoinRows * kQuads) : 1;
@@ -652,13 +708,13 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   griddep_wait();
   const Share k = scr.share[blockIdx.x];
   if (k.r < 0) return;
-  const int G = a.G, rb = (k.nq * G + kRows - 1) / kRows, h = k.item / rb, row0 = (k.item - h * rb) * kRows;
-  const int rows = min(kRows, k.nq * G - row0), first = blockIdx.y * kJoinRows;
+  const int G = a.G, rb = (k.nq * G + ROWS - 1) / ROWS, h = k.item / rb, row0 = (k.item - h * rb) * ROWS;
+  const int rows = min(ROWS, k.nq * G - row0), first = blockIdx.y * kJoinRows;
   if (first >= rows) return;
   const int w0 = blockIdx.x, parts = (int)((k.end - 1) / *scr.per) - w0 + 1;  // part p: worker w0 + p
   // the statistics of a row by 64 threads: maximum and sum
   const int tid = threadIdx.x, lane = tid & 31, mine = tid >> 6;
-  auto stat = [&](int p, int row) { return scr.stats[((size_t)(w0 + p) * 2 + (p == 0)) * kRows + row]; };
+  auto stat = [&](int p, int row) { return scr.stats[((size_t)(w0 + p) * 2 + (p == 0)) * ROWS + row]; };
   float m = -INFINITY, l = 0.f;
   if (first + mine < rows) {
     for (int p = tid & 63; p < parts; p += 64) {
@@ -693,7 +749,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     for (int p = group; p < parts; p += kGroups) {
       const float f = ex2(stat(p, first + row).x - ref);
       const float4 v =
-          *reinterpret_cast<const float4*>(scr.out + (((size_t)(w0 + p) * 2 + (p == 0)) * kRows + first + row) * DP + d);
+          *reinterpret_cast<const float4*>(scr.out + (((size_t)(w0 + p) * 2 + (p == 0)) * ROWS + first + row) * DP + d);
       o.x = fmaf(f, v.x, o.x);
       o.y = fmaf(f, v.y, o.y);
       o.z = fmaf(f, v.z, o.z);
@@ -721,25 +777,36 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   if (d == 0 && a.lse_out != nullptr) a.lse_out[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-// Warps per SM and ring stages: together about 190 KB of copies in flight per SM.
-template <bool Q8, int DP>
+// Tokens per unit, warps, ring stages and CTAs per SM: 130 to 200 KB of ring per SM, and as many
+// warps as the registers of the outputs (DP NB / 8 per thread) leave.
+template <bool Q8, int DP, int NB>
 struct Shape {
   static constexpr int TK = !Q8 && DP >= 128 ? 16 : 32;
   static constexpr int warps = 4;
-  static constexpr int stages = 3;
+  static constexpr int stages = NB == 4 ? 2 : 3;
   static constexpr int ctas = DP == 256 ? 1 : 2;  // per SM
 };
 
-constexpr int kMaxSms = 160;     // of the largest GB300 part; the scratch is sized without a device
-constexpr int kMaxWorkers = kMaxSms * 2 * 4;
+constexpr int kMaxSms = 160;  // of the largest GB300 part; the scratch is sized without a device
+constexpr int kMaxWorkers = kMaxSms * 3 * 4;
 
-int padded(int D) { return D <= 64 ? 64 : (D <= 128 ? 128 : 256); }
+int padded(int D, bool q8) { return D <= 64 && !q8 ? 64 : (D <= 128 ? 128 : 256); }  // (8-bit panels hold 128 elements)
+// Groups of eight query rows per item: what the call's largest block needs, up to 32 rows (their
+// outputs fill the registers; 16 with rows of 256 elements).
+int groups(int D, int max_q, int G) {
+  const int rows = max_q * G;
+  return rows <= 8 ? 1 : (rows <= 16 || D > 128 ? 2 : 4);
+}
 
-template <bool BFQ, bool Q8, int DP>
+size_t share_bytes() { return align256(sizeof(Share) * (size_t)kMaxWorkers); }
+size_t stats_bytes(int rows) { return align256(sizeof(float2) * (size_t)kMaxWorkers * 2 * rows); }
+
+template <bool BFQ, bool Q8, int DP, int NB>
 cudaError_t launch(const AttentionArgs& a, void* scratch, cudaStream_t s) {
-  using S = Shape<Q8, DP>;
-  using C = Cfg<BFQ, Q8, DP, S::TK, S::warps, S::stages>;
-  auto* kernel = attention_kernel<BFQ, Q8, DP, S::TK, S::warps, S::stages>;
+  using S = Shape<Q8, DP, NB>;
+  using C = Cfg<Q8, DP, NB, S::TK, S::warps, S::stages>;
+  static_assert(S::ctas * S::warps <= kMaxWorkers / kMaxSms, "scratch");
+  auto* kernel = attention_kernel<BFQ, Q8, DP, NB, S::TK, S::warps, S::stages, S::ctas>;
   static std::atomic<uint64_t> done;
   cudaError_t e = allow_smem(kernel, C::smem, done);
   if (e != cudaSuccess) return e;
@@ -748,30 +815,37 @@ cudaError_t launch(const AttentionArgs& a, void* scratch, cudaStream_t s) {
   Scratch scr;
   scr.per = reinterpret_cast<long long*>(at);
   scr.share = reinterpret_cast<Share*>(at + 256);
-  scr.stats = reinterpret_cast<float2*>(at + 256 + align256(sizeof(Share) * (size_t)kMaxWorkers));
-  scr.out = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(scr.stats) +
-                                     align256(sizeof(float2) * (size_t)kMaxWorkers * 2 * kRows));
+  scr.stats = reinterpret_cast<float2*>(at + 256 + share_bytes());
+  scr.out = reinterpret_cast<float*>(at + 256 + share_bytes() + stats_bytes(8 * NB));
   e = launch_chained(kernel, dim3(grid), dim3(S::warps * 32), C::smem, s, 1, a, scr);
   if (e != cudaSuccess) return e;
-  const int rows = std::min(kRows, a.max_q * a.G);  // of an item, at most
-  return launch_chained(join_kernel<BFQ, DP>, dim3(workers, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0, s, 1,
-                        a, scr);
+  const int rows = std::min(8 * NB, a.max_q * a.G);  // of an item, at most
+  return launch_chained(join_kernel<BFQ, DP, 8 * NB>, dim3(workers, (rows + kJoinRows - 1) / kJoinRows), dim3(kJoinThreads), 0,
+                        s, 1, a, scr);
+}
+
+template <bool BFQ, bool Q8, int DP>
+cudaError_t launch(const AttentionArgs& a, void* scratch, cudaStream_t s) {
+  const int n = groups(a.D, a.max_q, a.G);
+  if (n == 1) return launch<BFQ, Q8, DP, 1>(a, scratch, s);
+  if constexpr (DP <= 128)
+    if (n == 4) return launch<BFQ, Q8, DP, 4>(a, scratch, s);
+  return launch<BFQ, Q8, DP, 2>(a, scratch, s);
 }
 
 template <bool BFQ, bool Q8>
 cudaError_t launch(const AttentionArgs& a, void* scratch, cudaStream_t s) {
-  switch (padded(a.D)) {
-    case 64: return launch<BFQ, Q8, 64>(a, scratch, s);
-    case 128: return launch<BFQ, Q8, 128>(a, scratch, s);
-    default: return launch<BFQ, Q8, 256>(a, scratch, s);
-  }
+  const int D = padded(a.D, Q8);
+  if constexpr (!Q8)
+    if (D == 64) return launch<BFQ, Q8, 64>(a, scratch, s);
+  return D == 128 ? launch<BFQ, Q8, 128>(a, scratch, s) : launch<BFQ, Q8, 256>(a, scratch, s);
 }
 
 }  // namespace
 
-size_t paged_attention_scratch(int, int, int, int, int D, int) {
-  return 256 + align256(sizeof(Share) * (size_t)kMaxWorkers) + align256(sizeof(float2) * (size_t)kMaxWorkers * 2 * kRows) +
-         sizeof(float) * (size_t)kMaxWorkers * 2 * kRows * padded(D);
+size_t paged_attention_scratch(int, int, int Hq, int Hkv, int D, int max_q) {
+  const int rows = 8 * groups(D, max_q, Hq / Hkv);
+  return 256 + share_bytes() + stats_bytes(rows) + sizeof(float) * (size_t)kMaxWorkers * 2 * rows * padded(D, true);
 }
 
 cudaError_t launch_paged_attention(const AttentionArgs& a, void* scratch, cudaStream_t s) {
