@@ -1,0 +1,683 @@
+// attention_wide.cu — attention of larger blocks of queries over a paged cache of 16-bit
+// floats, on the 5th-generation tensor cores.
+//
+// With many query rows per cache head (G heads times the verified block's queries) the products
+// outgrow the register-operand instructions; here both run as tcgen05.mma with the tokens, then
+// the value elements, as the 128 rows and the query rows as the N columns:
+//   S [128 tokens x N]   = K [128 tokens x D] . Q^T    (both K-major)
+//   O [128 elements x N] += V^T [elements x 128 tokens] . P   (both MN-major)
+// so that keys and values are used as they lie in the pages (panels of 128-byte rows, 128-byte
+// swizzle, by tensor copies), each weight is written once as part of a 16-byte piece of its
+// token's row, and the output leaves with its elements in neighbouring lanes.
+//   * One persistent CTA per SM: warp 0 copies, warp 1 issues the products, warps 2..9 do the
+//     softmax: a thread owns one token (its TMEM lane) and half of the columns.  S is double
+//     buffered; the copies run up to three tiles ahead of the products.
+//   * The softmax reference of a column moves only when a score passes it by 2^kSlack (any
+//     reference is right; the weights stay below 2^kSlack, inside fp16's range): a vote per
+//     tile replaces the maximum over the tokens, and the output is rescaled in TMEM only then.
+//   * The work is dealt out in tiles of 128 tokens as for the other kernel, a CTA per worker.
+// Every mbarrier wait is bounded; a wait that gives up reports DSPARK_TIMEOUT and the CTA winds
+// down (the softmax warps leave together, by a vote).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "attention.cuh"
+#include "attention_wide.h"
+
+namespace dspark {
+namespace {
+
+using namespace attention;
+
+constexpr int kTile = 128;  // tokens
+constexpr int kSoftmaxWarps = 8, kSoftmaxThreads = 32 * kSoftmaxWarps, kThreads = 64 + kSoftmaxThreads;
+constexpr float kSlack = 8.f;
+constexpr float kUnset = -1e30f;  // the reference of a column that has seen nothing: any score passes it
+constexpr long long kWaitCycles = 4000000000ll;  // ~2 s
+
+// ---------------------------------------------------------------------------- wrappers
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "n"(1 << 18)  // suspended up to 262 us at a time
+      : "memory");
+  return ok != 0;
+}
+// False (and the flag set) if the phase stays open for kWaitCycles, or another role gave up.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, DeviceStatus* st, int where) {
+  if (mbar_test(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_test(bar, parity)) {
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *abort_flag = 1;
+      report_timeout(st, where);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_test(bar, parity))
+    if (clock64() - t0 > kWaitCycles) return;
+}
+// A box of a pool, seen as [pages][heads][tokens][D].
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, uint32_t bar, int d, int token, int head,
+                                        int page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(d), "r"(token), "r"(head), "r"(page)
+      : "memory");
+}
+// Shared-memory matrix descriptor, 128-byte swizzle: start, leading and stride byte offsets in
+// units of 16 bytes, version 1, swizzle mode 2.
+__device__ __forceinline__ uint64_t sw128(uint32_t at, uint32_t leading, uint32_t stride) {
+  return (uint64_t)((at >> 4) & 0x3FFFu) | (uint64_t)((leading >> 4) & 0x3FFFu) << 16 |
+         (uint64_t)((stride >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// Instruction descriptor of kind::f16: fp32 sums, A and B both bf16 or both fp16, 128 x N.
+template <bool BF>
+__device__ constexpr uint32_t idesc(int N, bool a_mn_major, bool b_mn_major) {
+  return (1u << 4) | ((BF ? 1u : 0u) << 7) | ((BF ? 1u : 0u) << 10) | ((a_mn_major ? 1u : 0u) << 15) |
+         ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(desc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// 16 columns of this warp's lanes.
+__device__ __forceinline__ void tmem_load(uint32_t at, float* x) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
+      : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_store(uint32_t at, const float* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "f"(x[8]), "f"(x[9]),
+      "f"(x[10]), "f"(x[11]), "f"(x[12]), "f"(x[13]), "f"(x[14]), "f"(x[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Barriers of the softmax warps.
+__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory"); }
+__device__ __forceinline__ bool softmax_any(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "n"(kSoftmaxThreads)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// ------------------------------------------------------------------------- shared memory
+
+template <int DP, int N>
+struct Plan {
+  static constexpr int panels = DP / 64;
+  static constexpr int tile = panels * kTile * 128;  // keys, or values, of a tile
+  static constexpr int k_stages = DP == 64 ? 4 : 3, v_stages = DP == 64 ? 4 : (N == 128 ? 2 : 3);
+  static constexpr int tmem_cols = N == 32 ? 128 : (N == 64 ? 256 : 512);  // S twice, O: 3 N, a power of two
+  // offsets, on 1 KB boundaries where products or copies read or write
+  static constexpr int q = 0;                                        // [panels][N][128]
+  static constexpr int p = q + panels * N * 128;                     // [(N + 63) / 64][128 tokens][128]
+  static constexpr int k = p + (N + 63) / 64 * kTile * 128;          // [k_stages][panels][128][128]
+  static constexpr int v = k + k_stages * tile;
+  static constexpr int reference = v + v_stages * tile;              // [N] float
+  static constexpr int factor = reference + 4 * N;                   // [N] float: rescaling, or one token's weights
+  static constexpr int sums = p;                                     // [4][N] float, while the weights are not in use
+  static constexpr int last = factor + 4 * N;                        // [N] int: the last position a column sees
+  static constexpr int place = last + 4 * N;                         // [N] int: its row of the output, or -1
+  static constexpr int odd = place + 4 * N;                          // [128] bytes: tokens to be added on their own
+  static constexpr int bars = odd + 128;
+  static constexpr int n_bars = 2 * (k_stages + v_stages) + 8;
+  static constexpr int start_off = bars + 8 * n_bars;                // long long
+  static constexpr int scan = start_off + 8;                         // [kThreads / 32] long long
+  static constexpr int start_r = scan + 8 * (kThreads / 32);         // int
+  static constexpr int tmem = start_r + 4, abort_flag = tmem + 4;
+  static constexpr int total = abort_flag + 4;
+  static_assert(total <= 232448, "227 KB");
+};
+
+struct Maps {
+  CUtensorMap k, v;
+};
+
+template <bool BFQ, int DP, int N>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_wide_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Maps maps, int box, Scratch scr) {
+  using L = Plan<DP, N>;
+  using H = Half16<BFQ>;
+  constexpr int C = N / 2;  // columns per softmax thread
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t base = smem_addr(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto bar = [&](int i) { return base + L::bars + 8 * i; };
+  const int k_full = 0, k_empty = L::k_stages, v_full = 2 * L::k_stages, v_empty = v_full + L::v_stages,
+            s_full = v_empty + L::v_stages, s_free = s_full + 2, p_ready = s_free + 2, o_done = p_ready + 1,
+            q_ready = o_done + 1, drained = q_ready + 1;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::abort_flag);
+  const long long worker = blockIdx.x, workers = gridDim.x;
+  const int G = a.G;
+
+  if (tid == 0) {
+    for (int i = 0; i < L::k_stages; ++i) mbar_init(bar(k_full + i), 1), mbar_init(bar(k_empty + i), 1);
+    for (int i = 0; i < L::v_stages; ++i) mbar_init(bar(v_full + i), 1), mbar_init(bar(v_empty + i), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(s_full + i), 1), mbar_init(bar(s_free + i), kSoftmaxWarps);
+    mbar_init(bar(p_ready), kSoftmaxWarps);
+    mbar_init(bar(o_done), 1);
+    mbar_init(bar(q_ready), kSoftmaxWarps);
+    mbar_init(bar(drained), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid < 128) smem[L::odd + tid] = 0;
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + L::tmem), "r"(L::tmem_cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  griddep_wait();
+  griddep_allow_next();
+  const Deal d = deal<kTile, N, 1, kThreads>(a, worker, workers, reinterpret_cast<long long*>(smem + L::scan),
+                                             reinterpret_cast<int*>(smem + L::start_r),
+                                             reinterpret_cast<long long*>(smem + L::start_off));
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::tmem), o_cols = tmem + 2 * N;
+  if (tid == 0) {
+    scr.share[worker].r = -1;
+    if (worker == 0) *scr.per = d.per;
+  }
+  const long long u_begin = worker * d.per, u_end = min(d.total, u_begin + d.per);
+  const bool aligned = (base & 1023u) == 0;  // (as the swizzle wants; so it is without static shared memory)
+  if (!aligned && tid == 0) report_bad_input(a.status, 612);
+  const bool work = aligned && u_begin < u_end;
+  Cursor use = {};
+  if (work)
+    use = stand<kTile, N>(a, *reinterpret_cast<int*>(smem + L::start_r), *reinterpret_cast<long long*>(smem + L::start_off));
+  const int tiles = work ? (int)(u_end - u_begin) : 0;
+
+  if (warp == 0) {
+    // ---- copies: a lane per box of a tile, its page looked up one tile ahead
+    const int boxes = kTile / box;
+    int page = -1, slot = 0;
+    bool inside = false;
+    auto look_up = [&]() {
+      const int pos = use.k.first + use.chunk * kTile + lane * box, nth = pos / a.page_size;
+      slot = pos - nth * a.page_size;
+      inside = lane < boxes && pos < use.k.len;
+      page = inside ? a.page_table[use.r * a.table_stride + nth] : -1;
+    };
+    if (tiles > 0) look_up();
+    int filled_k = 0, filled_v = 0;
+    for (int i = 0; i < tiles; ++i) {
+      const int h = use.k.blocks == 1 ? use.item : use.item / use.k.blocks;
+      const bool there = page >= 0 && page < a.num_pages;
+      if (inside && !there) report_bad_input(a.status, kBadPage);
+      const int from = there ? page : a.num_pages;  // past the pool: zeros
+      const int ks = i % L::k_stages, vs = i % L::v_stages;
+      if (i >= L::k_stages && !mbar_wait(bar(k_empty + ks), (i / L::k_stages - 1) & 1, abort_flag, a.status, 601)) break;
+      if (lane == 0) mbar_expect(bar(k_full + ks), L::tile);
+      __syncwarp();
+      if (lane < boxes)
+#pragma unroll
+        for (int n = 0; n < L::panels; ++n)
+          tma_box(base + L::k + ks * L::tile + n * (kTile * 128) + lane * box * 128, &maps.k, bar(k_full + ks), 64 * n, slot, h,
+                  from);
+      filled_k = i + 1;
+      if (i >= L::v_stages && !mbar_wait(bar(v_empty + vs), (i / L::v_stages - 1) & 1, abort_flag, a.status, 602)) break;
+      if (lane == 0) mbar_expect(bar(v_full + vs), L::tile);
+      __syncwarp();
+      if (lane < boxes)
+#pragma unroll
+        for (int n = 0; n < L::panels; ++n)
+          tma_box(base + L::v + vs * L::tile + n * (kTile * 128) + lane * box * 128, &maps.v, bar(v_full + vs), 64 * n, slot, h,
+                  from);
+      filled_v = i + 1;
+      if (i + 1 < tiles) {
+        advance<kTile, N>(a, use);
+        look_up();
+      }
+    }
+    // every copy lands before the CTA ends (at once, unless a role gave up)
+    for (int i = max(0, filled_k - L::k_stages); i < filled_k; ++i) mbar_drain(bar(k_full + i % L::k_stages), (i / L::k_stages) & 1);
+    for (int i = max(0, filled_v - L::v_stages); i < filled_v; ++i) mbar_drain(bar(v_full + i % L::v_stages), (i / L::v_stages) & 1);
+  } else if (warp == 1) {
+    // ---- products
+    if (lane == 0) {
+      constexpr uint32_t s_desc = idesc<BFQ>(N, false, false), o_desc = idesc<BFQ>(N, true, true);
+      auto scores = [&](int i) {
+        const int ks = i % L::k_stages;
+        if (!mbar_wait(bar(k_full + ks), (i / L::k_stages) & 1, abort_flag, a.status, 603)) return false;
+        if (i >= 2 && !mbar_wait(bar(s_free + (i & 1)), (i / 2 - 1) & 1, abort_flag, a.status, 604)) return false;
+        fence_after();
+        const uint32_t keys = base + L::k + ks * L::tile;
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk)
+          mma(tmem + (i & 1) * N, sw128(keys + kk / 4 * (kTile * 128) + kk % 4 * 32, 16, 1024),
+              sw128(base + L::q + kk / 4 * (N * 128) + kk % 4 * 32, 16, 1024), s_desc, kk > 0);
+        commit(bar(k_empty + ks));
+        commit(bar(s_full + (i & 1)));
+        return true;
+      };
+      int i = 0, items = 0;
+      bool ok = true;
+      while (ok && i < tiles) {
+        const int n = min(use.k.chunks - use.chunk, tiles - i);  // tiles of this item
+        ok = mbar_wait(bar(q_ready), items & 1, abort_flag, a.status, 605) && scores(i);
+        for (int t = 0; ok && t < n; ++t, ++i) {
+          if (t + 1 < n && !scores(i + 1)) ok = false;
+          const int vs = i % L::v_stages;
+          ok = ok && mbar_wait(bar(v_full + vs), (i / L::v_stages) & 1, abort_flag, a.status, 606) &&
+               mbar_wait(bar(p_ready), i & 1, abort_flag, a.status, 607);
+          if (!ok) break;
+          fence_after();
+          const uint32_t values = base + L::v + vs * L::tile;
+          // (rows of 64 elements: the upper half of the product repeats the lower)
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma(o_cols, sw128(values + kk * 2048, L::panels > 1 ? kTile * 128 : 0, 1024),
+                sw128(base + L::p + kk * 2048, kTile * 128, 1024), o_desc, 1);
+          commit(bar(v_empty + vs));
+          commit(bar(o_done));
+        }
+        ++items;
+        use.chunk = use.k.chunks - 1;
+        if (i < tiles) advance<kTile, N>(a, use);
+      }
+      // every product is done before the CTA gives its tensor memory back
+      commit(bar(drained));
+      mbar_drain(bar(drained), 0);
+    }
+    __syncwarp();
+  } else {
+    // ---- softmax
+    const int st = tid - 64, quarter = warp & 3, half = (warp - 2) >> 2, token = quarter * 32 + lane, c0 = half * C;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    float* reference = reinterpret_cast<float*>(smem + L::reference);
+    float* factor = reinterpret_cast<float*>(smem + L::factor);
+    float* sums = reinterpret_cast<float*>(smem + L::sums);
+    int* last = reinterpret_cast<int*>(smem + L::last);
+    int* place = reinterpret_cast<int*>(smem + L::place);
+    volatile unsigned char* odd = smem + L::odd;
+    const float c2 = a.scale * kLog2e;
+    float l[C];
+    bool ok = true;
+    int i = 0;
+    long long item_begin = u_begin - use.chunk;
+    while (i < tiles) {
+      const int n = min(use.k.chunks - use.chunk, tiles - i);
+      const int h = use.k.blocks == 1 ? use.item : use.item / use.k.blocks, row0 = (use.item - h * use.k.blocks) * N;
+      softmax_sync();  // the previous item's tables are no longer read
+      for (int e = st; e < N * (DP / 8); e += kSoftmaxThreads) {
+        const int row = e / (DP / 8), c = e % (DP / 8), rr = row0 + row, q = rr / G;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (rr < use.k.nq * G && c * 8 < a.D)
+          x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                              (int64_t)(use.k.q0 + q) * a.q_stride_token +
+                                              (int64_t)(h * G + rr - q * G) * a.q_stride_head + c * 8);
+        sts16(base + L::q + (c >> 3) * (N * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4), x);
+      }
+      if (st < N) {
+        const int rr = row0 + st, q = rr / G;
+        const bool there = rr < use.k.nq * G;
+        reference[st] = kUnset;
+        last[st] = there ? use.k.len - use.k.nq + q : -1;
+        place[st] = there ? (use.k.q0 + q) * a.Hq + h * G + rr - q * G : -1;
+      }
+      {
+        float zero[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) zero[e] = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; c += 16) tmem_store(o_cols + lanes + c0 + c, zero);
+        tmem_store_wait();
+      }
+#pragma unroll
+      for (int c = 0; c < C; ++c) l[c] = 0.f;
+      fence_smem();
+      fence_before();
+      softmax_sync();
+      if (lane == 0) mbar_arrive(bar(q_ready));
+
+      for (int t = 0; t < n; ++t, ++i) {
+        ok = ok && mbar_wait(bar(s_full + (i & 1)), (i >> 1) & 1, abort_flag, a.status, 608);
+        fence_after();
+        float x[C];
+#pragma unroll
+        for (int c = 0; c < C; c += 16) tmem_load(tmem + (i & 1) * N + lanes + c0 + c, x + c);
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(s_free + (i & 1)));
+
+        const int p0 = use.k.first + (use.chunk + t) * kTile, pos = p0 + token;
+        const bool edge = p0 + kTile > use.k.len - use.k.nq + 1 || (a.window > 0 && p0 < use.k.len - a.window);
+        if (edge) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            const int to = last[c0 + c];
+            if (pos > to || (a.window > 0 && pos <= to - a.window)) x[c] = -INFINITY;
+          }
+        }
+        // does a score pass its reference?  (A masked score stays -inf whatever the scale's sign.)
+        float most = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < C; c += 4) {
+          const float4 r = *reinterpret_cast<const float4*>(reference + c0 + c);
+          const float u0 = fmaf(x[c], c2, -r.x), u1 = fmaf(x[c + 1], c2, -r.y), u2 = fmaf(x[c + 2], c2, -r.z),
+                      u3 = fmaf(x[c + 3], c2, -r.w);
+          most = max3(most, edge && x[c] == -INFINITY ? -INFINITY : u0, edge && x[c + 1] == -INFINITY ? -INFINITY : u1);
+          most = max3(most, edge && x[c + 2] == -INFINITY ? -INFINITY : u2, edge && x[c + 3] == -INFINITY ? -INFINITY : u3);
+        }
+        bool waited = false;  // for the previous tile's product into O
+        auto wait_o = [&]() {
+          if (!waited && i > 0) ok = mbar_wait(bar(o_done), (i - 1) & 1, abort_flag, a.status, 609) && ok;
+          waited = true;
+        };
+        if (softmax_any(most > kSlack || !ok)) {
+          if (softmax_any(!ok)) goto done;
+          wait_o();
+          softmax_sync();
+          // new references: the columns' maxima, over lanes, then over the four quarters
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            float v = edge && x[c] == -INFINITY ? -INFINITY : x[c] * c2;
+#pragma unroll
+            for (int s = 16; s; s >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, s));
+            if (lane == 0) sums[quarter * N + c0 + c] = v;
+          }
+          softmax_sync();
+          if (st < N) {
+            const float was = reference[st];
+            const float now = fmaxf(was, fmaxf(fmaxf(sums[st], sums[N + st]), fmaxf(sums[2 * N + st], sums[3 * N + st])));
+            reference[st] = now;
+            factor[st] = ex2(was - now);
+          }
+          softmax_sync();
+          fence_after();
+#pragma unroll
+          for (int c = 0; c < C; c += 16) {
+            float o[16];
+            tmem_load(o_cols + lanes + c0 + c, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float f = factor[c0 + c + e];
+              o[e] *= f;
+              l[c + e] *= f;
+            }
+            tmem_store(o_cols + lanes + c0 + c, o);
+          }
+          tmem_store_wait();
+        }
+#pragma unroll
+        for (int c = 0; c < C; c += 4) {
+          const float4 r = *reinterpret_cast<const float4*>(reference + c0 + c);
+          const float rr[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[c + e] = edge && x[c + e] == -INFINITY ? 0.f : ex2(fmaf(x[c + e], c2, -rr[e]));
+            l[c + e] += x[c + e];
+          }
+        }
+        wait_o();
+        if (edge) {
+          // Tokens that no column sees hold anything (the rest of a page): their values are
+          // cleared.  One that only some columns see must not reach the others if it is not
+          // finite (0 x NaN): it is added on its own, and cleared for the product.
+          const int vs = i % L::v_stages;
+          ok = mbar_wait(bar(v_full + vs), (i / L::v_stages) & 1, abort_flag, a.status, 610) && ok;
+          const uint32_t values = base + L::v + vs * L::tile;
+          const uint32_t row = values + (half % L::panels) * (kTile * 128) + token * 128;
+          const bool mine = half < L::panels;  // this thread's half of the token's row
+          const int seen_from = a.window > 0 ? max(0, use.k.len - use.k.nq - a.window + 1) : 0;
+          const bool unseen = pos >= use.k.len || pos < seen_from;
+          const bool partly = !unseen && (pos > use.k.len - use.k.nq || (a.window > 0 && pos < use.k.len - a.window));
+          bool strange = false;
+          if (mine && partly) {
+            for (int c = 0; c < 8; ++c) {
+              const uint4 v = lds16(row + c * 16);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) strange |= (w[e] & H::kExp) == H::kExp || ((w[e] >> 16) & H::kExp) == H::kExp;
+            }
+          }
+          if (strange) odd[token] = 1;
+          if (softmax_any(strange)) {
+            for (int k = 0; k < kTile; ++k) {
+              if (!odd[k]) continue;
+              if (token == k) {
+#pragma unroll
+                for (int c = 0; c < C; ++c) factor[c0 + c] = x[c];
+              }
+              softmax_sync();
+              fence_after();
+              // this thread: element `token` of the value, its half of the columns
+              float v = 0.f;
+              if (token < DP) {
+                const uint32_t at = values + (token >> 6) * (kTile * 128) + k * 128 + ((((token & 63) >> 3) ^ (k & 7)) << 4) +
+                                    (token & 7) * 2;
+                uint32_t w;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=r"(w) : "r"(at));
+                v = H::lo(w);
+              }
+#pragma unroll
+              for (int c = 0; c < C; c += 16) {
+                float o[16];
+                tmem_load(o_cols + lanes + c0 + c, o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const int to = last[c0 + c + e], p = p0 + k;
+                  if (p <= to && (a.window == 0 || p > to - a.window)) o[e] = fmaf(factor[c0 + c + e], v, o[e]);
+                }
+                tmem_store(o_cols + lanes + c0 + c, o);
+              }
+              tmem_store_wait();
+              softmax_sync();
+            }
+          }
+          const bool clear = unseen || odd[token];
+          softmax_sync();
+          odd[token] = 0;
+          if (mine && clear)
+            for (int c = 0; c < 8; ++c) sts16(row + c * 16, make_uint4(0, 0, 0, 0));
+        }
+        // the weights: C 16-bit values of the token's row
+#pragma unroll
+        for (int c = 0; c < C; c += 8) {
+          const int piece = (c0 + c) / 8;
+          sts16(base + L::p + (piece >> 3) * (kTile * 128) + token * 128 + (((piece & 7) ^ (token & 7)) << 4),
+                make_uint4(H::pack(x[c], x[c + 1]), H::pack(x[c + 2], x[c + 3]), H::pack(x[c + 4], x[c + 5]),
+                           H::pack(x[c + 6], x[c + 7])));
+        }
+        fence_smem();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(p_ready));
+      }
+
+      // ---- the item, or this worker's part of it, ends
+      ok = mbar_wait(bar(o_done), (i - 1) & 1, abort_flag, a.status, 611) && ok;
+      fence_after();
+      if (softmax_any(!ok)) goto done;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+#pragma unroll
+        for (int s = 16; s; s >>= 1) l[c] += __shfl_xor_sync(~0u, l[c], s);
+        if (lane == 0) sums[quarter * N + c0 + c] = l[c];
+      }
+      softmax_sync();
+      const long long item_end = item_begin + use.k.chunks;
+      const bool whole = item_begin >= u_begin && item_end <= u_end;
+      const int part = item_begin >= u_begin;  // part 0 began before the worker's range
+      const size_t rows = (size_t)(worker * 2 + part) * N;
+      if (st < N) {
+        const float sum = (sums[st] + sums[N + st]) + (sums[2 * N + st] + sums[3 * N + st]);
+        if (whole) {
+          factor[st] = sum == 0.f ? 0.f : 1.f / sum;
+          if (place[st] >= 0 && a.lse_out != nullptr)
+            a.lse_out[place[st]] = sum == 0.f ? -INFINITY : (reference[st] + log2f(sum)) * kLn2;
+        } else {
+          scr.stats[rows + st] = make_float2(sum == 0.f ? -INFINITY : reference[st], sum);
+        }
+      }
+      softmax_sync();
+#pragma unroll
+      for (int c = 0; c < C; c += 16) {
+        float o[16];
+        tmem_load(o_cols + lanes + c0 + c, o);
+        if (token < DP) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int col = c0 + c + e;
+            if (whole) {
+              if (place[col] >= 0 && token < a.D)
+                static_cast<uint16_t*>(a.out)[(size_t)place[col] * a.D + token] =
+                    (uint16_t)H::pack(factor[col] == 0.f ? 0.f : o[e] * factor[col], 0.f);
+            } else {
+              scr.out[(rows + col) * DP + token] = o[e];
+            }
+          }
+        }
+      }
+      fence_before();
+      if (!whole && part == 1 && st == 0)
+        scr.share[worker] = Share{use.r, use.item, use.k.q0, use.k.nq, item_begin, item_end};
+      item_begin = item_end;
+      use.chunk = use.k.chunks - 1;
+      if (i < tiles) advance<kTile, N>(a, use);
+    }
+  done:;
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::tmem_cols) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------------------ host side
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> known{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 fn = known.load(std::memory_order_acquire);
+  if (fn == nullptr) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    known.store(fn, std::memory_order_release);
+  }
+  return fn;
+}
+
+// A pool as [pages][heads][tokens][D] with boxes of `box` tokens by 128 bytes, swizzled.
+bool encode_pool(CUtensorMap* map, const AttentionArgs& a, const void* pool, int box) {
+  auto fn = encoder();
+  if (fn == nullptr) return false;
+  // a dimension of one entry has no stride of its own: any that is allowed will do
+  const cuuint64_t row = (cuuint64_t)a.D * 2;
+  const cuuint64_t strides[3] = {a.token_stride ? (cuuint64_t)a.token_stride * 2 : row,
+                                 a.head_stride ? (cuuint64_t)a.head_stride * 2 : row,
+                                 a.page_stride ? (cuuint64_t)a.page_stride * 2 : row};
+  const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.page_size, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
+  const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(pool), dims, strides, boxes, ones,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tokens per box: the largest power of two that divides the page, 8 (the swizzle's period) to a
+// tile's 128; 0 where there is none.
+int box_tokens(int page_size) {
+  int box = kTile;
+  while (page_size % box != 0) box /= 2;
+  return box >= 8 ? box : 0;
+}
+
+int columns(int max_q, int G) {
+  const int rows = max_q * G;
+  return rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
+}
+
+template <bool BFQ, int DP, int N>
+cudaError_t launch(const AttentionArgs& a, const Maps& maps, int box, void* scratch, cudaStream_t s) {
+  auto* kernel = attention_wide_kernel<BFQ, DP, N>;
+  static std::atomic<uint64_t> done;
+  cudaError_t e = allow_smem(kernel, Plan<DP, N>::total, done);
+  if (e != cudaSuccess) return e;
+  const int workers = std::min(sm_count(), kMaxSms);
+  const Scratch scr = scratch_at(scratch, kMaxSms, N);
+  e = launch_chained(kernel, dim3(workers), dim3(kThreads), Plan<DP, N>::total, s, 1, a, maps, box, scr);
+  return e != cudaSuccess ? e : launch_join<BFQ, DP, N>(a, scr, workers, s);
+}
+
+template <bool BFQ, int DP>
+cudaError_t launch(const AttentionArgs& a, const Maps& maps, int box, void* scratch, cudaStream_t s) {
+  switch (columns(a.max_q, a.G)) {
+    case 32: return launch<BFQ, DP, 32>(a, maps, box, scratch, s);
+    case 64: return launch<BFQ, DP, 64>(a, maps, box, scratch, s);
+    default: return launch<BFQ, DP, 128>(a, maps, box, scratch, s);
+  }
+}
+
+}  // namespace
+
+size_t attention_wide_scratch(int Hq, int Hkv, int D, int max_q) {
+  return D > 128 ? 0 : attention::scratch_bytes(kMaxSms, columns(max_q, Hq / Hkv), D <= 64 ? 64 : 128);
+}
+
+bool launch_attention_wide(const AttentionArgs& a, void* scratch, cudaStream_t s, cudaError_t& e) {
+  if (a.dtype_kv == DSPARK_E4M3 || a.D > 128) return false;
+  const int box = box_tokens(a.page_size);
+  Maps maps;
+  if (box == 0 || !encode_pool(&maps.k, a, a.k_pool, box) || !encode_pool(&maps.v, a, a.v_pool, box)) return false;
+  const bool bf = a.dtype_q == DSPARK_BF16;
+  if (a.D <= 64) e = bf ? launch<true, 64>(a, maps, box, scratch, s) : launch<false, 64>(a, maps, box, scratch, s);
+  else e = bf ? launch<true, 128>(a, maps, box, scratch, s) : launch<false, 128>(a, maps, box, scratch, s);
+  return true;
+}
+
+}  // namespace dspark

@@ -325,6 +325,7 @@ dspark_status dspark_paged_attention(int T, int R, int Hq, int Hkv, int D, int n
     return fail(DSPARK_INVALID_ARG, "sizes must be positive (T=%d Hq=%d Hkv=%d window=%d)", T, Hq, Hkv, window);
   if (Hq % Hkv != 0) return fail(DSPARK_INVALID_ARG, "Hq=%d must be a multiple of Hkv=%d", Hq, Hkv);
   if (Hq / Hkv > 64) return fail(DSPARK_UNSUPPORTED_SHAPE, "Hq / Hkv = %d exceeds 64", Hq / Hkv);
+  if ((int64_t)T * Hq > INT32_MAX) return fail(DSPARK_UNSUPPORTED_SHAPE, "T * Hq must be below 2^31");
   if (max_q < 1) return fail(DSPARK_INVALID_ARG, "max_q=%d must be positive", max_q);
   if (max_q > dspark::kMaxQueries)
     return fail(DSPARK_UNSUPPORTED_SHAPE, "max_q=%d exceeds %d", max_q, dspark::kMaxQueries);
