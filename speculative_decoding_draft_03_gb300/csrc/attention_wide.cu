@@ -9,9 +9,9 @@
 // so that keys and values are used as they lie in the pages (panels of 128-byte rows, 128-byte
 // swizzle, by tensor copies), each weight is written once as part of a 16-byte piece of its
 // token's row, and the output leaves with its elements in neighbouring lanes.
-//   * One persistent CTA per SM: warp 0 copies, warp 1 issues the products, warps 2..9 do the
-//     softmax: a thread owns one token (its TMEM lane) and half of the columns.  S is double
-//     buffered; the copies run up to three tiles ahead of the products.
+//   * One persistent CTA per SM: warp 0 copies, warp 1 issues the products, the other 8 or 16 do
+//     the softmax: a thread owns one token (its TMEM lane) and 16 or 32 of the columns.  S is
+//     double buffered; the copies run up to three tiles ahead of the products.
 //   * The softmax reference of a column moves only when a score passes it by 2^kSlack (any
 //     reference is right; the weights stay below 2^kSlack, inside fp16's range): a vote per
 //     tile replaces the maximum over the tokens, and the output is rescaled in TMEM only then.
@@ -32,7 +32,8 @@ namespace {
 using namespace attention;
 
 constexpr int kTile = 128;  // tokens
-constexpr int kSoftmaxWarps = 8, kSoftmaxThreads = 32 * kSoftmaxWarps, kThreads = 64 + kSoftmaxThreads;
+// Softmax warps: four lane quarters times the column groups, of 16 columns (32 of 128).
+constexpr int softmax_warps(int N) { return N == 32 ? 8 : 16; }
 constexpr float kSlack = 8.f;
 constexpr float kUnset = -1e30f;  // the reference of a column that has seen nothing: any score passes it
 constexpr long long kWaitCycles = 4000000000ll;  // ~2 s
@@ -132,13 +133,17 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const float* x) {
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Barriers of the softmax warps.
-__device__ __forceinline__ void softmax_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void softmax_sync() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+template <int THREADS>
 __device__ __forceinline__ bool softmax_any(bool x) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)x), "n"(kSoftmaxThreads)
+      : "r"((uint32_t)x), "n"(THREADS)
       : "memory");
   return r != 0;
 }
@@ -152,6 +157,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 template <int DP, int N>
 struct Plan {
+  static constexpr int softmax = 32 * softmax_warps(N), threads = 64 + softmax;
+  static constexpr int groups = softmax_warps(N) / 4, columns = N / groups;  // column groups
   static constexpr int panels = DP / 64;
   static constexpr int tile = panels * kTile * 128;  // keys, or values, of a tile
   static constexpr int k_stages = DP == 64 ? 4 : 3, v_stages = DP == 64 ? 4 : (N == 128 ? 2 : 3);
@@ -170,8 +177,8 @@ struct Plan {
   static constexpr int bars = odd + 128;
   static constexpr int n_bars = 2 * (k_stages + v_stages) + 8;
   static constexpr int start_off = bars + 8 * n_bars;                // long long
-  static constexpr int scan = start_off + 8;                         // [kThreads / 32] long long
-  static constexpr int start_r = scan + 8 * (kThreads / 32);         // int
+  static constexpr int scan = start_off + 8;                         // [threads / 32] long long
+  static constexpr int start_r = scan + 8 * (threads / 32);         // int
   static constexpr int tmem = start_r + 4, abort_flag = tmem + 4;
   static constexpr int total = abort_flag + 4;
   static_assert(total <= 232448, "227 KB");
@@ -182,11 +189,11 @@ struct Maps {
 };
 
 template <bool BFQ, int DP, int N>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
     attention_wide_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Maps maps, int box, Scratch scr) {
   using L = Plan<DP, N>;
   using H = Half16<BFQ>;
-  constexpr int C = N / 2;  // columns per softmax thread
+  constexpr int C = L::columns;  // per softmax thread
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = smem_addr(smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -201,10 +208,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < L::k_stages; ++i) mbar_init(bar(k_full + i), 1), mbar_init(bar(k_empty + i), 1);
     for (int i = 0; i < L::v_stages; ++i) mbar_init(bar(v_full + i), 1), mbar_init(bar(v_empty + i), 1);
-    for (int i = 0; i < 2; ++i) mbar_init(bar(s_full + i), 1), mbar_init(bar(s_free + i), kSoftmaxWarps);
-    mbar_init(bar(p_ready), kSoftmaxWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(bar(s_full + i), 1), mbar_init(bar(s_free + i), L::softmax / 32);
+    mbar_init(bar(p_ready), L::softmax / 32);
     mbar_init(bar(o_done), 1);
-    mbar_init(bar(q_ready), kSoftmaxWarps);
+    mbar_init(bar(q_ready), L::softmax / 32);
     mbar_init(bar(drained), 1);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   griddep_wait();
   griddep_allow_next();
-  const Deal d = deal<kTile, N, 1, kThreads>(a, worker, workers, reinterpret_cast<long long*>(smem + L::scan),
+  const Deal d = deal<kTile, N, 1, L::threads>(a, worker, workers, reinterpret_cast<long long*>(smem + L::scan),
                                              reinterpret_cast<int*>(smem + L::start_r),
                                              reinterpret_cast<long long*>(smem + L::start_off));
   fence_before();
@@ -332,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else {
     // ---- softmax
-    const int st = tid - 64, quarter = warp & 3, half = (warp - 2) >> 2, token = quarter * 32 + lane, c0 = half * C;
+    const int st = tid - 64, quarter = warp & 3, group = (warp - 2) >> 2, token = quarter * 32 + lane, c0 = group * C;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     float* reference = reinterpret_cast<float*>(smem + L::reference);
     float* factor = reinterpret_cast<float*>(smem + L::factor);
@@ -348,8 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (i < tiles) {
       const int n = min(use.k.chunks - use.chunk, tiles - i);
       const int h = use.k.blocks == 1 ? use.item : use.item / use.k.blocks, row0 = (use.item - h * use.k.blocks) * N;
-      softmax_sync();  // the previous item's tables are no longer read
-      for (int e = st; e < N * (DP / 8); e += kSoftmaxThreads) {
+      softmax_sync<L::softmax>();  // the previous item's tables are no longer read
+      for (int e = st; e < N * (DP / 8); e += L::softmax) {
         const int row = e / (DP / 8), c = e % (DP / 8), rr = row0 + row, q = rr / G;
         uint4 x = make_uint4(0, 0, 0, 0);
         if (rr < use.k.nq * G && c * 8 < a.D)
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < C; ++c) l[c] = 0.f;
       fence_smem();
       fence_before();
-      softmax_sync();
+      softmax_sync<L::softmax>();
       if (lane == 0) mbar_arrive(bar(q_ready));
 
       for (int t = 0; t < n; ++t, ++i) {
@@ -414,10 +421,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!waited && i > 0) ok = mbar_wait(bar(o_done), (i - 1) & 1, abort_flag, a.status, 609) && ok;
           waited = true;
         };
-        if (softmax_any(most > kSlack || !ok)) {
-          if (softmax_any(!ok)) goto done;
+        if (softmax_any<L::softmax>(most > kSlack || !ok)) {
+          if (softmax_any<L::softmax>(!ok)) goto done;
           wait_o();
-          softmax_sync();
+          softmax_sync<L::softmax>();
           // new references: the columns' maxima, over lanes, then over the four quarters
 #pragma unroll
           for (int c = 0; c < C; ++c) {
@@ -426,14 +433,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int s = 16; s; s >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, s));
             if (lane == 0) sums[quarter * N + c0 + c] = v;
           }
-          softmax_sync();
+          softmax_sync<L::softmax>();
           if (st < N) {
             const float was = reference[st];
             const float now = fmaxf(was, fmaxf(fmaxf(sums[st], sums[N + st]), fmaxf(sums[2 * N + st], sums[3 * N + st])));
             reference[st] = now;
             factor[st] = ex2(was - now);
           }
-          softmax_sync();
+          softmax_sync<L::softmax>();
           fence_after();
 #pragma unroll
           for (int c = 0; c < C; c += 16) {
@@ -467,31 +474,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int vs = i % L::v_stages;
           ok = mbar_wait(bar(v_full + vs), (i / L::v_stages) & 1, abort_flag, a.status, 610) && ok;
           const uint32_t values = base + L::v + vs * L::tile;
-          const uint32_t row = values + (half % L::panels) * (kTile * 128) + token * 128;
-          const bool mine = half < L::panels;  // this thread's half of the token's row
+          constexpr int kPieces = L::panels * 8 / L::groups;  // this thread's part of the token's row
+          auto part_of_row = [&](int c) {
+            const int piece = group * kPieces + c;
+            return values + (piece >> 3) * (kTile * 128) + token * 128 + (((piece & 7) ^ (token & 7)) << 4);
+          };
           const int seen_from = a.window > 0 ? max(0, use.k.len - use.k.nq - a.window + 1) : 0;
           const bool unseen = pos >= use.k.len || pos < seen_from;
           const bool partly = !unseen && (pos > use.k.len - use.k.nq || (a.window > 0 && pos < use.k.len - a.window));
           bool strange = false;
-          if (mine && partly) {
-            for (int c = 0; c < 8; ++c) {
-              const uint4 v = lds16(row + c * 16);
+          if (partly) {
+            for (int c = 0; c < kPieces; ++c) {
+              const uint4 v = lds16(part_of_row(c));
               const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
               for (int e = 0; e < 4; ++e) strange |= (w[e] & H::kExp) == H::kExp || ((w[e] >> 16) & H::kExp) == H::kExp;
             }
           }
           if (strange) odd[token] = 1;
-          if (softmax_any(strange)) {
+          if (softmax_any<L::softmax>(strange)) {
             for (int k = 0; k < kTile; ++k) {
               if (!odd[k]) continue;
               if (token == k) {
 #pragma unroll
                 for (int c = 0; c < C; ++c) factor[c0 + c] = x[c];
               }
-              softmax_sync();
+              softmax_sync<L::softmax>();
               fence_after();
-              // this thread: element `token` of the value, its half of the columns
+              // this thread: element `token` of the value, its group of the columns
               float v = 0.f;
               if (token < DP) {
                 const uint32_t at = values + (token >> 6) * (kTile * 128) + k * 128 + ((((token & 63) >> 3) ^ (k & 7)) << 4) +
@@ -512,14 +522,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_store(o_cols + lanes + c0 + c, o);
               }
               tmem_store_wait();
-              softmax_sync();
+              softmax_sync<L::softmax>();
             }
           }
           const bool clear = unseen || odd[token];
-          softmax_sync();
+          softmax_sync<L::softmax>();
           odd[token] = 0;
-          if (mine && clear)
-            for (int c = 0; c < 8; ++c) sts16(row + c * 16, make_uint4(0, 0, 0, 0));
+          if (clear)
+            for (int c = 0; c < kPieces; ++c) sts16(part_of_row(c), make_uint4(0, 0, 0, 0));
         }
         // the weights: C 16-bit values of the token's row
 #pragma unroll
@@ -538,14 +548,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the item, or this worker's part of it, ends
       ok = mbar_wait(bar(o_done), (i - 1) & 1, abort_flag, a.status, 611) && ok;
       fence_after();
-      if (softmax_any(!ok)) goto done;
+      if (softmax_any<L::softmax>(!ok)) goto done;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
 #pragma unroll
         for (int s = 16; s; s >>= 1) l[c] += __shfl_xor_sync(~0u, l[c], s);
         if (lane == 0) sums[quarter * N + c0 + c] = l[c];
       }
-      softmax_sync();
+      softmax_sync<L::softmax>();
       const long long item_end = item_begin + use.k.chunks;
       const bool whole = item_begin >= u_begin && item_end <= u_end;
       const int part = item_begin >= u_begin;  // part 0 began before the worker's range
@@ -560,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           scr.stats[rows + st] = make_float2(sum == 0.f ? -INFINITY : reference[st], sum);
         }
       }
-      softmax_sync();
+      softmax_sync<L::softmax>();
 #pragma unroll
       for (int c = 0; c < C; c += 16) {
         float o[16];
@@ -650,7 +660,7 @@ cudaError_t launch(const AttentionArgs& a, const Maps& maps, int box, void* scra
   if (e != cudaSuccess) return e;
   const int workers = std::min(sm_count(), kMaxSms);
   const Scratch scr = scratch_at(scratch, kMaxSms, N);
-  e = launch_chained(kernel, dim3(workers), dim3(kThreads), Plan<DP, N>::total, s, 1, a, maps, box, scr);
+  e = launch_chained(kernel, dim3(workers), dim3(Plan<DP, N>::threads), Plan<DP, N>::total, s, 1, a, maps, box, scr);
   return e != cudaSuccess ? e : launch_join<BFQ, DP, N>(a, scr, workers, s);
 }
 
