@@ -9,8 +9,8 @@
 // so that keys and values are used as they lie in the pages (panels of 128-byte rows, 128-byte
 // swizzle, by tensor copies), each weight is written once as part of a 16-byte piece of its
 // token's row, and the output leaves with its elements in neighbouring lanes.
-//   * One persistent CTA per SM: warp 0 copies, warp 1 issues the products, the other 8 or 16 do
-//     the softmax: a thread owns one token (its TMEM lane) and 16 or 32 of the columns.  S is
+//   * One persistent CTA per SM: warps 0 and 2 copy, warp 1 issues the products, the other 8 or 16
+//     do the softmax: a thread owns one token (its TMEM lane) and 16 or 32 of the columns.  S is
 //     double buffered; the copies run up to three tiles ahead of the products.
 //   * The softmax reference of a column moves only when a score passes it by 2^kSlack (any
 //     reference is right; the weights stay below 2^kSlack, inside fp16's range): a vote per
@@ -157,7 +157,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 template <int DP, int N>
 struct Plan {
-  static constexpr int softmax = 32 * softmax_warps(N), threads = 64 + softmax;
+  static constexpr int softmax = 32 * softmax_warps(N), threads = 96 + softmax;
   static constexpr int groups = softmax_warps(N) / 4, columns = N / groups;  // column groups
   static constexpr int panels = DP / 64;
   static constexpr int tile = panels * kTile * 128;  // keys, or values, of a tile
@@ -244,8 +244,13 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
     use = stand<kTile, N>(a, *reinterpret_cast<int*>(smem + L::start_r), *reinterpret_cast<long long*>(smem + L::start_off));
   const int tiles = work ? (int)(u_end - u_begin) : 0;
 
-  if (warp == 0) {
-    // ---- copies: a lane per box of a tile, its page looked up one tile ahead
+  if (warp == 0 || warp == 2) {
+    // ---- copies, of keys (warp 0) and of values (warp 2: issuing a tile's boxes takes a warp
+    // most of a tile's time): a lane per box of a tile, its page looked up one tile ahead
+    const bool keys = warp == 0;
+    const int stages = keys ? L::k_stages : L::v_stages, full = keys ? k_full : v_full, empty = keys ? k_empty : v_empty;
+    const uint32_t ring = base + (keys ? L::k : L::v);
+    const CUtensorMap* map = keys ? &maps.k : &maps.v;
     const int boxes = kTile / box;
     int page = -1, slot = 0;
     bool inside = false;
@@ -256,55 +261,49 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
       page = inside ? a.page_table[use.r * a.table_stride + nth] : -1;
     };
     if (tiles > 0) look_up();
-    int filled_k = 0, filled_v = 0;
+    int filled = 0, stage = 0, phase = 1;  // (the first round finds every stage empty)
     for (int i = 0; i < tiles; ++i) {
       const int h = use.k.blocks == 1 ? use.item : use.item / use.k.blocks;
       const bool there = page >= 0 && page < a.num_pages;
       if (inside && !there) report_bad_input(a.status, kBadPage);
       const int from = there ? page : a.num_pages;  // past the pool: zeros
-      const int ks = i % L::k_stages, vs = i % L::v_stages;
-      if (i >= L::k_stages && !mbar_wait(bar(k_empty + ks), (i / L::k_stages - 1) & 1, abort_flag, a.status, 601)) break;
-      if (lane == 0) mbar_expect(bar(k_full + ks), L::tile);
+      if (i >= stages && !mbar_wait(bar(empty + stage), phase, abort_flag, a.status, 601)) break;
+      if (lane == 0) mbar_expect(bar(full + stage), L::tile);
       __syncwarp();
       if (lane < boxes)
 #pragma unroll
         for (int n = 0; n < L::panels; ++n)
-          tma_box(base + L::k + ks * L::tile + n * (kTile * 128) + lane * box * 128, &maps.k, bar(k_full + ks), 64 * n, slot, h,
-                  from);
-      filled_k = i + 1;
-      if (i >= L::v_stages && !mbar_wait(bar(v_empty + vs), (i / L::v_stages - 1) & 1, abort_flag, a.status, 602)) break;
-      if (lane == 0) mbar_expect(bar(v_full + vs), L::tile);
-      __syncwarp();
-      if (lane < boxes)
-#pragma unroll
-        for (int n = 0; n < L::panels; ++n)
-          tma_box(base + L::v + vs * L::tile + n * (kTile * 128) + lane * box * 128, &maps.v, bar(v_full + vs), 64 * n, slot, h,
-                  from);
-      filled_v = i + 1;
+          tma_box(ring + stage * L::tile + n * (kTile * 128) + lane * box * 128, map, bar(full + stage), 64 * n, slot, h, from);
+      filled = i + 1;
+      if (++stage == stages) stage = 0, phase ^= 1;
       if (i + 1 < tiles) {
         advance<kTile, N>(a, use);
         look_up();
       }
     }
     // every copy lands before the CTA ends (at once, unless a role gave up)
-    for (int i = max(0, filled_k - L::k_stages); i < filled_k; ++i) mbar_drain(bar(k_full + i % L::k_stages), (i / L::k_stages) & 1);
-    for (int i = max(0, filled_v - L::v_stages); i < filled_v; ++i) mbar_drain(bar(v_full + i % L::v_stages), (i / L::v_stages) & 1);
+    for (int i = max(0, filled - stages); i < filled; ++i) mbar_drain(bar(full + i % stages), (i / stages) & 1);
   } else if (warp == 1) {
     // ---- products
     if (lane == 0) {
       constexpr uint32_t s_desc = idesc<BFQ>(N, false, false), o_desc = idesc<BFQ>(N, true, true);
+      // descriptors of the first step; the others lie a constant further (in units of 16 bytes)
+      const uint64_t k_first = sw128(base + L::k, 16, 1024), q_first = sw128(base + L::q, 16, 1024);
+      // (rows of 64 elements: the upper half of the product repeats the lower)
+      const uint64_t v_first = sw128(base + L::v, L::panels > 1 ? kTile * 128 : 0, 1024),
+                     p_first = sw128(base + L::p, kTile * 128, 1024);
       auto scores = [&](int i) {
         const int ks = i % L::k_stages;
         if (!mbar_wait(bar(k_full + ks), (i / L::k_stages) & 1, abort_flag, a.status, 603)) return false;
         if (i >= 2 && !mbar_wait(bar(s_free + (i & 1)), (i / 2 - 1) & 1, abort_flag, a.status, 604)) return false;
         fence_after();
-        const uint32_t keys = base + L::k + ks * L::tile;
+        const uint64_t keys = k_first + (uint32_t)(ks * (L::tile / 16));
+        const uint32_t to = tmem + (i & 1) * N;
 #pragma unroll
         for (int kk = 0; kk < DP / 16; ++kk)
-          mma(tmem + (i & 1) * N, sw128(keys + kk / 4 * (kTile * 128) + kk % 4 * 32, 16, 1024),
-              sw128(base + L::q + kk / 4 * (N * 128) + kk % 4 * 32, 16, 1024), s_desc, kk > 0);
-        commit(bar(k_empty + ks));
+          mma(to, keys + (kk / 4 * (kTile * 8) + kk % 4 * 2), q_first + (kk / 4 * (N * 8) + kk % 4 * 2), s_desc, kk > 0);
         commit(bar(s_full + (i & 1)));
+        commit(bar(k_empty + ks));
         return true;
       };
       int i = 0, items = 0;
@@ -319,14 +318,11 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
                mbar_wait(bar(p_ready), i & 1, abort_flag, a.status, 607);
           if (!ok) break;
           fence_after();
-          const uint32_t values = base + L::v + vs * L::tile;
-          // (rows of 64 elements: the upper half of the product repeats the lower)
+          const uint64_t values = v_first + (uint32_t)(vs * (L::tile / 16));
 #pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            mma(o_cols, sw128(values + kk * 2048, L::panels > 1 ? kTile * 128 : 0, 1024),
-                sw128(base + L::p + kk * 2048, kTile * 128, 1024), o_desc, 1);
-          commit(bar(v_empty + vs));
+          for (int kk = 0; kk < kTile / 16; ++kk) mma(o_cols, values + kk * 128, p_first + kk * 128, o_desc, 1);
           commit(bar(o_done));
+          commit(bar(v_empty + vs));
         }
         ++items;
         use.chunk = use.k.chunks - 1;
@@ -339,7 +335,7 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
     __syncwarp();
   } else {
     // ---- softmax
-    const int st = tid - 64, quarter = warp & 3, group = (warp - 2) >> 2, token = quarter * 32 + lane, c0 = group * C;
+    const int st = tid - 96, quarter = warp & 3, group = (warp - 3) >> 2, token = quarter * 32 + lane, c0 = group * C;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     float* reference = reinterpret_cast<float*>(smem + L::reference);
     float* factor = reinterpret_cast<float*>(smem + L::factor);
