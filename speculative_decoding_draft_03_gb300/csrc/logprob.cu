@@ -640,6 +640,11 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_kernel(LogprobArgs a, int
 
 // --------------------------------------------------------------------------- backward
 
+// Written once: first to leave the cache (1024 rows of 151936 bf16: 97 us, with plain stores 100).
+__device__ __forceinline__ void store_stream16(void* p, uint4 v) {
+  asm volatile("st.global.cs.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 constexpr int kBackPieces = 4;  // 16-byte pieces per thread
 
 // grid: (pieces of a row / (256 x kBackPieces), rows).  `together`: a row's logits and its
@@ -698,7 +703,7 @@ __global__ void __launch_bounds__(kThreads) logprob_backward_kernel(LogprobArgs 
 #pragma unroll
       for (int i = 0; i < VE; ++i) x[i] = gradient(x[i], e + i);
       if (row.whole(piece)) {
-        store16(to + e, Piece<T>::pack(x));
+        store_stream16(to + e, Piece<T>::pack(x));
       } else {
 #pragma unroll
         for (int i = 0; i < VE; ++i)
