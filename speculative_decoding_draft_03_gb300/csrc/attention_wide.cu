@@ -1,5 +1,5 @@
-// attention_wide.cu — attention of larger blocks of queries over a paged cache of 16-bit
-// floats, on the 5th-generation tensor cores.
+// attention_wide.cu — attention of larger blocks of queries over a paged cache, on the
+// 5th-generation tensor cores.
 //
 // With many query rows per cache head (G heads times the verified block's queries) the products
 // outgrow the register-operand instructions; here both run as tcgen05.mma with the tokens, then
@@ -12,6 +12,8 @@
 //   * One persistent CTA per SM: warps 0 and 2 copy, warp 1 issues the products, the other 8 or 16
 //     do the softmax: a thread owns one token (its TMEM lane) and 16 or 32 of the columns.  S is
 //     double buffered; the copies run up to three tiles ahead of the products.
+//   * An e4m3 cache is copied as it is; four more warps turn each tile into fp16 (which holds every
+//     e4m3 value) for the products.  bf16 query rows are scaled by powers of two into fp16's range.
 //   * The softmax reference of a column moves only when a score passes it by 2^kSlack (any
 //     reference is right; the weights stay below 2^kSlack, inside fp16's range): a vote per
 //     tile replaces the maximum over the tokens, and the output is rescaled in TMEM only then.
@@ -32,8 +34,10 @@ namespace {
 using namespace attention;
 
 constexpr int kTile = 128;  // tokens
-// Softmax warps: four lane quarters times the column groups, of 16 columns (32 of 128).
-constexpr int softmax_warps(int N) { return N == 32 ? 8 : 16; }
+// Softmax warps: four lane quarters times the column groups, of 16 or 32 columns.  (With the four
+// converting warps of an e4m3 cache 16 of them would leave 80 registers a thread.)
+constexpr int softmax_warps(bool q8, int N) { return q8 || N == 32 ? 8 : 16; }
+constexpr int kConvertWarps = 4;
 constexpr float kSlack = 8.f;
 constexpr float kUnset = -1e30f;  // the reference of a column that has seen nothing: any score passes it
 constexpr long long kWaitCycles = 4000000000ll;  // ~2 s
@@ -155,30 +159,36 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // ------------------------------------------------------------------------- shared memory
 
-template <int DP, int N>
+template <bool Q8, int DP, int N>
 struct Plan {
-  static constexpr int softmax = 32 * softmax_warps(N), threads = 96 + softmax;
-  static constexpr int groups = softmax_warps(N) / 4, columns = N / groups;  // column groups
-  static constexpr int panels = DP / 64;
-  static constexpr int tile = panels * kTile * 128;  // keys, or values, of a tile
+  static constexpr int first_softmax = Q8 ? 3 + kConvertWarps : 3;  // warp
+  static constexpr int softmax = 32 * softmax_warps(Q8, N), threads = 32 * first_softmax + softmax;
+  static constexpr int groups = softmax_warps(Q8, N) / 4, columns = N / groups;  // column groups
+  static constexpr int panels = DP / 64;             // of 16-bit elements
+  static constexpr int tile = panels * kTile * 128;  // keys, or values, of a tile, as the products read them
+  static constexpr int copied = Q8 ? kTile * 128 : tile;  // ... and as they are copied
+  static constexpr int copy_panels = Q8 ? 1 : panels;
   static constexpr int k_stages = DP == 64 ? 4 : 3, v_stages = DP == 64 ? 4 : (N == 128 ? 2 : 3);
   static constexpr int tmem_cols = N == 32 ? 128 : (N == 64 ? 256 : 512);  // S twice, O: 3 N, a power of two
   // offsets, on 1 KB boundaries where products or copies read or write
   static constexpr int q = 0;                                        // [panels][N][128]
   static constexpr int p = q + panels * N * 128;                     // [(N + 63) / 64][128 tokens][128]
-  static constexpr int k = p + (N + 63) / 64 * kTile * 128;          // [k_stages][panels][128][128]
-  static constexpr int v = k + k_stages * tile;
-  static constexpr int reference = v + v_stages * tile;              // [N] float
+  static constexpr int k = p + (N + 63) / 64 * kTile * 128;          // [k_stages][copied]
+  static constexpr int v = k + k_stages * copied;                    // [v_stages][copied]
+  static constexpr int k16 = v + v_stages * copied;                  // e4m3: [tile] keys, then [2][tile] values, as fp16
+  static constexpr int v16 = k16 + (Q8 ? tile : 0);
+  static constexpr int reference = v16 + (Q8 ? 2 * tile : 0);        // [N] float
   static constexpr int factor = reference + 4 * N;                   // [N] float: rescaling, or one token's weights
   static constexpr int sums = p;                                     // [4][N] float, while the weights are not in use
   static constexpr int last = factor + 4 * N;                        // [N] int: the last position a column sees
   static constexpr int place = last + 4 * N;                         // [N] int: its row of the output, or -1
-  static constexpr int odd = place + 4 * N;                          // [128] bytes: tokens to be added on their own
+  static constexpr int up = place + 4 * N;                           // [N] float: scores in base 2 per product
+  static constexpr int odd = up + (Q8 ? 4 * N : 0);                  // [128] bytes: tokens to be added on their own
   static constexpr int bars = odd + 128;
-  static constexpr int n_bars = 2 * (k_stages + v_stages) + 8;
+  static constexpr int n_bars = 2 * (k_stages + v_stages) + 8 + (Q8 ? 6 : 0);
   static constexpr int start_off = bars + 8 * n_bars;                // long long
   static constexpr int scan = start_off + 8;                         // [threads / 32] long long
-  static constexpr int start_r = scan + 8 * (threads / 32);         // int
+  static constexpr int start_r = scan + 8 * (threads / 32);          // int
   static constexpr int tmem = start_r + 4, abort_flag = tmem + 4;
   static constexpr int total = abort_flag + 4;
   static_assert(total <= 232448, "227 KB");
@@ -188,11 +198,11 @@ struct Maps {
   CUtensorMap k, v;
 };
 
-template <bool BFQ, int DP, int N>
-__global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
+template <bool BFQ, bool Q8, int DP, int N>
+__global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
     attention_wide_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Maps maps, int box, Scratch scr) {
-  using L = Plan<DP, N>;
-  using H = Half16<BFQ>;
+  using L = Plan<Q8, DP, N>;
+  using H = Half16<BFQ && !Q8>;  // type of the products
   constexpr int C = L::columns;  // per softmax thread
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t base = smem_addr(smem);
@@ -200,14 +210,21 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
   auto bar = [&](int i) { return base + L::bars + 8 * i; };
   const int k_full = 0, k_empty = L::k_stages, v_full = 2 * L::k_stages, v_empty = v_full + L::v_stages,
             s_full = v_empty + L::v_stages, s_free = s_full + 2, p_ready = s_free + 2, o_done = p_ready + 1,
-            q_ready = o_done + 1, drained = q_ready + 1;
+            q_ready = o_done + 1, drained = q_ready + 1,
+            k16_full = drained + 1, k16_empty = k16_full + 1, v16_full = k16_empty + 1, v16_empty = v16_full + 2;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::abort_flag);
   const long long worker = blockIdx.x, workers = gridDim.x;
   const int G = a.G;
 
   if (tid == 0) {
-    for (int i = 0; i < L::k_stages; ++i) mbar_init(bar(k_full + i), 1), mbar_init(bar(k_empty + i), 1);
-    for (int i = 0; i < L::v_stages; ++i) mbar_init(bar(v_full + i), 1), mbar_init(bar(v_empty + i), 1);
+    constexpr int readers = Q8 ? kConvertWarps : 1;  // of a copied tile
+    for (int i = 0; i < L::k_stages; ++i) mbar_init(bar(k_full + i), 1), mbar_init(bar(k_empty + i), readers);
+    for (int i = 0; i < L::v_stages; ++i) mbar_init(bar(v_full + i), 1), mbar_init(bar(v_empty + i), readers);
+    if (Q8) {
+      mbar_init(bar(k16_full), kConvertWarps);
+      mbar_init(bar(k16_empty), 1);
+      for (int i = 0; i < 2; ++i) mbar_init(bar(v16_full + i), kConvertWarps), mbar_init(bar(v16_empty + i), 1);
+    }
     for (int i = 0; i < 2; ++i) mbar_init(bar(s_full + i), 1), mbar_init(bar(s_free + i), L::softmax / 32);
     mbar_init(bar(p_ready), L::softmax / 32);
     mbar_init(bar(o_done), 1);
@@ -268,12 +285,12 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
       if (inside && !there) report_bad_input(a.status, kBadPage);
       const int from = there ? page : a.num_pages;  // past the pool: zeros
       if (i >= stages && !mbar_wait(bar(empty + stage), phase, abort_flag, a.status, 601)) break;
-      if (lane == 0) mbar_expect(bar(full + stage), L::tile);
+      if (lane == 0) mbar_expect(bar(full + stage), L::copied);
       __syncwarp();
       if (lane < boxes)
 #pragma unroll
-        for (int n = 0; n < L::panels; ++n)
-          tma_box(ring + stage * L::tile + n * (kTile * 128) + lane * box * 128, map, bar(full + stage), 64 * n, slot, h, from);
+        for (int n = 0; n < L::copy_panels; ++n)
+          tma_box(ring + stage * L::copied + n * (kTile * 128) + lane * box * 128, map, bar(full + stage), 64 * n, slot, h, from);
       filled = i + 1;
       if (++stage == stages) stage = 0, phase ^= 1;
       if (i + 1 < tiles) {
@@ -286,15 +303,17 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
   } else if (warp == 1) {
     // ---- products
     if (lane == 0) {
-      constexpr uint32_t s_desc = idesc<BFQ>(N, false, false), o_desc = idesc<BFQ>(N, true, true);
+      constexpr uint32_t s_desc = idesc<BFQ && !Q8>(N, false, false), o_desc = idesc<BFQ && !Q8>(N, true, true);
       // descriptors of the first step; the others lie a constant further (in units of 16 bytes)
-      const uint64_t k_first = sw128(base + L::k, 16, 1024), q_first = sw128(base + L::q, 16, 1024);
+      const uint64_t k_first = sw128(base + (Q8 ? L::k16 : L::k), 16, 1024), q_first = sw128(base + L::q, 16, 1024);
       // (rows of 64 elements: the upper half of the product repeats the lower)
-      const uint64_t v_first = sw128(base + L::v, L::panels > 1 ? kTile * 128 : 0, 1024),
+      const uint64_t v_first = sw128(base + (Q8 ? L::v16 : L::v), L::panels > 1 ? kTile * 128 : 0, 1024),
                      p_first = sw128(base + L::p, kTile * 128, 1024);
       auto scores = [&](int i) {
-        const int ks = i % L::k_stages;
-        if (!mbar_wait(bar(k_full + ks), (i / L::k_stages) & 1, abort_flag, a.status, 603)) return false;
+        const int ks = Q8 ? 0 : i % L::k_stages;
+        if (!(Q8 ? mbar_wait(bar(k16_full), i & 1, abort_flag, a.status, 603)
+                 : mbar_wait(bar(k_full + ks), (i / L::k_stages) & 1, abort_flag, a.status, 603)))
+          return false;
         if (i >= 2 && !mbar_wait(bar(s_free + (i & 1)), (i / 2 - 1) & 1, abort_flag, a.status, 604)) return false;
         fence_after();
         const uint64_t keys = k_first + (uint32_t)(ks * (L::tile / 16));
@@ -303,7 +322,7 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
         for (int kk = 0; kk < DP / 16; ++kk)
           mma(to, keys + (kk / 4 * (kTile * 8) + kk % 4 * 2), q_first + (kk / 4 * (N * 8) + kk % 4 * 2), s_desc, kk > 0);
         commit(bar(s_full + (i & 1)));
-        commit(bar(k_empty + ks));
+        commit(bar(Q8 ? k16_empty : k_empty + ks));
         return true;
       };
       int i = 0, items = 0;
@@ -313,8 +332,8 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
         ok = mbar_wait(bar(q_ready), items & 1, abort_flag, a.status, 605) && scores(i);
         for (int t = 0; ok && t < n; ++t, ++i) {
           if (t + 1 < n && !scores(i + 1)) ok = false;
-          const int vs = i % L::v_stages;
-          ok = ok && mbar_wait(bar(v_full + vs), (i / L::v_stages) & 1, abort_flag, a.status, 606) &&
+          const int vs = Q8 ? i & 1 : i % L::v_stages;
+          ok = ok && mbar_wait(bar((Q8 ? v16_full : v_full) + vs), (Q8 ? i / 2 : i / L::v_stages) & 1, abort_flag, a.status, 606) &&
                mbar_wait(bar(p_ready), i & 1, abort_flag, a.status, 607);
           if (!ok) break;
           fence_after();
@@ -322,7 +341,7 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk) mma(o_cols, values + kk * 128, p_first + kk * 128, o_desc, 1);
           commit(bar(o_done));
-          commit(bar(v_empty + vs));
+          commit(bar((Q8 ? v16_empty : v_empty) + vs));
         }
         ++items;
         use.chunk = use.k.chunks - 1;
@@ -333,9 +352,40 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
       mbar_drain(bar(drained), 0);
     }
     __syncwarp();
+  } else if (Q8 && warp < L::first_softmax) {
+    // ---- e4m3 to fp16: a thread per token, 16 elements (one piece) into two pieces at a time
+    const int token = tid - 96;
+    auto convert = [&](uint32_t from, uint32_t to) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint4 x = lds16(from + token * 128 + ((c ^ (token & 7)) << 4));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[2 * e] = e4m3_to_half2(w[e]), h[2 * e + 1] = e4m3_to_half2(w[e] >> 16);
+        const uint32_t row = to + (c >> 2) * (kTile * 128) + token * 128;
+        const int piece = 2 * c & 7;
+        sts16(row + ((piece ^ (token & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+        sts16(row + (((piece + 1) ^ (token & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+      }
+      fence_smem();
+      __syncwarp();
+    };
+    for (int i = 0; i < tiles; ++i) {
+      const int ks = i % L::k_stages, vs = i % L::v_stages;
+      if (!mbar_wait(bar(k_full + ks), (i / L::k_stages) & 1, abort_flag, a.status, 613)) break;
+      if (i >= 1 && !mbar_wait(bar(k16_empty), (i - 1) & 1, abort_flag, a.status, 614)) break;
+      convert(base + L::k + ks * L::copied, base + L::k16);
+      if (lane == 0) mbar_arrive(bar(k_empty + ks)), mbar_arrive(bar(k16_full));
+      if (!mbar_wait(bar(v_full + vs), (i / L::v_stages) & 1, abort_flag, a.status, 615)) break;
+      if (i >= 2 && !mbar_wait(bar(v16_empty + (i & 1)), (i / 2 - 1) & 1, abort_flag, a.status, 616)) break;
+      convert(base + L::v + vs * L::copied, base + L::v16 + (i & 1) * L::tile);
+      if (lane == 0) mbar_arrive(bar(v_empty + vs)), mbar_arrive(bar(v16_full + (i & 1)));
+    }
+    __syncwarp();
   } else {
     // ---- softmax
-    const int st = tid - 96, quarter = warp & 3, group = (warp - 3) >> 2, token = quarter * 32 + lane, c0 = group * C;
+    const int st = tid - 32 * L::first_softmax, quarter = warp & 3, group = (warp - L::first_softmax) >> 2, token = quarter * 32 + lane, c0 = group * C;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     float* reference = reinterpret_cast<float*>(smem + L::reference);
     float* factor = reinterpret_cast<float*>(smem + L::factor);
@@ -343,7 +393,7 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
     int* last = reinterpret_cast<int*>(smem + L::last);
     int* place = reinterpret_cast<int*>(smem + L::place);
     volatile unsigned char* odd = smem + L::odd;
-    const float c2 = a.scale * kLog2e;
+    float* up = reinterpret_cast<float*>(smem + L::up);
     float l[C];
     bool ok = true;
     int i = 0;
@@ -351,6 +401,7 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
     while (i < tiles) {
       const int n = min(use.k.chunks - use.chunk, tiles - i);
       const int h = use.k.blocks == 1 ? use.item : use.item / use.k.blocks, row0 = (use.item - h * use.k.blocks) * N;
+      const float c2 = a.scale * kLog2e * (Q8 ? a.k_scale[h] : 1.f);  // scores in base 2 per product (e4m3: `up`)
       softmax_sync<L::softmax>();  // the previous item's tables are no longer read
       for (int e = st; e < N * (DP / 8); e += L::softmax) {
         const int row = e / (DP / 8), c = e % (DP / 8), rr = row0 + row, q = rr / G;
@@ -359,6 +410,28 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
           x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
                                               (int64_t)(use.k.q0 + q) * a.q_stride_token +
                                               (int64_t)(h * G + rr - q * G) * a.q_stride_head + c * 8);
+        if (Q8) {
+          // fp16 operands; a bf16 row is scaled by a power of two to a maximum in [1, 2) (what falls
+          // below 2^-24 of it is lost, far under the sums' rounding).  16 lanes hold a row.
+          static_assert(!Q8 || DP == 128, "a row per half warp");
+          uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          int e2 = 0;
+          if (BFQ) {
+            float top = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              top = max3(top, fabsf(Half16<true>::lo(w[j])), fabsf(Half16<true>::hi(w[j])));
+#pragma unroll
+            for (int s = 8; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, s));
+            if (top > 0.f && top < INFINITY) e2 = min(max(ilogbf(top), -126), 126);
+            const float down = ldexpf(1.f, -e2);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[j] = Half16<false>::pack(Half16<true>::lo(w[j]) * down, Half16<true>::hi(w[j]) * down);
+          }
+          if (c == 0) up[row] = c2 * ldexpf(1.f, e2);
+          x = make_uint4(w[0], w[1], w[2], w[3]);
+        }
         sts16(base + L::q + (c >> 3) * (N * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4), x);
       }
       if (st < N) {
@@ -402,13 +475,16 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
             if (pos > to || (a.window > 0 && pos <= to - a.window)) x[c] = -INFINITY;
           }
         }
+        auto scale_of = [&](int c) {
+          return Q8 ? *reinterpret_cast<const float4*>(up + c0 + c) : make_float4(c2, c2, c2, c2);
+        };
         // does a score pass its reference?  (A masked score stays -inf whatever the scale's sign.)
         float most = -INFINITY;
 #pragma unroll
         for (int c = 0; c < C; c += 4) {
-          const float4 r = *reinterpret_cast<const float4*>(reference + c0 + c);
-          const float u0 = fmaf(x[c], c2, -r.x), u1 = fmaf(x[c + 1], c2, -r.y), u2 = fmaf(x[c + 2], c2, -r.z),
-                      u3 = fmaf(x[c + 3], c2, -r.w);
+          const float4 r = *reinterpret_cast<const float4*>(reference + c0 + c), k = scale_of(c);
+          const float u0 = fmaf(x[c], k.x, -r.x), u1 = fmaf(x[c + 1], k.y, -r.y), u2 = fmaf(x[c + 2], k.z, -r.z),
+                      u3 = fmaf(x[c + 3], k.w, -r.w);
           most = max3(most, edge && x[c] == -INFINITY ? -INFINITY : u0, edge && x[c + 1] == -INFINITY ? -INFINITY : u1);
           most = max3(most, edge && x[c + 2] == -INFINITY ? -INFINITY : u2, edge && x[c + 3] == -INFINITY ? -INFINITY : u3);
         }
@@ -424,7 +500,7 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
           // new references: the columns' maxima, over lanes, then over the four quarters
 #pragma unroll
           for (int c = 0; c < C; ++c) {
-            float v = edge && x[c] == -INFINITY ? -INFINITY : x[c] * c2;
+            float v = edge && x[c] == -INFINITY ? -INFINITY : x[c] * (Q8 ? up[c0 + c] : c2);
 #pragma unroll
             for (int s = 16; s; s >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, s));
             if (lane == 0) sums[quarter * N + c0 + c] = v;
@@ -454,11 +530,11 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
         }
 #pragma unroll
         for (int c = 0; c < C; c += 4) {
-          const float4 r = *reinterpret_cast<const float4*>(reference + c0 + c);
-          const float rr[4] = {r.x, r.y, r.z, r.w};
+          const float4 r = *reinterpret_cast<const float4*>(reference + c0 + c), k = scale_of(c);
+          const float rr[4] = {r.x, r.y, r.z, r.w}, kk[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            x[c + e] = edge && x[c + e] == -INFINITY ? 0.f : ex2(fmaf(x[c + e], c2, -rr[e]));
+            x[c + e] = edge && x[c + e] == -INFINITY ? 0.f : ex2(fmaf(x[c + e], kk[e], -rr[e]));
             l[c + e] += x[c + e];
           }
         }
@@ -467,9 +543,9 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
           // Tokens that no column sees hold anything (the rest of a page): their values are
           // cleared.  One that only some columns see must not reach the others if it is not
           // finite (0 x NaN): it is added on its own, and cleared for the product.
-          const int vs = i % L::v_stages;
-          ok = mbar_wait(bar(v_full + vs), (i / L::v_stages) & 1, abort_flag, a.status, 610) && ok;
-          const uint32_t values = base + L::v + vs * L::tile;
+          const int vs = Q8 ? i & 1 : i % L::v_stages;
+          ok = mbar_wait(bar((Q8 ? v16_full : v_full) + vs), (Q8 ? i / 2 : i / L::v_stages) & 1, abort_flag, a.status, 610) && ok;
+          const uint32_t values = base + (Q8 ? L::v16 : L::v) + vs * L::tile;
           constexpr int kPieces = L::panels * 8 / L::groups;  // this thread's part of the token's row
           auto part_of_row = [&](int c) {
             const int piece = group * kPieces + c;
@@ -559,7 +635,7 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
       if (st < N) {
         const float sum = (sums[st] + sums[N + st]) + (sums[2 * N + st] + sums[3 * N + st]);
         if (whole) {
-          factor[st] = sum == 0.f ? 0.f : 1.f / sum;
+          factor[st] = sum == 0.f ? 0.f : (Q8 ? a.v_scale[h] : 1.f) / sum;
           if (place[st] >= 0 && a.lse_out != nullptr)
             a.lse_out[place[st]] = sum == 0.f ? -INFINITY : (reference[st] + log2f(sum)) * kLn2;
         } else {
@@ -578,7 +654,7 @@ __global__ void __launch_bounds__(Plan<DP, N>::threads, 1)
             if (whole) {
               if (place[col] >= 0 && token < a.D)
                 static_cast<uint16_t*>(a.out)[(size_t)place[col] * a.D + token] =
-                    (uint16_t)H::pack(factor[col] == 0.f ? 0.f : o[e] * factor[col], 0.f);
+                    (uint16_t)Half16<BFQ>::pack(factor[col] == 0.f ? 0.f : o[e] * factor[col], 0.f);
             } else {
               scr.out[(rows + col) * DP + token] = o[e];
             }
@@ -623,14 +699,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 bool encode_pool(CUtensorMap* map, const AttentionArgs& a, const void* pool, int box) {
   auto fn = encoder();
   if (fn == nullptr) return false;
+  const cuuint64_t size = a.dtype_kv == DSPARK_E4M3 ? 1 : 2;
   // a dimension of one entry has no stride of its own: any that is allowed will do
-  const cuuint64_t row = (cuuint64_t)a.D * 2;
-  const cuuint64_t strides[3] = {a.token_stride ? (cuuint64_t)a.token_stride * 2 : row,
-                                 a.head_stride ? (cuuint64_t)a.head_stride * 2 : row,
-                                 a.page_stride ? (cuuint64_t)a.page_stride * 2 : row};
+  const cuuint64_t row = (cuuint64_t)a.D * size;
+  const cuuint64_t strides[3] = {a.token_stride ? (cuuint64_t)a.token_stride * size : row,
+                                 a.head_stride ? (cuuint64_t)a.head_stride * size : row,
+                                 a.page_stride ? (cuuint64_t)a.page_stride * size : row};
   const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.page_size, (cuuint64_t)a.Hkv, (cuuint64_t)a.num_pages};
-  const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(pool), dims, strides, boxes, ones,
+  const cuuint32_t boxes[4] = {(cuuint32_t)(128 / size), (cuuint32_t)box, 1, 1}, ones[4] = {1, 1, 1, 1};
+  return fn(map, size == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(pool), dims, strides, boxes, ones,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -643,46 +720,53 @@ int box_tokens(int page_size) {
   return box >= 8 ? box : 0;
 }
 
-int columns(int max_q, int G) {
+// Columns of an item: what the call's largest block needs, up to 128 (64 over an e4m3 cache, whose
+// converted tiles take the shared memory).
+int columns(int max_q, int G, bool q8) {
   const int rows = max_q * G;
-  return rows <= 32 ? 32 : (rows <= 64 ? 64 : 128);
+  return rows <= 32 ? 32 : (rows <= 64 || q8 ? 64 : 128);
 }
 
-template <bool BFQ, int DP, int N>
+template <bool BFQ, bool Q8, int DP, int N>
 cudaError_t launch(const AttentionArgs& a, const Maps& maps, int box, void* scratch, cudaStream_t s) {
-  auto* kernel = attention_wide_kernel<BFQ, DP, N>;
+  using L = Plan<Q8, DP, N>;
+  auto* kernel = attention_wide_kernel<BFQ, Q8, DP, N>;
   static std::atomic<uint64_t> done;
-  cudaError_t e = allow_smem(kernel, Plan<DP, N>::total, done);
+  cudaError_t e = allow_smem(kernel, L::total, done);
   if (e != cudaSuccess) return e;
   const int workers = std::min(sm_count(), kMaxSms);
   const Scratch scr = scratch_at(scratch, kMaxSms, N);
-  e = launch_chained(kernel, dim3(workers), dim3(Plan<DP, N>::threads), Plan<DP, N>::total, s, 1, a, maps, box, scr);
+  e = launch_chained(kernel, dim3(workers), dim3(L::threads), L::total, s, 1, a, maps, box, scr);
   return e != cudaSuccess ? e : launch_join<BFQ, DP, N>(a, scr, workers, s);
 }
 
-template <bool BFQ, int DP>
+template <bool BFQ>
 cudaError_t launch(const AttentionArgs& a, const Maps& maps, int box, void* scratch, cudaStream_t s) {
-  switch (columns(a.max_q, a.G)) {
-    case 32: return launch<BFQ, DP, 32>(a, maps, box, scratch, s);
-    case 64: return launch<BFQ, DP, 64>(a, maps, box, scratch, s);
-    default: return launch<BFQ, DP, 128>(a, maps, box, scratch, s);
-  }
+  const bool q8 = a.dtype_kv == DSPARK_E4M3;
+  const int n = columns(a.max_q, a.G, q8);
+  if (q8)
+    return n == 32 ? launch<BFQ, true, 128, 32>(a, maps, box, scratch, s) : launch<BFQ, true, 128, 64>(a, maps, box, scratch, s);
+  if (a.D <= 64)
+    return n == 32 ? launch<BFQ, false, 64, 32>(a, maps, box, scratch, s)
+                   : (n == 64 ? launch<BFQ, false, 64, 64>(a, maps, box, scratch, s)
+                              : launch<BFQ, false, 64, 128>(a, maps, box, scratch, s));
+  return n == 32 ? launch<BFQ, false, 128, 32>(a, maps, box, scratch, s)
+                 : (n == 64 ? launch<BFQ, false, 128, 64>(a, maps, box, scratch, s)
+                            : launch<BFQ, false, 128, 128>(a, maps, box, scratch, s));
 }
 
 }  // namespace
 
 size_t attention_wide_scratch(int Hq, int Hkv, int D, int max_q) {
-  return D > 128 ? 0 : attention::scratch_bytes(kMaxSms, columns(max_q, Hq / Hkv), D <= 64 ? 64 : 128);
+  return D > 128 ? 0 : attention::scratch_bytes(kMaxSms, columns(max_q, Hq / Hkv, false), 128);
 }
 
 bool launch_attention_wide(const AttentionArgs& a, void* scratch, cudaStream_t s, cudaError_t& e) {
-  if (a.dtype_kv == DSPARK_E4M3 || a.D > 128) return false;
+  if (a.D > 128) return false;
   const int box = box_tokens(a.page_size);
   Maps maps;
   if (box == 0 || !encode_pool(&maps.k, a, a.k_pool, box) || !encode_pool(&maps.v, a, a.v_pool, box)) return false;
-  const bool bf = a.dtype_q == DSPARK_BF16;
-  if (a.D <= 64) e = bf ? launch<true, 64>(a, maps, box, scratch, s) : launch<false, 64>(a, maps, box, scratch, s);
-  else e = bf ? launch<true, 128>(a, maps, box, scratch, s) : launch<false, 128>(a, maps, box, scratch, s);
+  e = a.dtype_q == DSPARK_BF16 ? launch<true>(a, maps, box, scratch, s) : launch<false>(a, maps, box, scratch, s);
   return true;
 }
 
