@@ -1,4 +1,5 @@
-"""Thin ctypes binding of ``libdspark.so`` (argument marshalling only).
+"""Thin binding of ``libdspark.so`` (argument marshalling only): ctypes, and for the serving-side
+calls, which run many times per token, the compiled ``_marshal`` module.
 
 Every step of the path runs in the library's CUDA kernels; this module checks tensor
 placement/dtypes, passes ``data_ptr()``s and the current CUDA stream, and owns the
@@ -7,7 +8,9 @@ missing this module raises at import: there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -17,8 +20,6 @@ from . import build as _build
 F32, BF16, F16, E4M3 = 0, 1, 2, 3
 EARLY_STOP, FULL_SEARCH, CAPACITY_K, FIXED = 0, 1, 2, 3
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
-_LOGIT_DT = {**_DT, torch.float16: F16}
-_CACHE_DT = {torch.bfloat16: BF16, torch.float16: F16, torch.float8_e4m3fn: E4M3}
 
 
 class DSparkError(RuntimeError):
@@ -630,10 +631,20 @@ class Round:
         return max(codes)
 
 
-# The calls below take a few microseconds of GPU time at serving's small sizes, so their
-# marshalling is kept short: one look at each tensor, plain integers for pointers, and the
-# current stream as the raw handle.
+# The serving-side calls: their tensors are checked and passed on by the compiled module.
 
+def _load_marshal():
+    path = _build.MARSHAL
+    if not os.path.exists(path):
+        raise DSparkError(f"_marshal.so is not built ({path}); run __graft_entry__.build()")
+    spec = importlib.util.spec_from_file_location("_marshal", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.set_error(DSparkError)
+    return module
+
+
+_m = _load_marshal()
 _raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 
@@ -646,36 +657,16 @@ def _raw_stream(stream):
     return _raw_stream_of(_current_device())
 
 
-def _ptr(t, name, dtype, n=None):
-    """The address of a contiguous CUDA tensor of `dtype` (and n elements)."""
-    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda or not t.is_contiguous()
-            or (n is not None and t.numel() != n)):
-        _cuda(t, name, dtype)
-        raise DSparkError(f"{name} must hold {n} values, got {t.numel()}")
-    return t.data_ptr()
+def _made_on(stream):
+    """Where a call makes the buffers it was not given: on the stream that it runs on (a buffer
+    belongs to the stream of its making, and a workspace is cleared there)."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _opt(t, name, dtype, n=None):
-    return None if t is None else _ptr(t, name, dtype, n)
-
-
-def _rows(t, name, dtype=None):
-    """(address, rows, columns, row stride) of a 2-D CUDA tensor with contiguous rows."""
+def _on_gpu(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise DSparkError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype is not dtype:
-        raise DSparkError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2:
-        raise DSparkError(f"{name} must be 2-D")
-    n, m = t.shape
-    rs, cs = t.stride()
-    if m > 1 and cs != 1:
-        raise DSparkError(f"the rows of {name} must be contiguous")
-    if n <= 1 or rs < m:
-        if n > 1:
-            raise DSparkError(f"the rows of {name} overlap")
-        rs = m  # the stride of one row means nothing
-    return t.data_ptr(), n, m, rs
+    return t
 
 
 # ------------------------------------------------------------- token log probabilities
@@ -686,22 +677,16 @@ def token_logprobs(logits, tokens, temperature=1.0, top_k=0, out=None, stream=No
     float16 with any row stride; tokens [N] int32, rows with an id outside [0,V) (verification
     writes -1) are skipped and hold NaN / -1.  Returns dict logprob, entropy, lse [N] and, with
     top_k, top_ids, top_logprobs [N,top_k]."""
-    x, N, V, rs = _rows(logits, "logits")
-    dt = _LOGIT_DT.get(logits.dtype)
-    if dt is None:
-        raise DSparkError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
     if out is None:
+        N = _on_gpu(logits, "logits").shape[0]
         f = dict(dtype=torch.float32, device=logits.device)
-        out = dict(logprob=torch.empty(N, **f), entropy=torch.empty(N, **f), lse=torch.empty(N, **f))
-        if top_k > 0:
-            out["top_ids"] = torch.empty((N, top_k), dtype=torch.int32, device=logits.device)
-            out["top_logprobs"] = torch.empty((N, top_k), **f)
-    f32 = torch.float32
-    st = lib.dspark_token_logprobs(
-        N, V, rs, dt, x, _ptr(tokens, "tokens", torch.int32, N), temperature, top_k,
-        _ptr(out["logprob"], "logprob", f32, N), _ptr(out["entropy"], "entropy", f32, N), _ptr(out["lse"], "lse", f32, N),
-        _ptr(out["top_ids"], "top_ids", torch.int32, N * top_k) if top_k > 0 else None,
-        _ptr(out["top_logprobs"], "top_logprobs", f32, N * top_k) if top_k > 0 else None, _raw_stream(stream))
+        with _made_on(stream):
+            out = dict(logprob=torch.empty(N, **f), entropy=torch.empty(N, **f), lse=torch.empty(N, **f))
+            if top_k > 0:
+                out["top_ids"] = torch.empty((N, top_k), dtype=torch.int32, device=logits.device)
+                out["top_logprobs"] = torch.empty((N, top_k), **f)
+    st = _m.token_logprobs(logits, tokens, temperature, top_k, out["logprob"], out["entropy"], out["lse"],
+                           out.get("top_ids"), out.get("top_logprobs"), _raw_stream(stream))
     if st:
         _check(st, "dspark_token_logprobs")
     return out
@@ -712,20 +697,11 @@ def token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad_ent
     """The gradient of sum(grad_logprob * logprob + grad_entropy * entropy) for ``logits``
     (dspark_token_logprobs_backward), from token_logprobs' lse and entropy.  ``out`` [N,V] of the
     logits' type may be the logits themselves."""
-    x, N, V, rs = _rows(logits, "logits")
-    dt = _LOGIT_DT.get(logits.dtype)
-    if dt is None:
-        raise DSparkError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
     if out is None:
-        out = torch.empty((N, V), dtype=logits.dtype, device=logits.device)
-    y, n, v, gs = _rows(out, "out", logits.dtype)
-    if n != N or v != V:
-        raise DSparkError("out must have the logits' shape")
-    f32 = torch.float32
-    st = lib.dspark_token_logprobs_backward(
-        N, V, rs, gs, dt, x, _ptr(tokens, "tokens", torch.int32, N), temperature, _ptr(lse, "lse", f32, N),
-        _ptr(entropy, "entropy", f32, N), _ptr(grad_logprob, "grad_logprob", f32, N),
-        _opt(grad_entropy, "grad_entropy", f32, N), y, _raw_stream(stream))
+        with _made_on(stream):
+            out = torch.empty_like(_on_gpu(logits, "logits"), memory_format=torch.contiguous_format)
+    st = _m.token_logprobs_backward(logits, tokens, lse, entropy, grad_logprob, grad_entropy, temperature, out,
+                                    _raw_stream(stream))
     if st:
         _check(st, "dspark_token_logprobs_backward")
     return out
@@ -753,39 +729,34 @@ class CachePools:
             self.num_pages = t.shape[0]
             self.page_bytes = t.numel() // max(1, t.shape[0]) * t.element_size()
         self.array = (ctypes.c_void_p * max(1, self.n))(*[t.data_ptr() for t in self.tensors])
+        self.address = ctypes.addressof(self.array)
 
 
 def cache_pools(pools) -> CachePools:
     return CachePools(pools)
 
 
-def _tables(page_table, seq_len, ref_count, page_size):
-    """The leading arguments of the calls that change the tables."""
-    table, R, width, stride = _rows(page_table, "page_table", torch.int32)
-    return (R, ref_count.numel(), page_size, width, stride, table, _ptr(seq_len, "seq_len", torch.int32, R),
-            _ptr(ref_count, "ref_count", torch.int32))
+def _cache_ws(ws, page_table, ref_count, stream):
+    if ws is None:
+        with _made_on(stream):
+            ws = workspace(cache_workspace_size(_on_gpu(page_table, "page_table").shape[0],
+                                                _on_gpu(ref_count, "ref_count").numel()), page_table.device)
+    return ws
 
 
-def _cache_ws(ws, t, like):
-    return workspace(cache_workspace_size(t[0], t[1]), like.device) if ws is None else ws
-
-
-def _page_pools(pools, num_pages):
+def _page_pools(pools, ref_count):
     if not isinstance(pools, CachePools):
         pools = CachePools(pools or [])
-    if pools.n and pools.num_pages != num_pages:
-        raise DSparkError(f"the pools have {pools.num_pages} pages, ref_count {num_pages}")
+    if pools.n and pools.num_pages != ref_count.numel():
+        raise DSparkError(f"the pools have {pools.num_pages} pages, ref_count {ref_count.numel()}")
     return pools
 
 
 def cache_fork(page_table, seq_len, ref_count, src, dst, page_size, ws=None, stream=None):
     """Empty slots ``dst`` become copies of slots ``src`` that share their pages
     (dspark_cache_fork).  src, dst [F] int32."""
-    t = _tables(page_table, seq_len, ref_count, page_size)
-    F = src.numel()
-    ws = _cache_ws(ws, t, page_table)
-    st = lib.dspark_cache_fork(F, *t, _ptr(src, "src", torch.int32, F), _ptr(dst, "dst", torch.int32, F), ws.data_ptr(),
-                               ws.numel(), _raw_stream(stream))
+    st = _m.cache_fork(page_table, seq_len, ref_count, src, dst, page_size, _cache_ws(ws, page_table, ref_count, stream),
+                       _raw_stream(stream))
     if st:
         _check(st, "dspark_cache_fork")
 
@@ -794,55 +765,17 @@ def cache_reserve(page_table, seq_len, ref_count, n_new, page_size, pools, out=N
     """Room for ``n_new`` [R] int32 more tokens in every slot, with a copy of each partly filled
     shared page about to be written (dspark_cache_reserve).  ``pools``: cache_pools(...), a list
     of pools, or None to change the tables only.  Returns dict granted [R], copies [R,2]."""
-    t = _tables(page_table, seq_len, ref_count, page_size)
-    R = t[0]
     if out is None:
-        out = dict(granted=torch.empty(R, dtype=torch.int32, device=page_table.device),
-                   copies=torch.empty((R, 2), dtype=torch.int32, device=page_table.device))
-    pools = _page_pools(pools, t[1])
-    ws = _cache_ws(ws, t, page_table)
-    i32 = torch.int32
-    st = lib.dspark_cache_reserve(*t, _ptr(n_new, "n_new", i32, R), _ptr(out["granted"], "granted", i32, R),
-                                  _ptr(out["copies"], "copies", i32, 2 * R), pools.n, pools.array, pools.page_bytes,
-                                  ws.data_ptr(), ws.numel(), _raw_stream(stream))
+        i32 = dict(dtype=torch.int32, device=_on_gpu(page_table, "page_table").device)
+        with _made_on(stream):
+            out = dict(granted=torch.empty(page_table.shape[0], **i32),
+                       copies=torch.empty((page_table.shape[0], 2), **i32))
+    pools = _page_pools(pools, ref_count)
+    st = _m.cache_reserve(page_table, seq_len, ref_count, n_new, page_size, pools.n, pools.address, pools.page_bytes,
+                          out["granted"], out["copies"], _cache_ws(ws, page_table, ref_count, stream), _raw_stream(stream))
     if st:
         _check(st, "dspark_cache_reserve")
     return out
-
-
-def _strides(t, shape):
-    """The leading strides (0 where a dimension has one entry, whose stride means nothing)."""
-    return [s if n > 1 else 0 for s, n in zip(t.stride(), shape)][:-1]
-
-
-def _pool_args(k_pool, v_pool):
-    """(shape, strides, type code, addresses) of two pools [num_pages, Hkv, page_size, D] with
-    contiguous rows and the same strides."""
-    if not isinstance(k_pool, torch.Tensor) or not isinstance(v_pool, torch.Tensor) or not (k_pool.is_cuda and v_pool.is_cuda):
-        raise DSparkError("k_pool and v_pool must be CUDA tensors")
-    shape, kv = k_pool.shape, _CACHE_DT.get(k_pool.dtype)
-    if kv is None or v_pool.dtype is not k_pool.dtype:
-        raise DSparkError("the pools must share a type: bfloat16, float16 or float8_e4m3fn")
-    if len(shape) != 4 or v_pool.shape != shape or k_pool.stride(3) != 1 or v_pool.stride(3) != 1:
-        raise DSparkError("the pools must share a shape [num_pages, Hkv, page_size, D] with contiguous rows")
-    strides = _strides(k_pool, shape)
-    if v_pool.stride() != k_pool.stride() and _strides(v_pool, shape) != strides:
-        raise DSparkError("the pools must share their strides")
-    return shape, strides, kv, k_pool.data_ptr(), v_pool.data_ptr()
-
-
-def _token_rows(t, name, H, D):
-    """(address, tokens, token stride, head stride) of a CUDA tensor [T,H,D] of 16-bit floats
-    with contiguous rows (H, D None: any)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
-        raise DSparkError(f"{name} must be a CUDA tensor [T, heads, D]")
-    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float16:
-        raise DSparkError(f"{name} must be bfloat16 or float16, got {t.dtype}")
-    T, h, d = t.shape
-    st, sh, sd = t.stride()
-    if (H is not None and h != H) or d != D or sd != 1:
-        raise DSparkError(f"{name} must be [T, {'heads' if H is None else H}, {D}] with contiguous rows")
-    return t.data_ptr(), T, h, st if T > 1 else 0, sh if h > 1 else 0
 
 
 def cache_write(k, v, k_pool, v_pool, page_table, seq_len, q_start, granted=None, k_scale=None, v_scale=None, ws=None,
@@ -850,20 +783,11 @@ def cache_write(k, v, k_pool, v_pool, page_table, seq_len, q_start, granted=None
     """Writes the keys and values k, v [T,Hkv,D] of every slot's last tokens (rows q_start[r] ..
     q_start[r+1]-1) into one layer's pools [num_pages,Hkv,page_size,D] (dspark_cache_write), after
     cache_reserve made room.  Pools of float8_e4m3fn hold x / scale[head]."""
-    (P, H, ps, D), strides, kv, kp, vp = _pool_args(k_pool, v_pool)
-    ka = _token_rows(k, "k", H, D)
-    va = _token_rows(v, "v", H, D)
-    if k.dtype is not v.dtype or ka[1:] != va[1:]:
-        raise DSparkError("k and v must share their type, shape and strides")
-    table, R, width, ts = _rows(page_table, "page_table", torch.int32)
     if ws is None:
-        ws = workspace(256, k_pool.device)
-    i32, f32 = torch.int32, torch.float32
-    st = lib.dspark_cache_write(ka[1], R, H, D, P, ps, width, _CACHE_DT[k.dtype], kv, ka[0], va[0], ka[3], ka[4], kp, vp,
-                                *strides, table, ts, _ptr(seq_len, "seq_len", i32, R),
-                                _ptr(q_start, "q_start", i32, R + 1), _opt(granted, "granted", i32, R),
-                                _opt(k_scale, "k_scale", f32, H), _opt(v_scale, "v_scale", f32, H), ws.data_ptr(),
-                                ws.numel(), _raw_stream(stream))
+        with _made_on(stream):
+            ws = workspace(256, _on_gpu(k_pool, "k_pool").device)
+    st = _m.cache_write(k, v, k_pool, v_pool, page_table, seq_len, q_start, granted, k_scale, v_scale, ws,
+                        _raw_stream(stream))
     if st:
         _check(st, "dspark_cache_write")
 
@@ -871,10 +795,8 @@ def cache_write(k, v, k_pool, v_pool, page_table, seq_len, q_start, granted=None
 def cache_truncate(page_table, seq_len, ref_count, new_len, page_size, ws=None, stream=None):
     """Every slot keeps its first ``new_len`` [R] int32 tokens; pages past them are released
     (dspark_cache_truncate).  0 frees the slot."""
-    t = _tables(page_table, seq_len, ref_count, page_size)
-    ws = _cache_ws(ws, t, page_table)
-    st = lib.dspark_cache_truncate(*t, _ptr(new_len, "new_len", torch.int32, t[0]), ws.data_ptr(), ws.numel(),
-                                   _raw_stream(stream))
+    st = _m.cache_truncate(page_table, seq_len, ref_count, new_len, page_size, _cache_ws(ws, page_table, ref_count, stream),
+                           _raw_stream(stream))
     if st:
         _check(st, "dspark_cache_truncate")
 
@@ -882,13 +804,12 @@ def cache_truncate(page_table, seq_len, ref_count, new_len, page_size, ws=None, 
 def cache_compact(page_table, seq_len, ref_count, page_size, pools, out=None, ws=None, stream=None):
     """Moves the used pages to the lowest indexes, in the tables and in every pool
     (dspark_cache_compact).  Returns the number of pages moved, [1] int32."""
-    t = _tables(page_table, seq_len, ref_count, page_size)
     if out is None:
-        out = torch.empty(1, dtype=torch.int32, device=page_table.device)
-    pools = _page_pools(pools, t[1])
-    ws = _cache_ws(ws, t, page_table)
-    st = lib.dspark_cache_compact(*t, _ptr(out, "out", torch.int32, 1), pools.n, pools.array, pools.page_bytes,
-                                  ws.data_ptr(), ws.numel(), _raw_stream(stream))
+        with _made_on(stream):
+            out = torch.empty(1, dtype=torch.int32, device=_on_gpu(page_table, "page_table").device)
+    pools = _page_pools(pools, ref_count)
+    st = _m.cache_compact(page_table, seq_len, ref_count, page_size, pools.n, pools.address, pools.page_bytes, out,
+                          _cache_ws(ws, page_table, ref_count, stream), _raw_stream(stream))
     if st:
         _check(st, "dspark_cache_compact")
     return out
@@ -903,22 +824,17 @@ def paged_attention(q, k_pool, v_pool, page_table, seq_len, q_start, max_q, scal
     """Attention of every slot's last tokens over its paged context (dspark_paged_attention).
     q [T,Hq,D] bfloat16 or float16, rows q_start[r] .. q_start[r+1]-1 for slot r, at most
     ``max_q`` a slot.  Returns dict out [T,Hq,D], lse [T,Hq] float32."""
-    (P, H, ps, D), strides, kv, kp, vp = _pool_args(k_pool, v_pool)
-    qa, T, Hq, q_token, q_head = _token_rows(q, "q", None, D)
-    table, R, width, ts = _rows(page_table, "page_table", torch.int32)
-    if out is None:
-        out = dict(out=torch.empty((T, Hq, D), dtype=q.dtype, device=q.device),
-                   lse=torch.empty((T, Hq), dtype=torch.float32, device=q.device))
-    if ws is None:
-        ws = workspace(paged_attention_workspace_size(T, R, Hq, H, D, max_q), q.device)
-    i32, f32 = torch.int32, torch.float32
-    st = lib.dspark_paged_attention(T, R, Hq, H, D, P, ps, width, max_q, _CACHE_DT[q.dtype], kv, qa, q_token, q_head, kp,
-                                    vp, *strides, table, ts, _ptr(seq_len, "seq_len", i32, R),
-                                    _ptr(q_start, "q_start", i32, R + 1), scale, _opt(k_scale, "k_scale", f32, H),
-                                    _opt(v_scale, "v_scale", f32, H), window,
-                                    _ptr(out["out"], "out", q.dtype, T * Hq * D),
-                                    _opt(out.get("lse"), "lse", f32, T * Hq), ws.data_ptr(), ws.numel(),
-                                    _raw_stream(stream))
+    if out is None or ws is None:
+        T, Hq, D = _on_gpu(q, "q").shape
+        with _made_on(stream):
+            if out is None:
+                out = dict(out=torch.empty((T, Hq, D), dtype=q.dtype, device=q.device),
+                           lse=torch.empty((T, Hq), dtype=torch.float32, device=q.device))
+            if ws is None:
+                ws = workspace(paged_attention_workspace_size(T, page_table.shape[0], Hq, k_pool.shape[1], D, max_q),
+                               q.device)
+    st = _m.paged_attention(q, k_pool, v_pool, page_table, seq_len, q_start, max_q, scale, k_scale, v_scale, window,
+                            out["out"], out.get("lse"), ws, _raw_stream(stream))
     if st:
         _check(st, "dspark_paged_attention")
     return out

@@ -1,7 +1,9 @@
 """Build the CUDA library ``libdspark.so`` in-tree for sm_103a (GB300).
 
 Each translation unit is compiled in parallel with nvcc, then linked into one shared
-library with the shared CUDA runtime (the same ``libcudart.so.13`` PyTorch loads).
+library with the shared CUDA runtime (the same ``libcudart.so.13`` PyTorch loads).  Beside it
+stands ``_marshal.so``, the host-side marshalling of the serving calls, compiled with g++ against
+PyTorch's headers and linked to the library.
 """
 from __future__ import annotations
 
@@ -10,11 +12,13 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libdspark.so")
+MARSHAL = os.path.join(BUILD, "_marshal.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -36,6 +40,20 @@ def _headers():
                   glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
+def _marshal_commands(obj: str, target: str):
+    """Compiling and linking the marshalling module against the PyTorch that imports it."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cxx = os.environ.get("CXX") or "g++"
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+                "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                "-I", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "marshal.cpp"), "-o", obj]
+    link = [cxx, "-shared", "-o", target, obj, "-L", os.path.dirname(LIB), "-ldspark", "-Wl,-rpath,$ORIGIN",
+            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    return compile_, link
+
+
 def _stale(target, deps) -> bool:
     if not os.path.exists(target):
         return True
@@ -45,7 +63,8 @@ def _stale(target, deps) -> bool:
 
 def build(verbose: bool = False, force: bool = False, extra_flags=(), build_dir: str = BUILD) -> str:
     """Compile every csrc/*.cu and link libdspark.so in `build_dir` (the package's _build by
-    default; tests build variants with extra -D flags into their own directories)."""
+    default, where the marshalling module stands too; tests build variants with extra -D flags
+    into their own directories)."""
     os.makedirs(build_dir, exist_ok=True)
     lib = os.path.join(build_dir, "libdspark.so")
     nvcc = _nvcc()
@@ -59,10 +78,17 @@ def build(verbose: bool = False, force: bool = False, extra_flags=(), build_dir:
         if force or _stale(o, [s] + hdrs):
             jobs.append([nvcc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", s, "-o", o])
 
+    marshal = build_dir == BUILD
+    if marshal:
+        obj = os.path.join(build_dir, "marshal.o")
+        compile_, link = _marshal_commands(obj, MARSHAL + f".tmp{os.getpid()}")
+        if force or _stale(obj, [os.path.join(CSRC, "marshal.cpp")] + hdrs):
+            jobs.append(compile_)
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError("nvcc failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
+            raise RuntimeError("compilation failed:\n" + " ".join(cmd) + "\n" + r.stdout + r.stderr)
         if verbose and (r.stdout or r.stderr):
             print(r.stdout + r.stderr)
         return r
@@ -73,6 +99,9 @@ def build(verbose: bool = False, force: bool = False, extra_flags=(), build_dir:
         tmp = lib + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs])
         os.replace(tmp, lib)
+    if marshal and (force or _stale(MARSHAL, [obj, lib])):
+        run(link)
+        os.replace(MARSHAL + f".tmp{os.getpid()}", MARSHAL)
     return lib
 
 

@@ -314,6 +314,11 @@ def test_deterministic_on_any_stream_and_in_a_graph(b, new, cache):
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(out[k], first[k]) for k in first)
+    # buffers made by the call itself, on the stream that it runs on
+    for _ in range(3):
+        mine = b.paged_attention(*args, k_scale=ks, v_scale=vs, stream=side)
+        side.synchronize()
+        assert torch.equal(mine["out"], first["out"]) and torch.equal(mine["lse"], first["lse"])
     # without the normalisers
     only = b.paged_attention(*args, k_scale=ks, v_scale=vs, ws=ws, out=dict(out=torch.zeros_like(first["out"])))
     assert torch.equal(only["out"], first["out"])
