@@ -187,6 +187,24 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(CacheTables
   }
 }
 
+// The pools as a kernel takes them: room for few, or for all (4 KB of parameters, which cost the
+// host 1 us a launch more).
+template <int N>
+struct PoolList {
+  int n;
+  size_t page_bytes;
+  void* base[N];
+};
+constexpr int kFewPools = 24;
+template <int N>
+PoolList<N> pool_list(const PagePools& p) {
+  PoolList<N> l;
+  l.n = p.n;
+  l.page_bytes = p.page_bytes;
+  for (int i = 0; i < p.n; ++i) l.base[i] = p.base[i];
+  return l;
+}
+
 // One page of one pool, by a whole CTA.
 __device__ __forceinline__ void copy_page(char* pool, size_t page_bytes, int from, int to) {
   const uint4* src = reinterpret_cast<const uint4*>(pool + (size_t)from * page_bytes);
@@ -203,8 +221,9 @@ __device__ __forceinline__ void copy_page(char* pool, size_t page_bytes, int fro
   for (; i < n; i += kCopyThreads) store16(dst + i, load_once16(src + i));
 }
 
+template <int N>
 __global__ void __launch_bounds__(kCopyThreads) copy_on_write_kernel(const int32_t* copies, int R,
-                                                                     const __grid_constant__ PagePools pools) {
+                                                                     const __grid_constant__ PoolList<N> pools) {
   griddep_wait();
   const int items = R * pools.n;
   for (int i = blockIdx.x; i < items; i += gridDim.x) {
@@ -305,8 +324,9 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CacheTables 
   cluster.sync();  // no CTA leaves while another reads its totals
 }
 
+template <int N>
 __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(CacheTables t, CompactLists l,
-                                                                    const __grid_constant__ PagePools pools) {
+                                                                    const __grid_constant__ PoolList<N> pools) {
   griddep_wait();
   const int used = l.counts[0], moves = l.counts[1];
   if (moves == 0) return;
@@ -428,8 +448,11 @@ cudaError_t launch_cache_reserve(const CacheTables& t, const int32_t* n_new, int
                      words);
   if (e != cudaSuccess || pools.n == 0) return e;
   const int grid = (int)std::min<long long>((long long)t.R * pools.n, 8ll * sm_count());
-  return launch_chained(copy_on_write_kernel, dim3(grid), dim3(kCopyThreads), 0, s, 1,
-                        static_cast<const int32_t*>(copies), t.R, pools);
+  const int32_t* pairs = copies;
+  return pools.n <= kFewPools ? launch_chained(copy_on_write_kernel<kFewPools>, dim3(grid), dim3(kCopyThreads), 0, s, 1, pairs,
+                                               t.R, pool_list<kFewPools>(pools))
+                              : launch_chained(copy_on_write_kernel<kMaxPools>, dim3(grid), dim3(kCopyThreads), 0, s, 1, pairs,
+                                               t.R, pool_list<kMaxPools>(pools));
 }
 
 cudaError_t launch_cache_truncate(const CacheTables& t, const int32_t* new_len, cudaStream_t s) {
@@ -445,7 +468,11 @@ cudaError_t launch_cache_compact(const CacheTables& t, const CompactLists& l, in
   if (e != cudaSuccess) return e;
   e = launch_chained(compact_plan_kernel, dim3(ctas), dim3(kPlanThreads), smem, s, ctas, t, l, n_moves, words);
   if (e != cudaSuccess) return e;
-  return launch_chained(compact_move_kernel, dim3(8 * sm_count()), dim3(kCopyThreads), 0, s, 1, t, l, pools);
+  const dim3 grid(8 * sm_count());
+  return pools.n <= kFewPools ? launch_chained(compact_move_kernel<kFewPools>, grid, dim3(kCopyThreads), 0, s, 1, t, l,
+                                               pool_list<kFewPools>(pools))
+                              : launch_chained(compact_move_kernel<kMaxPools>, grid, dim3(kCopyThreads), 0, s, 1, t, l,
+                                               pool_list<kMaxPools>(pools));
 }
 
 cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t s) {

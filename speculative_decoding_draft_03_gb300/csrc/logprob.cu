@@ -279,43 +279,42 @@ __device__ void slice_best(const Row<T>& row, int seg0, int n, const uint32_t* s
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int turn = 0;
   if (threadIdx.x < kMaxTopK) sh.result[threadIdx.x] = {0u, 0x7FFFFFFF};
-  if (threadIdx.x == 0) sh.n_segs = sh.n_cand = 0;
-  // the thread's best segment; neighbouring segments (where likely ids gather) go to different
-  // warps
-  uint32_t top = 0;
-  const int turned = lane * kWarps + warp;
-  for (int i = turned; i < n; i += kThreads) top = max(top, seg_key[i]);
+  if (threadIdx.x == 0) sh.n_cand = 0, sh.n_segs = n <= kSegs ? n : 0;
 
   // 1. the segments worth another look
-  uint32_t floor_key = max(kth_floor(top, K, sh.floor_buf), kLowestKey);
-  int n_at = n;
-  if (n > kSegs) {
+  uint32_t floor_key = kLowestKey;
+  if (n <= kSegs) {
+    if (threadIdx.x < n) sh.segs[threadIdx.x] = threadIdx.x;
+  } else {
+    // the thread's best segment; neighbouring segments (where likely ids gather) go to different
+    // warps
+    uint32_t top = 0;
+    for (int i = lane * kWarps + warp; i < n; i += kThreads) top = max(top, seg_key[i]);
+    floor_key = max(kth_floor(top, K, sh.floor_buf), kLowestKey);
     auto at_least = [&](uint32_t k) {
       int c = 0;
       for (int i = threadIdx.x; i < n; i += kThreads) c += seg_key[i] >= k;
       return block_sum(c, sh.count, turn);
     };
-    n_at = at_least(floor_key);
+    int n_at = at_least(floor_key);
     if (n_at > kSegs) floor_key = bisect(floor_key, 0xFFFFFFFFu, K, kSegs, n_at, at_least);
-  } else {
-    __syncthreads();
-  }
-  if (n_at <= kSegs) {
-    for (int i = threadIdx.x; i < n; i += kThreads)
-      if (seg_key[i] >= floor_key) sh.segs[atomicAdd(&sh.n_segs, 1)] = i;
-  } else if (warp == 0) {
-    // more segments share the K-th largest maximum: those above it, then the first of them
-    int taken = 0;
-    for (int pass = 0; pass < 2; ++pass)
-      for (int i0 = 0; i0 < n && taken < K; i0 += 32) {
-        const int i = i0 + lane;
-        const bool take = i < n && (pass == 0 ? seg_key[i] > floor_key : seg_key[i] == floor_key);
-        const uint32_t m = __ballot_sync(~0u, take);
-        const int place = taken + __popc(m & ((1u << lane) - 1u));
-        if (take && place < K) sh.segs[place] = i;
-        taken = min(K, taken + __popc(m));
-      }
-    if (lane == 0) sh.n_segs = taken;
+    if (n_at <= kSegs) {
+      for (int i = threadIdx.x; i < n; i += kThreads)
+        if (seg_key[i] >= floor_key) sh.segs[atomicAdd(&sh.n_segs, 1)] = i;
+    } else if (warp == 0) {
+      // more segments share the K-th largest maximum: those above it, then the first of them
+      int taken = 0;
+      for (int pass = 0; pass < 2; ++pass)
+        for (int i0 = 0; i0 < n && taken < K; i0 += 32) {
+          const int i = i0 + lane;
+          const bool take = i < n && (pass == 0 ? seg_key[i] > floor_key : seg_key[i] == floor_key);
+          const uint32_t m = __ballot_sync(~0u, take);
+          const int place = taken + __popc(m & ((1u << lane) - 1u));
+          if (take && place < K) sh.segs[place] = i;
+          taken = min(K, taken + __popc(m));
+        }
+      if (lane == 0) sh.n_segs = taken;
+    }
   }
   __syncthreads();
 

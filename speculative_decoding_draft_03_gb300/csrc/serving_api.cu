@@ -107,7 +107,8 @@ dspark::CacheTables tables(int R, int num_pages, int page_size, int max_pages, i
 }
 
 dspark_status take_pools(dspark::PagePools& out, int n_pools, void* const* pools, size_t page_bytes) {
-  out = {};
+  out.n = 0;
+  out.page_bytes = 0;
   if (n_pools < 0) return fail(DSPARK_INVALID_ARG, "n_pools=%d is negative", n_pools);
   if (n_pools > dspark::kMaxPools)
     return fail(DSPARK_UNSUPPORTED_SHAPE, "n_pools=%d exceeds %d", n_pools, dspark::kMaxPools);
