@@ -26,9 +26,10 @@ constexpr int kCopyUnroll = 4;  // 16-byte pieces in flight per thread
 // where-codes of the status word
 enum { kBadLen = 40, kBadPage = 41, kBadCount = 42, kBadSlot = 43, kBadQueries = 44 };
 
-// One CTA walks a pool of up to this many pages; larger pools take a cluster of eight.  (One
-// CTA loads 1024 counts per round trip; the cluster pays two cluster barriers instead.)
-constexpr int kOneCtaPages = 4096;
+// One CTA walks a pool of up to this many pages; larger pools take a cluster of eight, whose
+// start and two cluster barriers cost more than a few round trips of loads (a round of 256 slots
+// over 6000 pages takes 39.5 us with one CTA, 40.8 with eight).
+constexpr int kOneCtaPages = 16384;
 int plan_ctas(int num_pages) { return num_pages <= kOneCtaPages ? 1 : 8; }
 int slice_words(int num_pages, int ctas) { return (((num_pages + 31) / 32) + ctas - 1) / ctas; }
 
@@ -115,7 +116,7 @@ __device__ Need slot_need(const CacheTables& t, const int32_t* n_new, int r, boo
 
 // Shared memory: end[R] (pages that slots 0..r take, held at kScanCap, which is more than any
 // pool has), flags[R], mask and before [words].
-constexpr int kCopies = 1, kTakesPages = 2;
+constexpr int kCopies = 1, kTakesPages = 2, kRefused = 4;
 __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(CacheTables t, const int32_t* n_new,
                                                                      int32_t* granted, int32_t* copies, int words) {
   extern __shared__ int smem[];
@@ -128,18 +129,25 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(CacheTables
   const int rank = cluster.block_rank(), ctas = cluster.num_blocks();
 
   griddep_wait();
+  griddep_allow_next();
+  // (the slots' loads, which depend on one another, overlap with those of the pool)
+  Need own = {};
+  if (threadIdx.x < t.R) own = slot_need(t, n_new, threadIdx.x, rank == 0);
   const int first_page = rank * words * 32;
   const int free_here = mask_slice(t.ref_count, t.num_pages, first_page, words, true, mask, before, warp_sums);
   int demand = 0;
   for (int base = 0; base < t.R; base += blockDim.x) {
     const int r = base + threadIdx.x;
-    Need k = {};
-    if (r < t.R) k = slot_need(t, n_new, r, rank == 0);
+    Need k = own;
+    if (base > 0) {
+      k = Need{};
+      if (r < t.R) k = slot_need(t, n_new, r, rank == 0);
+    }
     int total;
     const int upto = block_scan(k.pages, warp_sums, total);
     if (r < t.R) {
       end[r] = min(demand + upto, kScanCap);
-      flags[r] = (k.copy ? kCopies : 0) | (k.pages > 0 ? kTakesPages : 0);
+      flags[r] = (k.copy ? kCopies : 0) | (k.pages > 0 ? kTakesPages : 0) | (k.refused ? kRefused : 0);
     }
     demand = min(demand + total, kScanCap);
   }
@@ -169,18 +177,8 @@ __global__ void __launch_bounds__(kPlanThreads) cache_reserve_kernel(CacheTables
   }
   cluster.sync();  // lengths are read above and change below
   for (int r = rank * blockDim.x + threadIdx.x; r < t.R; r += ctas * blockDim.x) {
-    const int len = t.seq_len[r], n = n_new[r];
-    bool ok = n > 0 && len >= 0 && len <= t.max_pages * t.page_size;
-    if (ok && (flags[r] & kTakesPages)) {
-      ok = end[r] <= free_total;
-    } else if (ok) {  // it fits into its last page, or was refused
-      const int have = ceil_div_dev(len, t.page_size);
-      ok = (long long)len + n <= (long long)have * t.page_size;
-      if (ok) {
-        const int last = t.page_table[r * t.table_stride + have - 1];
-        ok = last >= 0 && last < t.num_pages;
-      }
-    }
+    const int len = r == threadIdx.x ? own.len : t.seq_len[r], n = r == threadIdx.x ? own.n : n_new[r];
+    const bool ok = n > 0 && !(flags[r] & kRefused) && (!(flags[r] & kTakesPages) || end[r] <= free_total);
     granted[r] = ok ? n : 0;
     if (ok) t.seq_len[r] = len + n;
     if (!(ok && (flags[r] & kCopies))) copies[2 * r] = copies[2 * r + 1] = -1;
@@ -357,14 +355,21 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(CacheTables 
 
 // ------------------------------------------------------------------------------- write
 
-// The request whose queries hold token t, with the number of its queries and the token's
-// place among them; -1 if the token belongs to none.
-__device__ __forceinline__ int request_of(const int32_t* q_start, int R, int t, int& i, int& n) {
-  const int r = upper_bound(q_start, R + 1, t) - 1;
-  if (r < 0 || r >= R) return -1;
-  i = t - q_start[r];
-  n = q_start[r + 1] - q_start[r];
-  return r;
+// The last r in [0, R] with q_start[r] <= t (-1: none), by a warp for one t: 32 places of the
+// remaining range are looked at per step, so R slots take log_32(R) loads one after the other.
+__device__ __forceinline__ int warp_request_of(const int32_t* q_start, int R, int t) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = R + 1;  // q_start[lo - 1] <= t < q_start[lo + n], where those exist
+  while (n > 0) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const uint32_t below = __ballot_sync(~0u, lane * step < n && q_start[at] <= t);
+    if (below == 0) break;
+    const int last = 31 - __clz(below);  // the places of a sorted array: below's bits are its lowest
+    const int end = lo + n;
+    lo += last * step + 1;
+    n = min(step - 1, end - lo);
+  }
+  return lo - 1;
 }
 
 template <typename T>
@@ -391,32 +396,42 @@ __device__ __forceinline__ uint2 quantise8(uint4 raw, float scale) {
   return make_uint2(w[0], w[1]);
 }
 
-// One thread per 8 elements of a row; both pools.
+// One thread per 8 elements of a row; both pools.  What bounds it at serving's sizes is the chain
+// of loads (the token's slot, its length, its page), so the rows are on their way meanwhile.
 template <typename T, bool QUANT>
 __global__ void __launch_bounds__(256) cache_write_kernel(CacheWriteArgs a) {
   griddep_wait();
+  griddep_allow_next();
   const int per_row = a.D / 8, per_token = a.Hkv * per_row;
-  const long long at = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (at >= (long long)a.T * per_token) return;
-  const int t = (int)(at / per_token), rest = (int)(at % per_token), h = rest / per_row, d = rest % per_row * 8;
-  int i, n;
-  const int r = request_of(a.q_start, a.R, t, i, n);
-  if (r < 0) return;
-  if (a.granted != nullptr && a.granted[r] == 0) return;
+  const long long total = (long long)a.T * per_token, at = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const bool mine = at < total;
+  const int t = (int)((mine ? at : total - 1) / per_token), rest = (int)(at - (long long)t * per_token);
+  const int h = rest / per_row, d = (rest - h * per_row) * 8;
+  uint4 k = make_uint4(0, 0, 0, 0), v = k;
+  if (mine) {
+    const int64_t from = t * a.in_stride_token + h * a.in_stride_head + d;
+    k = load_once16(static_cast<const T*>(a.k) + from);
+    v = load_once16(static_cast<const T*>(a.v) + from);
+  }
+  // the slot of the warp's first token; a later token's is there or further on
+  int r = warp_request_of(a.q_start, a.R, __shfl_sync(~0u, t, 0));
+  if (!mine) return;
+  while (r < a.R && a.q_start[r + 1] <= t) ++r;
+  if (r < 0 || r >= a.R || (a.granted != nullptr && a.granted[r] == 0)) return;
+  const int begin = a.q_start[r], n = a.q_start[r + 1] - begin, i = t - begin;
   const int len = a.seq_len[r];
   const long long pos = (long long)len - n + i;
-  if (i >= n || pos < 0 || pos >= (long long)a.max_pages * a.page_size) {
+  if (i < 0 || i >= n || pos < 0 || pos >= (long long)a.max_pages * a.page_size) {
     report_bad_input(a.status, kBadQueries);
     return;
   }
-  const int page = a.page_table[r * a.table_stride + pos / a.page_size];
+  const int nth = (int)pos / a.page_size;
+  const int page = a.page_table[r * a.table_stride + nth];
   if (page < 0 || page >= a.num_pages) {
     report_bad_input(a.status, kBadPage);
     return;
   }
-  const int64_t from = t * a.in_stride_token + h * a.in_stride_head + d;
-  const int64_t to = page * a.page_stride + h * a.head_stride + (pos % a.page_size) * a.token_stride + d;
-  const uint4 k = load_once16(static_cast<const T*>(a.k) + from), v = load_once16(static_cast<const T*>(a.v) + from);
+  const int64_t to = page * a.page_stride + h * a.head_stride + ((int)pos - nth * a.page_size) * a.token_stride + d;
   if (QUANT) {
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.k_pool) + to) = quantise8<T>(k, a.k_scale[h]);
     *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v_pool) + to) = quantise8<T>(v, a.v_scale[h]);

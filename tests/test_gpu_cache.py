@@ -245,6 +245,28 @@ def test_write(b, kind, H, D, ps, nhd):
             assert torch.equal(a.isnan(), c.isnan()) and torch.equal(a.nan_to_num(), c.nan_to_num())
 
 
+def test_write_of_few_among_many(b):
+    """Rows of no slot before the first and past the last, empty slots between, and many slots: a
+    warp's tokens lie in different slots."""
+    for R, lead, tail in ((1, 2, 1), (37, 1, 3), (1100, 5, 0), (4000, 3, 2)):
+        rng = np.random.default_rng(R)
+        new = (rng.random(R) < 0.4) * rng.integers(1, 4, R)
+        T = int(new.sum())
+        q_start = lead + np.concatenate([[0], np.cumsum(new)])
+        table = np.arange(R)[:, None]
+        k = torch.arange(1, lead + T + tail + 1, device="cuda").float().view(-1, 1, 1).expand(-1, 1, 16)
+        k = (k % 251).bfloat16().contiguous()
+        pool = [torch.zeros((R, 1, 4, 16), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        ws = b.workspace(256, "cuda")
+        b.cache_write(k, -k, pool[0], pool[1], _i32(table), _i32(new), _i32(q_start), ws=ws)
+        assert b.device_status(ws) == 0
+        want = torch.zeros((R, 1, 4, 16))
+        for r in range(R):
+            for i in range(new[r]):
+                want[r, 0, i] = float((q_start[r] + i + 1) % 251)
+        assert torch.equal(pool[0].float().cpu(), want) and torch.equal(pool[1].float().cpu(), -want)
+
+
 def test_write_reports_bad_places(b):
     pool = torch.zeros((4, 1, 4, 16), dtype=torch.bfloat16, device="cuda")
     x = torch.ones((3, 1, 16), dtype=torch.bfloat16, device="cuda")
