@@ -469,34 +469,65 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
       for (int t = 0; t < n; ++t, ++i) {
         ok = ok && mbar_wait(bar(s_full + (i & 1)), (i >> 1) & 1, abort_flag, a.status, 608);
         fence_after();
-        float x[C];
-#pragma unroll
-        for (int c = 0; c < C; c += 16) tmem_load(tmem + (i & 1) * N + lanes + c0 + c, x + c);
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(s_free + (i & 1)));
-
         const int p0 = use.k.first + (use.chunk + t) * kTile, pos = p0 + token;
         const bool edge = p0 + kTile > use.k.len - use.k.nq + 1 || (a.window > 0 && p0 < use.k.len - a.window);
-        if (edge) {
+        // 16 columns of this token's scores (products), those that a column does not see -inf.  A
+        // warp with 16 columns holds them; one with 32 reads them again at each use, its registers
+        // being full of sums (128 query rows: 211 us so, 282 us with 32 held; 64 query rows, whose
+        // warps have 16: 156 us so, 141 us held).
+        constexpr bool kHeld = C == 16;
+        float x[16];
+        auto release = [&]() {  // S may be written again
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(s_free + (i & 1)));
+        };
+        auto fetch = [&](int c) {
+          tmem_load(tmem + (i & 1) * N + lanes + c0 + c, x);
+          if (kHeld) release();
+          if (edge) {
 #pragma unroll
-          for (int c = 0; c < C; ++c) {
-            const int to = last[c0 + c];
-            if (pos > to || (a.window > 0 && pos <= to - a.window)) x[c] = -INFINITY;
+            for (int e = 0; e < 16; ++e) {
+              const int to = last[c0 + c + e];
+              if (pos > to || (a.window > 0 && pos <= to - a.window)) x[e] = -INFINITY;
+            }
           }
-        }
+        };
+        auto refetch = [&](int c) {
+          if (!kHeld) fetch(c);
+        };
         auto scale_of = [&](int c) {
           return Q8 ? *reinterpret_cast<const float4*>(up + c0 + c) : make_float4(c2, c2, c2, c2);
         };
-        // does a score pass its reference?  (A masked score stays -inf whatever the scale's sign.)
+        // scores to weights about the references (a masked score has weight 0 whatever the scale's sign)
+        auto weigh = [&](int c) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 r = *reinterpret_cast<const float4*>(reference + c0 + c + e), k = scale_of(c + e);
+            const float rr[4] = {r.x, r.y, r.z, r.w}, kk[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              x[e + j] = edge && x[e + j] == -INFINITY ? 0.f : ex2(fmaf(x[e + j], kk[j], -rr[j]));
+          }
+        };
+        auto add = [&](int c) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) l[c + e] += x[e];
+        };
+
+        // does a score pass its reference?
         float most = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < C; c += 4) {
-          const float4 r = *reinterpret_cast<const float4*>(reference + c0 + c), k = scale_of(c);
-          const float u0 = fmaf(x[c], k.x, -r.x), u1 = fmaf(x[c + 1], k.y, -r.y), u2 = fmaf(x[c + 2], k.z, -r.z),
-                      u3 = fmaf(x[c + 3], k.w, -r.w);
-          most = max3(most, edge && x[c] == -INFINITY ? -INFINITY : u0, edge && x[c + 1] == -INFINITY ? -INFINITY : u1);
-          most = max3(most, edge && x[c + 2] == -INFINITY ? -INFINITY : u2, edge && x[c + 3] == -INFINITY ? -INFINITY : u3);
+        for (int c = 0; c < C; c += 16) {
+          fetch(c);
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 r = *reinterpret_cast<const float4*>(reference + c0 + c + e), k = scale_of(c + e);
+            const float u0 = fmaf(x[e], k.x, -r.x), u1 = fmaf(x[e + 1], k.y, -r.y), u2 = fmaf(x[e + 2], k.z, -r.z),
+                        u3 = fmaf(x[e + 3], k.w, -r.w);
+            most = max3(most, edge && x[e] == -INFINITY ? -INFINITY : u0, edge && x[e + 1] == -INFINITY ? -INFINITY : u1);
+            most = max3(most, edge && x[e + 2] == -INFINITY ? -INFINITY : u2, edge && x[e + 3] == -INFINITY ? -INFINITY : u3);
+          }
         }
         bool waited = false;  // for the previous tile's product into O
         auto wait_o = [&]() {
@@ -509,11 +540,15 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
           softmax_sync<L::softmax>();
           // new references: the columns' maxima, over lanes, then over the four quarters
 #pragma unroll
-          for (int c = 0; c < C; ++c) {
-            float v = edge && x[c] == -INFINITY ? -INFINITY : x[c] * (Q8 ? up[c0 + c] : c2);
+          for (int c = 0; c < C; c += 16) {
+            refetch(c);
 #pragma unroll
-            for (int s = 16; s; s >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, s));
-            if (lane == 0) sums[quarter * N + c0 + c] = v;
+            for (int e = 0; e < 16; ++e) {
+              float v = edge && x[e] == -INFINITY ? -INFINITY : x[e] * (Q8 ? up[c0 + c + e] : c2);
+#pragma unroll
+              for (int s = 16; s; s >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, s));
+              if (lane == 0) sums[quarter * N + c0 + c + e] = v;
+            }
           }
           softmax_sync<L::softmax>();
           if (st < N) {
@@ -538,18 +573,13 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
           }
           tmem_store_wait();
         }
-#pragma unroll
-        for (int c = 0; c < C; c += 4) {
-          const float4 r = *reinterpret_cast<const float4*>(reference + c0 + c), k = scale_of(c);
-          const float rr[4] = {r.x, r.y, r.z, r.w}, kk[4] = {k.x, k.y, k.z, k.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[c + e] = edge && x[c + e] == -INFINITY ? 0.f : ex2(fmaf(x[c + e], kk[e], -rr[e]));
-            l[c + e] += x[c + e];
-          }
+        if (kHeld) {
+          weigh(0);
+          add(0);
+          wait_o();
         }
-        wait_o();
         if (edge) {
+          wait_o();
           // Tokens that no column sees hold anything (the rest of a page): their values are
           // cleared.  One that only some columns see must not reach the others if it is not
           // finite (0 x NaN): it is added on its own, and cleared for the product.
@@ -577,9 +607,16 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
           if (softmax_any<L::softmax>(strange)) {
             for (int k = 0; k < kTile; ++k) {
               if (!odd[k]) continue;
-              if (token == k) {
 #pragma unroll
-                for (int c = 0; c < C; ++c) factor[c0 + c] = x[c];
+              for (int c = 0; c < C; c += 16) {
+                if (!kHeld) {
+                  fetch(c);
+                  weigh(c);
+                }
+                if (token == k) {
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) factor[c0 + c + e] = x[e];
+                }
               }
               softmax_sync<L::softmax>();
               fence_after();
@@ -615,12 +652,22 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
         }
         // the weights: C 16-bit values of the token's row
 #pragma unroll
-        for (int c = 0; c < C; c += 8) {
-          const int piece = (c0 + c) / 8;
-          sts16(base + L::p + (piece >> 3) * (kTile * 128) + token * 128 + (((piece & 7) ^ (token & 7)) << 4),
-                make_uint4(H::pack(x[c], x[c + 1]), H::pack(x[c + 2], x[c + 3]), H::pack(x[c + 4], x[c + 5]),
-                           H::pack(x[c + 6], x[c + 7])));
+        for (int c = 0; c < C; c += 16) {
+          if (!kHeld) {
+            fetch(c);
+            weigh(c);
+            add(c);
+          }
+          wait_o();  // the previous weights have been used
+#pragma unroll
+          for (int e = 0; e < 16; e += 8) {
+            const int piece = (c0 + c + e) / 8;
+            sts16(base + L::p + (piece >> 3) * (kTile * 128) + token * 128 + (((piece & 7) ^ (token & 7)) << 4),
+                  make_uint4(H::pack(x[e], x[e + 1]), H::pack(x[e + 2], x[e + 3]), H::pack(x[e + 4], x[e + 5]),
+                             H::pack(x[e + 6], x[e + 7])));
+          }
         }
+        if (!kHeld) release();
         fence_smem();
         fence_before();
         __syncwarp();
