@@ -2,7 +2,8 @@
 // and their gradient.
 //
 // Forward.  One pass over a row, by a thread-block cluster whose CTAs take contiguous slices
-// and join through distributed shared memory (no scratch, no second launch).  A thread keeps
+// and leave what they found in the first one's shared memory (no scratch, no second launch);
+// the first one joins it, selects, and writes the outputs.  A thread keeps
 // base-2 softmax statistics about a running reference, r ~ max of x c (c = log2(e) / T):
 //   s = sum 2^u, w = sum 2^u u, u = x c - r;  lse = (r + log2 s) ln 2,
 //   entropy = (log2 s - w / s) ln 2,  ln p_v = (x_v c - r - log2 s) ln 2.
@@ -29,6 +30,7 @@ constexpr int kPer = 2;              // 16-byte pieces of a segment per lane: se
 constexpr int kSegPieces = 32 * kPer;
 constexpr int kSteps = 4;            // segments in flight per warp
 constexpr int kRing = kPer * kSteps * kThreads * 16;  // bytes
+constexpr int kLongSlice = 128;       // segments
 constexpr int kSegs = 32;            // segments that are read again, at most (>= kMaxTopK)
 constexpr int kCand = 256;           // candidates that are ranked by counting, at most
 
@@ -133,6 +135,16 @@ __device__ __forceinline__ float max_of(const float (&x)[N]) {
   for (int i = 1; i + 1 < N; i += 2) m = max3(m, x[i], x[i + 1]);
   return fmaxf(m, x[N - 1]);
 }
+// Order-preserving code of a number (-0 as +0); elements outside the row have code 0, below
+// -inf's.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
 // ------------------------------------------------------------------- statistics of a row
 
 // Softmax statistics about the reference r (in base 2).  r is held at kLowRef or above: a
@@ -145,11 +157,16 @@ __device__ __forceinline__ Stats2 join(Stats2 a, Stats2 b) {
   const float r = fmaxf(a.r, b.r), da = fmaxf(a.r - r, -200.f), db = fmaxf(b.r - r, -200.f), fa = ex2(da), fb = ex2(db);
   return {r, a.s * fa + b.s * fb, fmaf(da, a.s, a.w) * fa + fmaf(db, b.s, b.w) * fb};
 }
+// (the same in every lane)
 __device__ __forceinline__ Stats2 warp_join(Stats2 a) {
+  const float r = value_of(__reduce_max_sync(~0u, key_of(a.r))), d = fmaxf(a.r - r, -200.f), f = ex2(d);
+  float s = a.s * f, w = fmaf(d, a.s, a.w) * f;
 #pragma unroll
-  for (int d = 16; d; d >>= 1)
-    a = join(a, {__shfl_xor_sync(~0u, a.r, d), __shfl_xor_sync(~0u, a.s, d), __shfl_xor_sync(~0u, a.w, d)});
-  return a;
+  for (int i = 16; i; i >>= 1) {
+    s += __shfl_xor_sync(~0u, s, i);
+    w += __shfl_xor_sync(~0u, w, i);
+  }
+  return {r, s, w};
 }
 
 // Statistics about the largest logit m, the difference taken before the product: right for any
@@ -190,15 +207,23 @@ __device__ __noinline__ Softmax row_softmax(const T* row, int V, float c, Softma
 
 // ------------------------------------------------------------------------ the best K
 
-// Order-preserving code of a logit (-0 as +0); elements outside the row have code 0, below
-// -inf's.
-__device__ __forceinline__ uint32_t key_of(float x) {
-  const uint32_t b = __float_as_uint(x + 0.f);
-  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ float value_of(uint32_t key) {
-  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+
 constexpr uint32_t kLowestKey = 0x007FFFFFu;  // of -inf
 
 struct Best {
@@ -212,7 +237,8 @@ struct TopShared {
   Best result[kMaxTopK];
   int segs[kSegs];
   int count[2][kWarps];
-  int n_segs, n_cand, ties;
+  int2 near[kCand];
+  int n_segs, n_near, n_cand;
   Best warp_best[kWarps];
   alignas(16) uint32_t floor_buf[32];
 };
@@ -236,9 +262,10 @@ constexpr int kWarpBest = 32 / kWarps;
 __device__ __forceinline__ uint32_t kth_floor(uint32_t v, int K, uint32_t* buf) {
   static_assert(kWarpBest * kWarps == 32 && kMaxTopK <= 32, "one value per lane");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // half as many values again as K are enough to place it well
+  const int take = min(kWarpBest, (K + K / 2 + kWarps - 1) / kWarps);
   uint32_t mine = 0;
-#pragma unroll
-  for (int i = 0; i < kWarpBest; ++i) {
+  for (int i = 0; i < take; ++i) {
     const uint32_t m = __reduce_max_sync(~0u, v);
     if (lane == i) mine = m;
     const uint32_t at = __ballot_sync(~0u, v == m);
@@ -247,14 +274,13 @@ __device__ __forceinline__ uint32_t kth_floor(uint32_t v, int K, uint32_t* buf) 
   if (lane < kWarpBest) buf[kWarpBest * warp + lane] = mine;
   __syncthreads();
   const uint32_t x = buf[lane];
-  int place = 0;
+  int above = 0;  // values larger than this one
 #pragma unroll
   for (int j = 0; j < 32; j += 4) {
     const uint4 w = *reinterpret_cast<const uint4*>(buf + j);
-    place += (w.x > x || (w.x == x && j < lane)) + (w.y > x || (w.y == x && j + 1 < lane)) +
-             (w.z > x || (w.z == x && j + 2 < lane)) + (w.w > x || (w.w == x && j + 3 < lane));
+    above += (w.x > x) + (w.y > x) + (w.z > x) + (w.w > x);
   }
-  return __shfl_sync(~0u, x, __ffs(__ballot_sync(~0u, place == K - 1)) - 1);
+  return __reduce_min_sync(~0u, above < K ? x : ~0u);
 }
 
 // A key with between K and `most` of the counted keys at or above it, or (ties) the K-th
@@ -271,15 +297,17 @@ __device__ __forceinline__ uint32_t bisect(uint32_t lo, uint32_t hi, int K, int 
   return lo;
 }
 
-// The K best elements of the CTA's slice (segments [seg0, seg0 + n)), into sh.result, fewer if
-// the slice has fewer (the rest: key 0).  seg_key: the segments' largest keys.
+// The K <= V best elements of the row, into sh.result (a row with a NaN may leave fewer: the rest
+// have key 0).  seg_key: the n segments' largest keys; ring: kRing bytes.  Its loops stay rolled:
+// this code runs once per row, and its instructions come from far (with the elements in unrolled
+// registers it took 13000 cycles a row beside two streaming CTAs).
 template <typename T>
-__device__ void slice_best(const Row<T>& row, int seg0, int n, const uint32_t* seg_key, int K, TopShared& sh) {
+__device__ void row_best(const Row<T>& row, int n, const uint32_t* seg_key, int K, unsigned char* ring, TopShared& sh) {
   constexpr int VE = Piece<T>::n;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int turn = 0;
   if (threadIdx.x < kMaxTopK) sh.result[threadIdx.x] = {0u, 0x7FFFFFFF};
-  if (threadIdx.x == 0) sh.n_cand = 0, sh.n_segs = n <= kSegs ? n : 0;
+  if (threadIdx.x == 0) sh.n_near = sh.n_cand = 0, sh.n_segs = n <= kSegs ? n : 0;
 
   // 1. the segments worth another look
   uint32_t floor_key = kLowestKey;
@@ -291,101 +319,135 @@ __device__ void slice_best(const Row<T>& row, int seg0, int n, const uint32_t* s
     uint32_t top = 0;
     for (int i = lane * kWarps + warp; i < n; i += kThreads) top = max(top, seg_key[i]);
     floor_key = max(kth_floor(top, K, sh.floor_buf), kLowestKey);
-    auto at_least = [&](uint32_t k) {
-      int c = 0;
-      for (int i = threadIdx.x; i < n; i += kThreads) c += seg_key[i] >= k;
-      return block_sum(c, sh.count, turn);
-    };
-    int n_at = at_least(floor_key);
-    if (n_at > kSegs) floor_key = bisect(floor_key, 0xFFFFFFFFu, K, kSegs, n_at, at_least);
-    if (n_at <= kSegs) {
+    auto gather = [&]() {
       for (int i = threadIdx.x; i < n; i += kThreads)
-        if (seg_key[i] >= floor_key) sh.segs[atomicAdd(&sh.n_segs, 1)] = i;
-    } else if (warp == 0) {
-      // more segments share the K-th largest maximum: those above it, then the first of them
-      int taken = 0;
-      for (int pass = 0; pass < 2; ++pass)
-        for (int i0 = 0; i0 < n && taken < K; i0 += 32) {
-          const int i = i0 + lane;
-          const bool take = i < n && (pass == 0 ? seg_key[i] > floor_key : seg_key[i] == floor_key);
-          const uint32_t m = __ballot_sync(~0u, take);
-          const int place = taken + __popc(m & ((1u << lane) - 1u));
-          if (take && place < K) sh.segs[place] = i;
-          taken = min(K, taken + __popc(m));
+        if (seg_key[i] >= floor_key) {
+          const int k = atomicAdd(&sh.n_segs, 1);
+          if (k < kSegs) sh.segs[k] = i;
         }
-      if (lane == 0) sh.n_segs = taken;
+      __syncthreads();
+    };
+    gather();
+    int n_at = sh.n_segs;
+    if (n_at > kSegs) {
+      auto at_least = [&](uint32_t k) {
+        int c = 0;
+        for (int i = threadIdx.x; i < n; i += kThreads) c += seg_key[i] >= k;
+        return block_sum(c, sh.count, turn);
+      };
+      floor_key = bisect(floor_key, 0xFFFFFFFFu, K, kSegs, n_at, at_least);
+      __syncthreads();
+      if (threadIdx.x == 0) sh.n_segs = 0;
+      __syncthreads();
+      if (n_at <= kSegs) {
+        gather();
+      } else if (warp == 0) {
+        // more segments share the K-th largest maximum: those above it, then the first of them
+        int taken = 0;
+        for (int pass = 0; pass < 2; ++pass)
+          for (int i0 = 0; i0 < n && taken < K; i0 += 32) {
+            const int i = i0 + lane;
+            const bool take = i < n && (pass == 0 ? seg_key[i] > floor_key : seg_key[i] == floor_key);
+            const uint32_t m = __ballot_sync(~0u, take);
+            const int place = taken + __popc(m & ((1u << lane) - 1u));
+            if (take && place < K) sh.segs[place] = i;
+            taken = min(K, taken + __popc(m));
+          }
+        if (lane == 0) sh.n_segs = taken;
+      }
     }
   }
   __syncthreads();
 
-  // 2. their elements, in registers as they are stored
-  constexpr int kMine = kSegs / kWarps * kPer;  // pieces per thread
+  // 2. their elements, into the ring; a thread reads what it copied
+  static_assert(kSegs * kSegPieces * 16 <= kRing && kSegPieces == 64, "the ring holds them");
   const int segs = sh.n_segs;
-  uint4 raw[kMine];
-  int piece[kMine];  // -1: none
-#pragma unroll
-  for (int j = 0; j < kMine; ++j) {
-    const int k = j / kPer * kWarps + warp;
-    piece[j] = k < segs ? (seg0 + sh.segs[k]) * kSegPieces + j % kPer * 32 + lane : -1;
-    raw[j] = make_uint4(0, 0, 0, 0);
-    if (k < segs && row.whole(piece[j])) raw[j] = *reinterpret_cast<const uint4*>(row.at + row.first(piece[j]));
-  }
+  auto pieces = [&](auto f) {
+#pragma unroll 1
+    for (int k = warp; k < 2 * segs; k += kWarps)
+      f(sh.segs[k >> 1] * kSegPieces + (k & 1) * 32 + lane, (k * 32 + lane) * 16);
+  };
+  const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+  pieces([&](int piece, int at) {
+    if (row.whole(piece)) {
+      copy16(ring_at + at, row.at + row.first(piece));
+    } else {  // -inf outside the row
+      float x[VE];
+      row.load(piece, x);
+      sts16(ring_at + at, Piece<T>::pack(x));
+    }
+  });
+  copy_commit();
+  copy_wait<0>();
   // f(key, id) of every element of this thread
   auto each = [&](auto f) {
+    pieces([&](int piece, int at) {
+      float x[VE];
+      Piece<T>::unpack(lds16(ring_at + at), x);
 #pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-      if (piece[j] < 0 || piece[j] >= row.pieces) continue;
-      const int id0 = row.first(piece[j]);
-      if (row.whole(piece[j])) {
-        float x[VE];
-        Piece<T>::unpack(raw[j], x);
-#pragma unroll
-        for (int i = 0; i < VE; ++i) f(key_of(x[i]), id0 + i);
-      } else {
-        for (int i = 0; i < VE; ++i)
-          if (id0 + i >= 0 && id0 + i < row.V) f(key_of(Piece<T>::value(row.at[id0 + i])), id0 + i);
+      for (int i = 0; i < VE; ++i) {
+        const int id = row.first(piece) + i;
+        if (id >= 0 && id < row.V) f(key_of(x[i]), id);
       }
-    }
+    });
   };
 
-  // 3. a threshold that leaves few of them
-  auto at_least = [&](uint32_t k) {
-    int c = 0;
-    each([&](uint32_t key, int) { c += key >= k; });
-    return block_sum(c, sh.count, turn);
+  // 3. those at or above the threshold (the segments': an element below it is not among the best)
+  auto clear = [&]() {
+    if (threadIdx.x == 0) sh.n_near = sh.n_cand = 0;
   };
-  float most[kMine], best = -INFINITY;
-#pragma unroll
-  for (int j = 0; j < kMine; ++j) {
-    most[j] = -INFINITY;
-    if (piece[j] < 0 || piece[j] >= row.pieces) continue;
-    float x[VE];
-    if (row.whole(piece[j])) Piece<T>::unpack(raw[j], x);
-    else row.load(piece[j], x);
-    most[j] = max_of(x);
-    best = fmaxf(best, most[j]);
-  }
-  floor_key = max(floor_key, kth_floor(key_of(best), K, sh.floor_buf));
-  const float floor = value_of(floor_key);
-#pragma unroll
-  for (int j = 0; j < kMine; ++j) {
-    if (piece[j] < 0 || piece[j] >= row.pieces || !(most[j] >= floor)) continue;
-    const int id0 = row.first(piece[j]);
-    float x[VE];
-    if (row.whole(piece[j])) Piece<T>::unpack(raw[j], x);
-    else row.load(piece[j], x);
-#pragma unroll
-    for (int i = 0; i < VE; ++i)
-      if (x[i] >= floor && id0 + i >= 0 && id0 + i < row.V) {
-        const int k = atomicAdd(&sh.n_cand, 1);
-        if (k < kCand) sh.cand[k] = {key_of(x[i]), id0 + i};
+  auto collect = [&]() {  // their number; kCand + 1: more than are held
+    const float floor = value_of(floor_key);
+    pieces([&](int piece, int at) {
+      float x[VE];
+      Piece<T>::unpack(lds16(ring_at + at), x);
+      if (max_of(x) >= floor) {
+        const int k = atomicAdd(&sh.n_near, 1);
+        if (k < kCand) sh.near[k] = make_int2(at, row.first(piece));
       }
+    });
+    __syncthreads();
+    const int near = sh.n_near;  // pieces that hold some: now a thread per element
+    for (int t = threadIdx.x; t < min(near, kCand) * VE; t += kThreads) {
+      const int2 p = sh.near[t / VE];
+      const float x = Piece<T>::value(reinterpret_cast<const T*>(ring + p.x)[t % VE]);
+      const int id = p.y + t % VE;
+      if (x >= floor && id >= 0 && id < row.V) {
+        const int k = atomicAdd(&sh.n_cand, 1);
+        if (k < kCand) sh.cand[k] = {key_of(x), id};
+      }
+    }
+    __syncthreads();
+    return near <= kCand ? min(sh.n_cand, kCand + 1) : kCand + 1;
+  };
+  auto closer = [&]() {
+    float best = -INFINITY;
+    pieces([&](int, int at) {
+      float x[VE];
+      Piece<T>::unpack(lds16(ring_at + at), x);
+      best = fmaxf(best, max_of(x));
+    });
+    floor_key = max(floor_key, kth_floor(key_of(best), K, sh.floor_buf));
+  };
+  int n_el = kCand + 1;
+#pragma unroll 1
+  for (int i = n > kSegs ? 0 : 1; i < 2 && n_el > kCand; ++i) {
+    if (i == 1) {  // no threshold so far, or the best lie together
+      closer();
+      clear();
+      __syncthreads();
+    }
+    n_el = collect();
   }
-  __syncthreads();
-  int n_el = sh.n_cand;
   if (n_el > kCand) {  // too many: a higher threshold, if ties leave one
+    auto at_least = [&](uint32_t k) {
+      int c = 0;
+      each([&](uint32_t key, int) { c += key >= k; });
+      return block_sum(c, sh.count, turn);
+    };
     floor_key = bisect(floor_key, 0xFFFFFFFFu, K, kCand, n_el, at_least);
-    if (threadIdx.x == 0) sh.n_cand = 0;
+    __syncthreads();
+    clear();
     __syncthreads();
     if (n_el <= kCand)
       each([&](uint32_t key, int id) {
@@ -398,6 +460,7 @@ __device__ void slice_best(const Row<T>& row, int seg0, int n, const uint32_t* s
     for (int k = threadIdx.x; k < n_el; k += kThreads) {
       const Best mine = sh.cand[k];
       int place = 0;
+#pragma unroll 4
       for (int i = 0; i < n_el; ++i) place += before(sh.cand[i], mine);
       if (place < K) sh.result[place] = mine;
     }
@@ -431,19 +494,6 @@ __device__ void slice_best(const Row<T>& row, int seg0, int n, const uint32_t* s
 
 // --------------------------------------------------------------------------- forward
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
 // Packed pairs, each half rounded like its scalar operation.
 __device__ __forceinline__ void fma_pair(float& a, float& b, float x0, float x1, float y0, float y1, float z0, float z1) {
   asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
@@ -485,19 +535,19 @@ __device__ __forceinline__ void take(Running& st, const float (&x)[N], float mos
 
 // One cluster per row.  A thread copies the pieces that it will read into a ring of its own,
 // kSteps ahead (the ring holds what registers cannot: 32 KB per CTA in flight, no barriers).
-// Dynamic shared memory: the ring, and a key per segment of the slice (top_k > 0).
+// Dynamic shared memory: the ring, and a key per segment of the row (top_k > 0).
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, 3) logprob_kernel(LogprobArgs a, int slice) {
+__global__ void __launch_bounds__(kThreads, 4) logprob_kernel(LogprobArgs a, int slice) {
   constexpr int VE = Piece<T>::n;
   extern __shared__ __align__(16) unsigned char dynamic[];
   uint32_t* seg_key = reinterpret_cast<uint32_t*>(dynamic + kRing);
-  __shared__ Stats2 part[kWarps];
+  __shared__ Stats2 part[8 * kWarps];
   __shared__ Softmax slow_part[kWarps];
-  __shared__ Stats2 mine;
   __shared__ TopShared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int ctas = cluster.num_blocks(), rank = cluster.block_rank();
   const int n = blockIdx.x / ctas, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (ctas > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // running: may be written to
   griddep_wait();
   griddep_allow_next();
   const int tok = a.tokens[n];
@@ -534,6 +584,8 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_kernel(LogprobArgs a, int
   };
 #pragma unroll
   for (int i = 0; i < kSteps - 1; ++i) issue();
+  if (ctas > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  uint32_t* const to_key = cluster.map_shared_rank(seg_key, 0);
   Running run = {kLowRef, 0.f, 0.f, 0.f, 0.f};
   for (int g = seg0 + warp; g < seg1; g += kWarps) {
     issue();
@@ -563,40 +615,23 @@ __global__ void __launch_bounds__(kThreads, 3) logprob_kernel(LogprobArgs a, int
     get = get + kPer * kThreads * 16 == kRing ? 0 : get + kPer * kThreads * 16;
     if (TOP) {
       const uint32_t k = __reduce_max_sync(~0u, key_of(most));
-      if (lane == 0) seg_key[g - seg0] = k;
+      if (lane == 0) to_key[g] = k;
     }
   }
   Stats2 st = join({run.r, run.s0, run.w0}, {run.r, run.s1, run.w1});
   st = warp_join(st);
-  if (lane == 0) part[warp] = st;
-  __syncthreads();
-  st = part[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) st = join(st, part[w]);
-  if (TOP) slice_best(row, seg0, seg1 - seg0, seg_key, a.top_k, sh);
+  if (lane == 0) *cluster.map_shared_rank(part + rank * kWarps + warp, 0) = st;
   if (ctas > 1) {
-    if (threadIdx.x == 0) mine = st;
-    cluster.sync();
-    if (rank != 0) {
-      cluster.sync();  // its shared memory is read until then
-      return;
-    }
-    for (int r = 1; r < ctas; ++r) st = join(st, *cluster.map_shared_rank(&mine, r));
-    if (TOP) {
-      const int total = ctas * a.top_k;  // <= 8 * 32 = kCand
-      for (int k = threadIdx.x; k < total; k += kThreads)
-        sh.cand[k] = cluster.map_shared_rank(&sh, k / a.top_k)->result[k % a.top_k];
-      __syncthreads();
-      for (int k = threadIdx.x; k < total; k += kThreads) {
-        const Best me = sh.cand[k];
-        int place = 0;
-        for (int i = 0; i < total; ++i) place += before(sh.cand[i], me);
-        if (me.key != 0 && place < a.top_k) sh.result[place] = me;
-      }
-      __syncthreads();
-    }
-    cluster.sync();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (rank != 0) return;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else {
+    __syncthreads();
   }
+  st = {kLowRef, 0.f, 0.f};
+  for (int w = lane; w < ctas * kWarps; w += 32) st = join(st, part[w]);
+  st = warp_join(st);
+  if (TOP) row_best(row, segs, seg_key, a.top_k, dynamic, sh);
 
   // ln p of a logit: (x c - r - log2 s) ln 2, or from the careful statistics
   float l2 = log2f(st.s);
@@ -722,11 +757,13 @@ template <typename T>
 cudaError_t forward(const LogprobArgs& a, cudaStream_t s) {
   const int pieces = (a.V + 2 * Piece<T>::n - 2) / Piece<T>::n, segs = (pieces + kSegPieces - 1) / kSegPieces;  // at most, any shift
   // CTAs per row: enough rows keep every SM busy by themselves; few are split over a cluster
-  // while a slice keeps its threads in work
+  // while a slice keeps its threads in work, to two CTAs per SM where slices are long
   int ctas = 1;
-  while (ctas < 8 && (long long)a.N * ctas < 2ll * sm_count() && segs > ctas * 2 * kWarps) ctas *= 2;
+  while (ctas < 8 && segs > ctas * 2 * kWarps &&
+         (long long)a.N * ctas < (segs > ctas * kLongSlice ? 2ll : 1ll) * sm_count())
+    ctas *= 2;
   const int slice = (segs + ctas - 1) / ctas;
-  const size_t smem = kRing + (a.top_k > 0 ? sizeof(uint32_t) * slice : 0);
+  const size_t smem = kRing + (a.top_k > 0 ? sizeof(uint32_t) * segs : 0);
   auto* kernel = a.top_k > 0 ? logprob_kernel<T, true> : logprob_kernel<T, false>;
   static std::atomic<uint64_t> done[2];
   const cudaError_t e = allow_smem(kernel, kMaxSmem, done[a.top_k > 0]);

@@ -84,6 +84,36 @@ def test_many_rows_and_few(b):
         _check(b, x, np.arange(N) % 3001, 1.0, 4)
 
 
+@pytest.mark.parametrize("dtype,N,V,K", [(torch.bfloat16, 2500, 1500, 5), (torch.float32, 900, 20011, 20),
+                                         (torch.float16, 700, 40, 0), (torch.float32, 1300, 1, 1),
+                                         (torch.bfloat16, 333, 70001, 32)])
+def test_many_rows_in_turn(b, dtype, N, V, K):
+    x = _logits(N, V, dtype, N)
+    rng = np.random.default_rng(N)
+    tokens = rng.integers(0, V, N)
+    tokens[rng.random(N) < 0.3] = -1
+    tokens[N // 3: N // 3 + 50] = V  # skipped in a run
+    x[5, : V // 2] = -math.inf
+    x[N - 1, :] = -math.inf
+    _check(b, x, tokens, 0.9, K)
+    _check(b, x, np.where(np.arange(N) == N - 2, 0, -1), 0.9, K)  # one row is left
+    _check(b, x, np.full(N, -1), 0.9, K)
+
+
+@pytest.mark.parametrize("N", [3, 400])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_best_ids_gathered(b, dtype, N):
+    """Sorted rows, and the best in one place: more candidates pass the first threshold than fit."""
+    V = 12345
+    x = torch.linspace(-20, 20, V, dtype=torch.float64).expand(N, V).clone()
+    x[1] = x[1].flip(0)
+    x[2, 6000:6700] += 30
+    x = x.to(dtype)
+    tokens = np.arange(N) % V
+    _check(b, x, tokens, 1.0, 32)
+    _check(b, x, tokens, 1.0, 1)
+
+
 def test_skipped_rows_are_not_read(b):
     x = _logits(6, 777, torch.float32, 3)
     x[1] = math.nan
