@@ -487,7 +487,7 @@ DSPARK_API dspark_status dspark_token_logprobs_backward(
  * workspace's status word (dspark_workspace_status) and touch nothing.  Page choices depend
  * only on the tables (never on timing).  Workspace of all five calls:
  * dspark_cache_workspace_size().
- * Limits: R <= 8192, num_pages <= 4194304, max_pages * page_size < 2^31, n_pools <= 512.
+ * Limits: R <= 8192, num_pages <= 4194304, max_pages * page_size < 2^31 - 256, n_pools <= 512.
  * ---------------------------------------------------------------------------------- */
 DSPARK_API size_t dspark_cache_workspace_size(int R, int num_pages);
 
@@ -552,7 +552,8 @@ DSPARK_API dspark_status dspark_cache_compact(
  *   s_j = scale * (q . k_j) * k_scale[head],  w = softmax(s),
  *   out[t,h,:] = v_scale[head] * sum_j w_j v_j,  lse_out[t,h] = ln sum_j exp s_j.
  * A query that sees nothing gets out 0 and lse -inf.  What a query does not see has no
- * influence on it, NaN and infinities included.
+ * influence on it, NaN and infinities included.  A seen position whose page id is out of range
+ * is reported and read as zeros.
  *
  *   q        [T,Hq,D] with strides between tokens and heads; DSPARK_BF16 or DSPARK_F16.
  *   dtype_kv the type of q, or DSPARK_E4M3 with k_scale, v_scale [Hkv] (NULL otherwise).
@@ -563,7 +564,7 @@ DSPARK_API dspark_status dspark_cache_compact(
  * floats, with an e4m3 cache to fp16) for the product with v.  Deterministic.
  * Queries that belong to no request (before q_start[0], past q_start[R]) are not written.
  * Limits: D a multiple of 16, 16..256; Hq a multiple of Hkv, Hq / Hkv <= 64; R <= 8192;
- * max_pages * page_size < 2^31.
+ * max_pages * page_size < 2^31 - 256.
  * Workspace: dspark_paged_attention_workspace_size() (0 for unsupported sizes).
  * ---------------------------------------------------------------------------------- */
 DSPARK_API size_t dspark_paged_attention_workspace_size(int T, int R, int Hq, int Hkv, int D, int max_q);

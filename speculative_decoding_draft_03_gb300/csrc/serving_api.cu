@@ -85,8 +85,9 @@ dspark_status check_geometry(int R, int num_pages, int page_size, int max_pages,
   if (R > dspark::kMaxSlots) return fail(DSPARK_UNSUPPORTED_SHAPE, "R=%d exceeds %d", R, dspark::kMaxSlots);
   if (num_pages > dspark::kMaxPages)
     return fail(DSPARK_UNSUPPORTED_SHAPE, "num_pages=%d exceeds %d", num_pages, dspark::kMaxPages);
-  if ((int64_t)max_pages * page_size >= (int64_t)1 << 31)
-    return fail(DSPARK_UNSUPPORTED_SHAPE, "max_pages * page_size must be below 2^31");
+  // (a tile's positions go past the last page by less than 256 before they are tested)
+  if ((int64_t)max_pages * page_size >= ((int64_t)1 << 31) - 256)
+    return fail(DSPARK_UNSUPPORTED_SHAPE, "max_pages * page_size must be below 2^31 - 256");
   if (table_stride < max_pages)
     return fail(DSPARK_INVALID_ARG, "table_stride %lld is below max_pages=%d", (long long)table_stride, max_pages);
   return DSPARK_OK;
@@ -347,7 +348,9 @@ dspark_status dspark_paged_attention(int T, int R, int Hq, int Hkv, int D, int n
   a.q_stride_token = q_stride_token; a.q_stride_head = q_stride_head; a.k_pool = k_pool; a.v_pool = v_pool;
   a.page_stride = page_stride; a.head_stride = head_stride; a.token_stride = token_stride;
   a.page_table = page_table; a.table_stride = table_stride; a.seq_len = seq_len; a.q_start = q_start;
-  a.scale = scale; a.k_scale = k_scale; a.v_scale = v_scale; a.window = window; a.out = out; a.lse_out = lse_out;
+  a.scale = scale; a.k_scale = k_scale; a.v_scale = v_scale; a.out = out; a.lse_out = lse_out;
+  // a window as long as the table hides nothing; kept below it, position - window stays within 32 bits
+  a.window = window < (int64_t)max_pages * page_size ? window : 0;
   a.status = static_cast<dspark::DeviceStatus*>(workspace);
   return launched(dspark::launch_paged_attention(a, static_cast<unsigned char*>(workspace) + 256,
                                                  static_cast<cudaStream_t>(stream)),

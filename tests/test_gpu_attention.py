@@ -153,6 +153,12 @@ def test_window(b, window, dtype, cache):
     _check(b, _case([1, 50, 333, 700, 65], [1, 6, 4, 1, 3], 8, 2, 64, 16, dtype, cache, seed=window), window=window)
 
 
+@pytest.mark.parametrize("Hq,window", [(4, 2 ** 31 - 1), (4, 2 ** 31 - 9), (32, 2 ** 31 - 1)])
+def test_window_beyond_any_context(b, Hq, window):
+    """Windows near 32 bits with more queries than context (negative positions), narrow and wide blocks."""
+    _check(b, _case([2, 30, 0, 70], [8, 8, 3, 5], Hq, 2, 64, 16, torch.bfloat16, seed=9), window=window)
+
+
 @pytest.mark.parametrize("dtype,cache", TYPES)
 def test_long_context(b, dtype, cache):
     _check(b, _case([20011, 3, 9000], [1, 1, 2], 8, 2, 128, 16, dtype, cache, seed=1, garbage=False))

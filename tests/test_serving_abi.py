@@ -96,6 +96,16 @@ def test_cache_fork(b):
     assert call(F=0, null=[3, 4]) == OK
 
 
+def test_cache_length_limit(b):
+    """Positions, rounded up to a tile, stay within 32 bits."""
+    def call(max_pages, F=1):
+        return b.lib.dspark_cache_fork(F, *_tables(dict(max_pages=max_pages, page_size=64, stride=1 << 25)), P[3], P[4],
+                                       P[5], 1 << 30, None)
+
+    assert call(1 << 25) == UNSUPPORTED and call((1 << 25) - 4) == UNSUPPORTED
+    assert call((1 << 25) - 5, F=0) == OK
+
+
 def test_cache_reserve(b):
     pools = (ctypes.c_void_p * 2)(P[10], P[11])
 
