@@ -18,6 +18,10 @@
 //     reference is right; the weights stay below 2^kSlack, inside fp16's range): a vote per
 //     tile replaces the maximum over the tokens, and the output is rescaled in TMEM only then.
 //   * The work is dealt out in tiles of 128 tokens as for the other kernel, a CTA per worker.
+// What bounds it: to 32 columns the device memory (the verified block of 32 requests of 1 K to 8 K
+// tokens: 640 MB in 121 us, 5.3 TB/s; items' starts and ends cost the rest); from 64 on the chain
+// of a tile from its scores over the weights to its product (64 rows: 141 us, 128 rows: 211 us or
+// 219 TFLOP/s); with an e4m3 cache the shared memory, about 210 KB a tile (32 rows: 133 us).
 // Every mbarrier wait is bounded; a wait that gives up reports DSPARK_TIMEOUT and the CTA winds
 // down (the softmax warps leave together, by a vote).
 #include <cuda.h>

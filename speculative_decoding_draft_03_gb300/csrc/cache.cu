@@ -8,6 +8,9 @@
 // mask in shared memory with a running count per word, the CTAs exchange their totals
 // through distributed shared memory, and every needed page is then found by two binary
 // searches, independently of the others.  Moving page data is a plain streaming copy.
+// What bounds them: latency (a round of 256 slots with 64 forks over 6000 pages and 4 layers is
+// eight launches of 39.5 us together, whose bytes take 13 us), and for compaction the device memory
+// (537 MB moved in 78 us).
 #include <cooperative_groups.h>
 
 #include <algorithm>

@@ -17,6 +17,10 @@
 // Element order inside a product is free as long as both operands agree, and is chosen so that
 // a thread reads 16 contiguous bytes of a key row at a time and the query fragments are 16
 // contiguous bytes of a query row.
+// What bounds it: with a 16-bit cache the device memory (32 requests of 1 K to 8 K tokens, 8 heads
+// of 128 elements, one new token: 692 MB in 113 us, 6.1 TB/s, 4 us of it joining); with an e4m3
+// cache the warps' chains of conversions and products (two contexts of 115 K tokens: 517 MB in 99
+// us, of which the main kernel takes 87).
 #include <algorithm>
 
 #include "attention.cuh"
@@ -521,7 +525,9 @@ struct Shape {
 
 constexpr int kMaxWorkers = kMaxSms * 2 * 4;
 
-// Query rows of a cache head (at most, over the requests) above which the other kernel is faster.
+// Query rows of a cache head (at most, over the requests) above which the other kernel is faster:
+// 32 requests of 1 K to 8 K tokens, 16-bit cache: 16 rows 104 us here and 122 there, 20 rows 145 and
+// 118, 64 rows 230 and 141; e4m3 cache: 16 rows 99 and 127, 20 rows 164 and 130.
 constexpr int kWideRows = 16;
 
 int padded(int D, bool q8) { return D <= 64 && !q8 ? 64 : (D <= 128 ? 128 : 256); }  // (8-bit panels hold 128 elements)
