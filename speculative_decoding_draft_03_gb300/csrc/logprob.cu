@@ -365,12 +365,12 @@ __device__ void row_best(const Row<T>& row, int n, const uint32_t* seg_key, int 
   __syncthreads();
 
   // 2. their elements, into the ring; a thread reads what it copied
-  static_assert(kSegs * kSegPieces * 16 <= kRing && kSegPieces == 64, "the ring holds them");
+  static_assert(kSegs * kSegPieces * 16 <= kRing, "the ring holds them");
   const int segs = sh.n_segs;
   auto pieces = [&](auto f) {
 #pragma unroll 1
-    for (int k = warp; k < 2 * segs; k += kWarps)
-      f(sh.segs[k >> 1] * kSegPieces + (k & 1) * 32 + lane, (k * 32 + lane) * 16);
+    for (int k = warp; k < kPer * segs; k += kWarps)
+      f(sh.segs[k / kPer] * kSegPieces + k % kPer * 32 + lane, (k * 32 + lane) * 16);
   };
   const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
   pieces([&](int piece, int at) {
