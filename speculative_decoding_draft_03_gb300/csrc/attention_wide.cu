@@ -408,22 +408,41 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
     int* place = reinterpret_cast<int*>(smem + L::place);
     volatile unsigned char* odd = smem + L::odd;
     float* up = reinterpret_cast<float*>(smem + L::up);
+    // The query rows of an item, 16-byte pieces per thread; they are asked for while the item before
+    // is drained (short contexts change items every few tiles).
+    constexpr int kQ = N * (DP / 8) / L::softmax;
+    static_assert(kQ * L::softmax == N * (DP / 8), "whole pieces");
+    constexpr bool kAhead = kQ <= 4;  // (what registers hold)
+    const float per_g = 1.f / (float)G;
+    auto query_of = [&](int row) { return (int)(((float)row + 0.5f) * per_g); };  // row / G, exact below 2^20
+    uint4 ahead[kQ];
+    auto fetch_q = [&]() {
+      const int h = use.k.blocks == 1 ? use.item : use.item / use.k.blocks, row0 = (use.item - h * use.k.blocks) * N;
+#pragma unroll
+      for (int j = 0; j < kQ; ++j) {
+        const int e = st + j * L::softmax, c = e % (DP / 8), rr = row0 + e / (DP / 8), q = query_of(rr);
+        ahead[j] = make_uint4(0, 0, 0, 0);
+        if (rr < use.k.nq * G && c * 8 < a.D)
+          ahead[j] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                     (int64_t)(use.k.q0 + q) * a.q_stride_token +
+                                                     (int64_t)(h * G + rr - q * G) * a.q_stride_head + c * 8);
+      }
+    };
     float l[C];
     bool ok = true;
     int i = 0;
     long long item_begin = u_begin - use.chunk;
+    if (kAhead && tiles > 0) fetch_q();
     while (i < tiles) {
       const int n = min(use.k.chunks - use.chunk, tiles - i);
       const int h = use.k.blocks == 1 ? use.item : use.item / use.k.blocks, row0 = (use.item - h * use.k.blocks) * N;
       const float c2 = a.scale * kLog2e * (Q8 ? a.k_scale[h] : 1.f);  // scores in base 2 per product (e4m3: `up`)
       softmax_sync<L::softmax>();  // the previous item's tables are no longer read
-      for (int e = st; e < N * (DP / 8); e += L::softmax) {
-        const int row = e / (DP / 8), c = e % (DP / 8), rr = row0 + row, q = rr / G;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (rr < use.k.nq * G && c * 8 < a.D)
-          x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                              (int64_t)(use.k.q0 + q) * a.q_stride_token +
-                                              (int64_t)(h * G + rr - q * G) * a.q_stride_head + c * 8);
+      if (!kAhead) fetch_q();
+#pragma unroll
+      for (int j = 0; j < kQ; ++j) {
+        const int e = st + j * L::softmax, row = e / (DP / 8), c = e % (DP / 8);
+        uint4 x = ahead[j];
         if (Q8) {
           // fp16 operands; a bf16 row is scaled by a power of two to a maximum in [1, 2) (what falls
           // below 2^-24 of it is lost, far under the sums' rounding).  16 lanes hold a row.
@@ -433,23 +452,26 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
           if (BFQ) {
             float top = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              top = max3(top, fabsf(Half16<true>::lo(w[j])), fabsf(Half16<true>::hi(w[j])));
+            for (int k = 0; k < 4; ++k)
+              top = max3(top, fabsf(Half16<true>::lo(w[k])), fabsf(Half16<true>::hi(w[k])));
 #pragma unroll
             for (int s = 8; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, s));
             if (top > 0.f && top < INFINITY) e2 = min(max(ilogbf(top), -126), 126);
             const float down = ldexpf(1.f, -e2);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[j] = Half16<false>::pack(Half16<true>::lo(w[j]) * down, Half16<true>::hi(w[j]) * down);
+            for (int k = 0; k < 4; ++k)
+              w[k] = Half16<false>::pack(Half16<true>::lo(w[k]) * down, Half16<true>::hi(w[k]) * down);
           }
           if (c == 0) up[row] = c2 * ldexpf(1.f, e2);
           x = make_uint4(w[0], w[1], w[2], w[3]);
         }
         sts16(base + L::q + (c >> 3) * (N * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4), x);
       }
+      fence_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(q_ready));  // the first scores are computed meanwhile
       if (st < N) {
-        const int rr = row0 + st, q = rr / G;
+        const int rr = row0 + st, q = query_of(rr);
         const bool there = rr < use.k.nq * G;
         reference[st] = kUnset;
         last[st] = there ? use.k.len - use.k.nq + q : -1;
@@ -465,10 +487,8 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
       }
 #pragma unroll
       for (int c = 0; c < C; ++c) l[c] = 0.f;
-      fence_smem();
       fence_before();
       softmax_sync<L::softmax>();
-      if (lane == 0) mbar_arrive(bar(q_ready));
 
       for (int t = 0; t < n; ++t, ++i) {
         ok = ok && mbar_wait(bar(s_full + (i & 1)), (i >> 1) & 1, abort_flag, a.status, 608);
@@ -679,17 +699,32 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
       }
 
       // ---- the item, or this worker's part of it, ends
+      const long long item_end = item_begin + use.k.chunks;
+      const Share ended{use.r, use.item, use.k.q0, use.k.nq, item_begin, item_end};
+      use.chunk = use.k.chunks - 1;
+      if (i < tiles) {
+        advance<kTile, N>(a, use);
+        if (kAhead) fetch_q();
+      }
       ok = mbar_wait(bar(o_done), (i - 1) & 1, abort_flag, a.status, 611) && ok;
       fence_after();
       if (softmax_any<L::softmax>(!ok)) goto done;
+      // the columns' sums over the warp, 16 at a time: each step halves the columns a lane holds
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
+      for (int c = 0; c < C; c += 16) {
 #pragma unroll
-        for (int s = 16; s; s >>= 1) l[c] += __shfl_xor_sync(~0u, l[c], s);
-        if (lane == 0) sums[quarter * N + c0 + c] = l[c];
+        for (int w = 8; w; w >>= 1) {
+          const bool upper = lane & (2 * w);
+#pragma unroll
+          for (int e = 0; e < w; ++e) {
+            const float keep = upper ? l[c + e + w] : l[c + e], give = upper ? l[c + e] : l[c + e + w];
+            l[c + e] = keep + __shfl_xor_sync(~0u, give, 2 * w);
+          }
+        }
+        l[c] += __shfl_xor_sync(~0u, l[c], 1);
+        if ((lane & 1) == 0) sums[quarter * N + c0 + c + (lane >> 1)] = l[c];
       }
       softmax_sync<L::softmax>();
-      const long long item_end = item_begin + use.k.chunks;
       const bool whole = item_begin >= u_begin && item_end <= u_end;
       const int part = item_begin >= u_begin;  // part 0 began before the worker's range
       const size_t rows = (size_t)(worker * 2 + part) * N;
@@ -708,26 +743,28 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
       for (int c = 0; c < C; c += 16) {
         float o[16];
         tmem_load(o_cols + lanes + c0 + c, o);
-        if (token < DP) {
+        if (token >= DP) continue;
+        if (!whole) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int col = c0 + c + e;
-            if (whole) {
-              if (place[col] >= 0 && token < a.D)
-                static_cast<uint16_t*>(a.out)[(size_t)place[col] * a.D + token] =
-                    (uint16_t)Half16<BFQ>::pack(factor[col] == 0.f ? 0.f : o[e] * factor[col], 0.f);
-            } else {
-              scr.out[(rows + col) * DP + token] = o[e];
-            }
-          }
+          for (int e = 0; e < 16; ++e) scr.out[(rows + c0 + c + e) * DP + token] = o[e];
+          continue;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(factor + c0 + c + e);
+          const int4 p = *reinterpret_cast<const int4*>(place + c0 + c + e);
+          const float ff[4] = {f.x, f.y, f.z, f.w};
+          const int pp[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (pp[k] >= 0 && token < a.D)
+              static_cast<uint16_t*>(a.out)[(size_t)pp[k] * a.D + token] =
+                  (uint16_t)Half16<BFQ>::pack(ff[k] == 0.f ? 0.f : o[e + k] * ff[k], 0.f);
         }
       }
       fence_before();
-      if (!whole && part == 1 && st == 0)
-        scr.share[worker] = Share{use.r, use.item, use.k.q0, use.k.nq, item_begin, item_end};
+      if (!whole && part == 1 && st == 0) scr.share[worker] = ended;
       item_begin = item_end;
-      use.chunk = use.k.chunks - 1;
-      if (i < tiles) advance<kTile, N>(a, use);
     }
   done:;
   }
