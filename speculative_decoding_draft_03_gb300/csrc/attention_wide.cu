@@ -104,6 +104,11 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, ui
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(d), "r"(token), "r"(head), "r"(page)
       : "memory");
 }
+__device__ __forceinline__ float warp_max(float x) {
+  float m;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
+}
 // Shared-memory matrix descriptor, 128-byte swizzle: start, leading and stride byte offsets in
 // units of 16 bytes, version 1, swizzle mode 2.
 __device__ __forceinline__ uint64_t sw128(uint32_t at, uint32_t leading, uint32_t stride) {
@@ -566,13 +571,13 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
 #pragma unroll
           for (int c = 0; c < C; c += 16) {
             refetch(c);
+            float mine = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float v = edge && x[e] == -INFINITY ? -INFINITY : x[e] * (Q8 ? up[c0 + c + e] : c2);
-#pragma unroll
-              for (int s = 16; s; s >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, s));
-              if (lane == 0) sums[quarter * N + c0 + c + e] = v;
+              const float v = warp_max(edge && x[e] == -INFINITY ? -INFINITY : x[e] * (Q8 ? up[c0 + c + e] : c2));
+              if (lane == e) mine = v;
             }
+            if (lane < 16) sums[quarter * N + c0 + c + lane] = mine;
           }
           softmax_sync<L::softmax>();
           if (st < N) {
@@ -582,20 +587,22 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
             factor[st] = ex2(was - now);
           }
           softmax_sync<L::softmax>();
-          fence_after();
+          if (t > 0) {  // (an item's first tile finds its outputs and sums empty)
+            fence_after();
 #pragma unroll
-          for (int c = 0; c < C; c += 16) {
-            float o[16];
-            tmem_load(o_cols + lanes + c0 + c, o);
+            for (int c = 0; c < C; c += 16) {
+              float o[16];
+              tmem_load(o_cols + lanes + c0 + c, o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float f = factor[c0 + c + e];
-              o[e] *= f;
-              l[c + e] *= f;
+              for (int e = 0; e < 16; ++e) {
+                const float f = factor[c0 + c + e];
+                o[e] *= f;
+                l[c + e] *= f;
+              }
+              tmem_store(o_cols + lanes + c0 + c, o);
             }
-            tmem_store(o_cols + lanes + c0 + c, o);
+            tmem_store_wait();
           }
-          tmem_store_wait();
         }
         if (kHeld) {
           weigh(0);
