@@ -19,9 +19,10 @@
 //     tile replaces the maximum over the tokens, and the output is rescaled in TMEM only then.
 //   * The work is dealt out in tiles of 128 tokens as for the other kernel, a CTA per worker.
 // What bounds it: to 32 columns the device memory (the verified block of 32 requests of 1 K to 8 K
-// tokens: 640 MB in 121 us, 5.3 TB/s; items' starts and ends cost the rest); from 64 on the chain
-// of a tile from its scores over the weights to its product (64 rows: 141 us, 128 rows: 211 us or
-// 219 TFLOP/s); with an e4m3 cache the shared memory, about 210 KB a tile (32 rows: 133 us).
+// tokens: 640 MB in 113 us, 5.7 TB/s; items' starts and ends cost the rest); from 64 on the chain
+// of a tile from its scores over the weights to its product (64 rows: 130 us, 128 rows: 194 us or
+// 239 TFLOP/s), and the item's drain where contexts are short (200 requests of 50 to 600 tokens,
+// 64 rows: 148 us); with an e4m3 cache the shared memory, about 210 KB a tile (32 rows: 112 us).
 // Every mbarrier wait is bounded; a wait that gives up reports DSPARK_TIMEOUT and the CTA winds
 // down (the softmax warps leave together, by a vote).
 #include <cuda.h>
@@ -414,10 +415,11 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
     volatile unsigned char* odd = smem + L::odd;
     float* up = reinterpret_cast<float*>(smem + L::up);
     // The query rows of an item, 16-byte pieces per thread; they are asked for while the item before
-    // is drained (short contexts change items every few tiles).
+    // is drained (short contexts change items every few tiles), but with 128 columns, whose warps
+    // have no registers left (64 query rows: 130 us so, 134 us without; 128 rows: 204 and 194).
     constexpr int kQ = N * (DP / 8) / L::softmax;
     static_assert(kQ * L::softmax == N * (DP / 8), "whole pieces");
-    constexpr bool kAhead = kQ <= 4;  // (what registers hold)
+    constexpr bool kAhead = N <= 64;
     const float per_g = 1.f / (float)G;
     auto query_of = [&](int row) { return (int)(((float)row + 0.5f) * per_g); };  // row / G, exact below 2^20
     uint4 ahead[kQ];
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
         // 16 columns of this token's scores (products), those that a column does not see -inf.  A
         // warp with 16 columns holds them; one with 32 reads them again at each use, its registers
         // being full of sums (128 query rows: 211 us so, 282 us with 32 held; 64 query rows, whose
-        // warps have 16: 156 us so, 141 us held).
+        // warps have 16: 156 us so, 141 us held; both before the items overlapped).
         constexpr bool kHeld = C == 16;
         float x[16];
         auto release = [&]() {  // S may be written again

@@ -526,8 +526,8 @@ struct Shape {
 constexpr int kMaxWorkers = kMaxSms * 2 * 4;
 
 // Query rows of a cache head (at most, over the requests) above which the other kernel is faster:
-// 32 requests of 1 K to 8 K tokens, 16-bit cache: 16 rows 104 us here and 122 there, 20 rows 145 and
-// 118, 64 rows 230 and 141; e4m3 cache: 16 rows 99 and 127, 20 rows 164 and 130.
+// 32 requests of 1 K to 8 K tokens, 16-bit cache: 12 rows 110 us here and 110 there, 16 rows 104 and
+// 102, 20 rows 145 and 112; e4m3 cache: 12 rows 79 and 98, 16 rows 86 and 106, 20 rows 164 and 113.
 constexpr int kWideRows = 16;
 
 int padded(int D, bool q8) { return D <= 64 && !q8 ? 64 : (D <= 128 ? 128 : 256); }  // (8-bit panels hold 128 elements)
