@@ -819,6 +819,16 @@ def paged_attention_workspace_size(T, R, Hq, Hkv, D, max_q) -> int:
     return int(lib.dspark_paged_attention_workspace_size(T, R, Hq, Hkv, D, max_q))
 
 
+def _attention_workspace(nbytes, device):
+    """A workspace of which only the status block is cleared: the call writes the rest before it
+    reads it."""
+    ws = torch.empty(max(256, nbytes) + 256, dtype=torch.uint8, device=device)
+    off = (-ws.data_ptr()) % 256
+    ws = ws[off:off + max(256, nbytes)]
+    ws[:256].zero_()
+    return ws
+
+
 def paged_attention(q, k_pool, v_pool, page_table, seq_len, q_start, max_q, scale, k_scale=None, v_scale=None,
                     window=0, out=None, ws=None, stream=None):
     """Attention of every slot's last tokens over its paged context (dspark_paged_attention).
@@ -831,8 +841,8 @@ def paged_attention(q, k_pool, v_pool, page_table, seq_len, q_start, max_q, scal
                 out = dict(out=torch.empty((T, Hq, D), dtype=q.dtype, device=q.device),
                            lse=torch.empty((T, Hq), dtype=torch.float32, device=q.device))
             if ws is None:
-                ws = workspace(paged_attention_workspace_size(T, page_table.shape[0], Hq, k_pool.shape[1], D, max_q),
-                               q.device)
+                ws = _attention_workspace(
+                    paged_attention_workspace_size(T, page_table.shape[0], Hq, k_pool.shape[1], D, max_q), q.device)
     st = _m.paged_attention(q, k_pool, v_pool, page_table, seq_len, q_start, max_q, scale, k_scale, v_scale, window,
                             out["out"], out.get("lse"), ws, _raw_stream(stream))
     if st:
@@ -874,12 +884,16 @@ class PagedCache:
                     stream=stream)
 
     def attend(self, layer, q, q_start, max_q, scale, window=0, out=None, stream=None):
-        """Each (T, Hq, max_q) keeps a workspace of its own, made on its first call."""
+        """The scratch is made on the first call of a stream and a size class (heads and max_q decide
+        it, the number of rows does not) and kept: calls on one stream share it in order, calls on
+        two streams never do.  Calls captured on one stream share theirs, and clear its status word:
+        replays of graphs that do so must not overlap."""
         T, Hq, D = q.shape
-        key = (T, Hq, max_q)
-        if key not in self._attention_ws:
-            n = paged_attention_workspace_size(T, self.seq_len.numel(), Hq, self.k.shape[2], D, max_q)
-            self._attention_ws[key] = workspace(n, q.device)
+        n = paged_attention_workspace_size(T, self.seq_len.numel(), Hq, self.k.shape[2], D, max_q)
+        with _made_on(stream):
+            key = (_raw_stream(None), torch.cuda.is_current_stream_capturing(), n)
+            if key not in self._attention_ws:
+                self._attention_ws[key] = _attention_workspace(n, q.device)
         return paged_attention(q, self.k[layer], self.v[layer], self.page_table, self.seq_len, q_start, max_q, scale,
                                k_scale=self.k_scale, v_scale=self.v_scale, window=window, out=out,
                                ws=self._attention_ws[key], stream=stream)

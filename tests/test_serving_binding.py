@@ -1,0 +1,89 @@
+"""The binding's own host logic around the serving-side calls, on the CPU: the library's work is
+replaced by stand-ins that record what they were given."""
+import contextlib
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def b():
+    from speculative_decoding_draft_03_gb300 import build
+    build.build()
+    from speculative_decoding_draft_03_gb300 import binding
+    return binding
+
+
+class Streams:
+    """Stands for the CUDA streams: which one is current, and on which each buffer was made."""
+
+    def __init__(self, b, monkeypatch):
+        self.current, self.made, self.calls, self.capturing = 7, [], [], False
+        zeros, empty = torch.zeros, torch.empty
+
+        @contextlib.contextmanager
+        def switched(stream):
+            before, self.current = self.current, stream
+            yield
+            self.current = before
+
+        def noting(make):
+            def f(*a, **kw):
+                t = make(*a, **{**kw, "device": "cpu"})
+                self.made.append((self.current, t.numel()))
+                return t
+            return f
+
+        def attention(q, k, v, table, lens, q_start, max_q, scale, ws=None, stream=None, **kw):
+            self.calls.append((stream if stream is not None else self.current, ws))
+
+        monkeypatch.setattr(torch.cuda, "stream", switched)
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.capturing)
+        monkeypatch.setattr(torch, "zeros", noting(zeros))
+        monkeypatch.setattr(torch, "empty", noting(empty))
+        monkeypatch.setattr(b, "_raw_stream", lambda s: self.current if s is None else s)
+        monkeypatch.setattr(b, "paged_attention", attention)
+
+
+def _cache(b, slots=32):
+    c = object.__new__(b.PagedCache)
+    c.page_table, c.seq_len = torch.zeros((slots, 4), dtype=torch.int32), torch.zeros(slots, dtype=torch.int32)
+    c.k = c.v = torch.zeros((2, 8, 8, 16, 128), dtype=torch.bfloat16)
+    c.k_scale = c.v_scale = None
+    c._attention_ws = {}
+    return c
+
+
+def test_attend_keeps_one_scratch_for_any_number_of_rows(b, monkeypatch):
+    c, s = _cache(b), Streams(b, monkeypatch)
+    for T in (1, 17, 32, 100, 256):
+        c.attend(0, torch.zeros((T, 32, 128), dtype=torch.bfloat16).as_strided((T, 32, 128), (4096, 128, 1)), None, 8, 0.1)
+    assert len({ws.data_ptr() for _, ws in s.calls}) == 1 and len(c._attention_ws) == 1
+    # one more for each class of query rows, however many sizes there are
+    for max_q in range(1, 129):
+        c.attend(0, torch.ones((4, 32, 128), dtype=torch.bfloat16), None, max_q, 0.1)
+    assert len(c._attention_ws) <= 6
+
+
+def test_attend_makes_its_scratch_on_the_stream_it_runs_on(b, monkeypatch):
+    c, s = _cache(b), Streams(b, monkeypatch)
+    q = torch.ones((4, 32, 128), dtype=torch.bfloat16)
+    for stream in (None, 11, 12, 11, None):
+        s.made.clear()
+        c.attend(0, q, None, 4, 0.1, stream=stream)
+        assert all(on == (stream or 7) for on, _ in s.made)
+    by_stream = {}
+    for stream, ws in s.calls:
+        by_stream.setdefault(stream, set()).add(ws.data_ptr())
+    assert set(by_stream) == {7, 11, 12}
+    assert all(len(v) == 1 for v in by_stream.values()) and len(set.union(*by_stream.values())) == 3
+    # a capture does not take the scratch of the stream's eager calls
+    s.capturing = True
+    c.attend(0, q, None, 4, 0.1)
+    assert s.calls[-1][1].data_ptr() not in by_stream[7]
+
+
+def test_attend_clears_only_the_status_block(b):
+    ws = b._attention_workspace(5000, "cpu")
+    assert ws.numel() == 5000 and ws.data_ptr() % 256 == 0 and (ws[:256] == 0).all()
+    assert b._attention_workspace(0, "cpu").numel() == 256
