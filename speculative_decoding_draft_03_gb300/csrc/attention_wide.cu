@@ -807,7 +807,12 @@ bool encode_pool(CUtensorMap* map, const AttentionArgs& a, const void* pool, int
   auto fn = encoder();
   if (fn == nullptr) return false;
   const cuuint64_t size = a.dtype_kv == DSPARK_E4M3 ? 1 : 2;
-  // a dimension of one entry has no stride of its own: any that is allowed will do
+  // Entries that lie on one another (a pool expanded over its heads, say) are not something a map
+  // can say: the other kernel reads them.  A dimension of one entry has no stride of its own: any
+  // that is allowed will do.
+  if ((a.token_stride == 0 && a.page_size > 1) || (a.head_stride == 0 && a.Hkv > 1) ||
+      (a.page_stride == 0 && a.num_pages > 1))
+    return false;
   const cuuint64_t row = (cuuint64_t)a.D * size;
   const cuuint64_t strides[3] = {a.token_stride ? (cuuint64_t)a.token_stride * size : row,
                                  a.head_stride ? (cuuint64_t)a.head_stride * size : row,
