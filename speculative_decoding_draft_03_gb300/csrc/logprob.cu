@@ -700,17 +700,19 @@ __global__ void __launch_bounds__(kThreads) logprob_backward_kernel(LogprobArgs 
   const Row<T> out(a.grad_out, n * a.grad_stride, a.V);
   T* to = const_cast<T*>(out.at);
   const float lse = a.lse[n], H = a.entropy[n];
-  const bool none = tok < 0 || tok >= a.V || lse == -INFINITY;
+  bool none = tok < 0 || tok >= a.V;
   const float gl = a.grad_logprob[n], ge = a.grad_entropy ? a.grad_entropy[n] : 0.f;
   // ln p = (x - at) / T - log_sum.  A large lse (masks of the type's lowest value in the whole
   // row) has no digits left for the sum beside the maximum: the two are taken again, by one
-  // CTA that then writes the whole row (which may lie in the logits' place).
+  // CTA that then writes the whole row (which may lie in the logits' place).  So is an infinite
+  // one: the lowest value over T < 1 passes fp32's range, but only a row of -inf has nothing left.
   float at = 0.f, log_sum = lse;
   const bool apart = !none && fabsf(lse) > kLargeLse;
   if (apart) {
     if (blockIdx.x != 0) return;
     bool bad;
     const Softmax st = row_softmax(row.at, a.V, a.inv_temp * kLog2e, part, bad);
+    none = st.m == -INFINITY;
     at = st.m;
     log_sum = log2f(st.s) * kLn2;
   }
