@@ -48,3 +48,49 @@ def test_gradient_of_rows_at_the_ends_of_the_range(b, dtype, T):
         tol[tokens[n]] += 4 * E * abs(gl[n]) / T
         bad = np.abs(g[n] - want[n]) > tol
         assert not bad.any(), (n, g[n][bad][:3], want[n][bad][:3], tol[bad][:3])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("N", [3, 400])
+def test_likely_ids_after_unlikely_ones(b, dtype, N):
+    """The first tokens of a row are J nats less likely than the rest, which are equally likely: the
+    sums must be taken about the likely ones, however late they come.
+
+    With s = about V terms of 1, log2 s <= 15 is off by one step of it (2^-20), which is 11 e; the
+    difference with the mean, the constant ln 2 (10.4 e/2), and two roundings of values up to 10.4
+    (8 e each) make 32 e, and the log probability one more product's 10.4 e."""
+    V = 30000
+    for J in (3.0, 5.5, 8.0, 10.75):
+        x = torch.full((N, V), J - 2.0)
+        x[:, :4200] = -2.0
+        x = x.to(dtype)
+        tokens = np.full(N, V - 7)
+        t = torch.as_tensor(tokens, dtype=torch.int32).cuda()
+        o = b.token_logprobs(x.cuda(), t)
+        lp, H, _, _, _ = ref.token_logprobs(x[:1].double().numpy(), tokens[:1], 1.0, 0)
+        assert (o["entropy"].double().cpu() - H[0]).abs().max() <= 32 * E, J
+        assert (o["logprob"].double().cpu() - lp[0]).abs().max() <= 43 * E, J
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_entropy_of_confident_rows(b, dtype):
+    """It is never negative, and 0 where one id has all the weight."""
+    V = 5000
+    rng = np.random.default_rng(3)
+    x = torch.full((600, V), -math.inf)
+    x[:, 0] = torch.as_tensor(rng.uniform(-20, 20, 600))
+    at = rng.integers(1, V, 600)
+    x[np.arange(600), at] = x[:, 0] + torch.as_tensor(rng.uniform(0, 40, 600)).float()
+    x[:40, 0] = -math.inf
+    x = x.to(dtype)
+    o = b.token_logprobs(x.cuda(), _ids(at))
+    H = o["entropy"].cpu()
+    assert (H >= 0).all() and (H[:40] == 0).all()
+    lp, want, _, _, _ = ref.token_logprobs(x.double().numpy(), at, 1.0, 0)
+    # two terms: log2 s and w / s, at most 5 each, carry a handful of roundings of 2^-24 relative
+    assert np.abs(H.double().numpy() - want).max() <= 24 * E
+    assert np.abs(o["logprob"].cpu().double().numpy() - lp).max() <= 24 * E + 2 * E * np.abs(lp).max()
+
+
+def _ids(a):
+    return torch.as_tensor(a, dtype=torch.int32).cuda()
