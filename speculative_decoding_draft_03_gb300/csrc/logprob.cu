@@ -22,6 +22,8 @@
 // (96% of the copy rate).
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "serving.cuh"
 
 namespace dspark {
@@ -30,7 +32,10 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLargeLse = 1024.f;  // an lse beyond it is known to 2^-14 at best
+// A normaliser below this one is known well enough for the gradient: to 2^-19 for fp32, and to 2^-17
+// where the gradient is rounded to 16 bits (2^-12 at best).
+template <typename T>
+constexpr float kLargeLse = sizeof(T) == 4 ? 64.f : 256.f;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kPer = 2;              // 16-byte pieces of a segment per lane: segments of 1 KB
 constexpr int kSegPieces = 32 * kPer;
@@ -690,12 +695,11 @@ __device__ __forceinline__ void store_stream16(void* p, uint4 v) {
 
 constexpr int kBackPieces = 4;  // 16-byte pieces per thread
 
-// grid: (pieces of a row / (256 x kBackPieces), rows).  `together`: a row's logits and its
-// gradient lie alike on the 16-byte grid.
+// grid: (pieces of a row / (256 x kBackPieces), rows).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) logprob_backward_kernel(LogprobArgs a) {
   constexpr int VE = Piece<T>::n;
-  __shared__ Softmax part[kWarps];
+  __shared__ float2 part[kWarps];
   griddep_wait();
   griddep_allow_next();
   const int n = blockIdx.y, tok = a.tokens[n];
@@ -705,61 +709,87 @@ __global__ void __launch_bounds__(kThreads) logprob_backward_kernel(LogprobArgs 
   const float lse = a.lse[n], H = a.entropy[n];
   bool none = tok < 0 || tok >= a.V;
   const float gl = a.grad_logprob[n], ge = a.grad_entropy ? a.grad_entropy[n] : 0.f;
-  // ln p = (x - at) / T - log_sum.  A large lse (masks of the type's lowest value in the whole
-  // row) has no digits left for the sum beside the maximum: the two are taken again, by one
-  // CTA that then writes the whole row (which may lie in the logits' place).  So is an infinite
-  // one: the lowest value over T < 1 passes fp32's range, but only a row of -inf has nothing left.
+  // ln p = (x - at) / T - log_sum.  A large lse has too few digits left behind the point (masks of
+  // the type's lowest value in the whole row: none): maximum and sum are taken again, by one CTA
+  // that then writes the whole row (which may lie in the logits' place).  So they are for an
+  // infinite one: the lowest value over T < 1 passes fp32's range, but only a row of -inf has nothing
+  // left.  (1024 rows of 151936 bf16: 199 us if all are taken again, 16 rows 55 us: one CTA's
+  // chain of loads.)
   float at = 0.f, log_sum = lse;
-  const bool apart = !none && fabsf(lse) > kLargeLse;
+  const bool apart = !none && fabsf(lse) > kLargeLse<T>;
   if (apart) {
     if (blockIdx.x != 0) return;
-    bool bad;
-    const Softmax st = row_softmax(row.at, a.V, a.inv_temp * kLog2e, part, bad);
-    none = st.m == -INFINITY;
-    at = st.m;
-    log_sum = log2f(st.s) * kLn2;
+    const float c = a.inv_temp * kLog2e;
+    float m = -INFINITY, s = 0.f;
+    auto rebase = [&](float to) {  // (m = -inf: s is 0)
+      if (to > m) s *= ex2((m - to) * c), m = to;
+    };
+    for (int piece = threadIdx.x; piece < row.pieces; piece += kThreads) {
+      float x[VE];
+      row.load(piece, x);
+      rebase(max_of(x));
+      if (m > -INFINITY)
+#pragma unroll
+        for (int i = 0; i < VE; ++i) s += ex2((x[i] - m) * c);
+    }
+    float most = value_of(__reduce_max_sync(~0u, key_of(m)));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5].x = most;
+    __syncthreads();
+    for (int w = 0; w < kWarps; ++w) most = fmaxf(most, part[w].x);
+    rebase(most);
+#pragma unroll
+    for (int i = 16; i; i >>= 1) s += __shfl_xor_sync(~0u, s, i);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5].y = s;
+    __syncthreads();
+    s = 0.f;
+    for (int w = 0; w < kWarps; ++w) s += part[w].y;
+    none = most == -INFINITY;
+    at = most;
+    log_sum = log2f(s) * kLn2;
   }
   const float A = fmaf(ge, H, gl);
-  auto gradient = [&](float x, int v) {
+  auto gradient = [&](float x, int v, auto again) {
     // ln p held above -300, where p is 0 whatever the mask's value: 0 x -inf does not arise
-    const float lp = fmaxf(apart ? (x - at) * a.inv_temp - log_sum : fmaf(x, a.inv_temp, -log_sum), -300.f);
-    const float d = -ex2(lp * kLog2e) * fmaf(ge, lp, A) * a.inv_temp;
+    const float lp = fmaxf(again ? (x - at) * a.inv_temp - log_sum : fmaf(x, a.inv_temp, -log_sum), -300.f);
+    const float p = again ? exp2f(lp * kLog2e) : ex2(lp * kLog2e);  // (exp2f: small ones too, which low temperatures make)
+    const float d = -p * fmaf(ge, lp, A) * a.inv_temp;
     return none ? 0.f : (v == tok ? fmaf(gl, a.inv_temp, d) : d);
   };
-  if (apart) {
-    for (int v = threadIdx.x; v < a.V; v += kThreads)
-      to[v] = Piece<T>::rounded(gradient(Piece<T>::value(row.at[v]), v));
-    return;
-  }
-  const int piece0 = blockIdx.x * (kThreads * kBackPieces) + threadIdx.x;
-  if (row.shift == out.shift) {
+  auto write = [&](int block, auto again) {
+    if (row.shift == out.shift) {
+      const int piece0 = block * (kThreads * kBackPieces) + threadIdx.x;
 #pragma unroll
-    for (int u = 0; u < kBackPieces; ++u) {
-      const int piece = piece0 + u * kThreads;
-      if (piece >= row.pieces) return;
-      const int e = row.first(piece);
-      float x[VE];
-      if (none) {
+      for (int u = 0; u < kBackPieces; ++u) {
+        const int piece = piece0 + u * kThreads;
+        if (piece >= row.pieces) return;
+        const int e = row.first(piece);
+        float x[VE];
+        if (none) {
 #pragma unroll
-        for (int i = 0; i < VE; ++i) x[i] = 0.f;
-      } else {
-        row.load(piece, x);
+          for (int i = 0; i < VE; ++i) x[i] = 0.f;
+        } else {
+          row.load(piece, x);
+        }
+#pragma unroll
+        for (int i = 0; i < VE; ++i) x[i] = gradient(x[i], e + i, again);
+        if (row.whole(piece)) {
+          store_stream16(to + e, Piece<T>::pack(x));
+        } else {
+#pragma unroll
+          for (int i = 0; i < VE; ++i)
+            if (e + i >= 0 && e + i < a.V) to[e + i] = Piece<T>::rounded(x[i]);
+        }
       }
-#pragma unroll
-      for (int i = 0; i < VE; ++i) x[i] = gradient(x[i], e + i);
-      if (row.whole(piece)) {
-        store_stream16(to + e, Piece<T>::pack(x));
-      } else {
-#pragma unroll
-        for (int i = 0; i < VE; ++i)
-          if (e + i >= 0 && e + i < a.V) to[e + i] = Piece<T>::rounded(x[i]);
-      }
+    } else {
+      const int e0 = block * (kThreads * kBackPieces * VE) - row.shift;
+      for (int v = max(e0, 0) + threadIdx.x; v < min(e0 + kThreads * kBackPieces * VE, a.V); v += kThreads)
+        to[v] = Piece<T>::rounded(gradient(none ? 0.f : Piece<T>::value(row.at[v]), v, again));
     }
-    return;
-  }
-  const int e0 = blockIdx.x * (kThreads * kBackPieces * VE) - row.shift;
-  for (int v = max(e0, 0) + threadIdx.x; v < min(e0 + kThreads * kBackPieces * VE, a.V); v += kThreads)
-    to[v] = Piece<T>::rounded(gradient(none ? 0.f : Piece<T>::value(row.at[v]), v));
+  };
+  if (apart)
+    for (int block = 0; block < gridDim.x; ++block) write(block, std::true_type());
+  else
+    write(blockIdx.x, std::false_type());
 }
 
 constexpr size_t kMaxSmem = kRing + sizeof(uint32_t) * (kMaxLogprobV / 4 / kSegPieces + 2);

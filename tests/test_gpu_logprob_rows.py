@@ -94,3 +94,41 @@ def test_entropy_of_confident_rows(b, dtype):
 
 def _ids(a):
     return torch.as_tensor(a, dtype=torch.int32).cuda()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("shift,T", [(40.0, 1.0), (200.0, 1.0), (-900.0, 1.0), (0.0, 0.03125), (30.0, 0.0625)])
+@pytest.mark.parametrize("off", [0, 3])
+def test_gradient_of_rows_with_a_large_normaliser(b, dtype, shift, T, off):
+    """Logits far from zero, or divided by a small temperature (a power of two, which is exact).
+    Relatively, p is off by its sum's and exponent's roundings and, where it comes from a stored
+    normaliser, by at most half a step of one below 64 (32 e)."""
+    N, V = 12, 1003
+    x = (_logits(N, V, torch.float32, 31) + shift).to(dtype)
+    wide = torch.zeros((N, V + off), dtype=dtype, device="cuda")
+    dev = wide[:, off:]  # (with off, rows lie otherwise on the 16-byte grid than their gradient)
+    dev.copy_(x)
+    tokens = np.random.default_rng(5).integers(0, V, N)
+    gl, ge = (np.random.default_rng(k).standard_normal(N).astype(np.float32) for k in (6, 7))
+    t = _ids(tokens)
+    o = b.token_logprobs(dev, t, T)
+    g = torch.empty((N, V), dtype=dtype, device="cuda")
+    b.token_logprobs_backward(dev, t, o["lse"], o["entropy"], torch.from_numpy(gl).cuda(), torch.from_numpy(ge).cuda(), T, out=g)
+    x64, gl, ge = x.double().numpy(), gl.astype(np.float64), ge.astype(np.float64)
+    want = ref.token_logprobs_grad(x64, tokens, T, gl, ge)
+    _, H, lse, _, _ = ref.token_logprobs(x64, tokens, T, 0)
+    got = g.cpu().double().numpy()
+    for n in range(N):
+        lp = x64[n] / T - lse[n]
+        p = np.exp(lp)
+        parts = (abs(gl[n]) * p + abs(ge[n]) * p * (np.abs(lp) + H[n] + 1)) / T
+        tol = E * (V / 256 + 64 + 32 + 4 * np.abs(lp)) * parts + HALF_STEP[dtype] * np.abs(want[n])
+        tol = tol + 2.0 ** -25 * (dtype == torch.float16) + 1e-38
+        tol[tokens[n]] += 4 * E * abs(gl[n]) / T
+        bad = np.abs(got[n] - want[n]) > tol
+        assert not bad.any(), (n, np.argmax(bad), got[n][bad][:3], want[n][bad][:3], tol[bad][:3])
+    in_place = dev.clone() if off == 0 else dev
+    b.token_logprobs_backward(in_place, t, o["lse"], o["entropy"], torch.from_numpy(gl).float().cuda(),
+                              torch.from_numpy(ge).float().cuda(), T, out=in_place)
+    if off == 0:
+        assert torch.equal(in_place, g)
