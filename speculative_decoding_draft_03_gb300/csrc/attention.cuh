@@ -63,6 +63,7 @@ struct Half16<true> {
   static __device__ __forceinline__ float lo(uint32_t x) { return __uint_as_float(x << 16); }
   static __device__ __forceinline__ float hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
   static constexpr uint32_t kExp = 0x7F80u;  // exponent bits: all set for NaN and infinities
+  static constexpr float kLift = 0.f;
 };
 template <>
 struct Half16<false> {
@@ -82,6 +83,11 @@ struct Half16<false> {
     return __half2float(__ushort_as_half((unsigned short)(x >> 16)));
   }
   static constexpr uint32_t kExp = 0x7C00u;
+  // Weights are rounded as multiples of 2^-kLift of the largest: fp16 loses digits below 2^-14 and
+  // everything below 2^-25, which the normaliser would still count.  What a context of L tokens loses
+  // is then at most L 2^-32 of its sum.  (A larger lift would pass fp16's range where scores are so
+  // large that their difference with the reference rounds up.)
+  static constexpr float kLift = 7.f;
 };
 __device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t two) {
   uint32_t r;

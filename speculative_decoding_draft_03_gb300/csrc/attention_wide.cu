@@ -14,9 +14,10 @@
 //     double buffered; the copies run up to three tiles ahead of the products.
 //   * An e4m3 cache is copied as it is; four more warps turn each tile into fp16 (which holds every
 //     e4m3 value) for the products.  bf16 query rows are scaled by powers of two into fp16's range.
-//   * The softmax reference of a column moves only when a score passes it by 2^kSlack (any
-//     reference is right; the weights stay below 2^kSlack, inside fp16's range): a vote per
-//     tile replaces the maximum over the tokens, and the output is rescaled in TMEM only then.
+//   * The softmax reference of a column moves only when a score passes the one that set it by
+//     2^kSlack (any reference is right; the weights stay below 2^(kSlack + kLift), inside fp16's
+//     range): a vote per tile replaces the maximum over the tokens, and the output is rescaled in
+//     TMEM only then.
 //   * The work is dealt out in tiles of 128 tokens as for the other kernel, a CTA per worker.
 // What bounds it: to 32 columns the device memory (the verified block of 32 requests of 1 K to 8 K
 // tokens: 640 MB in 113 us, 5.7 TB/s; items' starts and ends cost the rest); from 64 on the chain
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
           if (!waited && i > 0) ok = mbar_wait(bar(o_done), (i - 1) & 1, abort_flag, a.status, 609) && ok;
           waited = true;
         };
-        if (softmax_any<L::softmax>(most > kSlack || !ok)) {
+        if (softmax_any<L::softmax>(most > kSlack + H::kLift || !ok)) {
           if (softmax_any<L::softmax>(!ok)) goto done;
           wait_o();
           softmax_sync<L::softmax>();
@@ -584,7 +585,8 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
           softmax_sync<L::softmax>();
           if (st < N) {
             const float was = reference[st];
-            const float now = fmaxf(was, fmaxf(fmaxf(sums[st], sums[N + st]), fmaxf(sums[2 * N + st], sums[3 * N + st])));
+            const float now = fmaxf(
+                was, fmaxf(fmaxf(sums[st], sums[N + st]), fmaxf(sums[2 * N + st], sums[3 * N + st])) - H::kLift);
             reference[st] = now;
             factor[st] = ex2(was - now);
           }

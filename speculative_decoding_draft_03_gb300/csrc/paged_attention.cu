@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) attention_kernel(const __gri
       }
     }
 
-    // mask and softmax about the running maximum
+    // mask and softmax about the running maximum less kLift
     const int p0 = use.k.first + use.chunk * TK;
     // a unit that not every query sees whole
     const bool edge = p0 + TK > use.k.len - use.k.nq + 1 || (a.window > 0 && p0 < use.k.len - a.window);
@@ -300,6 +300,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) attention_kernel(const __gri
       for (int z = 0; z < 2; ++z) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) top[nb][z] = fmaxf(top[nb][z], __shfl_xor_sync(~0u, top[nb][z], d));
+        top[nb][z] -= H::kLift;
         grows |= top[nb][z] > m[nb][z];
       }
     if (__any_sync(~0u, grows)) {
