@@ -6,7 +6,8 @@ The target is a small random transformer (embedding, layers of grouped-query att
 residual, unembedding): it stands for a real one, whose calls of the cache and of the attention
 would be the same.  Everything of a round runs on the device without a host read: lengths, page
 choices, verify lengths and accepted counts stay there, and the block of verified rows is ragged
-inside buffers of fixed size.
+inside buffers of fixed size.  A request that the pool has no room for emits nothing that round, and
+goes on once pages are given back.
 
     python examples/serving_loop.py --rounds 8
 """
@@ -101,7 +102,9 @@ class ServingLoop:
         dev = "cuda"
         n = [len(p) - 1 for p in prompts]
         q_start = torch.tensor([sum(n[:r]) for r in range(self.R + 1)], dtype=torch.int32, device=dev)
-        self.cache.reserve(torch.tensor(n, dtype=torch.int32, device=dev))
+        want = torch.tensor(n, dtype=torch.int32, device=dev)
+        if not torch.equal(self.cache.reserve(want)["granted"], want):
+            raise RuntimeError("the pool has no room for the prompts")
         tokens = torch.tensor([t for p in prompts for t in p[:-1]], dtype=torch.int32, device=dev)
         if tokens.numel():
             self.target.forward(tokens, self.cache, q_start, max(n))
@@ -109,7 +112,8 @@ class ServingLoop:
 
     def step(self):
         """One round.  Returns dict tokens [R,gamma+1] (-1 past n_out), n_out, n_acc, ell, and of the
-        emitted tokens logprob, entropy [R,gamma+1], top_ids, top_logprobs [R,gamma+1,top_k]."""
+        emitted tokens logprob, entropy [R,gamma+1], top_ids, top_logprobs [R,gamma+1,top_k].  n_out
+        is 0 for a request whose block found no room."""
         w, c, R, G1 = self.w, self.cache, self.R, self.gamma + 1
         d = b.markov_draft(w["U"], w["W1"], w["W2"], w["h"], w["conf_w"], w["conf_b"], w["conf_logit_scale"],
                            w["conf_temp"], w["temperature"], self.x0, w["req_id"], w["seed"], self.rounds)
@@ -122,22 +126,24 @@ class ServingLoop:
         i = (self.row_index - q_start[r]).clamp(max=self.gamma)
         block = torch.cat([self.x0[:, None], d["x"]], 1)
         before = c.seq_len.clone()
-        c.reserve(n_new)
+        room = c.reserve(n_new)["granted"] > 0
         logits = self.target.forward(block[r, i], c, q_start, G1)
         v = b.verify_ragged(logits, q_start[:-1].contiguous(), w["U"], w["W1"], w["W2"], self.x0, d["x"], d["logq"],
                             d["lse"], ell, w["temperature"], w["req_id"], w["seed"], self.rounds)
         c.truncate(before + 1 + v["n_acc"])  # the anchor and the accepted drafts stay
+        n_out, n_acc = v["n_out"] * room, v["n_acc"] * room
+        answer = torch.where(room[:, None], v["tokens"], -1)
         # row i of a request gave its token i: what was emitted keeps its row's log probability
-        mine = (self.row_index < q_start[-1]) & (i < v["n_out"][r])
-        emitted = torch.where(mine, v["tokens"][r, i], -1).to(torch.int32)
+        mine = (self.row_index < q_start[-1]) & (i < n_out[r])
+        emitted = torch.where(mine, answer[r, i], -1).to(torch.int32)
         lp = b.token_logprobs(logits, emitted, w["temperature"], self.top_k)
         row = (q_start[:-1, None] + torch.arange(G1, device="cuda")).clamp(max=self.T - 1).long()
-        there = torch.arange(G1, device="cuda") < v["n_out"][:, None]
+        there = torch.arange(G1, device="cuda") < n_out[:, None]
         pick = lambda t, none: torch.where(there.view(R, G1, *[1] * (t.dim() - 1)), t[row], none)
-        last = (v["n_out"] - 1).long()
-        self.x0 = v["tokens"].gather(1, last[:, None])[:, 0].contiguous()
+        last = (n_out - 1).clamp(min=0).long()
+        self.x0 = torch.where(room, answer.gather(1, last[:, None])[:, 0], self.x0)
         self.rounds += 1
-        return dict(tokens=v["tokens"], n_out=v["n_out"], n_acc=v["n_acc"], ell=ell,
+        return dict(tokens=answer, n_out=n_out, n_acc=n_acc, ell=ell,
                     logprob=pick(lp["logprob"], math.nan), entropy=pick(lp["entropy"], math.nan),
                     top_ids=pick(lp["top_ids"], -1), top_logprobs=pick(lp["top_logprobs"], math.nan))
 

@@ -576,6 +576,18 @@ DSPARK_API dspark_status dspark_paged_attention(
     int64_t table_stride, const int32_t* seq_len, const int32_t* q_start, float scale, const float* k_scale,
     const float* v_scale, int window, void* out, float* lse_out, void* workspace, size_t ws_bytes, void* stream);
 
+/* The same for a block that dspark_cache_reserve was asked to make room for: the queries of a slot
+ * whose entry of granted [R] (NULL: none such) is 0 see nothing (out 0, lse -inf), as
+ * dspark_cache_write stores nothing for it.  Without it such queries count as the slot's last
+ * positions, which they are not. */
+DSPARK_API dspark_status dspark_paged_attention_granted(
+    int T, int R, int Hq, int Hkv, int D, int num_pages, int page_size, int max_pages, int max_q, int dtype_q,
+    int dtype_kv, const void* q, int64_t q_stride_token, int64_t q_stride_head, const void* k_pool,
+    const void* v_pool, int64_t page_stride, int64_t head_stride, int64_t token_stride, const int32_t* page_table,
+    int64_t table_stride, const int32_t* seq_len, const int32_t* q_start, const int32_t* granted, float scale,
+    const float* k_scale, const float* v_scale, int window, void* out, float* lse_out, void* workspace,
+    size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

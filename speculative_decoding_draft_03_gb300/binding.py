@@ -103,6 +103,9 @@ def _load_library():
     lib.dspark_paged_attention.argtypes = ([i32] * 11 + [P, i64, i64, P, P, i64, i64, i64, P, i64, P, P, f32, P, P,
                                            i32, P, P, P, sz, P])
     lib.dspark_paged_attention.restype = i32
+    lib.dspark_paged_attention_granted.argtypes = ([i32] * 11 + [P, i64, i64, P, P, i64, i64, i64, P, i64, P, P, P, f32,
+                                                                 P, P, i32, P, P, P, sz, P])
+    lib.dspark_paged_attention_granted.restype = i32
     for fn in ("dspark_markov_draft", "dspark_schedule", "dspark_verify", "dspark_workspace_status"):
         getattr(lib, fn).restype = i32
     return lib
@@ -830,10 +833,11 @@ def _attention_workspace(nbytes, device):
 
 
 def paged_attention(q, k_pool, v_pool, page_table, seq_len, q_start, max_q, scale, k_scale=None, v_scale=None,
-                    window=0, out=None, ws=None, stream=None):
+                    window=0, out=None, ws=None, stream=None, granted=None):
     """Attention of every slot's last tokens over its paged context (dspark_paged_attention).
     q [T,Hq,D] bfloat16 or float16, rows q_start[r] .. q_start[r+1]-1 for slot r, at most
-    ``max_q`` a slot.  Returns dict out [T,Hq,D], lse [T,Hq] float32."""
+    ``max_q`` a slot.  The queries of a slot whose entry of ``granted`` [R] int32 is 0 (cache_reserve
+    found no room for them) see nothing.  Returns dict out [T,Hq,D], lse [T,Hq] float32."""
     if out is None or ws is None:
         T, Hq, D = _on_gpu(q, "q").shape
         with _made_on(stream):
@@ -844,7 +848,7 @@ def paged_attention(q, k_pool, v_pool, page_table, seq_len, q_start, max_q, scal
                 ws = _attention_workspace(
                     paged_attention_workspace_size(T, page_table.shape[0], Hq, k_pool.shape[1], D, max_q), q.device)
     st = _m.paged_attention(q, k_pool, v_pool, page_table, seq_len, q_start, max_q, scale, k_scale, v_scale, window,
-                            out["out"], out.get("lse"), ws, _raw_stream(stream))
+                            out["out"], out.get("lse"), ws, _raw_stream(stream), granted)
     if st:
         _check(st, "dspark_paged_attention")
     return out
@@ -853,7 +857,9 @@ def paged_attention(q, k_pool, v_pool, page_table, seq_len, q_start, max_q, scal
 class PagedCache:
     """A paged key-value cache: the tables of ``slots`` requests over ``num_pages`` pages, and
     the pools [layers, num_pages, Hkv, page_size, D] of keys and values.  Methods launch kernels
-    only (buffers are made once), so a serving step over it can be captured as a CUDA graph."""
+    only (buffers are made once), so a serving step over it can be captured as a CUDA graph.  A slot
+    that ``reserve`` had no room for has granted 0: nothing is written for it, and its queries see
+    nothing, until the next ``reserve``."""
 
     def __init__(self, slots, num_pages, page_size, max_pages, layers, Hkv, D, dtype=torch.bfloat16, device="cuda",
                  k_scale=None, v_scale=None):
@@ -867,6 +873,7 @@ class PagedCache:
         self.k_scale, self.v_scale = k_scale, v_scale
         self.pools = cache_pools([*self.k.unbind(0), *self.v.unbind(0)])
         self.plan = dict(granted=torch.empty(slots, **i32), copies=torch.empty((slots, 2), **i32))
+        self.not_refused = torch.ones(slots, **i32)  # by the last reserve
         self.moves = torch.empty(1, **i32)
         self.ws = workspace(cache_workspace_size(slots, num_pages), device)
         self._attention_ws = {}
@@ -875,8 +882,11 @@ class PagedCache:
         cache_fork(self.page_table, self.seq_len, self.ref_count, src, dst, self.page_size, ws=self.ws, stream=stream)
 
     def reserve(self, n_new, stream=None):
-        return cache_reserve(self.page_table, self.seq_len, self.ref_count, n_new, self.page_size, self.pools,
+        plan = cache_reserve(self.page_table, self.seq_len, self.ref_count, n_new, self.page_size, self.pools,
                              out=self.plan, ws=self.ws, stream=stream)
+        with _made_on(stream):
+            torch.le(n_new, plan["granted"], out=self.not_refused)
+        return plan
 
     def write(self, layer, k, v, q_start, stream=None):
         cache_write(k, v, self.k[layer], self.v[layer], self.page_table, self.seq_len, q_start,
@@ -896,7 +906,7 @@ class PagedCache:
                 self._attention_ws[key] = _attention_workspace(n, q.device)
         return paged_attention(q, self.k[layer], self.v[layer], self.page_table, self.seq_len, q_start, max_q, scale,
                                k_scale=self.k_scale, v_scale=self.v_scale, window=window, out=out,
-                               ws=self._attention_ws[key], stream=stream)
+                               ws=self._attention_ws[key], stream=stream, granted=self.not_refused)
 
     def truncate(self, new_len, stream=None):
         cache_truncate(self.page_table, self.seq_len, self.ref_count, new_len, self.page_size, ws=self.ws,

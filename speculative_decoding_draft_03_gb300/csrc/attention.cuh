@@ -118,6 +118,7 @@ __device__ __forceinline__ Request request(const AttentionArgs& a, int r, bool r
     return k;
   }
   if (k.nq == 0) return k;
+  if (a.granted != nullptr && a.granted[r] == 0) k.len = 0;  // its queries see nothing
   if (a.window > 0) k.first = max(0, k.len - k.nq - a.window + 1) / TK * TK;
   k.chunks = max(1, (k.len - k.first + TK - 1) / TK);
   k.blocks = (k.nq * a.G + ROWS - 1) / ROWS;

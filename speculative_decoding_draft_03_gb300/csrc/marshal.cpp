@@ -253,19 +253,20 @@ int cache_compact(PyObject* const* a) {
                               address(a[9]));
 }
 
-// (q, k_pool, v_pool, page_table, seq_len, q_start, max_q, scale, k_scale, v_scale, window, out, lse, ws, stream)
+// (q, k_pool, v_pool, page_table, seq_len, q_start, max_q, scale, k_scale, v_scale, window, out, lse, ws, stream,
+//  granted)
 int paged_attention(PyObject* const* a) {
   const Pools p = pools(a[1], a[2]);
   const int64_t H = p.size[1], D = p.size[3];
   const TokenRows q = token_rows(a[0], "q", -1, D);
   const Rows t = page_table(a[3]);
   const Workspace w = workspace(a[13]);
-  return dspark_paged_attention(
+  return dspark_paged_attention_granted(
       to_int(q.T, "q"), t.n, to_int(q.heads, "Hq"), to_int(H, "Hkv"), to_int(D, "D"), to_int(p.size[0], "num_pages"),
       to_int(p.size[2], "page_size"), t.m, integer(a[6], "max_q"), cache_type(q.type), p.type, q.p, q.token, q.head, p.k, p.v,
       p.stride[0], p.stride[1], p.stride[2], static_cast<int32_t*>(t.p), t.stride,
       flat<int32_t>(a[4], "seq_len", at::kInt, t.n), flat<int32_t>(a[5], "q_start", at::kInt, (int64_t)t.n + 1),
-      (float)number(a[7]), flat_or_null<float>(a[8], "k_scale", at::kFloat, H),
+      flat_or_null<int32_t>(a[15], "granted", at::kInt, t.n), (float)number(a[7]), flat_or_null<float>(a[8], "k_scale", at::kFloat, H),
       flat_or_null<float>(a[9], "v_scale", at::kFloat, H), integer(a[10], "window"),
       flat(a[11], "out", q.type, q.T * q.heads * D), flat_or_null<float>(a[12], "lse", at::kFloat, q.T * q.heads), w.p, w.bytes,
       address(a[14]));
@@ -308,7 +309,7 @@ PyMethodDef g_methods[] = {
     method<cache_write, 12>("cache_write"),
     method<cache_truncate, 7>("cache_truncate"),
     method<cache_compact, 10>("cache_compact"),
-    method<paged_attention, 15>("paged_attention"),
+    method<paged_attention, 16>("paged_attention"),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -102,6 +102,7 @@ struct AttentionArgs {
   int64_t table_stride;
   const int32_t* seq_len;
   const int32_t* q_start;
+  const int32_t* granted;  // may be null
   float scale;
   const float* k_scale;
   const float* v_scale;

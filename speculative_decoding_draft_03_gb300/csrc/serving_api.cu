@@ -322,6 +322,21 @@ dspark_status dspark_paged_attention(int T, int R, int Hq, int Hkv, int D, int n
                                      const int32_t* seq_len, const int32_t* q_start, float scale,
                                      const float* k_scale, const float* v_scale, int window, void* out,
                                      float* lse_out, void* workspace, size_t ws_bytes, void* stream) {
+  return dspark_paged_attention_granted(T, R, Hq, Hkv, D, num_pages, page_size, max_pages, max_q, dtype_q, dtype_kv, q,
+                                        q_stride_token, q_stride_head, k_pool, v_pool, page_stride, head_stride,
+                                        token_stride, page_table, table_stride, seq_len, q_start, nullptr, scale,
+                                        k_scale, v_scale, window, out, lse_out, workspace, ws_bytes, stream);
+}
+
+dspark_status dspark_paged_attention_granted(int T, int R, int Hq, int Hkv, int D, int num_pages, int page_size,
+                                             int max_pages, int max_q, int dtype_q, int dtype_kv, const void* q,
+                                             int64_t q_stride_token, int64_t q_stride_head, const void* k_pool,
+                                             const void* v_pool, int64_t page_stride, int64_t head_stride,
+                                             int64_t token_stride, const int32_t* page_table, int64_t table_stride,
+                                             const int32_t* seq_len, const int32_t* q_start, const int32_t* granted,
+                                             float scale, const float* k_scale, const float* v_scale, int window,
+                                             void* out, float* lse_out, void* workspace, size_t ws_bytes,
+                                             void* stream) {
   CHECK(check_geometry(R, num_pages, page_size, max_pages, table_stride));
   if (T < 0 || Hq < 1 || Hkv < 1 || window < 0)
     return fail(DSPARK_INVALID_ARG, "sizes must be positive (T=%d Hq=%d Hkv=%d window=%d)", T, Hq, Hkv, window);
@@ -348,7 +363,7 @@ dspark_status dspark_paged_attention(int T, int R, int Hq, int Hkv, int D, int n
   a.q_stride_token = q_stride_token; a.q_stride_head = q_stride_head; a.k_pool = k_pool; a.v_pool = v_pool;
   a.page_stride = page_stride; a.head_stride = head_stride; a.token_stride = token_stride;
   a.page_table = page_table; a.table_stride = table_stride; a.seq_len = seq_len; a.q_start = q_start;
-  a.scale = scale; a.k_scale = k_scale; a.v_scale = v_scale; a.out = out; a.lse_out = lse_out;
+  a.granted = granted; a.scale = scale; a.k_scale = k_scale; a.v_scale = v_scale; a.out = out; a.lse_out = lse_out;
   // a window as long as the table hides nothing; kept below it, position - window stays within 32 bits
   a.window = window < (int64_t)max_pages * page_size ? window : 0;
   a.status = static_cast<dspark::DeviceStatus*>(workspace);

@@ -50,6 +50,7 @@ def _cache(b, slots=32):
     c.page_table, c.seq_len = torch.zeros((slots, 4), dtype=torch.int32), torch.zeros(slots, dtype=torch.int32)
     c.k = c.v = torch.zeros((2, 8, 8, 16, 128), dtype=torch.bfloat16)
     c.k_scale = c.v_scale = None
+    c.not_refused = torch.ones(slots, dtype=torch.int32)
     c._attention_ws = {}
     return c
 
@@ -87,3 +88,22 @@ def test_attend_clears_only_the_status_block(b):
     ws = b._attention_workspace(5000, "cpu")
     assert ws.numel() == 5000 and ws.data_ptr() % 256 == 0 and (ws[:256] == 0).all()
     assert b._attention_workspace(0, "cpu").numel() == 256
+
+
+def test_refusals_of_the_granted_form(b):
+    """The entry point with `granted` refuses what the one without refuses, and takes a null."""
+    import ctypes
+
+    from tests.test_serving_abi import INVALID, OK, P, UNSUPPORTED
+    need = b.paged_attention_workspace_size(3, 4, 8, 2, 64, 1)
+
+    def call(T=3, Hq=8, max_q=1, granted=P[9], null=(), scale=0.1):
+        p = [None if i in null else x for i, x in enumerate(P)]
+        return b.lib.dspark_paged_attention_granted(T, 4, Hq, 2, 64, 64, 16, 8, max_q, 1, 1, p[0], 512, 64, p[1], p[2], 2048,
+                                                    1024, 64, p[3], 8, p[4], p[5], granted, scale, None, None, 0, p[6], p[7],
+                                                    p[8], need, None)
+
+    assert call(Hq=7) == INVALID and call(max_q=129) == UNSUPPORTED and call(scale=float("inf")) == INVALID
+    for i in (0, 1, 2, 3, 4, 5, 6, 8):
+        assert call(null=[i]) == INVALID, i
+    assert call(T=0, null=[0, 6]) == OK and call(T=0, null=[0, 6], granted=None) == OK
