@@ -872,7 +872,8 @@ class PagedCache:
         self.v = torch.zeros_like(self.k)
         self.k_scale, self.v_scale = k_scale, v_scale
         self.pools = cache_pools([*self.k.unbind(0), *self.v.unbind(0)])
-        self.plan = dict(granted=torch.empty(slots, **i32), copies=torch.empty((slots, 2), **i32))
+        # (until the first reserve nothing has been refused, and nothing copied)
+        self.plan = dict(granted=torch.ones(slots, **i32), copies=torch.full((slots, 2), -1, **i32))
         self.not_refused = torch.ones(slots, **i32)  # by the last reserve
         self.moves = torch.empty(1, **i32)
         self.ws = workspace(cache_workspace_size(slots, num_pages), device)

@@ -168,3 +168,11 @@ def test_loop_on_a_pool_that_runs_out(b):
         assert (torch.tensor(lps[r], device="cuda") - want).abs().max() < 0.15
     with pytest.raises(RuntimeError):
         _loop(torch.bfloat16, _prompts([30, 9, 20]), page_size=8, num_pages=9)
+
+
+def test_write_before_any_reservation_reports_its_places(b):
+    """Nothing has been refused yet: rows that have no place are reported, not passed over."""
+    c = b.PagedCache(2, 4, 8, 2, 1, 1, 16)
+    x = torch.ones((2, 1, 16), device="cuda").bfloat16()
+    c.write(0, x, x, _i32([0, 1, 2]))
+    assert c.status() == 1 and (c.k == 0).all()
