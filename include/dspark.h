@@ -516,9 +516,10 @@ DSPARK_API dspark_status dspark_cache_reserve(
 /* Writes the keys and values of the last tokens of every slot into one layer's pools: rows
  * q_start[r] .. q_start[r+1] - 1 of k and v [T,Hkv,D] are the slot's last positions.
  * granted (NULL: all) skips slots whose entry is 0.  k and v have strides between tokens and
- * heads.  dtype_in is DSPARK_BF16 or DSPARK_F16; dtype_kv the same, or DSPARK_E4M3: then
- * element x of head h is stored as x / scale[h], rounded to nearest even and held within
- * +-448 (k_scale, v_scale [Hkv] > 0; they must be NULL otherwise).  T = 0 does nothing. */
+ * heads; the pools' strides may be 0 only where there is one page, head or token.  dtype_in is
+ * DSPARK_BF16 or DSPARK_F16; dtype_kv the same, or DSPARK_E4M3: then element x of head h is stored
+ * as x / scale[h], rounded to nearest even and held within +-448 (k_scale, v_scale [Hkv] > 0; they
+ * must be NULL otherwise).  T = 0 does nothing. */
 DSPARK_API dspark_status dspark_cache_write(
     int T, int R, int Hkv, int D, int num_pages, int page_size, int max_pages, int dtype_in, int dtype_kv,
     const void* k, const void* v, int64_t in_stride_token, int64_t in_stride_head, void* k_pool, void* v_pool,

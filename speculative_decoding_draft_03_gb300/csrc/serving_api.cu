@@ -259,6 +259,8 @@ dspark_status dspark_cache_write(int T, int R, int Hkv, int D, int num_pages, in
   CHECK(check_geometry(R, num_pages, page_size, max_pages, table_stride));
   if (T < 0 || Hkv < 1) return fail(DSPARK_INVALID_ARG, "sizes must be positive (T=%d Hkv=%d)", T, Hkv);
   CHECK(check_rows(D, dtype_in, dtype_kv, k_pool, v_pool, page_stride, head_stride, token_stride, k_scale, v_scale));
+  if ((page_stride == 0 && num_pages > 1) || (head_stride == 0 && Hkv > 1) || (token_stride == 0 && page_size > 1))
+    return fail(DSPARK_INVALID_ARG, "rows of a pool that is written to must not lie on one another");
   CHECK_PTR(page_table);
   CHECK_PTR(seq_len);
   CHECK_PTR(q_start);

@@ -107,3 +107,18 @@ def test_refusals_of_the_granted_form(b):
     for i in (0, 1, 2, 3, 4, 5, 6, 8):
         assert call(null=[i]) == INVALID, i
     assert call(T=0, null=[0, 6]) == OK and call(T=0, null=[0, 6], granted=None) == OK
+
+
+def test_write_refuses_pools_whose_rows_lie_on_one_another(b):
+    """Which of two heads' rows such a pool would hold is chance."""
+    from tests.test_serving_abi import INVALID, OK, P
+
+    def call(H=2, pages=64, ps=16, strides=(2048, 1024, 64), T=3):
+        return b.lib.dspark_cache_write(T, 4, H, 64, pages, ps, 8, 1, 1, P[0], P[1], 128, 64, P[2], P[3], *strides, P[4], 8,
+                                        P[5], P[6], None, None, None, P[7], 256, None)
+
+    for strides in ((0, 1024, 64), (2048, 0, 64), (2048, 1024, 0)):
+        assert call(strides=strides) == INVALID, strides
+        assert "lie on one another" in b.lib.dspark_last_error_message().decode()
+        assert call(strides=strides, T=0) == INVALID
+    assert call(H=1, pages=1, ps=1, strides=(0, 0, 0), T=0) == OK
