@@ -641,13 +641,27 @@ def _load_marshal():
     if not os.path.exists(path):
         raise DSparkError(f"_marshal.so is not built ({path}); run __graft_entry__.build()")
     spec = importlib.util.spec_from_file_location("_marshal", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    try:
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        raise DSparkError(f"_marshal.so does not load ({e}); run __graft_entry__.build() with this PyTorch "
+                          f"({torch.__version__})") from e
     module.set_error(DSparkError)
     return module
 
 
-_m = _load_marshal()
+class _Marshal:
+    """Stands for the module until the first serving-side call loads it: whoever makes none of these
+    calls needs the library alone."""
+
+    def __getattr__(self, name):
+        global _m
+        _m = _load_marshal()
+        return getattr(_m, name)
+
+
+_m = _Marshal()
 _raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 

@@ -61,6 +61,13 @@ def _stale(target, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _holds(path, text) -> bool:
+    if not os.path.exists(path):
+        return False
+    with open(path) as f:
+        return f.read() == text
+
+
 def build(verbose: bool = False, force: bool = False, extra_flags=(), build_dir: str = BUILD) -> str:
     """Compile every csrc/*.cu and link libdspark.so in `build_dir` (the package's _build by
     default, where the marshalling module stands too; tests build variants with extra -D flags
@@ -80,7 +87,9 @@ def build(verbose: bool = False, force: bool = False, extra_flags=(), build_dir:
 
     marshal = build_dir == BUILD
     if marshal:
-        obj = os.path.join(build_dir, "marshal.o")
+        # (named after the PyTorch that it is compiled against: another one compiles its own)
+        import torch
+        obj = os.path.join(build_dir, f"marshal-{torch.__version__}.o")
         compile_, link = _marshal_commands(obj, MARSHAL + f".tmp{os.getpid()}")
         if force or _stale(obj, [os.path.join(CSRC, "marshal.cpp")] + hdrs):
             jobs.append(compile_)
@@ -99,9 +108,12 @@ def build(verbose: bool = False, force: bool = False, extra_flags=(), build_dir:
         tmp = lib + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs])
         os.replace(tmp, lib)
-    if marshal and (force or _stale(MARSHAL, [obj, lib])):
+    stamp = os.path.join(build_dir, "marshal.stamp")
+    if marshal and (force or _stale(MARSHAL, [obj, lib]) or not _holds(stamp, torch.__version__)):
         run(link)
         os.replace(MARSHAL + f".tmp{os.getpid()}", MARSHAL)
+        with open(stamp, "w") as f:
+            f.write(torch.__version__)
     return lib
 
 

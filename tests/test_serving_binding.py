@@ -122,3 +122,59 @@ def test_write_refuses_pools_whose_rows_lie_on_one_another(b):
         assert "lie on one another" in b.lib.dspark_last_error_message().decode()
         assert call(strides=strides, T=0) == INVALID
     assert call(H=1, pages=1, ps=1, strides=(0, 0, 0), T=0) == OK
+
+
+def test_calls_of_a_round_do_not_need_the_marshalling_module(b, tmp_path):
+    """Importing the binding, and the calls that go through ctypes, work where it is not built; the
+    serving-side calls say so."""
+    import subprocess
+    import sys
+
+    code = f"""
+import torch
+from speculative_decoding_draft_03_gb300 import build
+build.MARSHAL = {str(tmp_path / "none.so")!r}
+from speculative_decoding_draft_03_gb300 import binding as b
+assert b.schedule_workspace_size(4, 4) > 0 and b.cache_workspace_size(4, 64) > 0
+t = torch.zeros(4, dtype=torch.int32)
+for path in (build.MARSHAL, {str(tmp_path / "bad.so")!r}):
+    build.MARSHAL = path
+    try:
+        b.cache_truncate(t.view(1, 4), t, t, t, 16, ws=t)
+    except b.DSparkError as e:
+        assert "_marshal.so" in str(e), e
+    else:
+        raise AssertionError("not refused")
+"""
+    (tmp_path / "bad.so").write_bytes(b"not a library")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                       cwd=b._build.os.path.dirname(b._build.HERE))
+    assert r.returncode == 0, r.stderr
+
+
+def test_another_pytorch_compiles_its_own_marshalling_module(b, monkeypatch, tmp_path):
+    import os
+    import subprocess
+    import types
+
+    build, ran = b._build, []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return types.SimpleNamespace(returncode=0, stdout="", stderr="")
+
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "LIB", os.path.join(tmp_path, "libdspark.so"))
+    monkeypatch.setattr(build, "MARSHAL", os.path.join(tmp_path, "_marshal.so"))
+    monkeypatch.setattr(subprocess, "run", run)
+    build.build(build_dir=str(tmp_path))
+    assert sum("marshal.cpp" in a for cmd in ran for a in cmd) == 1
+    ran.clear()
+    build.build(build_dir=str(tmp_path))
+    assert ran == []
+    monkeypatch.setattr(torch, "__version__", "99.0")
+    build.build(build_dir=str(tmp_path))
+    assert [any("marshal.cpp" in a for a in cmd) for cmd in ran].count(True) == 1  # compiled again
+    assert any(cmd[cmd.index("-o") + 1].startswith(build.MARSHAL) for cmd in ran)  # and linked
+    assert not any(a.endswith(".cu") for cmd in ran for a in cmd)
