@@ -24,6 +24,9 @@ from speculative_decoding_draft_03_gb300 import binding as b  # noqa: E402
 from speculative_decoding_draft_03_gb300 import workloads as wl  # noqa: E402
 
 
+MAX_BLOCK = 128  # queries of a request in one attention call, at most
+
+
 class ToyTarget:
     """layers x (grouped-query attention + residual) between an embedding and an unembedding."""
 
@@ -98,15 +101,17 @@ class ServingLoop:
         self.rounds = 0
 
     def prefill(self, prompts):
-        """Every token but the last goes into the cache; the last is the first anchor."""
+        """Every token but the last goes into the cache, in blocks that one attention call takes; the
+        last is the first anchor."""
         dev = "cuda"
-        n = [len(p) - 1 for p in prompts]
-        q_start = torch.tensor([sum(n[:r]) for r in range(self.R + 1)], dtype=torch.int32, device=dev)
-        want = torch.tensor(n, dtype=torch.int32, device=dev)
-        if not torch.equal(self.cache.reserve(want)["granted"], want):
-            raise RuntimeError("the pool has no room for the prompts")
-        tokens = torch.tensor([t for p in prompts for t in p[:-1]], dtype=torch.int32, device=dev)
-        if tokens.numel():
+        for at in range(0, max(len(p) - 1 for p in prompts), MAX_BLOCK):
+            blocks = [p[at:min(at + MAX_BLOCK, len(p) - 1)] for p in prompts]
+            n = [len(x) for x in blocks]
+            q_start = torch.tensor([sum(n[:r]) for r in range(self.R + 1)], dtype=torch.int32, device=dev)
+            want = torch.tensor(n, dtype=torch.int32, device=dev)
+            if not torch.equal(self.cache.reserve(want)["granted"], want):
+                raise RuntimeError("the pool has no room for the prompts")
+            tokens = torch.tensor([t for x in blocks for t in x], dtype=torch.int32, device=dev)
             self.target.forward(tokens, self.cache, q_start, max(n))
         self.x0 = torch.tensor([p[-1] for p in prompts], dtype=torch.int32, device=dev)
 

@@ -176,3 +176,23 @@ def test_write_before_any_reservation_reports_its_places(b):
     x = torch.ones((2, 1, 16), device="cuda").bfloat16()
     c.write(0, x, x, _i32([0, 1, 2]))
     assert c.status() == 1 and (c.k == 0).all()
+
+
+def test_loop_with_long_prompts(b):
+    """Prompts of more tokens than an attention call takes queries go in block by block."""
+    from tests.test_gpu_serving_loop import _loop, _prompts
+    prompts = _prompts([300, 9, 129, 130, 257])
+    loop = _loop(torch.bfloat16, prompts, page_size=16, num_pages=125)
+    assert loop.cache.seq_len.tolist() == [299, 8, 128, 129, 256]
+    seqs, lps = [list(p) for p in prompts], [[] for _ in prompts]
+    for _ in range(4):
+        o = loop.step()
+        for r, n in enumerate(o["n_out"].tolist()):
+            seqs[r] += o["tokens"][r, :n].tolist()
+            lps[r] += o["logprob"][r, :n].tolist()
+    assert loop.cache.status() == 0
+    for r, seq in enumerate(seqs):
+        dense = torch.log_softmax(loop.target.dense(torch.tensor(seq, device="cuda")), 1)
+        at = len(prompts[r]) - 1
+        want = dense[torch.arange(at, len(seq) - 1), torch.tensor(seq[at + 1:], device="cuda")]
+        assert (torch.tensor(lps[r], device="cuda") - want).abs().max() < 0.15
