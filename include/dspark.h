@@ -561,8 +561,10 @@ DSPARK_API dspark_status dspark_cache_compact(
  *   max_q    an upper bound of every nq, 1..128; a request with more, or one whose queries
  *            do not lie within [0,T), is reported and its rows are not written.
  *   out      [T,Hq,D] of q's type, contiguous; lse_out [T,Hq] fp32 or NULL.
- * Scores, softmax statistics and sums are fp32; the weights are rounded to q's type (16-bit
- * floats, with an e4m3 cache to fp16) for the product with v.  Deterministic.
+ * Scores, softmax statistics and sums are fp32 (scores past 2^24 in magnitude have no digits left
+ * for their differences); the weights are rounded to q's type (16-bit floats, with an e4m3 cache to
+ * fp16) for the product with v: half a step each, and in fp16 at most 2^-32 of the largest more.
+ * Deterministic.
  * Queries that belong to no request (before q_start[0], past q_start[R]) are not written.
  * Limits: D a multiple of 16, 16..256; Hq a multiple of Hkv, Hq / Hkv <= 64; R <= 8192;
  * max_pages * page_size < 2^31 - 256.

@@ -693,7 +693,8 @@ def token_logprobs(logits, tokens, temperature=1.0, top_k=0, out=None, stream=No
     ``top_k`` best alternatives (dspark_token_logprobs).  logits [N,V] float32, bfloat16 or
     float16 with any row stride; tokens [N] int32, rows with an id outside [0,V) (verification
     writes -1) are skipped and hold NaN / -1.  Returns dict logprob, entropy, lse [N] and, with
-    top_k, top_ids, top_logprobs [N,top_k]."""
+    top_k, top_ids, top_logprobs [N,top_k].  No graph is recorded, whatever the logits require: their
+    gradient is token_logprobs_backward's."""
     if out is None:
         N = _on_gpu(logits, "logits").shape[0]
         f = dict(dtype=torch.float32, device=logits.device)

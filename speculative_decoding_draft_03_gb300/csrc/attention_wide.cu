@@ -21,9 +21,12 @@
 //   * The work is dealt out in tiles of 128 tokens as for the other kernel, a CTA per worker.
 // What bounds it: to 32 columns the device memory (the verified block of 32 requests of 1 K to 8 K
 // tokens: 640 MB in 113 us, 5.7 TB/s; items' starts and ends cost the rest); from 64 on the chain
-// of a tile from its scores over the weights to its product (64 rows: 130 us, 128 rows: 194 us or
-// 239 TFLOP/s), and the item's drain where contexts are short (200 requests of 50 to 600 tokens,
-// 64 rows: 148 us); with an e4m3 cache the shared memory, about 210 KB a tile (32 rows: 112 us).
+// of a tile from its scores over the weights to its product (64 rows: 133 us, 128 rows: 196 us or
+// 236 TFLOP/s: no weight is stored before the last tile's product has ended), and the item's drain
+// where contexts are short (200 requests of 50 to 600 tokens, 64 rows: 149 us); with an e4m3 cache
+// the chain of copy, conversion and product (32 rows: 112 us, some 3000 cycles a tile, of which its
+// 210 KB of shared-memory traffic are 1640; the keys' converted tile is single buffered, and the same
+// warps convert keys and values in turn).
 // Every mbarrier wait is bounded; a wait that gives up reports DSPARK_TIMEOUT and the CTA winds
 // down (the softmax warps leave together, by a vote).
 #include <cuda.h>
@@ -685,7 +688,8 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
           if (clear)
             for (int c = 0; c < kPieces; ++c) sts16(part_of_row(c), make_uint4(0, 0, 0, 0));
         }
-        // the weights: C 16-bit values of the token's row
+        // the weights: C 16-bit values of the token's row (rounded as the instruction wants both
+        // operands; the normaliser adds them unrounded)
 #pragma unroll
         for (int c = 0; c < C; c += 16) {
           if (!kHeld) {

@@ -14,12 +14,13 @@
 // earlier segments), so only those few segments are read again, from the L2 cache.
 // What bounds it: the copy rate of the device memory, and the selection at the end of each row,
 // some 7000 cycles of one CTA while the others of its SM stream.  Measured: 1536 rows of 129280
-// bf16, 30% of them skipped (278 MB): 47.7 us (87% of the copy rate), with the best 5 ids 55.8
-// us, with 20 61 us; 256 rows of 151936 fp32, 30% skipped (109 MB), with the best 20: 30 us (one
-// wave of CTAs, whose selections all come at its end; without ids 22 us).
+// bf16, 30% of them skipped (278 MB): 48.0 us (87% of the copy rate), with the best 5 ids 56
+// us, with 20 61 us; 256 rows of 151936 fp32, 30% skipped (109 MB), with the best 20: 30 us (2.4
+// slices an SM, so that some SMs take three: 22 us without ids; and the selections of all rows
+// come together at the end).
 //
-// Backward.  Elementwise, one read and one write of the row: 1024 rows of 151936 bf16 in 97 us
-// (96% of the copy rate).
+// Backward.  Elementwise, one read and one write of the row: 1024 rows of 151936 bf16, 10% of them
+// skipped (591 MB), in 95 us (93% of the copy rate); 300 rows of 50257 fp32 (115 MB) in 20.6 us (83%).
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -33,7 +34,7 @@ namespace cg = cooperative_groups;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 // A normaliser below this one is known well enough for the gradient: to 2^-19 for fp32, and to 2^-17
-// where the gradient is rounded to 16 bits (2^-12 at best).
+// where the gradient is rounded to 16 bits (2^-11 at best).
 template <typename T>
 constexpr float kLargeLse = sizeof(T) == 4 ? 64.f : 256.f;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
