@@ -125,6 +125,12 @@ __device__ __forceinline__ Request request(const AttentionArgs& a, int r, bool r
   return k;
 }
 
+// Does a query of request k see the position, or a later one?  (The first unit may begin before all
+// that they see.)
+__device__ __forceinline__ bool seen(const AttentionArgs& a, const Request& k, int pos) {
+  return a.window == 0 || pos > k.len - k.nq - a.window;
+}
+
 // A share that a worker leaves to the joining kernel: the item's place and its units.
 struct Share {
   int r, item, q0, nq;   // item: cache head * row blocks + row block; r < 0: none

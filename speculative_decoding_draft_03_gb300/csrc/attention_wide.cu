@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP, N>::threads, 1)
     auto look_up = [&]() {
       const int pos = use.k.first + use.chunk * kTile + lane * box, nth = pos / a.page_size;
       slot = pos - nth * a.page_size;
-      inside = lane < boxes && pos < use.k.len;
+      inside = lane < boxes && pos < use.k.len && seen(a, use.k, pos + box - 1);
       page = inside ? a.page_table[use.r * a.table_stride + nth] : -1;
     };
     if (tiles > 0) look_up();

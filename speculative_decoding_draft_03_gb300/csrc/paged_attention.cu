@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) attention_kernel(const __gri
       const int h = get.k.blocks == 1 ? get.item : get.item / get.k.blocks;
       const uint32_t at = ring + put * C::stage;
       const bool there = pos < get.k.len && page >= 0 && page < a.num_pages;
-      if (pos < get.k.len && !there) report_bad_input(a.status, kBadPage);
+      if (pos < get.k.len && !there && seen(a, get.k, pos)) report_bad_input(a.status, kBadPage);
       int64_t from = -1;  // in 16-byte pieces; -1: nothing there, zeros instead
       if (there)
         from = ((int64_t)page * a.page_stride + (int64_t)h * a.head_stride + (int64_t)slot * a.token_stride) * C::kBytes / 16;

@@ -235,3 +235,22 @@ def test_many_short_contexts(b, dtype, cache):
     lens = rng.integers(0, 500, 220).tolist()
     new = [min(n, int(x)) for n, x in zip(lens, rng.integers(0, 9, 220))]
     _check(b, _case(lens, new, 32, 2, 128, 16, dtype, cache, seed=2, garbage=False))
+
+
+@pytest.mark.parametrize("gone", [-1, 1 << 20])
+@pytest.mark.parametrize("dtype,cache", TYPES[:3])
+@pytest.mark.parametrize("Hq,D,ps", [(4, 64, 8), (4, 64, 5), (4, 256, 16), (32, 128, 8), (32, 64, 16)])
+def test_pages_before_every_window_may_be_gone(b, dtype, cache, Hq, D, ps, gone):
+    """Pages that no query sees any more need not be in the table, and are not reported; one that the
+    first query still sees is."""
+    lens, new, window = [37, 300, 513, 90], [1, 3, 5, 2], 21
+    c = _case(lens, new, Hq, 2, D, ps, dtype, cache, seed=23, garbage=False)
+    want = _check(b, c, window=window)
+    for r, (n, m) in enumerate(zip(lens, new)):
+        c["table"][r, : max(0, n - m - window + 1) // ps] = gone
+    o, ws = _run(b, c, D ** -0.5, window)
+    assert b.device_status(ws) == 0
+    assert torch.equal(o["out"], want["out"]) and torch.equal(o["lse"], want["lse"])
+    c["table"][1, (300 - 3 - window + 1) // ps] = gone
+    o, ws = _run(b, c, D ** -0.5, window)
+    assert b.device_status(ws) == 1
