@@ -933,5 +933,8 @@ class PagedCache:
                              out=self.moves, ws=self.ws, stream=stream)
 
     def status(self) -> int:
-        """The worst device status of the cache's workspaces (0 OK, 1 bad device data)."""
-        return max(device_status(w) for w in (self.ws, *self._attention_ws.values()))
+        """The worst device status of the cache's workspaces (0 OK, 1 bad device data, 5 a bounded wait
+        gave up)."""
+        codes = [device_status(w) for w in (self.ws, *self._attention_ws.values())]
+        # (scratch made in a capture holds anything until the graph's first replay clears its status)
+        return max(c if c in (1, 5) else 0 for c in codes)

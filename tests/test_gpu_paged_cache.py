@@ -196,3 +196,23 @@ def test_loop_with_long_prompts(b):
         at = len(prompts[r]) - 1
         want = dense[torch.arange(at, len(seq) - 1), torch.tensor(seq[at + 1:], device="cuda")]
         assert (torch.tensor(lps[r], device="cuda") - want).abs().max() < 0.15
+
+
+def test_status_of_a_captured_block(b):
+    """Before the graph's first replay its scratch holds what was there; after a replay, its reports."""
+    c = _filled(b, [40, 33])
+    q, q_start = torch.randn((4, 8, 64), device="cuda").bfloat16(), _i32([0, 2, 4])
+    torch.full((96 << 20,), 0x5A, dtype=torch.uint8, device="cuda")  # what freed memory may hold
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = c.attend(0, q, q_start, 2, 0.125)
+    for ws in c._attention_ws.values():
+        ws[:256] = 0x5A
+    assert c.status() == 0
+    graph.replay()
+    assert c.status() == 0
+    want = b.paged_attention(q, c.k[0], c.v[0], c.page_table, c.seq_len, q_start, 2, 0.125)
+    assert torch.equal(out["out"], want["out"])
+    c.page_table[1, 0] = 99
+    graph.replay()
+    assert c.status() == 1
