@@ -532,6 +532,10 @@ constexpr int kMaxWorkers = kMaxSms * 2 * 4;
 // Query rows of a cache head (at most, over the requests) above which the other kernel is faster:
 // 32 requests of 1 K to 8 K tokens, 16-bit cache: 12 rows 110 us here and 110 there, 16 rows 104 and
 // 102, 20 rows 145 and 112; e4m3 cache: 12 rows 79 and 98, 16 rows 86 and 106, 20 rows 164 and 113.
+// Rows of 64 elements: 16 rows 85 and 83, 24 rows 113 and 85, 64 rows 171 and 104.  200 requests of 50
+// to 600 tokens: 16 rows 85 and 118, 24 rows 136 and 121, 64 rows 201 and 158; with 64 elements 24 rows
+// 100 and 125, 32 rows 110 and 109; with an e4m3 cache 32 rows 195 and 177, 64 rows 274 and 307.  (The
+// lengths are on the device, so the rule cannot ask for them.)
 constexpr int kWideRows = 16;
 
 int padded(int D, bool q8) { return D <= 64 && !q8 ? 64 : (D <= 128 ? 128 : 256); }  // (8-bit panels hold 128 elements)
