@@ -4,7 +4,8 @@
  * recurrent-head draft, verification on a flattened target batch, the fixed-cutoff
  * scheduler, the acceptance-overlap diagnostic and sequential temperature scaling; and the
  * operators a serving loop needs beside a round: token log probabilities (with their
- * gradient), the paged key-value cache and attention over it.
+ * gradient), the paged key-value cache and attention over it, rotary positions and the
+ * adjustment of logits by penalties, biases and masks.
  *
  * The method is the one described on the pages about DSpark (Cheng, Yu, Shao et al.,
  * "DSpark: Confidence-Scheduled Speculative Decoding with Semi-Autoregressive
@@ -590,6 +591,104 @@ DSPARK_API dspark_status dspark_paged_attention_granted(
     int64_t table_stride, const int32_t* seq_len, const int32_t* q_start, const int32_t* granted, float scale,
     const float* k_scale, const float* v_scale, int window, void* out, float* lse_out, void* workspace,
     size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Attention of long blocks: dspark_paged_attention_granted without a bound on a request's
+ * queries (a chunk of a prompt, a whole prompt, or both beside requests that decode).
+ *
+ * Arguments, results and refusals are dspark_paged_attention_granted's, but for max_q, which
+ * this call does not have.  Blocks of D > 128, over pages that no multiple of 8 tokens
+ * divides, or over pools whose entries lie on one another, are computed 16 or 32 query rows
+ * at a time, much slower.
+ * Workspace: dspark_chunk_attention_workspace_size() (0 for unsupported sizes).
+ * ---------------------------------------------------------------------------------- */
+DSPARK_API size_t dspark_chunk_attention_workspace_size(int T, int R, int Hq, int Hkv, int D);
+
+DSPARK_API dspark_status dspark_chunk_attention(
+    int T, int R, int Hq, int Hkv, int D, int num_pages, int page_size, int max_pages, int dtype_q, int dtype_kv,
+    const void* q, int64_t q_stride_token, int64_t q_stride_head, const void* k_pool, const void* v_pool,
+    int64_t page_stride, int64_t head_stride, int64_t token_stride, const int32_t* page_table, int64_t table_stride,
+    const int32_t* seq_len, const int32_t* q_start, const int32_t* granted, float scale, const float* k_scale,
+    const float* v_scale, int window, void* out, float* lse_out, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Rotary positions.
+ *
+ * Every head of row t of x [T,H,D] has its pairs i < rot_dim / 2 turned by an angle
+ * a = positions[t] * f_i:
+ *   (y_u, y_w) = magnitude * (x_u cos a - x_w sin a, x_w cos a + x_u sin a),
+ * with (u, w) = (i, i + rot_dim/2), or (2i, 2i + 1) where interleaved is 1.  Elements from
+ * rot_dim on stay as they are.  inverse = 1 turns by -a: the transposed map, and so the
+ * gradient for x from the gradient for y (with the same magnitude).
+ *
+ *   rates     [rot_dim/2] int64: f_i as turns per position, f_i / (2 pi), in units of 2^-64
+ *             (an unsigned 64-bit fraction).  The angle is then exact at every position: its
+ *             error is 2^-25 half turns at most (1e-7 radians), whatever the position.
+ *   positions [T] int32, any value (a negative one turns back).
+ *   dtype     DSPARK_F32, DSPARK_BF16 or DSPARK_F16; products and sums are fp32, rounded once.
+ *   strides   (in elements) between tokens and heads; D contiguous elements a row, which
+ *             need only their type's alignment.  out may be x itself (same strides); beyond
+ *             that the two must not overlap, and a row of out must not lie on another.
+ * T = 0 does nothing.  No workspace.
+ * Limits: D <= 1024; rot_dim even, 2..D; H * D <= 2^26.
+ * ---------------------------------------------------------------------------------- */
+DSPARK_API dspark_status dspark_rotary(
+    int T, int H, int D, int rot_dim, int dtype, int interleaved, int inverse, const void* x, int64_t x_stride_token,
+    int64_t x_stride_head, const int32_t* positions, const int64_t* rates, float magnitude, void* out,
+    int64_t out_stride_token, int64_t out_stride_head, void* stream);
+
+/* dspark_cache_write with the rotation on the way: rows q_start[r] .. q_start[r+1] - 1 are the
+ * slot's last positions, seq_len[r] - n .. seq_len[r] - 1; their keys are turned by their position
+ * (as dspark_rotary turns them) and stored with the values as they are, in one layer's pools, and
+ * their queries are turned into q_out [T,Hq,D] (which may be q itself, with the same strides).
+ * The turned keys are fp32 until the one rounding to the pools' type (e4m3: divided by their
+ * scale before it).  Hq = 0: keys and values alone (q and q_out may be NULL).  Rows of no slot and
+ * of slots that granted refuses are written nowhere, in q_out neither.  Other arguments, errors and
+ * limits are dspark_cache_write's and dspark_rotary's, with rot_dim a multiple of 16 and rows on
+ * 16-byte boundaries. */
+DSPARK_API dspark_status dspark_cache_append(
+    int T, int R, int Hq, int Hkv, int D, int rot_dim, int interleaved, int num_pages, int page_size, int max_pages,
+    int dtype_in, int dtype_kv, const void* q, int64_t q_stride_token, int64_t q_stride_head, const void* k,
+    const void* v, int64_t in_stride_token, int64_t in_stride_head, void* q_out, int64_t q_out_stride_token,
+    int64_t q_out_stride_head, void* k_pool, void* v_pool, int64_t page_stride, int64_t head_stride,
+    int64_t token_stride, const int32_t* page_table, int64_t table_stride, const int32_t* seq_len,
+    const int32_t* q_start, const int32_t* granted, const float* k_scale, const float* v_scale, const int64_t* rates,
+    float magnitude, void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Logits adjusted before tokens are taken from them (or verified, or given probabilities).
+ *
+ * Slot r has rows n = q_start[r] .. q_start[r+1] - 1 of logits [N,V], one after each token fed in
+ * for it (tokens[n]).  Row number i of the slot follows the sequence
+ *   history[r, 0 .. history_len[r] - 1], tokens[q_start[r]] .. tokens[q_start[r] + i],
+ * so that each row of a verified block counts the drafts before it.  Entries of the sequence below
+ * prompt_len[r] are the prompt's, the others answers; ids outside [0,V) count for nothing.  Then
+ *   x_v = x_v > 0 ? x_v / repetition[r] : x_v * repetition[r]   where v is in the sequence,
+ *   x_v -= frequency[r] * n_v + presence[r] * 1[n_v > 0],       n_v: answers equal to v,
+ *   x_v += bias[r,i] for every i with bias_ids[r,i] = v (in order),
+ *   x_v = -inf                                                  where the row's mask bit v is 0,
+ * in fp32, rounded once to the logits' type.
+ *
+ *   row_stride, out_stride  elements between rows (>= V); rows need only their type's alignment.
+ *   dtype       DSPARK_F32, DSPARK_BF16 or DSPARK_F16, also out's.  out may be logits itself (same
+ *               stride); beyond that the two must not overlap.  Rows of no slot are not written.
+ *   tokens      [N] int32, or NULL: the history is the whole sequence of every row.
+ *   history     [R, history_width] int32, rows history_stride apart, or NULL; lengths past the
+ *               width (or below 0) are held there.  prompt_len [R] or NULL (nothing is a prompt's).
+ *   repetition  [R] > 0; frequency, presence [R]; each may be NULL (no such penalty).
+ *   bias_ids, bias  [R, n_bias]; n_bias = 0: none.
+ *   mask        mask_rows rows of bits, id v at bit v % 32 of word v / 32, rows mask_stride words
+ *               apart, or NULL.  mask_row [N]: which one row n goes by (out of range: none); NULL:
+ *               mask row n.
+ * N = 0 does nothing.  Deterministic.  No workspace.
+ * Limits: V <= 1048576; R <= 8192.
+ * ---------------------------------------------------------------------------------- */
+DSPARK_API dspark_status dspark_adjust_logits(
+    int N, int V, int R, int dtype, const void* logits, int64_t row_stride, const int32_t* tokens,
+    const int32_t* q_start, const int32_t* history, int64_t history_stride, int history_width,
+    const int32_t* history_len, const int32_t* prompt_len, const float* repetition, const float* frequency,
+    const float* presence, int n_bias, const int32_t* bias_ids, const float* bias, const uint32_t* mask,
+    int64_t mask_stride, int mask_rows, const int32_t* mask_row, void* out, int64_t out_stride, void* stream);
 
 #ifdef __cplusplus
 }

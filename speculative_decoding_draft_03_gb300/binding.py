@@ -11,6 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import importlib.util
+import math
 import os
 
 import torch
@@ -19,6 +20,7 @@ from . import build as _build
 
 F32, BF16, F16, E4M3 = 0, 1, 2, 3
 EARLY_STOP, FULL_SEARCH, CAPACITY_K, FIXED = 0, 1, 2, 3
+MAX_BLOCK = 128  # queries of a slot in one paged_attention call, at most (chunk_attention takes any number)
 _DT = {torch.float32: F32, torch.bfloat16: BF16}
 
 
@@ -106,6 +108,19 @@ def _load_library():
     lib.dspark_paged_attention_granted.argtypes = ([i32] * 11 + [P, i64, i64, P, P, i64, i64, i64, P, i64, P, P, P, f32,
                                                                  P, P, i32, P, P, P, sz, P])
     lib.dspark_paged_attention_granted.restype = i32
+    lib.dspark_chunk_attention_workspace_size.argtypes = [i32] * 5
+    lib.dspark_chunk_attention_workspace_size.restype = sz
+    lib.dspark_chunk_attention.argtypes = ([i32] * 10 + [P, i64, i64, P, P, i64, i64, i64, P, i64, P, P, P, f32, P, P, i32,
+                                                         P, P, P, sz, P])
+    lib.dspark_chunk_attention.restype = i32
+    lib.dspark_rotary.argtypes = [i32] * 7 + [P, i64, i64, P, P, f32, P, i64, i64, P]
+    lib.dspark_rotary.restype = i32
+    lib.dspark_cache_append.argtypes = ([i32] * 12 + [P, i64, i64, P, P, i64, i64, P, i64, i64, P, P, i64, i64, i64, P, i64]
+                                        + [P] * 5 + [P, f32, P, sz, P])
+    lib.dspark_cache_append.restype = i32
+    lib.dspark_adjust_logits.argtypes = ([i32] * 4 + [P, i64, P, P, P, i64, i32] + [P] * 5 + [i32, P, P, P, i64, i32, P, P,
+                                                                                             i64, P])
+    lib.dspark_adjust_logits.restype = i32
     for fn in ("dspark_markov_draft", "dspark_schedule", "dspark_verify", "dspark_workspace_status"):
         getattr(lib, fn).restype = i32
     return lib
@@ -869,6 +884,151 @@ def paged_attention(q, k_pool, v_pool, page_table, seq_len, q_start, max_q, scal
     return out
 
 
+def chunk_attention_workspace_size(T, R, Hq, Hkv, D) -> int:
+    return int(lib.dspark_chunk_attention_workspace_size(T, R, Hq, Hkv, D))
+
+
+def chunk_attention(q, k_pool, v_pool, page_table, seq_len, q_start, scale, k_scale=None, v_scale=None, window=0, out=None,
+                    ws=None, stream=None, granted=None):
+    """paged_attention without a bound on a slot's queries: chunks of prompts, beside slots that
+    decode (dspark_chunk_attention).  Returns dict out [T,Hq,D], lse [T,Hq] float32."""
+    _here(q, "q")
+    if out is None or ws is None:
+        T, Hq, D = q.shape
+        with _made_on(stream):
+            if out is None:
+                out = dict(out=torch.empty((T, Hq, D), dtype=q.dtype, device=q.device),
+                           lse=torch.empty((T, Hq), dtype=torch.float32, device=q.device))
+            if ws is None:
+                ws = _attention_workspace(
+                    chunk_attention_workspace_size(T, page_table.shape[0], Hq, k_pool.shape[1], D), q.device)
+    st = _m.chunk_attention(q, k_pool, v_pool, page_table, seq_len, q_start, scale, k_scale, v_scale, window, out["out"],
+                            out.get("lse"), ws, _raw_stream(stream), granted)
+    if st:
+        _check(st, "dspark_chunk_attention")
+    return out
+
+
+# ------------------------------------------------------------------- rotary positions
+
+def rotary_rates(rot_dim, base=10000.0, scaling="none", factor=1.0, original_len=None, low=1.0, high=32.0, factors=None,
+                 device="cuda") -> torch.Tensor:
+    """What rotary and cache_append take as the pairs' turns per position: int64 [rot_dim/2], units of
+    2^-64 turns, computed in float64 from f_i = base^(-2i/rot_dim) radians per position and
+
+      scaling="none"    f_i
+      scaling="linear"  f_i / factor (positions interpolated)
+      scaling="ntk"     base * factor^(rot_dim/(rot_dim-2)) in the place of base
+      scaling="bands"   f_i where a pair makes more than ``high`` turns within ``original_len``
+                        positions, f_i / factor where it makes fewer than ``low``, and a blend, linear
+                        in the turns, between
+      scaling="yarn"    the same with a blend linear in the pair's index (its magnitude is
+                        rotary_magnitude(factor))
+
+    ``factors`` [rot_dim/2], if given, divides the result pair by pair."""
+    if rot_dim < 2 or rot_dim % 2:
+        raise DSparkError(f"rot_dim={rot_dim} must be even and positive")
+    if not (base > 0 and math.isfinite(base) and factor > 0 and math.isfinite(factor)):
+        raise DSparkError("base and factor must be positive and finite")
+    if scaling not in ("none", "linear", "ntk", "bands", "yarn"):
+        raise DSparkError(f"scaling={scaling!r} must be none, linear, ntk, bands or yarn")
+    pairs = rot_dim // 2
+    if scaling == "ntk" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = [base ** (-2.0 * i / rot_dim) for i in range(pairs)]
+    if scaling == "linear":
+        f = [x / factor for x in f]
+    elif scaling in ("bands", "yarn"):
+        if original_len is None or original_len <= 0 or not 0 < low < high:
+            raise DSparkError(f"scaling={scaling!r} needs original_len > 0 and 0 < low < high")
+        if scaling == "bands":
+            kept = [min(1.0, max(0.0, (original_len * x / math.tau - low) / (high - low))) for x in f]
+        else:
+            if base <= 1:
+                raise DSparkError("scaling='yarn' needs base > 1")
+            index = lambda turns: rot_dim * math.log(original_len / (math.tau * turns)) / (2.0 * math.log(base))
+            first, last = max(0, math.floor(index(high))), min(rot_dim - 1, math.ceil(index(low)))
+            kept = [1.0 - min(1.0, max(0.0, (i - first) / max(last - first, 0.001))) for i in range(pairs)]
+        f = [x * (k + (1.0 - k) / factor) for x, k in zip(f, kept)]
+    if factors is not None:
+        factors = [float(x) for x in factors]
+        if len(factors) != pairs or not all(x > 0 and math.isfinite(x) for x in factors):
+            raise DSparkError(f"factors must hold {pairs} positive values")
+        f = [x / y for x, y in zip(f, factors)]
+    turns = [round(math.fmod(x / math.tau, 1.0) * 2.0 ** 64) % (1 << 64) for x in f]
+    return torch.tensor([t - (1 << 64) if t >= 1 << 63 else t for t in turns], dtype=torch.int64, device=device)
+
+
+def rotary_magnitude(factor) -> float:
+    """The magnitude that goes with scaling="yarn"."""
+    return 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+
+
+def _here(t, name):
+    if _current_device is not None and _on_gpu(t, name).get_device() != _current_device():
+        raise DSparkError(f"{name} lies on cuda:{t.get_device()}, the current device is cuda:{_current_device()}")
+    return t
+
+
+def rotary(x, positions, rates, interleaved=False, magnitude=1.0, inverse=False, out=None, stream=None):
+    """x [T,H,D] float32, bfloat16 or float16 with the first 2 * len(rates) elements of every head
+    turned by their row's position, positions [T] int32 (dspark_rotary); rates: rotary_rates(...).
+    Pairs are (i, i + rot_dim/2), or neighbours where ``interleaved``.  ``inverse`` turns back: the
+    gradient for x from the gradient for the result (no graph is recorded, whatever x requires).
+    ``out`` may be x itself."""
+    _here(x, "x")
+    if out is None:
+        with _made_on(stream):
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    st = _m.rotary(x, positions, rates, bool(interleaved), magnitude, bool(inverse), out, _raw_stream(stream))
+    if st:
+        _check(st, "dspark_rotary")
+    return out
+
+
+def cache_append(q, k, v, k_pool, v_pool, page_table, seq_len, q_start, rates, interleaved=False, magnitude=1.0,
+                 granted=None, k_scale=None, v_scale=None, q_out=None, ws=None, stream=None):
+    """cache_write with rotary positions on the way (dspark_cache_append): every slot's last tokens'
+    keys k [T,Hkv,D] are turned by their position in the slot and stored with the values, and their
+    queries q [T,Hq,D] turned into q_out (made where it is not given; q itself will do).  Returns
+    q_out; None where q is."""
+    _here(k, "k")
+    if ws is None or (q_out is None and q is not None):
+        with _made_on(stream):
+            if ws is None:
+                ws = workspace(256, k.device)
+            if q_out is None and q is not None:
+                q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    st = _m.cache_append(q, k, v, k_pool, v_pool, page_table, seq_len, q_start, rates, bool(interleaved), magnitude, granted,
+                         k_scale, v_scale, q_out, ws, _raw_stream(stream))
+    if st:
+        _check(st, "dspark_cache_append")
+    return q_out
+
+
+# --------------------------------------------------------------- adjustment of logits
+
+def adjust_logits(logits, tokens, q_start, history=None, history_len=None, prompt_len=None, repetition=None,
+                  frequency=None, presence=None, bias_ids=None, bias=None, mask=None, mask_row=None, out=None, stream=None):
+    """Logits [N,V] with penalties for repeated tokens, biases and grammar masks (dspark_adjust_logits).
+    Rows q_start[r] .. q_start[r+1]-1 are slot r's, each after the token tokens[n] that was fed in for
+    it: a row's sequence is history[r, :history_len[r]] and its block's tokens up to its own.
+    history [R,L] int32; prompt_len [R] int32; repetition, frequency, presence [R] float32;
+    bias_ids, bias [R,B] int32, float32; mask [M, (V+31)/32 or more] int32 of allowed ids' bits, row
+    mask_row[n] of it for row n (none where that is negative), or row n without mask_row.  What is
+    None is left out.  ``out`` may be the logits themselves.  Rows of no slot are not written (in a
+    result made here they hold anything)."""
+    _here(logits, "logits")
+    if out is None:
+        with _made_on(stream):
+            out = torch.empty_like(logits, memory_format=torch.contiguous_format)
+    st = _m.adjust_logits(logits, tokens, q_start, history, history_len, prompt_len, repetition, frequency, presence, bias_ids,
+                          bias, mask, mask_row, out, _raw_stream(stream))
+    if st:
+        _check(st, "dspark_adjust_logits")
+    return out
+
+
 class PagedCache:
     """A paged key-value cache: the tables of ``slots`` requests over ``num_pages`` pages, and
     the pools [layers, num_pages, Hkv, page_size, D] of keys and values.  Methods launch kernels
@@ -909,17 +1069,29 @@ class PagedCache:
                     granted=self.plan["granted"], k_scale=self.k_scale, v_scale=self.v_scale, ws=self.ws,
                     stream=stream)
 
+    def append(self, layer, q, k, v, q_start, rates, interleaved=False, magnitude=1.0, q_out=None, stream=None):
+        """``write`` with rotary positions on the way; returns the turned queries (cache_append)."""
+        return cache_append(q, k, v, self.k[layer], self.v[layer], self.page_table, self.seq_len, q_start, rates,
+                            interleaved=interleaved, magnitude=magnitude, granted=self.plan["granted"],
+                            k_scale=self.k_scale, v_scale=self.v_scale, q_out=q_out, ws=self.ws, stream=stream)
+
     def attend(self, layer, q, q_start, max_q, scale, window=0, out=None, stream=None):
-        """The scratch is made on the first call of a stream and a size class (heads and max_q decide
+        """Blocks of more than 128 queries a slot (max_q) go to chunk_attention.  The scratch is made on the first call of a stream and a size class (heads and max_q decide
         it, the number of rows does not) and kept: calls on one stream share it in order, calls on
         two streams never do.  Calls captured on one stream share theirs, and clear its status word:
         replays of graphs that do so must not overlap."""
         T, Hq, D = q.shape
-        n = paged_attention_workspace_size(T, self.seq_len.numel(), Hq, self.k.shape[2], D, max_q)
+        long = max_q > MAX_BLOCK
+        n = (chunk_attention_workspace_size(T, self.seq_len.numel(), Hq, self.k.shape[2], D) if long else
+             paged_attention_workspace_size(T, self.seq_len.numel(), Hq, self.k.shape[2], D, max_q))
         with _made_on(stream):
             key = (_raw_stream(None), torch.cuda.is_current_stream_capturing(), n)
             if key not in self._attention_ws:
                 self._attention_ws[key] = _attention_workspace(n, q.device)
+        if long:
+            return chunk_attention(q, self.k[layer], self.v[layer], self.page_table, self.seq_len, q_start, scale,
+                                   k_scale=self.k_scale, v_scale=self.v_scale, window=window, out=out,
+                                   ws=self._attention_ws[key], stream=stream, granted=self.not_refused)
         return paged_attention(q, self.k[layer], self.v[layer], self.page_table, self.seq_len, q_start, max_q, scale,
                                k_scale=self.k_scale, v_scale=self.v_scale, window=window, out=out,
                                ws=self._attention_ws[key], stream=stream, granted=self.not_refused)

@@ -27,14 +27,21 @@ const char* name_of(at::ScalarType t) {
     case at::kBFloat16: return "torch.bfloat16";
     case at::kHalf: return "torch.float16";
     case at::kInt: return "torch.int32";
+    case at::kLong: return "torch.int64";
     case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
     default: return c10::toString(t);
   }
 }
 
+thread_local int g_device = -1;  // of the call's tensors
+
 const at::Tensor& cuda(PyObject* o, const char* name) {
   if (!THPVariable_Check(o) || !THPVariable_Unpack(o).is_cuda()) refuse(std::string(name) + " must be a CUDA tensor");
-  return THPVariable_Unpack(o);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  const int at = t.get_device();
+  if (g_device < 0) g_device = at;
+  else if (at != g_device) refuse(std::string(name) + " lies on another device than the other tensors");
+  return t;
 }
 void typed(const at::Tensor& t, const char* name, at::ScalarType type) {
   if (t.scalar_type() != type) refuse(std::string(name) + " must be " + name_of(type) + ", got " + name_of(t.scalar_type()));
@@ -90,11 +97,11 @@ Rows rows(PyObject* o, const char* name) {
   else if (stride < m) refuse("the rows of " + std::string(name) + " overlap");
   return {const_cast<void*>(t.const_data_ptr()), to_int(n, name), to_int(m, name), stride, t.scalar_type()};
 }
-int logit_type(at::ScalarType t) {
+int logit_type(at::ScalarType t, const char* name = "logits") {
   if (t == at::kFloat) return DSPARK_F32;
   if (t == at::kBFloat16) return DSPARK_BF16;
   if (t == at::kHalf) return DSPARK_F16;
-  refuse(std::string("logits must be float32, bfloat16 or float16, got ") + name_of(t));
+  refuse(std::string(name) + " must be float32, bfloat16 or float16, got " + name_of(t));
 }
 int cache_type(at::ScalarType t) {
   if (t == at::kBFloat16) return DSPARK_BF16;
@@ -272,6 +279,108 @@ int paged_attention(PyObject* const* a) {
       address(a[14]));
 }
 
+// (q, k_pool, v_pool, page_table, seq_len, q_start, scale, k_scale, v_scale, window, out, lse, ws, stream, granted)
+int chunk_attention(PyObject* const* a) {
+  const Pools p = pools(a[1], a[2]);
+  const int64_t H = p.size[1], D = p.size[3];
+  const TokenRows q = token_rows(a[0], "q", -1, D);
+  const Rows t = page_table(a[3]);
+  const Workspace w = workspace(a[12]);
+  return dspark_chunk_attention(
+      to_int(q.T, "q"), t.n, to_int(q.heads, "Hq"), to_int(H, "Hkv"), to_int(D, "D"), to_int(p.size[0], "num_pages"),
+      to_int(p.size[2], "page_size"), t.m, cache_type(q.type), p.type, q.p, q.token, q.head, p.k, p.v, p.stride[0], p.stride[1],
+      p.stride[2], static_cast<int32_t*>(t.p), t.stride, flat<int32_t>(a[4], "seq_len", at::kInt, t.n),
+      flat<int32_t>(a[5], "q_start", at::kInt, (int64_t)t.n + 1), flat_or_null<int32_t>(a[14], "granted", at::kInt, t.n),
+      (float)number(a[6]), flat_or_null<float>(a[7], "k_scale", at::kFloat, H), flat_or_null<float>(a[8], "v_scale", at::kFloat, H),
+      integer(a[9], "window"), flat(a[10], "out", q.type, q.T * q.heads * D),
+      flat_or_null<float>(a[11], "lse", at::kFloat, q.T * q.heads), w.p, w.bytes, address(a[13]));
+}
+
+// A CUDA tensor [T, heads, D] of any strides but the last.
+TokenRows head_rows(PyObject* o, const char* name) {
+  const at::Tensor& t = cuda(o, name);
+  if (t.dim() != 3 || (t.size(2) > 1 && t.stride(2) != 1)) refuse(std::string(name) + " must be [T, heads, D] with contiguous rows");
+  return {const_cast<void*>(t.const_data_ptr()), t.size(0), t.size(1), t.size(0) > 1 ? t.stride(0) : 0,
+          t.size(1) > 1 ? t.stride(1) : 0, t.scalar_type()};
+}
+int rotating(PyObject* rates) {
+  const at::Tensor& t = cuda(rates, "rates");
+  if (t.dim() != 1) refuse("rates must be 1-D, one for each pair");
+  return to_int(2 * t.size(0), "rates");
+}
+
+// (x, positions, rates, interleaved, magnitude, inverse, out, stream)
+int rotary(PyObject* const* a) {
+  const TokenRows x = head_rows(a[0], "x"), y = head_rows(a[6], "out");
+  const int64_t D = THPVariable_Unpack(a[0]).size(2);
+  if (y.type != x.type || y.T != x.T || y.heads != x.heads || THPVariable_Unpack(a[6]).size(2) != D)
+    refuse("out must have the shape and type of x");
+  const int rot = rotating(a[2]);
+  return dspark_rotary(to_int(x.T, "x"), to_int(x.heads, "x"), to_int(D, "D"), rot, logit_type(x.type, "x"),
+                       integer(a[3], "interleaved"), integer(a[5], "inverse"), x.p, x.token, x.head,
+                       flat<int32_t>(a[1], "positions", at::kInt, x.T), flat<int64_t>(a[2], "rates", at::kLong, rot / 2),
+                       (float)number(a[4]), y.p, y.token, y.head, address(a[7]));
+}
+
+// (q, k, v, k_pool, v_pool, page_table, seq_len, q_start, rates, interleaved, magnitude, granted, k_scale, v_scale, q_out,
+//  ws, stream)
+int cache_append(PyObject* const* a) {
+  const Pools p = pools(a[3], a[4]);
+  const int64_t H = p.size[1], D = p.size[3];
+  const TokenRows k = token_rows(a[1], "k", H, D), v = token_rows(a[2], "v", H, D);
+  if (k.type != v.type || k.T != v.T || k.token != v.token || k.head != v.head)
+    refuse("k and v must share their type, shape and strides");
+  TokenRows q = {}, y = {};
+  if (a[0] != Py_None) {
+    q = token_rows(a[0], "q", -1, D), y = token_rows(a[14], "q_out", q.heads, D);
+    if (q.type != k.type || q.T != k.T) refuse("q must have as many tokens as k, and its type");
+    if (y.type != q.type || y.T != q.T) refuse("q_out must have the shape and type of q");
+    if (q.heads < 1) refuse("q must have a head");
+  }
+  const Rows t = page_table(a[5]);
+  const Workspace w = workspace(a[15]);
+  const int rot = rotating(a[8]);
+  return dspark_cache_append(
+      to_int(k.T, "k"), t.n, to_int(q.heads, "Hq"), to_int(H, "Hkv"), to_int(D, "D"), rot, integer(a[9], "interleaved"),
+      to_int(p.size[0], "num_pages"), to_int(p.size[2], "page_size"), t.m, cache_type(k.type), p.type, q.p, q.token, q.head, k.p,
+      v.p, k.token, k.head, y.p, y.token, y.head, p.k, p.v, p.stride[0], p.stride[1], p.stride[2], static_cast<int32_t*>(t.p),
+      t.stride, flat<int32_t>(a[6], "seq_len", at::kInt, t.n), flat<int32_t>(a[7], "q_start", at::kInt, (int64_t)t.n + 1),
+      flat_or_null<int32_t>(a[11], "granted", at::kInt, t.n), flat_or_null<float>(a[12], "k_scale", at::kFloat, H),
+      flat_or_null<float>(a[13], "v_scale", at::kFloat, H), flat<int64_t>(a[8], "rates", at::kLong, rot / 2),
+      (float)number(a[10]), w.p, w.bytes, address(a[16]));
+}
+
+// (logits, tokens, q_start, history, history_len, prompt_len, repetition, frequency, presence, bias_ids, bias, mask,
+//  mask_row, out, stream)
+int adjust_logits(PyObject* const* a) {
+  const Rows x = rows(a[0], "logits"), y = rows(a[13], "out");
+  if (y.type != x.type || y.n != x.n || y.m != x.m) refuse("out must have the logits' shape and type");
+  const int64_t R = cuda(a[2], "q_start").numel() - 1;
+  Rows h = {}, b = {}, m = {};
+  if (a[3] != Py_None) {
+    h = rows(a[3], "history");
+    if (h.type != at::kInt || h.n != R) refuse("history must be torch.int32, a row for each of the " + std::to_string(R) + " slots");
+  }
+  if (a[9] != Py_None) {
+    b = rows(a[9], "bias_ids");
+    if (b.n != R) refuse("bias_ids must have a row for each of the " + std::to_string(R) + " slots");
+  }
+  if (a[11] != Py_None) {
+    m = rows(a[11], "mask");
+    if (m.type != at::kInt || m.m < (x.m + 31) / 32)
+      refuse("mask must be torch.int32 with at least " + std::to_string((x.m + 31) / 32) + " words a row");
+  }
+  const int64_t nb = R * (int64_t)b.m;
+  return dspark_adjust_logits(
+      x.n, x.m, to_int(R, "q_start"), logit_type(x.type), x.p, x.stride, flat_or_null<int32_t>(a[1], "tokens", at::kInt, x.n),
+      flat<int32_t>(a[2], "q_start", at::kInt, -1), static_cast<int32_t*>(h.p), h.stride, h.m,
+      flat_or_null<int32_t>(a[4], "history_len", at::kInt, R), flat_or_null<int32_t>(a[5], "prompt_len", at::kInt, R),
+      flat_or_null<float>(a[6], "repetition", at::kFloat, R), flat_or_null<float>(a[7], "frequency", at::kFloat, R),
+      flat_or_null<float>(a[8], "presence", at::kFloat, R), b.m, flat_or_null<int32_t>(a[9], "bias_ids", at::kInt, nb),
+      flat_or_null<float>(a[10], "bias", at::kFloat, nb), static_cast<uint32_t*>(m.p), m.stride, m.n,
+      flat_or_null<int32_t>(a[12], "mask_row", at::kInt, x.n), y.p, y.stride, address(a[14]));
+}
+
 // A Python function of N positional arguments around F.
 template <int (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -279,6 +388,7 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     PyErr_Format(PyExc_TypeError, "%d arguments are wanted, got %zd", N, n);
     return nullptr;
   }
+  g_device = -1;
   try {
     const int status = F(args);
     return PyErr_Occurred() ? nullptr : PyLong_FromLong(status);
@@ -310,6 +420,10 @@ PyMethodDef g_methods[] = {
     method<cache_truncate, 7>("cache_truncate"),
     method<cache_compact, 10>("cache_compact"),
     method<paged_attention, 16>("paged_attention"),
+    method<chunk_attention, 15>("chunk_attention"),
+    method<rotary, 8>("rotary"),
+    method<cache_append, 17>("cache_append"),
+    method<adjust_logits, 15>("adjust_logits"),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

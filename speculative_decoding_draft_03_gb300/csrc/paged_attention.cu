@@ -585,9 +585,17 @@ size_t paged_attention_scratch(int, int, int Hq, int Hkv, int D, int max_q) {
                   attention_wide_scratch(Hq, Hkv, D, max_q));
 }
 
+size_t attention_rows_scratch(int Hq, int Hkv, int D) {
+  return scratch_bytes(kMaxWorkers, 8 * groups(D, kMaxQueries, Hq / Hkv), padded(D, true));
+}
+
 cudaError_t launch_paged_attention(const AttentionArgs& a, void* scratch, cudaStream_t s) {
   cudaError_t e;
   if (a.max_q * a.G > kWideRows && launch_attention_wide(a, scratch, s, e)) return e;
+  return launch_attention_rows(a, scratch, s);
+}
+
+cudaError_t launch_attention_rows(const AttentionArgs& a, void* scratch, cudaStream_t s) {
   const bool q8 = a.dtype_kv == DSPARK_E4M3;
   if (a.dtype_q == DSPARK_BF16) return q8 ? launch<true, true>(a, scratch, s) : launch<true, false>(a, scratch, s);
   return q8 ? launch<false, true>(a, scratch, s) : launch<false, false>(a, scratch, s);

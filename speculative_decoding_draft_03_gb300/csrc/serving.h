@@ -1,5 +1,6 @@
 // serving.h — argument blocks and launcher declarations of the serving-side operators
-// (token log probabilities, the paged cache, attention over it).
+// (token log probabilities, the paged cache, attention over it, rotary positions, the adjustment of
+// logits).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -114,5 +115,79 @@ struct AttentionArgs {
 constexpr int kMaxQueries = 128;
 size_t paged_attention_scratch(int T, int R, int Hq, int Hkv, int D, int max_q);
 cudaError_t launch_paged_attention(const AttentionArgs& a, void* scratch, cudaStream_t s);
+
+
+// Attention of a block of any length: the products of chunk_attention.cu where the shape allows them,
+// else the kernel that takes every shape.
+size_t chunk_attention_scratch(int Hq, int Hkv, int D);
+cudaError_t launch_chunk_attention(const AttentionArgs& a, void* scratch, cudaStream_t s);
+// (of paged_attention.cu: by 16 or 32 query rows, whatever the shape)
+size_t attention_rows_scratch(int Hq, int Hkv, int D);
+cudaError_t launch_attention_rows(const AttentionArgs& a, void* scratch, cudaStream_t s);
+
+constexpr int kMaxRotaryDim = 1024;
+
+struct RotaryArgs {
+  int T, H, D, rot, dtype, interleaved, inverse;
+  const void* x;
+  int64_t x_token, x_head;
+  const int32_t* positions;
+  const int64_t* rates;
+  float magnitude;
+  void* out;
+  int64_t out_token, out_head;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t s);
+
+struct AppendArgs {
+  int T, R, Hq, Hkv, D, rot, interleaved, num_pages, page_size, max_pages, dtype_in, dtype_kv;
+  const void* q;  // null with Hq = 0
+  int64_t q_token, q_head;
+  const void* k;
+  const void* v;
+  int64_t in_token, in_head;
+  void* q_out;
+  int64_t q_out_token, q_out_head;
+  void* k_pool;
+  void* v_pool;
+  int64_t page_stride, head_stride, token_stride;
+  const int32_t* page_table;
+  int64_t table_stride;
+  const int32_t* seq_len;
+  const int32_t* q_start;
+  const int32_t* granted;
+  const float* k_scale;
+  const float* v_scale;
+  const int64_t* rates;
+  float magnitude;
+  DeviceStatus* status;
+};
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s);
+
+struct AdjustArgs {
+  int N, V, R, dtype;
+  const void* logits;
+  int64_t row_stride;
+  const int32_t* tokens;
+  const int32_t* q_start;
+  const int32_t* history;
+  int64_t history_stride;
+  int history_width;
+  const int32_t* history_len;
+  const int32_t* prompt_len;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  int n_bias;
+  const int32_t* bias_ids;
+  const float* bias;
+  const uint32_t* mask;
+  int64_t mask_stride;
+  int mask_rows;
+  const int32_t* mask_row;
+  void* out;
+  int64_t out_stride;
+};
+cudaError_t launch_adjust_logits(const AdjustArgs& a, cudaStream_t s);
 
 }  // namespace dspark

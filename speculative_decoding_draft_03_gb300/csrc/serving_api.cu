@@ -160,6 +160,30 @@ dspark_status check_strided(const void* p, int64_t stride_token, int64_t stride_
   return DSPARK_OK;
 }
 
+// What both attention calls ask of their arguments (but for the bound of the queries).
+dspark_status check_attention(int T, int R, int Hq, int Hkv, int D, int num_pages, int page_size, int max_pages,
+                              int64_t table_stride, int window, float scale) {
+  CHECK(check_geometry(R, num_pages, page_size, max_pages, table_stride));
+  if (T < 0 || Hq < 1 || Hkv < 1 || window < 0)
+    return fail(DSPARK_INVALID_ARG, "sizes must be positive (T=%d Hq=%d Hkv=%d window=%d)", T, Hq, Hkv, window);
+  if (Hq % Hkv != 0) return fail(DSPARK_INVALID_ARG, "Hq=%d must be a multiple of Hkv=%d", Hq, Hkv);
+  if (Hq / Hkv > 64) return fail(DSPARK_UNSUPPORTED_SHAPE, "Hq / Hkv = %d exceeds 64", Hq / Hkv);
+  if ((int64_t)T * Hq > INT32_MAX) return fail(DSPARK_UNSUPPORTED_SHAPE, "T * Hq must be below 2^31");
+  if (!isfinite(scale)) return fail(DSPARK_INVALID_ARG, "scale must be finite");
+  return DSPARK_OK;
+}
+
+// --------------------------------------------------------------------------- rotary positions
+
+dspark_status check_turn(int D, int rot_dim, int interleaved, const int64_t* rates, float magnitude) {
+  if (rot_dim < 2 || rot_dim > D || rot_dim % 2 != 0)
+    return fail(DSPARK_INVALID_ARG, "rot_dim=%d must be even and lie in 2..D=%d", rot_dim, D);
+  if (interleaved != 0 && interleaved != 1) return fail(DSPARK_INVALID_ARG, "interleaved=%d must be 0 or 1", interleaved);
+  CHECK_PTR(rates);
+  if (!isfinite(magnitude)) return fail(DSPARK_INVALID_ARG, "magnitude must be finite");
+  return DSPARK_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -339,16 +363,10 @@ dspark_status dspark_paged_attention_granted(int T, int R, int Hq, int Hkv, int 
                                              float scale, const float* k_scale, const float* v_scale, int window,
                                              void* out, float* lse_out, void* workspace, size_t ws_bytes,
                                              void* stream) {
-  CHECK(check_geometry(R, num_pages, page_size, max_pages, table_stride));
-  if (T < 0 || Hq < 1 || Hkv < 1 || window < 0)
-    return fail(DSPARK_INVALID_ARG, "sizes must be positive (T=%d Hq=%d Hkv=%d window=%d)", T, Hq, Hkv, window);
-  if (Hq % Hkv != 0) return fail(DSPARK_INVALID_ARG, "Hq=%d must be a multiple of Hkv=%d", Hq, Hkv);
-  if (Hq / Hkv > 64) return fail(DSPARK_UNSUPPORTED_SHAPE, "Hq / Hkv = %d exceeds 64", Hq / Hkv);
-  if ((int64_t)T * Hq > INT32_MAX) return fail(DSPARK_UNSUPPORTED_SHAPE, "T * Hq must be below 2^31");
+  CHECK(check_attention(T, R, Hq, Hkv, D, num_pages, page_size, max_pages, table_stride, window, scale));
   if (max_q < 1) return fail(DSPARK_INVALID_ARG, "max_q=%d must be positive", max_q);
   if (max_q > dspark::kMaxQueries)
     return fail(DSPARK_UNSUPPORTED_SHAPE, "max_q=%d exceeds %d", max_q, dspark::kMaxQueries);
-  if (!isfinite(scale)) return fail(DSPARK_INVALID_ARG, "scale must be finite");
   CHECK(check_rows(D, dtype_q, dtype_kv, k_pool, v_pool, page_stride, head_stride, token_stride, k_scale, v_scale));
   CHECK_PTR(page_table);
   CHECK_PTR(seq_len);
@@ -372,6 +390,170 @@ dspark_status dspark_paged_attention_granted(int T, int R, int Hq, int Hkv, int 
   return launched(dspark::launch_paged_attention(a, static_cast<unsigned char*>(workspace) + 256,
                                                  static_cast<cudaStream_t>(stream)),
                   "paged_attention");
+}
+
+size_t dspark_chunk_attention_workspace_size(int T, int R, int Hq, int Hkv, int D) {
+  if (T < 0 || R < 1 || R > dspark::kMaxSlots || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > 64 || D < 16 ||
+      D > 256 || D % 16 != 0)
+    return 0;
+  return 256 + dspark::chunk_attention_scratch(Hq, Hkv, D);
+}
+
+dspark_status dspark_chunk_attention(int T, int R, int Hq, int Hkv, int D, int num_pages, int page_size, int max_pages,
+                                     int dtype_q, int dtype_kv, const void* q, int64_t q_stride_token,
+                                     int64_t q_stride_head, const void* k_pool, const void* v_pool, int64_t page_stride,
+                                     int64_t head_stride, int64_t token_stride, const int32_t* page_table,
+                                     int64_t table_stride, const int32_t* seq_len, const int32_t* q_start,
+                                     const int32_t* granted, float scale, const float* k_scale, const float* v_scale,
+                                     int window, void* out, float* lse_out, void* workspace, size_t ws_bytes,
+                                     void* stream) {
+  CHECK(check_attention(T, R, Hq, Hkv, D, num_pages, page_size, max_pages, table_stride, window, scale));
+  CHECK(check_rows(D, dtype_q, dtype_kv, k_pool, v_pool, page_stride, head_stride, token_stride, k_scale, v_scale));
+  CHECK_PTR(page_table);
+  CHECK_PTR(seq_len);
+  CHECK_PTR(q_start);
+  CHECK(check_workspace(workspace, ws_bytes, dspark_chunk_attention_workspace_size(T, R, Hq, Hkv, D)));
+  if (T == 0) return DSPARK_OK;
+  CHECK_PTR(q);
+  CHECK_PTR(out);
+  CHECK_ALIGN(out, 16);
+  CHECK(check_strided(q, q_stride_token, q_stride_head, "q"));
+  dspark::AttentionArgs a = {};
+  a.T = T; a.R = R; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.D = D; a.num_pages = num_pages;
+  a.page_size = page_size; a.max_pages = max_pages; a.max_q = T; a.dtype_q = dtype_q; a.dtype_kv = dtype_kv; a.q = q;
+  a.q_stride_token = q_stride_token; a.q_stride_head = q_stride_head; a.k_pool = k_pool; a.v_pool = v_pool;
+  a.page_stride = page_stride; a.head_stride = head_stride; a.token_stride = token_stride;
+  a.page_table = page_table; a.table_stride = table_stride; a.seq_len = seq_len; a.q_start = q_start;
+  a.granted = granted; a.scale = scale; a.k_scale = k_scale; a.v_scale = v_scale; a.out = out; a.lse_out = lse_out;
+  a.window = window < (int64_t)max_pages * page_size ? window : 0;  // (as above)
+  a.status = static_cast<dspark::DeviceStatus*>(workspace);
+  return launched(dspark::launch_chunk_attention(a, static_cast<unsigned char*>(workspace) + 256,
+                                                 static_cast<cudaStream_t>(stream)),
+                  "chunk_attention");
+}
+
+dspark_status dspark_rotary(int T, int H, int D, int rot_dim, int dtype, int interleaved, int inverse, const void* x,
+                            int64_t x_stride_token, int64_t x_stride_head, const int32_t* positions,
+                            const int64_t* rates, float magnitude, void* out, int64_t out_stride_token,
+                            int64_t out_stride_head, void* stream) {
+  if (T < 0 || H < 1 || D < 1) return fail(DSPARK_INVALID_ARG, "sizes must be positive (T=%d H=%d D=%d)", T, H, D);
+  if (!is_float_type(dtype)) return fail(DSPARK_INVALID_ARG, "bad dtype %d", dtype);
+  CHECK(check_turn(D, rot_dim, interleaved, rates, magnitude));
+  if (inverse != 0 && inverse != 1) return fail(DSPARK_INVALID_ARG, "inverse=%d must be 0 or 1", inverse);
+  if (D > dspark::kMaxRotaryDim)
+    return fail(DSPARK_UNSUPPORTED_SHAPE, "D=%d exceeds %d", D, dspark::kMaxRotaryDim);
+  if ((int64_t)H * D > (1 << 26)) return fail(DSPARK_UNSUPPORTED_SHAPE, "H * D must be at most 2^26");
+  if (x_stride_token < 0 || x_stride_head < 0 || out_stride_token < 0 || out_stride_head < 0)
+    return fail(DSPARK_INVALID_ARG, "strides must not be negative");
+  if ((out_stride_token < D && T > 1) || (out_stride_head < D && H > 1))
+    return fail(DSPARK_INVALID_ARG, "rows of out must not lie on one another");
+  if (T == 0) return DSPARK_OK;
+  CHECK_PTR(x);
+  CHECK_PTR(positions);
+  CHECK_PTR(out);
+  CHECK_ALIGN(x, size_of(dtype));
+  CHECK_ALIGN(out, size_of(dtype));
+  if (out == x && ((T > 1 && out_stride_token != x_stride_token) || (H > 1 && out_stride_head != x_stride_head)))
+    return fail(DSPARK_INVALID_ARG, "a result in the place of x has the strides of x");
+  const dspark::RotaryArgs a = {T, H, D, rot_dim, dtype, interleaved, inverse, x, x_stride_token, x_stride_head, positions,
+                                rates, magnitude, out, out_stride_token, out_stride_head};
+  return launched(dspark::launch_rotary(a, static_cast<cudaStream_t>(stream)), "rotary");
+}
+
+dspark_status dspark_cache_append(int T, int R, int Hq, int Hkv, int D, int rot_dim, int interleaved, int num_pages,
+                                  int page_size, int max_pages, int dtype_in, int dtype_kv, const void* q,
+                                  int64_t q_stride_token, int64_t q_stride_head, const void* k, const void* v,
+                                  int64_t in_stride_token, int64_t in_stride_head, void* q_out,
+                                  int64_t q_out_stride_token, int64_t q_out_stride_head, void* k_pool, void* v_pool,
+                                  int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                                  const int32_t* page_table, int64_t table_stride, const int32_t* seq_len,
+                                  const int32_t* q_start, const int32_t* granted, const float* k_scale,
+                                  const float* v_scale, const int64_t* rates, float magnitude, void* workspace,
+                                  size_t ws_bytes, void* stream) {
+  CHECK(check_geometry(R, num_pages, page_size, max_pages, table_stride));
+  if (T < 0 || Hq < 0 || Hkv < 1)
+    return fail(DSPARK_INVALID_ARG, "sizes must be positive (T=%d Hq=%d Hkv=%d)", T, Hq, Hkv);
+  CHECK(check_rows(D, dtype_in, dtype_kv, k_pool, v_pool, page_stride, head_stride, token_stride, k_scale, v_scale));
+  CHECK(check_turn(D, rot_dim, interleaved, rates, magnitude));
+  if (rot_dim % 16 != 0) return fail(DSPARK_UNSUPPORTED_SHAPE, "rot_dim=%d must be a multiple of 16", rot_dim);
+  if (((int64_t)Hq + 2 * (int64_t)Hkv) * D > (1 << 26))
+    return fail(DSPARK_UNSUPPORTED_SHAPE, "(Hq + 2 Hkv) * D must be at most 2^26");
+  if ((page_stride == 0 && num_pages > 1) || (head_stride == 0 && Hkv > 1) || (token_stride == 0 && page_size > 1))
+    return fail(DSPARK_INVALID_ARG, "rows of a pool that is written to must not lie on one another");
+  CHECK_PTR(page_table);
+  CHECK_PTR(seq_len);
+  CHECK_PTR(q_start);
+  CHECK(check_workspace(workspace, ws_bytes, 256));
+  if (T == 0) return DSPARK_OK;
+  CHECK_PTR(k);
+  CHECK_PTR(v);
+  CHECK(check_strided(k, in_stride_token, in_stride_head, "k"));
+  CHECK(check_strided(v, in_stride_token, in_stride_head, "v"));
+  if (Hq > 0) {
+    CHECK_PTR(q);
+    CHECK_PTR(q_out);
+    CHECK(check_strided(q, q_stride_token, q_stride_head, "q"));
+    CHECK(check_strided(q_out, q_out_stride_token, q_out_stride_head, "q_out"));
+    if ((q_out_stride_token < D && T > 1) || (q_out_stride_head < D && Hq > 1))
+      return fail(DSPARK_INVALID_ARG, "rows of q_out must not lie on one another");
+    if (q_out == q && ((T > 1 && q_out_stride_token != q_stride_token) || (Hq > 1 && q_out_stride_head != q_stride_head)))
+      return fail(DSPARK_INVALID_ARG, "queries turned in place have the strides of q");
+  }
+  dspark::AppendArgs a = {};
+  a.T = T; a.R = R; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.rot = rot_dim; a.interleaved = interleaved;
+  a.num_pages = num_pages; a.page_size = page_size; a.max_pages = max_pages; a.dtype_in = dtype_in; a.dtype_kv = dtype_kv;
+  a.q = q; a.q_token = q_stride_token; a.q_head = q_stride_head; a.k = k; a.v = v; a.in_token = in_stride_token;
+  a.in_head = in_stride_head; a.q_out = q_out; a.q_out_token = q_out_stride_token; a.q_out_head = q_out_stride_head;
+  a.k_pool = k_pool; a.v_pool = v_pool; a.page_stride = page_stride; a.head_stride = head_stride;
+  a.token_stride = token_stride; a.page_table = page_table; a.table_stride = table_stride; a.seq_len = seq_len;
+  a.q_start = q_start; a.granted = granted; a.k_scale = k_scale; a.v_scale = v_scale; a.rates = rates;
+  a.magnitude = magnitude; a.status = static_cast<dspark::DeviceStatus*>(workspace);
+  return launched(dspark::launch_cache_append(a, static_cast<cudaStream_t>(stream)), "cache_append");
+}
+
+dspark_status dspark_adjust_logits(int N, int V, int R, int dtype, const void* logits, int64_t row_stride,
+                                   const int32_t* tokens, const int32_t* q_start, const int32_t* history,
+                                   int64_t history_stride, int history_width, const int32_t* history_len,
+                                   const int32_t* prompt_len, const float* repetition, const float* frequency,
+                                   const float* presence, int n_bias, const int32_t* bias_ids, const float* bias,
+                                   const uint32_t* mask, int64_t mask_stride, int mask_rows, const int32_t* mask_row,
+                                   void* out, int64_t out_stride, void* stream) {
+  if (N < 0 || V < 1 || R < 1) return fail(DSPARK_INVALID_ARG, "sizes must be positive (N=%d V=%d R=%d)", N, V, R);
+  if (V > dspark::kMaxLogprobV) return fail(DSPARK_UNSUPPORTED_SHAPE, "V=%d exceeds %d", V, dspark::kMaxLogprobV);
+  if (R > dspark::kMaxSlots) return fail(DSPARK_UNSUPPORTED_SHAPE, "R=%d exceeds %d", R, dspark::kMaxSlots);
+  if (!is_float_type(dtype)) return fail(DSPARK_INVALID_ARG, "bad dtype %d", dtype);
+  if (row_stride < V) return fail(DSPARK_INVALID_ARG, "row_stride %lld is below V=%d", (long long)row_stride, V);
+  if (out_stride < V) return fail(DSPARK_INVALID_ARG, "out_stride %lld is below V=%d", (long long)out_stride, V);
+  if (history != nullptr) {
+    if (history_width < 0 || history_stride < history_width)
+      return fail(DSPARK_INVALID_ARG, "history_stride %lld is below history_width=%d", (long long)history_stride, history_width);
+    CHECK_PTR(history_len);
+  }
+  if (n_bias < 0) return fail(DSPARK_INVALID_ARG, "n_bias=%d is negative", n_bias);
+  if (n_bias > 0) {
+    CHECK_PTR(bias_ids);
+    CHECK_PTR(bias);
+  }
+  if (mask != nullptr) {
+    if (mask_rows < 0 || mask_stride < (V + 31) / 32)
+      return fail(DSPARK_INVALID_ARG, "a mask has mask_rows=%d rows of at least %d words", mask_rows, (V + 31) / 32);
+    if (mask_row == nullptr && mask_rows < N)
+      return fail(DSPARK_INVALID_ARG, "without mask_row there is a mask row for each of the %d rows, got %d", N, mask_rows);
+  } else if (mask_row != nullptr) {
+    return fail(DSPARK_INVALID_ARG, "mask_row goes with a mask");
+  }
+  if (N == 0) return DSPARK_OK;
+  CHECK_PTR(logits);
+  CHECK_ALIGN(logits, size_of(dtype));
+  CHECK_PTR(q_start);
+  CHECK_PTR(out);
+  CHECK_ALIGN(out, size_of(dtype));
+  if (out == logits && out_stride != row_stride)
+    return fail(DSPARK_INVALID_ARG, "a result in the logits' place has the logits' row stride");
+  const dspark::AdjustArgs a = {N, V, R, dtype, logits, row_stride, tokens, q_start, history, history_stride, history_width,
+                                history_len, prompt_len, repetition, frequency, presence, n_bias, bias_ids, bias, mask,
+                                mask_stride, mask_rows, mask_row, out, out_stride};
+  return launched(dspark::launch_adjust_logits(a, static_cast<cudaStream_t>(stream)), "adjust_logits");
 }
 
 }  // extern "C"
