@@ -1,12 +1,796 @@
-// chunk_attention.cu — attention of long blocks of queries (a chunk of a prompt) over a paged cache.
-#include "serving.cuh"
+// chunk_attention.cu — attention of long blocks of queries (a chunk of a prompt) over a paged cache, on
+// the 5th-generation tensor cores.
+//
+// A block of n queries does 4 D G n flops per seen key, so from some hundred queries on the products
+// bound it, not the cache.  Here the query rows are the 128 rows of the products and the tokens their
+// columns:
+//   S [128 rows x 128 tokens] = Q . K^T      (both K-major, in shared memory)
+//   O [128 rows x D]         += P . V        (P from tensor memory, where it takes S's place; V MN-major)
+//   * Rows are a request's queries, token by token with the G heads of a cache head side by side, so that
+//     heads share every key and value and a block's diagonal is narrow.  An item is 256 rows: two row
+//     tiles A and B that share the copied keys and values, one in its softmax while the other's products
+//     run.
+//   * A softmax thread owns a row: maximum, sum and reference stay in its registers and no thread waits
+//     for another.  The reference moves only when a score passes it by 2^kSlack (any reference is right;
+//     the weights stay inside their type's range); only then is O rescaled, by the warp that needs it.
+//   * One persistent CTA per SM.  Warps 0 and 2 copy keys and values by page boxes (tensor copies), warp
+//     1 issues the products, eight warps (two groups) do the softmax.  Values of tiles at the diagonal, at
+//     a window's edge or at the context's end pass warp 3 first, which clears what no row of the item
+//     sees, and what only some see if it is not finite (0 x NaN); the rows that see such a token add it
+//     on their own.
+//   * An e4m3 cache is copied as it is; four more warps turn each tile into fp16 (which holds every e4m3
+//     value), and look at the values as warp 3 does otherwise.  bf16 query rows are scaled by powers of
+//     two into fp16's range.
+//   * The work is dealt out in tiles of 128 tokens that an item sees, evenly over the CTAs; items that
+//     several share are joined by a second kernel, in a fixed order.
+// Every mbarrier wait is bounded; a wait that gives up reports DSPARK_TIMEOUT and the CTA winds down.
+#include <algorithm>
+
+#include "attention_tc.cuh"
 
 namespace dspark {
+namespace {
 
-size_t chunk_attention_scratch(int Hq, int Hkv, int D) { return attention_rows_scratch(Hq, Hkv, D); }
+using namespace attention;
+
+constexpr int kRowsOf = 128;           // a row tile
+constexpr int kItem = 2 * kRowsOf;     // an item
+constexpr int kGroupThreads = 128;     // of a softmax group
+
+// ---------------------------------------------------------------------------- wrappers
+
+// A (the weights) from tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(desc), "r"(accumulate)
+      : "memory");
+}
+#define R8(x, i) "=f"(x[i]), "=f"(x[i + 1]), "=f"(x[i + 2]), "=f"(x[i + 3]), "=f"(x[i + 4]), "=f"(x[i + 5]), "=f"(x[i + 6]), "=f"(x[i + 7])
+// 32 columns of this warp's lanes.
+__device__ __forceinline__ void tmem_load32(uint32_t at, float* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+      "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+      : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)
+      : "r"(at)
+      : "memory");
+}
+// 128 columns: a tile's scores.
+__device__ __forceinline__ void tmem_load128(uint32_t at, float* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24), R8(x, 32), R8(x, 40), R8(x, 48), R8(x, 56), R8(x, 64), R8(x, 72), R8(x, 80),
+        R8(x, 88), R8(x, 96), R8(x, 104), R8(x, 112), R8(x, 120)
+      : "r"(at), "r"(at + 32), "r"(at + 64), "r"(at + 96)
+      : "memory");
+}
+#undef R8
+__device__ __forceinline__ float tmem_load1(uint32_t at) {
+  float x;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=f"(x) : "r"(at) : "memory");
+  return x;
+}
+// 16 packed columns (32 weights).
+__device__ __forceinline__ void tmem_store_u16(uint32_t at, const uint32_t* x) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]), "r"(x[10]),
+      "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15])
+      : "memory");
+}
+struct Two {
+  unsigned long long v;
+};
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void apart(Two x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v)); }
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
+// ------------------------------------------------------------------------------- the plan
+
+// The tiles that a block of rows (an item without its head) sees.
+struct Block {
+  int first, tiles;       // first: position of the first tile's first token
+  int last0, last1;       // last position that the first and the last row see (below 0: nothing)
+};
+__device__ __forceinline__ Block block_of(const AttentionArgs& a, const Request& k, int b) {
+  Block x;
+  const int row0 = b * kItem, before = k.len - k.nq;
+  const int i0 = row0 / a.G, i1 = min(k.nq - 1, (row0 + kItem - 1) / a.G);
+  x.last0 = before + i0;
+  x.last1 = before + i1;
+  x.first = a.window > 0 ? max(0, x.last0 - a.window + 1) / kTile * kTile : 0;
+  x.tiles = x.last1 < x.first ? 1 : (x.last1 - x.first) / kTile + 1;
+  return x;
+}
+
+// Where a CTA stands: tile t of block b of head h of request r.
+struct Place {
+  Request k;
+  Block x;
+  int r, h, b, t;
+};
+__device__ __forceinline__ void next_item(const AttentionArgs& a, Place& c) {
+  c.t = 0;
+  if (++c.b == c.k.blocks) {
+    c.b = 0;
+    if (++c.h == a.Hkv) {
+      c.h = 0;
+      do {
+        if (++c.r >= a.R) return;
+        c.k = request<kTile, kItem>(a, c.r, false);
+      } while (c.k.chunks == 0);
+    }
+  }
+  c.x = block_of(a, c.k, c.b);
+}
+__device__ __forceinline__ bool two_tiles(const AttentionArgs& a, const Place& c) { return c.k.nq * a.G - c.b * kItem > kRowsOf; }
+// Does a row of the item not see all of the tile that begins at p0?
+__device__ __forceinline__ bool at_edge(const AttentionArgs& a, const Block& x, int p0) {
+  return p0 + kTile - 1 > x.last0 || (a.window > 0 && p0 <= x.last1 - a.window);
+}
+
+// ------------------------------------------------------------------------- shared memory
+
+template <bool Q8, int DP>
+struct Plan {
+  static constexpr int softmax_warp = Q8 ? 8 : 4;  // the first
+  static constexpr int threads = 32 * softmax_warp + 2 * kGroupThreads;
+  static constexpr int panels = DP / 64;
+  static constexpr int tile = panels * kTile * 128;  // keys, or values, of a tile, as the products read them
+  static constexpr int raw = kTile * 128;            // ... of an e4m3 cache, as they are copied
+  static constexpr int k_stages = Q8 ? 2 : (DP == 64 ? 4 : 2), v_stages = Q8 ? 2 : (DP == 64 ? 4 : 3);
+  static constexpr int q = 0;                           // [2][panels][128 rows][128]
+  static constexpr int k = q + 2 * tile;                // [k_stages][tile]
+  static constexpr int v = k + k_stages * tile;         // [v_stages][tile]
+  static constexpr int k_raw = v + v_stages * tile;     // e4m3: [raw]
+  static constexpr int v_raw = k_raw + (Q8 ? raw : 0);  // [raw]
+  static constexpr int odd = v_raw + (Q8 ? raw : 0);    // [v_stages][4] words: tokens that rows add on their own
+  static constexpr int bars = odd + 16 * v_stages;
+  // barriers
+  static constexpr int k_full = 0, k_empty = k_full + k_stages, v_full = k_empty + k_stages, v_empty = v_full + v_stages,
+                       v_ok = v_empty + v_stages, s_full = v_ok + v_stages, p_ready = s_full + 2, o_done = p_ready + 2,
+                       q_ready = o_done + 2, drained = q_ready + 2, kr_full = drained + 1, kr_empty = kr_full + 1,
+                       vr_full = kr_empty + 1, vr_empty = vr_full + 1, n_bars = vr_empty + 1;
+  static constexpr int scan = bars + 8 * n_bars;     // [32] long long
+  static constexpr int start_off = scan + 8 * 32;    // long long
+  static constexpr int start_r = start_off + 8;      // int, then head, block, tile
+  static constexpr int tmem = start_r + 16, abort_flag = tmem + 4;
+  static constexpr int total = abort_flag + 4;
+  static_assert(total <= 232448, "227 KB");
+  static_assert(k + 8 * kMaxSlots <= odd, "the requests' units, before the copies begin");
+};
+
+template <int REGS>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+// Deals the tiles out evenly: where this worker begins is left in shared memory.
+template <typename L>
+__device__ Deal deal_tiles(const AttentionArgs& a, long long worker, long long workers, unsigned char* smem) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long* units = reinterpret_cast<long long*>(smem + L::k);  // [R]: of a head
+  long long* scan = reinterpret_cast<long long*>(smem + L::scan);
+  int* start = reinterpret_cast<int*>(smem + L::start_r);
+  long long* start_off = reinterpret_cast<long long*>(smem + L::start_off);
+  // a request's tiles: by its thread, or by the warp where it has many blocks
+  for (int base = warp * 32; base < a.R; base += L::threads) {
+    const int r = base + lane;
+    Request k = {};
+    if (r < a.R) k = request<kTile, kItem>(a, r, worker == 0);
+    const int blocks = k.chunks > 0 ? k.blocks : 0;
+    long long n = 0;
+    if (blocks <= 8)
+      for (int b = 0; b < blocks; ++b) n += block_of(a, k, b).tiles;
+    for (uint32_t many = __ballot_sync(~0u, blocks > 8); many != 0; many &= many - 1) {
+      const int from = __ffs(many) - 1;
+      Request big = {};
+      big.len = __shfl_sync(~0u, k.len, from);
+      big.nq = __shfl_sync(~0u, k.nq, from);
+      const int of = __shfl_sync(~0u, blocks, from);
+      long long mine = 0;
+      for (int b = lane; b < of; b += 32) mine += block_of(a, big, b).tiles;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(~0u, mine, d);
+      if (lane == from) n = mine;
+    }
+    if (r < a.R) units[r] = n;
+  }
+  __syncthreads();
+  const int slice = (a.R + L::threads - 1) / L::threads, r_lo = min(tid * slice, a.R), r_hi = min(r_lo + slice, a.R);
+  long long mine = 0;
+  for (int r = r_lo; r < r_hi; ++r) mine += a.Hkv * units[r];
+  long long upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(~0u, upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 31) scan[warp] = upto;
+  __syncthreads();
+  Deal deal;
+  deal.total = 0;
+  for (int w = 0; w < L::threads / 32; ++w) {
+    if (w < warp) upto += scan[w];
+    deal.total += scan[w];
+  }
+  deal.per = max((long long)kMinUnits, (deal.total + workers - 1) / workers);
+  const long long u = worker * deal.per;
+  if (u >= upto - mine && u < upto) {
+    long long off = u - (upto - mine);
+    int r = r_lo;
+    while (off >= a.Hkv * units[r]) off -= a.Hkv * units[r++];
+    start[0] = r;
+    start[1] = (int)(off / units[r]);
+    *start_off = off % units[r];
+  }
+  __syncthreads();
+  if (warp == 0 && u < deal.total) {  // the block, by a warp
+    const Request k = request<kTile, kItem>(a, start[0], false);
+    long long off = *start_off;
+    for (int base = 0;; base += 32) {
+      const int b = base + lane, n = b < k.blocks ? block_of(a, k, b).tiles : 0;
+      int sum = n;  // (32 times less than 2^24 tiles)
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(~0u, sum, d);
+        if (lane >= d) sum += o;
+      }
+      const uint32_t past = __ballot_sync(~0u, sum > off);
+      if (past != 0 || base >= k.blocks) {
+        if (past != 0 && lane == __ffs(past) - 1) {
+          start[2] = b;
+          start[3] = (int)(off - (sum - n));
+        }
+        break;
+      }
+      off -= __shfl_sync(~0u, sum, 31);
+    }
+  }
+  __syncthreads();
+  return deal;
+}
+
+// BFQ: queries and outputs bf16, else fp16.  Q8: an e4m3 cache.  DP: elements of a row, padded.
+template <bool BFQ, bool Q8, int DP>
+__global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
+    chunk_attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Maps maps, int box, Scratch scr) {
+  using L = Plan<Q8, DP>;
+  using H = Half16<BFQ && !Q8>;  // type of the products
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t base = smem_addr(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto bar = [&](int i) { return base + L::bars + 8 * i; };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::abort_flag);
+  volatile uint32_t* odd = reinterpret_cast<volatile uint32_t*>(smem + L::odd);
+  const long long worker = blockIdx.x, workers = gridDim.x;
+  const int G = a.G;
+
+  if (tid == 0) {
+    constexpr int writers = Q8 ? kGroupThreads / 32 : 1;
+    for (int i = 0; i < L::k_stages; ++i) mbar_init(bar(L::k_full + i), writers), mbar_init(bar(L::k_empty + i), 1);
+    for (int i = 0; i < L::v_stages; ++i) {
+      mbar_init(bar(L::v_full + i), writers), mbar_init(bar(L::v_empty + i), 1), mbar_init(bar(L::v_ok + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(L::s_full + i), 1), mbar_init(bar(L::p_ready + i), kGroupThreads / 32);
+      mbar_init(bar(L::o_done + i), 1), mbar_init(bar(L::q_ready + i), kGroupThreads / 32);
+    }
+    mbar_init(bar(L::drained), 1);
+    mbar_init(bar(L::kr_full), 1), mbar_init(bar(L::kr_empty), kGroupThreads / 32);
+    mbar_init(bar(L::vr_full), 1), mbar_init(bar(L::vr_empty), kGroupThreads / 32);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base + L::tmem) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  griddep_wait();
+  griddep_allow_next();
+  const Deal d = deal_tiles<L>(a, worker, workers, smem);
+  fence_smem();  // (its table lay where copies will land)
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::tmem);
+  if (tid == 0) {
+    scr.share[worker].r = -1;
+    if (worker == 0) *scr.per = d.per;
+  }
+  const long long u_begin = worker * d.per, u_end = min(d.total, u_begin + d.per);
+  const bool aligned = (base & 1023u) == 0;  // (as the swizzle wants; so it is without static shared memory)
+  if (!aligned && tid == 0) report_bad_input(a.status, 632);
+  const int tiles = aligned && u_begin < u_end ? (int)(u_end - u_begin) : 0;
+  auto stand = [&]() {
+    Place p = {};
+    if (tiles > 0) {
+      const volatile int* start = reinterpret_cast<const volatile int*>(smem + L::start_r);
+      p.r = start[0], p.h = start[1], p.b = start[2], p.t = start[3];
+      p.k = request<kTile, kItem>(a, p.r, false);
+      p.x = block_of(a, p.k, p.b);
+    }
+    return p;
+  };
+  // The register file, 65536 less what the launch rounds off: 384 threads of 168, or 512 of 128.
+  if (warp < L::softmax_warp) {
+  fewer_registers<Q8 ? 72 : 88>();
+  if (warp == 0 || warp == 2) {
+    // ---- copies, of keys (warp 0) and of values (warp 2): a lane per box of a tile, its page looked up
+    // one tile ahead
+    Place use = stand();
+    const bool keys = warp == 0;
+    const int stages = Q8 ? 1 : (keys ? L::k_stages : L::v_stages);
+    const int full = Q8 ? (keys ? L::kr_full : L::vr_full) : (keys ? L::k_full : L::v_full),
+              empty = Q8 ? (keys ? L::kr_empty : L::vr_empty) : (keys ? L::k_empty : L::v_empty);
+    constexpr int bytes = Q8 ? L::raw : L::tile, panels = Q8 ? 1 : L::panels;
+    const uint32_t ring = base + (Q8 ? (keys ? L::k_raw : L::v_raw) : (keys ? L::k : L::v));
+    const CUtensorMap* map = keys ? &maps.k : &maps.v;
+    const int boxes = kTile / box;
+    int page = -1, slot = 0;
+    bool inside = false;
+    auto look_up = [&]() {
+      const int pos = use.x.first + use.t * kTile + lane * box, nth = pos / a.page_size;
+      slot = pos - nth * a.page_size;
+      inside = lane < boxes && pos <= use.x.last1 && (a.window == 0 || pos + box - 1 > use.x.last0 - a.window);
+      page = inside ? a.page_table[use.r * a.table_stride + nth] : -1;
+    };
+    if (tiles > 0) look_up();
+    int filled = 0, stage = 0, phase = 1;  // (the first round finds every stage empty)
+    for (int i = 0; i < tiles; ++i) {
+      const bool there = page >= 0 && page < a.num_pages;
+      if (inside && !there) report_bad_input(a.status, kBadPage);
+      const int from = there ? page : a.num_pages;  // past the pool: zeros
+      if (i >= stages && !mbar_wait(bar(empty + stage), phase, abort_flag, a.status, 621)) break;
+      if (lane == 0) mbar_expect(bar(full + stage), bytes);
+      __syncwarp();
+      if (lane < boxes)
+#pragma unroll
+        for (int n = 0; n < panels; ++n)
+          tma_box(ring + stage * bytes + n * (kTile * 128) + lane * box * 128, map, bar(full + stage), 64 * n, slot, use.h, from);
+      filled = i + 1;
+      if (++stage == stages) stage = 0, phase ^= 1;
+      if (i + 1 < tiles) {
+        if (++use.t == use.x.tiles) next_item(a, use);
+        look_up();
+      }
+    }
+    // every copy lands before the CTA ends (at once, unless a role gave up)
+    for (int i = max(0, filled - stages); i < filled; ++i) mbar_drain(bar(full + i % stages), (i / stages) & 1);
+  } else if (warp == 1) {
+    // ---- products.  The tensor cores execute them in the order of their issue, so that S of the next tile
+    // may follow the product that reads the weights in its place.
+    if (lane == 0) {
+      Place use = stand();
+      constexpr uint32_t s_desc = idesc<BFQ && !Q8>(kTile, false, false), o_desc = idesc<BFQ && !Q8>(DP, false, true);
+      const uint64_t q_first = sw128(base + L::q, 16, 1024), k_first = sw128(base + L::k, 16, 1024),
+                     v_first = sw128(base + L::v, L::panels > 1 ? kTile * 128 : 0, 1024);
+      auto scores = [&](int x, int i, bool wait) {
+        const int ks = i % L::k_stages;
+        if (wait && !mbar_wait(bar(L::k_full + ks), (i / L::k_stages) & 1, abort_flag, a.status, 622)) return false;
+        fence_after();
+        const uint64_t rows = q_first + (uint32_t)(x * (L::tile / 16)), keys = k_first + (uint32_t)(ks * (L::tile / 16));
+#pragma unroll
+        for (int kk = 0; kk < DP / 16; ++kk) {
+          const uint32_t step = kk / 4 * (kTile * 8) + kk % 4 * 2;
+          mma(tmem + x * kTile, rows + step, keys + step, s_desc, kk > 0);
+        }
+        commit(bar(L::s_full + x));
+        return true;
+      };
+      int i = 0, done[2] = {0, 0}, items[2] = {0, 0};
+      bool ok = true;
+      while (ok && i < tiles) {
+        const int n = min(use.x.tiles - use.t, tiles - i), both = two_tiles(a, use) ? 2 : 1;
+        for (int x = 0; ok && x < both; ++x)
+          ok = mbar_wait(bar(L::q_ready + x), items[x]++ & 1, abort_flag, a.status, 623) && scores(x, i, x == 0);
+        if (ok) commit(bar(L::k_empty + i % L::k_stages));
+        for (int t = 0; ok && t < n; ++t, ++i) {
+          const int vs = i % L::v_stages, round = (i / L::v_stages) & 1;
+          for (int x = 0; ok && x < both; ++x) {
+            if (x == 0)
+              ok = mbar_wait(bar(L::v_full + vs), round, abort_flag, a.status, 624) &&
+                   (Q8 || mbar_wait(bar(L::v_ok + vs), round, abort_flag, a.status, 625));
+            ok = ok && mbar_wait(bar(L::p_ready + x), done[x]++ & 1, abort_flag, a.status, 626);
+            if (!ok) break;
+            fence_after();
+            // an item's first product begins its sums, unless rows have added tokens on their own
+            uint32_t add = t > 0;
+            if (t == 0 && at_edge(a, use.x, use.x.first + use.t * kTile))
+              add = (odd[4 * vs] | odd[4 * vs + 1] | odd[4 * vs + 2] | odd[4 * vs + 3]) != 0;
+            const uint64_t values = v_first + (uint32_t)(vs * (L::tile / 16));
+            const uint32_t weights = tmem + x * kTile, to = tmem + 2 * kTile + x * DP;
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk) mma_ts(to, weights + 8 * kk, values + kk * 128, o_desc, kk > 0 || add);
+            if (t + 1 == n) commit(bar(L::o_done + x));
+            if (x == both - 1) commit(bar(L::v_empty + vs));
+            if (t + 1 < n) ok = scores(x, i + 1, x == 0);
+          }
+          if (ok && t + 1 < n) commit(bar(L::k_empty + (i + 1) % L::k_stages));
+        }
+        if (i < tiles) next_item(a, use);
+      }
+      // every product is done before the CTA gives its tensor memory back
+      commit(bar(L::drained));
+      mbar_drain(bar(L::drained), 0);
+    }
+    __syncwarp();
+  } else if (!Q8 && warp == 3) {
+    Place use = stand();
+    // ---- the values at edges: four tokens a lane
+    for (int i = 0; i < tiles; ++i) {
+      const int vs = i % L::v_stages;
+      if (!mbar_wait(bar(L::v_full + vs), (i / L::v_stages) & 1, abort_flag, a.status, 627)) break;
+      const int p0 = use.x.first + use.t * kTile;
+      if (at_edge(a, use.x, p0)) {
+        for (int j = 0; j < 4; ++j) {
+          const int token = 32 * j + lane, pos = p0 + token;
+          const uint32_t row = base + L::v + vs * L::tile + token * 128;
+          auto piece = [&](int c) { return row + (c >> 3) * (kTile * 128) + (((c & 7) ^ (token & 7)) << 4); };
+          const bool unseen = pos > use.x.last1 || (a.window > 0 && pos <= use.x.last0 - a.window);
+          const bool partly = !unseen && (pos > use.x.last0 || (a.window > 0 && pos <= use.x.last1 - a.window));
+          bool strange = false;
+          if (partly)
+#pragma unroll 4
+            for (int c = 0; c < L::panels * 8; ++c) {
+              const uint4 v = lds16(piece(c));
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) strange |= (w[e] & H::kExp) == H::kExp || ((w[e] >> 16) & H::kExp) == H::kExp;
+            }
+          const uint32_t strangers = __ballot_sync(~0u, strange);
+          if (lane == 0) odd[4 * vs + j] = strangers;
+          if (unseen || strange)
+            for (int c = 0; c < L::panels * 8; ++c) sts16(piece(c), make_uint4(0, 0, 0, 0));
+        }
+        fence_smem();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(bar(L::v_ok + vs));
+      if (i + 1 < tiles && ++use.t == use.x.tiles) next_item(a, use);
+    }
+  } else if (Q8 && warp >= 4 && warp < 8) {
+    // ---- e4m3 to fp16: a thread per token, 16 elements (one piece) into two pieces at a time
+    Place use = stand();
+    const int token = tid - 128;
+    for (int i = 0; i < tiles; ++i) {
+      const int ks = i % L::k_stages, vs = i % L::v_stages, p0 = use.x.first + use.t * kTile, pos = p0 + token;
+      auto convert = [&](uint32_t from, uint32_t to, bool clear, bool look) {
+        bool strange = false;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const uint4 x = lds16(from + token * 128 + ((c ^ (token & 7)) << 4));
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[2 * e] = e4m3_to_half2(w[e]), h[2 * e + 1] = e4m3_to_half2(w[e] >> 16);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (look) strange |= (h[e] & H::kExp) == H::kExp || ((h[e] >> 16) & H::kExp) == H::kExp;
+            if (clear) h[e] = 0;
+          }
+          const uint32_t row = to + (c >> 2) * (kTile * 128) + token * 128;
+          const int piece = 2 * c & 7;
+          sts16(row + ((piece ^ (token & 7)) << 4), make_uint4(h[0], h[1], h[2], h[3]));
+          sts16(row + (((piece + 1) ^ (token & 7)) << 4), make_uint4(h[4], h[5], h[6], h[7]));
+        }
+        return strange;
+      };
+      if (!mbar_wait(bar(L::kr_full), i & 1, abort_flag, a.status, 628)) break;
+      if (i >= L::k_stages && !mbar_wait(bar(L::k_empty + ks), (i / L::k_stages - 1) & 1, abort_flag, a.status, 629)) break;
+      convert(base + L::k_raw, base + L::k + ks * L::tile, false, false);
+      fence_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kr_empty)), mbar_arrive(bar(L::k_full + ks));
+      if (!mbar_wait(bar(L::vr_full), i & 1, abort_flag, a.status, 630)) break;
+      if (i >= L::v_stages && !mbar_wait(bar(L::v_empty + vs), (i / L::v_stages - 1) & 1, abort_flag, a.status, 631)) break;
+      const uint32_t to = base + L::v + vs * L::tile;
+      if (at_edge(a, use.x, p0)) {
+        const bool unseen = pos > use.x.last1 || (a.window > 0 && pos <= use.x.last0 - a.window);
+        const bool partly = !unseen && (pos > use.x.last0 || (a.window > 0 && pos <= use.x.last1 - a.window));
+        const bool strange = convert(base + L::v_raw, to, unseen, partly);
+        const uint32_t strangers = __ballot_sync(~0u, strange);
+        if (lane == 0) odd[4 * vs + warp - 4] = strangers;
+        if (strange)
+          for (int c = 0; c < L::panels * 8; ++c)
+            sts16(to + (c >> 3) * (kTile * 128) + token * 128 + (((c & 7) ^ (token & 7)) << 4), make_uint4(0, 0, 0, 0));
+      } else {
+        convert(base + L::v_raw, to, false, false);
+      }
+      fence_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::vr_empty)), mbar_arrive(bar(L::v_full + vs));
+      if (i + 1 < tiles && ++use.t == use.x.tiles) next_item(a, use);
+    }
+  }
+  } else {
+    more_registers<Q8 ? 184 : 208>();
+    // ---- softmax: group x has row tile x; a thread, the row of its TMEM lane
+    Place use = stand();
+    const int x = (warp - L::softmax_warp) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + x * kTile, o_at = tmem + lanes + 2 * kTile + x * DP;
+    const uint32_t q_row = base + L::q + x * L::tile + row * 128;
+    const float flip = a.scale < 0.f ? -1.f : 1.f;
+    long long item_begin = u_begin - use.t;
+    int i = 0, done = 0, items = 0;  // tiles and items of this group
+    bool ok = true;
+    while (ok && i < tiles) {
+      const int n = min(use.x.tiles - use.t, tiles - i);
+      if (x == 0 || two_tiles(a, use)) {
+        const int rr = use.b * kItem + x * kRowsOf + row;
+        const bool there = rr < use.k.nq * G;
+        const int q = there ? rr / G : 0, head = use.h * G + (there ? rr - q * G : 0);
+        const int last = there ? use.k.len - use.k.nq + q : -1;
+        // the row tile's first and last row
+        const int tile_row = use.b * kItem + x * kRowsOf;
+        const int last0 = use.k.len - use.k.nq + tile_row / G,
+                  last1 = use.k.len - use.k.nq + min(use.k.nq - 1, (tile_row + kRowsOf - 1) / G);
+        // the query row; scores in base 2 per product are c2 times what the products give (never 0, so that
+        // what is masked stays -inf)
+        float c2 = fabsf(a.scale) * kLog2e * (Q8 ? a.k_scale[use.h] : 1.f);
+        {
+          uint4 piece[DP / 8];
+          const uint16_t* from_q = static_cast<const uint16_t*>(a.q) + (int64_t)(use.k.q0 + q) * a.q_stride_token +
+                                   (int64_t)head * a.q_stride_head;
+#pragma unroll
+          for (int c = 0; c < DP / 8; ++c)
+            piece[c] = there && c * 8 < a.D ? *reinterpret_cast<const uint4*>(from_q + c * 8) : make_uint4(0, 0, 0, 0);
+          int e2 = 0;
+          if (Q8 && BFQ) {
+            // fp16 operands: the row is scaled by a power of two to a maximum in [1, 2) (what falls below
+            // 2^-24 of it is lost, far under the sums' rounding)
+            float top = 0.f;
+#pragma unroll
+            for (int c = 0; c < DP / 8; ++c) {
+              const uint32_t w[4] = {piece[c].x, piece[c].y, piece[c].z, piece[c].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top = max3(top, fabsf(Half16<true>::lo(w[e])), fabsf(Half16<true>::hi(w[e])));
+            }
+            if (top > 0.f && top < INFINITY) e2 = min(max(ilogbf(top), -126), 126);
+          }
+          const float down = (Q8 && BFQ ? ldexpf(1.f, -e2) : 1.f) * flip;
+          c2 = fmaxf(c2 * (Q8 && BFQ ? ldexpf(1.f, e2) : 1.f), 1e-37f);
+#pragma unroll
+          for (int c = 0; c < DP / 8; ++c) {
+            uint32_t w[4] = {piece[c].x, piece[c].y, piece[c].z, piece[c].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (Q8 && BFQ) w[e] = Half16<false>::pack(Half16<true>::lo(w[e]) * down, Half16<true>::hi(w[e]) * down);
+              else if (flip < 0.f) w[e] ^= 0x80008000u;
+            }
+            sts16(q_row + (c >> 3) * (kTile * 128) + (((c & 7) ^ (row & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+          }
+          fence_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::q_ready + x));
+        }
+
+        float ref = kUnset;
+        Two sum0 = two(0.f, 0.f), sum1 = two(0.f, 0.f);
+        for (int t = 0; t < n; ++t, ++done) {
+          ok = mbar_wait(bar(L::s_full + x), done & 1, abort_flag, a.status, 633);
+          if (__any_sync(~0u, !ok)) {
+            ok = false;
+            break;
+          }
+          fence_after();  // (and the tile before is in O: its product was issued before this S)
+          const int p0 = use.x.first + (use.t + t) * kTile;
+          const bool edge = p0 + kTile - 1 > last0 || (a.window > 0 && p0 <= last1 - a.window);
+          const int hi = last - p0, lo = a.window > 0 ? hi - a.window + 1 : 0;  // the columns that this row sees
+          // a new reference where a score passes the old one by too much
+          auto refer = [&](float most) {
+            if (!__any_sync(~0u, most > ref + (kSlack + H::kLift))) return;
+            const float now = fmaxf(ref, most - H::kLift), f = ex2(ref - now);
+            ref = now;
+            const Two ff = two(f, f), zero = two(0.f, 0.f);
+            sum0 = fma2(sum0, ff, zero), sum1 = fma2(sum1, ff, zero);
+            if (t == 0) return;
+#pragma unroll
+            for (int c = 0; c < DP; c += 16) {
+              float o[16];
+              tmem_load(o_at + c, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= f;
+              tmem_store(o_at + c, o);
+            }
+          };
+          if (at_edge(a, use.x, p0)) {
+            const int vs = (i + t) % L::v_stages;
+            ok = mbar_wait(bar((Q8 ? L::v_full : L::v_ok) + vs), ((i + t) / L::v_stages) & 1, abort_flag, a.status, 634);
+            if (__any_sync(~0u, !ok)) {
+              ok = false;
+              break;
+            }
+            // (uniform over the group: nobody writes these words before the tile's products are done)
+            if ((odd[4 * vs] | odd[4 * vs + 1] | odd[4 * vs + 2] | odd[4 * vs + 3]) != 0) {
+              float most = -INFINITY;
+              for (int c = 0; c < kTile; c += 16) {
+                float y[16];
+                tmem_load(s_at + c, y);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (c + e <= hi && c + e >= lo) most = fmaxf(most, y[e]);
+              }
+              refer(most * c2);
+              if (t == 0) {
+                float zero[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) zero[e] = 0.f;
+                for (int c = 0; c < DP; c += 16) tmem_store(o_at + c, zero);
+              }
+              tmem_store_wait();
+              for (int k = 0; k < kTile; ++k) {
+                if (((odd[4 * vs + (k >> 5)] >> (k & 31)) & 1u) == 0) continue;
+                const int pos = p0 + k, nth = pos / a.page_size, page = a.page_table[use.r * a.table_stride + nth];
+                const float p = ex2(fmaf(tmem_load1(s_at + k), c2, -ref));
+                const bool sees = k <= hi && k >= lo && page >= 0 && page < a.num_pages;
+                const int64_t at = page * a.page_stride + use.h * a.head_stride + (pos - nth * a.page_size) * a.token_stride;
+                for (int c = 0; c < DP; c += 16) {
+                  float o[16];
+                  tmem_load(o_at + c, o);
+                  if (sees && c < a.D) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                      float v;
+                      if (Q8) v = Half16<false>::lo(e4m3_to_half2(static_cast<const uint8_t*>(a.v_pool)[at + c + e]));
+                      else v = H::lo(static_cast<const uint16_t*>(a.v_pool)[at + c + e]);
+                      o[e] = fmaf(p, v, o[e]);
+                    }
+                  }
+                  tmem_store(o_at + c, o);
+                  tmem_store_wait();
+                }
+              }
+            }
+          }
+          float s[kTile];
+          tmem_load128(s_at, s);
+          if (edge) {
+#pragma unroll
+            for (int k = 0; k < kTile; ++k)
+              if (k > hi || k < lo) s[k] = -INFINITY;
+          }
+          float m0 = max3(s[0], s[1], s[2]), m1 = max3(s[3], s[4], s[5]);
+#pragma unroll
+          for (int k = 6; k + 3 < kTile; k += 4) m0 = max3(m0, s[k], s[k + 1]), m1 = max3(m1, s[k + 2], s[k + 3]);
+          refer(fmaxf(max3(m0, s[kTile - 2], s[kTile - 1]), m1) * c2);
+          // scores to weights, 32 at a time, in the place of the scores (rounded as the product wants them;
+          // the normaliser adds them unrounded)
+          const Two cc = two(c2, c2), rr2 = two(-ref, -ref);
+#pragma unroll
+          for (int c = 0; c < kTile; c += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float p0_, p1_, p2_, p3_;
+              apart(fma2(two(s[c + e], s[c + e + 1]), cc, rr2), p0_, p1_);
+              apart(fma2(two(s[c + e + 2], s[c + e + 3]), cc, rr2), p2_, p3_);
+              p0_ = ex2(p0_), p1_ = ex2(p1_), p2_ = ex2(p2_), p3_ = ex2(p3_);
+              sum0 = add2(sum0, two(p0_, p1_)), sum1 = add2(sum1, two(p2_, p3_));
+              w[e / 2] = H::pack(p0_, p1_), w[e / 2 + 1] = H::pack(p2_, p3_);
+            }
+            tmem_store_u16(s_at + c / 2, w);
+          }
+          tmem_store_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::p_ready + x));
+        }
+        if (!ok) break;
+
+        // ---- the item, or this worker's part of it, ends
+        ok = mbar_wait(bar(L::o_done + x), items++ & 1, abort_flag, a.status, 635);
+        if (__any_sync(~0u, !ok)) {
+          ok = false;
+          break;
+        }
+        fence_after();
+        float l0, l1, l2, l3;
+        apart(sum0, l0, l1), apart(sum1, l2, l3);
+        const float sum = (l0 + l1) + (l2 + l3);
+        const long long item_end = item_begin + use.x.tiles;
+        const int64_t place = (int64_t)(use.k.q0 + q) * a.Hq + head;
+        const bool whole = item_begin >= u_begin && item_end <= u_end;
+        const int part = item_begin >= u_begin;  // part 0 began before the worker's range
+        const size_t out_row = (size_t)(worker * 2 + part) * kItem + x * kRowsOf + row;
+        const float f = sum == 0.f ? 0.f : (Q8 ? a.v_scale[use.h] : 1.f) / sum;
+        if (there && whole && a.lse_out != nullptr) a.lse_out[place] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+        if (there && !whole) scr.stats[out_row] = make_float2(sum == 0.f ? -INFINITY : ref, sum);
+#pragma unroll
+        for (int c = 0; c < DP; c += 32) {
+          float o[32];
+          tmem_load32(o_at + c, o);
+          if (!there) continue;
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(scr.out + out_row * DP + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            continue;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            if (c + e >= a.D) continue;
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[j] = sum == 0.f ? 0u : Half16<BFQ>::pack(o[e + 2 * j] * f, o[e + 2 * j + 1] * f);
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + place * a.D + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        fence_before();
+        if (!whole && part == 1 && x == 0 && row == 0)
+          scr.share[worker] = Share{use.r, use.h * use.k.blocks + use.b, use.k.q0, use.k.nq, item_begin, item_end};
+      }
+      i += n;
+      item_begin += use.x.tiles;
+      if (i < tiles) next_item(a, use);
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+// ------------------------------------------------------------------------------ host side
+
+template <bool BFQ, bool Q8, int DP>
+cudaError_t launch(const AttentionArgs& a, const Maps& maps, int box, void* scratch, cudaStream_t s) {
+  using L = Plan<Q8, DP>;
+  auto* kernel = chunk_attention_kernel<BFQ, Q8, DP>;
+  static std::atomic<uint64_t> done;
+  cudaError_t e = allow_smem(kernel, L::total, done);
+  if (e != cudaSuccess) return e;
+  const int workers = std::min(sm_count(), kMaxSms);
+  const Scratch scr = scratch_at(scratch, kMaxSms, kItem);
+  e = launch_chained(kernel, dim3(workers), dim3(L::threads), L::total, s, 1, a, maps, box, scr);
+  return e != cudaSuccess ? e : launch_join<BFQ, DP, kItem>(a, scr, workers, s);
+}
+
+}  // namespace
+
+size_t chunk_attention_scratch(int Hq, int Hkv, int D) {
+  return std::max(attention_rows_scratch(Hq, Hkv, D), D > 128 ? 0 : scratch_bytes(kMaxSms, kItem, 128));
+}
 
 cudaError_t launch_chunk_attention(const AttentionArgs& a, void* scratch, cudaStream_t s) {
-  return launch_attention_rows(a, scratch, s);
+  const int box = box_tokens(a.page_size);
+  Maps maps;
+  if (a.D > 128 || box == 0 || !encode_pool(&maps.k, a, a.k_pool, box) || !encode_pool(&maps.v, a, a.v_pool, box))
+    return launch_attention_rows(a, scratch, s);
+  const bool bf = a.dtype_q == DSPARK_BF16;
+  if (a.dtype_kv == DSPARK_E4M3)
+    return bf ? launch<true, true, 128>(a, maps, box, scratch, s) : launch<false, true, 128>(a, maps, box, scratch, s);
+  if (a.D <= 64)
+    return bf ? launch<true, false, 64>(a, maps, box, scratch, s) : launch<false, false, 64>(a, maps, box, scratch, s);
+  return bf ? launch<true, false, 128>(a, maps, box, scratch, s) : launch<false, false, 128>(a, maps, box, scratch, s);
 }
 
 }  // namespace dspark
