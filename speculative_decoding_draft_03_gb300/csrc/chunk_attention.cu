@@ -39,12 +39,47 @@ constexpr int kGroupThreads = 128;     // of a softmax group
 
 // ---------------------------------------------------------------------------- wrappers
 
-// A (the weights) from tensor memory.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, uint32_t accumulate) {
+// mbar_wait, out of line where the phase is still open: the roles' loops share the instruction cache, and a
+// dozen copies of it cost more than the calls (512 queries at 65536 tokens of an e4m3 cache: 470 us so, 580
+// inlined).
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, DeviceStatus* st, int where) {
+  const long long t0 = clock64();
+  while (!mbar_sleep(bar, parity)) {
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *abort_flag = 1;
+      report_timeout(st, where);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, DeviceStatus* st, int where) {
+  return mbar_test(bar, parity) || wait_on(bar, parity, abort_flag, st, where);
+}
+// Products and commits by one elected lane of a warp; descriptors by their lower halves (the upper ones: rows
+// of 128 bytes in groups of eight, swizzled).  A (the weights) from tensor memory in the second.
+constexpr uint32_t kUpper = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ void mma_one(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(desc), "r"(accumulate)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "elect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"(accumulate), "n"(kUpper)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_one(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %5};\n\t"
+      "elect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(desc), "r"(accumulate), "n"(kUpper)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
       : "memory");
 }
 #define R8(x, i) "=f"(x[i]), "=f"(x[i + 1]), "=f"(x[i + 2]), "=f"(x[i + 3]), "=f"(x[i + 4]), "=f"(x[i + 5]), "=f"(x[i + 6]), "=f"(x[i + 7])
@@ -55,19 +90,6 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, float* x) {
       "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
       : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)
       : "r"(at)
-      : "memory");
-}
-// 128 columns: a tile's scores.
-__device__ __forceinline__ void tmem_load128(uint32_t at, float* x) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24), R8(x, 32), R8(x, 40), R8(x, 48), R8(x, 56), R8(x, 64), R8(x, 72), R8(x, 80),
-        R8(x, 88), R8(x, 96), R8(x, 104), R8(x, 112), R8(x, 120)
-      : "r"(at), "r"(at + 32), "r"(at + 64), "r"(at + 96)
       : "memory");
 }
 #undef R8
@@ -108,11 +130,17 @@ __device__ __forceinline__ Two add2(Two a, Two b) {
 
 // The tiles that a block of rows (an item without its head) sees.
 struct Block {
+  int b;                  // its number
   int first, tiles;       // first: position of the first tile's first token
   int last0, last1;       // last position that the first and the last row see (below 0: nothing)
 };
-__device__ __forceinline__ Block block_of(const AttentionArgs& a, const Request& k, int b) {
+// The nth block of a request in the order of the deal: first, last, second, last but one ... (causal blocks
+// see more and more tiles, and an item costs something whatever it sees: every CTA gets short and long ones).
+__device__ __forceinline__ int nth_block(const Request& k, int n) { return n & 1 ? k.blocks - 1 - (n >> 1) : n >> 1; }
+__device__ __forceinline__ Block block_of(const AttentionArgs& a, const Request& k, int n) {
+  const int b = nth_block(k, n);
   Block x;
+  x.b = b;
   const int row0 = b * kItem, before = k.len - k.nq;
   const int i0 = row0 / a.G, i1 = min(k.nq - 1, (row0 + kItem - 1) / a.G);
   x.last0 = before + i0;
@@ -122,16 +150,16 @@ __device__ __forceinline__ Block block_of(const AttentionArgs& a, const Request&
   return x;
 }
 
-// Where a CTA stands: tile t of block b of head h of request r.
+// Where a CTA stands: tile t of the nth block of head h of request r.
 struct Place {
   Request k;
   Block x;
-  int r, h, b, t;
+  int r, h, n, t;
 };
 __device__ __forceinline__ void next_item(const AttentionArgs& a, Place& c) {
   c.t = 0;
-  if (++c.b == c.k.blocks) {
-    c.b = 0;
+  if (++c.n == c.k.blocks) {
+    c.n = 0;
     if (++c.h == a.Hkv) {
       c.h = 0;
       do {
@@ -140,9 +168,9 @@ __device__ __forceinline__ void next_item(const AttentionArgs& a, Place& c) {
       } while (c.k.chunks == 0);
     }
   }
-  c.x = block_of(a, c.k, c.b);
+  c.x = block_of(a, c.k, c.n);
 }
-__device__ __forceinline__ bool two_tiles(const AttentionArgs& a, const Place& c) { return c.k.nq * a.G - c.b * kItem > kRowsOf; }
+__device__ __forceinline__ bool two_tiles(const AttentionArgs& a, const Place& c) { return c.k.nq * a.G - c.x.b * kItem > kRowsOf; }
 // Does a row of the item not see all of the tile that begins at p0?
 __device__ __forceinline__ bool at_edge(const AttentionArgs& a, const Block& x, int p0) {
   return p0 + kTile - 1 > x.last0 || (a.window > 0 && p0 <= x.last1 - a.window);
@@ -210,9 +238,9 @@ __device__ Deal deal_tiles(const AttentionArgs& a, long long worker, long long w
       Request big = {};
       big.len = __shfl_sync(~0u, k.len, from);
       big.nq = __shfl_sync(~0u, k.nq, from);
-      const int of = __shfl_sync(~0u, blocks, from);
+      big.blocks = __shfl_sync(~0u, blocks, from);
       long long mine = 0;
-      for (int b = lane; b < of; b += 32) mine += block_of(a, big, b).tiles;
+      for (int b = lane; b < big.blocks; b += 32) mine += block_of(a, big, b).tiles;
 #pragma unroll
       for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(~0u, mine, d);
       if (lane == from) n = mine;
@@ -296,8 +324,8 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
       mbar_init(bar(L::v_full + i), writers), mbar_init(bar(L::v_empty + i), 1), mbar_init(bar(L::v_ok + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(L::s_full + i), 1), mbar_init(bar(L::p_ready + i), kGroupThreads / 32);
-      mbar_init(bar(L::o_done + i), 1), mbar_init(bar(L::q_ready + i), kGroupThreads / 32);
+      mbar_init(bar(L::s_full + i), 1), mbar_init(bar(L::o_done + i), 1), mbar_init(bar(L::q_ready + i), kGroupThreads / 32);
+      mbar_init(bar(L::p_ready + i), kGroupThreads / 32);
     }
     mbar_init(bar(L::drained), 1);
     mbar_init(bar(L::kr_full), 1), mbar_init(bar(L::kr_empty), kGroupThreads / 32);
@@ -316,22 +344,23 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + L::tmem);
+  constexpr uint32_t tmem = 0;  // (an allocation of all 512 columns begins at the first)
   if (tid == 0) {
     scr.share[worker].r = -1;
     if (worker == 0) *scr.per = d.per;
   }
   const long long u_begin = worker * d.per, u_end = min(d.total, u_begin + d.per);
-  const bool aligned = (base & 1023u) == 0;  // (as the swizzle wants; so it is without static shared memory)
+  // (shared memory as the swizzle wants it, which it is without static arrays; tensor memory as said above)
+  const bool aligned = (base & 1023u) == 0 && *reinterpret_cast<volatile uint32_t*>(smem + L::tmem) == tmem;
   if (!aligned && tid == 0) report_bad_input(a.status, 632);
   const int tiles = aligned && u_begin < u_end ? (int)(u_end - u_begin) : 0;
   auto stand = [&]() {
     Place p = {};
     if (tiles > 0) {
       const volatile int* start = reinterpret_cast<const volatile int*>(smem + L::start_r);
-      p.r = start[0], p.h = start[1], p.b = start[2], p.t = start[3];
+      p.r = start[0], p.h = start[1], p.n = start[2], p.t = start[3];
       p.k = request<kTile, kItem>(a, p.r, false);
-      p.x = block_of(a, p.k, p.b);
+      p.x = block_of(a, p.k, p.n);
     }
     return p;
   };
@@ -343,13 +372,13 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
     // one tile ahead
     Place use = stand();
     const bool keys = warp == 0;
+    const int boxes = kTile / box;
     const int stages = Q8 ? 1 : (keys ? L::k_stages : L::v_stages);
     const int full = Q8 ? (keys ? L::kr_full : L::vr_full) : (keys ? L::k_full : L::v_full),
               empty = Q8 ? (keys ? L::kr_empty : L::vr_empty) : (keys ? L::k_empty : L::v_empty);
     constexpr int bytes = Q8 ? L::raw : L::tile, panels = Q8 ? 1 : L::panels;
     const uint32_t ring = base + (Q8 ? (keys ? L::k_raw : L::v_raw) : (keys ? L::k : L::v));
     const CUtensorMap* map = keys ? &maps.k : &maps.v;
-    const int boxes = kTile / box;
     int page = -1, slot = 0;
     bool inside = false;
     auto look_up = [&]() {
@@ -364,7 +393,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
       const bool there = page >= 0 && page < a.num_pages;
       if (inside && !there) report_bad_input(a.status, kBadPage);
       const int from = there ? page : a.num_pages;  // past the pool: zeros
-      if (i >= stages && !mbar_wait(bar(empty + stage), phase, abort_flag, a.status, 621)) break;
+      if (i >= stages && !wait_for(bar(empty + stage), phase, abort_flag, a.status, 621)) break;
       if (lane == 0) mbar_expect(bar(full + stage), bytes);
       __syncwarp();
       if (lane < boxes)
@@ -380,70 +409,118 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
     }
     // every copy lands before the CTA ends (at once, unless a role gave up)
     for (int i = max(0, filled - stages); i < filled; ++i) mbar_drain(bar(full + i % stages), (i / stages) & 1);
+    __syncwarp();
   } else if (warp == 1) {
     // ---- products.  The tensor cores execute them in the order of their issue, so that S of the next tile
-    // may follow the product that reads the weights in its place.
-    if (lane == 0) {
-      Place use = stand();
-      constexpr uint32_t s_desc = idesc<BFQ && !Q8>(kTile, false, false), o_desc = idesc<BFQ && !Q8>(DP, false, true);
-      const uint64_t q_first = sw128(base + L::q, 16, 1024), k_first = sw128(base + L::k, 16, 1024),
-                     v_first = sw128(base + L::v, L::panels > 1 ? kTile * 128 : 0, 1024);
-      auto scores = [&](int x, int i, bool wait) {
-        const int ks = i % L::k_stages;
-        if (wait && !mbar_wait(bar(L::k_full + ks), (i / L::k_stages) & 1, abort_flag, a.status, 622)) return false;
-        fence_after();
-        const uint64_t rows = q_first + (uint32_t)(x * (L::tile / 16)), keys = k_first + (uint32_t)(ks * (L::tile / 16));
+    // may follow the product that reads the weights in its place.  What happens between two products is time
+    // that the tensor cores stand still: all there is to know and to wait for is settled before the weights are
+    // awaited, and the whole warp goes along, in branches that votes make uniform, with one lane elected at
+    // each product, so that the descriptors are formed in uniform registers (2048 queries at 32768 tokens:
+    // 797 us so, 969 by one lane in a branch of its own, 988 with the lane chosen by its number).
+    auto all = [](bool x) { return __all_sync(~0u, x) != 0; };
+    Place use = stand();
+    constexpr uint32_t s_desc = idesc<BFQ && !Q8>(kTile, false, false), o_desc = idesc<BFQ && !Q8>(DP, false, true);
+    // (the descriptors' lower halves; the upper one is a constant)
+    const uint32_t q_first = (uint32_t)sw128(base + L::q, 16, 1024), k_first = (uint32_t)sw128(base + L::k, 16, 1024),
+                   v_first = (uint32_t)sw128(base + L::v, L::panels > 1 ? kTile * 128 : 0, 1024);
+    uint32_t q_round[2] = {0, 0}, p_round[2] = {0, 0};
+    int ks = 0, vs = 0;
+    uint32_t k_round = 0, v_round = 0;
+    auto wait = [&](uint32_t at, uint32_t parity, int where) { return all(wait_for(at, parity, abort_flag, a.status, where)); };
+    auto scores = [&](int x) {
+      const uint32_t rows = q_first + x * (L::tile / 16), keys = k_first + ks * (L::tile / 16);
 #pragma unroll
-        for (int kk = 0; kk < DP / 16; ++kk) {
-          const uint32_t step = kk / 4 * (kTile * 8) + kk % 4 * 2;
-          mma(tmem + x * kTile, rows + step, keys + step, s_desc, kk > 0);
-        }
-        commit(bar(L::s_full + x));
-        return true;
-      };
-      int i = 0, done[2] = {0, 0}, items[2] = {0, 0};
-      bool ok = true;
-      while (ok && i < tiles) {
-        const int n = min(use.x.tiles - use.t, tiles - i), both = two_tiles(a, use) ? 2 : 1;
-        for (int x = 0; ok && x < both; ++x)
-          ok = mbar_wait(bar(L::q_ready + x), items[x]++ & 1, abort_flag, a.status, 623) && scores(x, i, x == 0);
-        if (ok) commit(bar(L::k_empty + i % L::k_stages));
-        for (int t = 0; ok && t < n; ++t, ++i) {
-          const int vs = i % L::v_stages, round = (i / L::v_stages) & 1;
-          for (int x = 0; ok && x < both; ++x) {
-            if (x == 0)
-              ok = mbar_wait(bar(L::v_full + vs), round, abort_flag, a.status, 624) &&
-                   (Q8 || mbar_wait(bar(L::v_ok + vs), round, abort_flag, a.status, 625));
-            ok = ok && mbar_wait(bar(L::p_ready + x), done[x]++ & 1, abort_flag, a.status, 626);
-            if (!ok) break;
-            fence_after();
-            // an item's first product begins its sums, unless rows have added tokens on their own
-            uint32_t add = t > 0;
-            if (t == 0 && at_edge(a, use.x, use.x.first + use.t * kTile))
-              add = (odd[4 * vs] | odd[4 * vs + 1] | odd[4 * vs + 2] | odd[4 * vs + 3]) != 0;
-            const uint64_t values = v_first + (uint32_t)(vs * (L::tile / 16));
-            const uint32_t weights = tmem + x * kTile, to = tmem + 2 * kTile + x * DP;
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk) mma_ts(to, weights + 8 * kk, values + kk * 128, o_desc, kk > 0 || add);
-            if (t + 1 == n) commit(bar(L::o_done + x));
-            if (x == both - 1) commit(bar(L::v_empty + vs));
-            if (t + 1 < n) ok = scores(x, i + 1, x == 0);
-          }
-          if (ok && t + 1 < n) commit(bar(L::k_empty + (i + 1) % L::k_stages));
-        }
-        if (i < tiles) next_item(a, use);
+      for (int kk = 0; kk < DP / 16; ++kk) {
+        const uint32_t step = kk / 4 * (kTile * 8) + kk % 4 * 2;
+        mma_one(tmem + x * kTile, rows + step, keys + step, s_desc, kk > 0);
       }
-      // every product is done before the CTA gives its tensor memory back
-      commit(bar(L::drained));
-      mbar_drain(bar(L::drained), 0);
+      commit_one(bar(L::s_full + x));
+    };
+    const int total = __shfl_sync(~0u, tiles, 0);
+    bool both = all(total > 0 && two_tiles(a, use));
+    bool ok = total > 0 && wait(bar(L::k_full), 0, 622);
+    for (int x = 0; ok && x < (both ? 2 : 1); ++x) {
+      ok = wait(bar(L::q_ready + x), 0, 623);
+      q_round[x] = 1;
+      fence_after();
+      if (ok) scores(x);
     }
+    if (ok) commit_one(bar(L::k_empty));
+    // what there is to know of a unit's products: where its values lie, whether its item ends with it, whether it
+    // has both row tiles, and whether its first product adds (the first of an item does not, unless rows have
+    // added tokens on their own)
+    struct Unit {
+      uint32_t values, v_at, add;
+      bool ends, two, last;
+    };
+    auto open_unit = [&](int i, bool goes_on) {  // the unit at `use`; moves on to the next
+      Unit u;
+      u.last = i + 1 == total;
+      u.ends = all(u.last || use.t + 1 == use.x.tiles);
+      u.two = both;
+      u.values = v_first + vs * (L::tile / 16);
+      u.v_at = bar(vs);
+      u.add = goes_on;
+      const bool edge = !goes_on && all(at_edge(a, use.x, use.x.first + use.t * kTile));
+      ok = ok && wait(u.v_at + 8 * (Q8 ? L::v_full : L::v_ok), v_round, 624);
+      if (edge) u.add = all((odd[4 * vs] | odd[4 * vs + 1] | odd[4 * vs + 2] | odd[4 * vs + 3]) != 0);
+      if (++vs == L::v_stages) vs = 0, v_round ^= 1;
+      if (!u.ends) ++use.t;
+      else if (!u.last) next_item(a, use), both = all(two_tiles(a, use));
+      return u;
+    };
+    auto open_keys = [&]() {
+      if (++ks == L::k_stages) ks = 0, k_round ^= 1;
+      ok = ok && wait(bar(L::k_full + ks), k_round, 622);
+    };
+    Unit now = {};
+    if (ok) now = open_unit(0, false);
+    if (ok && !now.last) open_keys();
+    for (int i = 0; ok && i < total; ++i) {
+      auto product = [&](int x) {
+        ok = wait(bar(L::p_ready + x), p_round[x], 626);
+        p_round[x] ^= 1;
+        if (!ok) return;
+        fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_ts_one(tmem + 2 * kTile + x * DP, tmem + x * kTile + 8 * kk, now.values + kk * 128, o_desc, kk > 0 ? 1u : now.add);
+        if (now.ends) commit_one(bar(L::o_done + x));
+      };
+      auto next = [&](int x) {
+        if (now.ends) {
+          ok = ok && wait(bar(L::q_ready + x), q_round[x], 623);
+          q_round[x] ^= 1;
+          fence_after();
+        }
+        if (ok) scores(x);
+      };
+      // (both: of the unit after this one; what comes after the next is looked up while the tensor cores work)
+      const bool next0 = !now.last, next1 = next0 && both;
+      product(0);
+      if (ok && next0) next(0);
+      Unit then = {};
+      if (ok && next0) then = open_unit(i + 1, !now.ends);
+      if (!ok) break;
+      if (now.two) product(1);
+      if (!ok) break;
+      commit_one(now.v_at + 8 * L::v_empty);
+      if (next1) next(1);
+      if (!ok || !next0) break;
+      commit_one(bar(L::k_empty + ks));
+      if (!then.last) open_keys();
+      now = then;
+    }
+    // every product is done before the CTA gives its tensor memory back
+    commit_one(bar(L::drained));
+    mbar_drain(bar(L::drained), 0);
     __syncwarp();
   } else if (!Q8 && warp == 3) {
     Place use = stand();
     // ---- the values at edges: four tokens a lane
     for (int i = 0; i < tiles; ++i) {
       const int vs = i % L::v_stages;
-      if (!mbar_wait(bar(L::v_full + vs), (i / L::v_stages) & 1, abort_flag, a.status, 627)) break;
+      if (!wait_for(bar(L::v_full + vs), (i / L::v_stages) & 1, abort_flag, a.status, 627)) break;
       const int p0 = use.x.first + use.t * kTile;
       if (at_edge(a, use.x, p0)) {
         for (int j = 0; j < 4; ++j) {
@@ -499,14 +576,14 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
         }
         return strange;
       };
-      if (!mbar_wait(bar(L::kr_full), i & 1, abort_flag, a.status, 628)) break;
-      if (i >= L::k_stages && !mbar_wait(bar(L::k_empty + ks), (i / L::k_stages - 1) & 1, abort_flag, a.status, 629)) break;
+      if (!wait_for(bar(L::kr_full), i & 1, abort_flag, a.status, 628)) break;
+      if (i >= L::k_stages && !wait_for(bar(L::k_empty + ks), (i / L::k_stages - 1) & 1, abort_flag, a.status, 629)) break;
       convert(base + L::k_raw, base + L::k + ks * L::tile, false, false);
       fence_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kr_empty)), mbar_arrive(bar(L::k_full + ks));
-      if (!mbar_wait(bar(L::vr_full), i & 1, abort_flag, a.status, 630)) break;
-      if (i >= L::v_stages && !mbar_wait(bar(L::v_empty + vs), (i / L::v_stages - 1) & 1, abort_flag, a.status, 631)) break;
+      if (!wait_for(bar(L::vr_full), i & 1, abort_flag, a.status, 630)) break;
+      if (i >= L::v_stages && !wait_for(bar(L::v_empty + vs), (i / L::v_stages - 1) & 1, abort_flag, a.status, 631)) break;
       const uint32_t to = base + L::v + vs * L::tile;
       if (at_edge(a, use.x, p0)) {
         const bool unseen = pos > use.x.last1 || (a.window > 0 && pos <= use.x.last0 - a.window);
@@ -533,64 +610,73 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
     const int x = (warp - L::softmax_warp) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + x * kTile, o_at = tmem + lanes + 2 * kTile + x * DP;
-    const uint32_t q_row = base + L::q + x * L::tile + row * 128;
-    const float flip = a.scale < 0.f ? -1.f : 1.f;
     long long item_begin = u_begin - use.t;
-    int i = 0, done = 0, items = 0;  // tiles and items of this group
-    bool ok = true;
-    while (ok && i < tiles) {
+    // The item's row of this thread: its query's number (of the request) and head, or none.  Its query is
+    // fetched and laid out for the products; scores in base 2 are c2 times what they give (never 0, so that
+    // what is masked stays -inf).
+    bool there;
+    int query, head;
+    float c2;
+    auto fetch = [&]() {
+      const int rr = use.x.b * kItem + x * kRowsOf + row;
+      there = rr < use.k.nq * G;
+      query = there ? rr / G : 0;
+      head = use.h * G + (there ? rr - query * G : 0);
+      const uint16_t* from = static_cast<const uint16_t*>(a.q) + (int64_t)(use.k.q0 + query) * a.q_stride_token +
+                             (int64_t)head * a.q_stride_head;
+      uint4 piece[DP / 8];
+#pragma unroll
+      for (int c = 0; c < DP / 8; ++c)
+        piece[c] = there && c * 8 < a.D ? *reinterpret_cast<const uint4*>(from + c * 8) : make_uint4(0, 0, 0, 0);
+      int e2 = 0;
+      if (Q8 && BFQ) {
+        // fp16 operands: the row is scaled by a power of two to a maximum in [1, 2) (what falls below 2^-24 of
+        // it is lost, far under the sums' rounding)
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < DP / 8; ++c) {
+          const uint32_t w[4] = {piece[c].x, piece[c].y, piece[c].z, piece[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max3(top, fabsf(Half16<true>::lo(w[e])), fabsf(Half16<true>::hi(w[e])));
+        }
+        if (top > 0.f && top < INFINITY) e2 = min(max(ilogbf(top), -126), 126);
+      }
+      // (a negative scale turns the row's signs)
+      const float down = ldexpf(a.scale < 0.f ? -1.f : 1.f, -e2);
+      const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+      c2 = fmaxf(fabsf(a.scale) * kLog2e * (Q8 ? a.k_scale[use.h] : 1.f) * ldexpf(1.f, e2), 1e-37f);
+      const uint32_t to = base + L::q + x * L::tile + row * 128;
+#pragma unroll
+      for (int c = 0; c < DP / 8; ++c) {
+        uint32_t w[4] = {piece[c].x, piece[c].y, piece[c].z, piece[c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (Q8 && BFQ) w[e] = Half16<false>::pack(Half16<true>::lo(w[e]) * down, Half16<true>::hi(w[e]) * down);
+          else w[e] ^= flip;
+        }
+        sts16(to + (c >> 3) * (kTile * 128) + (((c & 7) ^ (row & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
+      }
+      fence_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::q_ready + x));
+    };
+    int i = 0, done = 0, items = 0;  // tiles; tiles and items of this group
+    bool ok = true, mine = x == 0 || two_tiles(a, use);
+    if (tiles > 0 && mine) fetch();
+    while (i < tiles) {
       const int n = min(use.x.tiles - use.t, tiles - i);
-      if (x == 0 || two_tiles(a, use)) {
-        const int rr = use.b * kItem + x * kRowsOf + row;
-        const bool there = rr < use.k.nq * G;
-        const int q = there ? rr / G : 0, head = use.h * G + (there ? rr - q * G : 0);
-        const int last = there ? use.k.len - use.k.nq + q : -1;
+      // what the end of the item wants to know, when the next one has been opened
+      const long long item_end = item_begin + use.x.tiles;
+      const bool whole = item_begin >= u_begin && item_end <= u_end;
+      const int part = item_begin >= u_begin;  // part 0 began before the worker's range
+      float ref = kUnset;
+      Two sum0 = two(0.f, 0.f), sum1 = two(0.f, 0.f);
+      if (mine) {
+        const int last = there ? use.k.len - use.k.nq + query : -1;
         // the row tile's first and last row
-        const int tile_row = use.b * kItem + x * kRowsOf;
+        const int tile_row = use.x.b * kItem + x * kRowsOf;
         const int last0 = use.k.len - use.k.nq + tile_row / G,
                   last1 = use.k.len - use.k.nq + min(use.k.nq - 1, (tile_row + kRowsOf - 1) / G);
-        // the query row; scores in base 2 per product are c2 times what the products give (never 0, so that
-        // what is masked stays -inf)
-        float c2 = fabsf(a.scale) * kLog2e * (Q8 ? a.k_scale[use.h] : 1.f);
-        {
-          uint4 piece[DP / 8];
-          const uint16_t* from_q = static_cast<const uint16_t*>(a.q) + (int64_t)(use.k.q0 + q) * a.q_stride_token +
-                                   (int64_t)head * a.q_stride_head;
-#pragma unroll
-          for (int c = 0; c < DP / 8; ++c)
-            piece[c] = there && c * 8 < a.D ? *reinterpret_cast<const uint4*>(from_q + c * 8) : make_uint4(0, 0, 0, 0);
-          int e2 = 0;
-          if (Q8 && BFQ) {
-            // fp16 operands: the row is scaled by a power of two to a maximum in [1, 2) (what falls below
-            // 2^-24 of it is lost, far under the sums' rounding)
-            float top = 0.f;
-#pragma unroll
-            for (int c = 0; c < DP / 8; ++c) {
-              const uint32_t w[4] = {piece[c].x, piece[c].y, piece[c].z, piece[c].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) top = max3(top, fabsf(Half16<true>::lo(w[e])), fabsf(Half16<true>::hi(w[e])));
-            }
-            if (top > 0.f && top < INFINITY) e2 = min(max(ilogbf(top), -126), 126);
-          }
-          const float down = (Q8 && BFQ ? ldexpf(1.f, -e2) : 1.f) * flip;
-          c2 = fmaxf(c2 * (Q8 && BFQ ? ldexpf(1.f, e2) : 1.f), 1e-37f);
-#pragma unroll
-          for (int c = 0; c < DP / 8; ++c) {
-            uint32_t w[4] = {piece[c].x, piece[c].y, piece[c].z, piece[c].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (Q8 && BFQ) w[e] = Half16<false>::pack(Half16<true>::lo(w[e]) * down, Half16<true>::hi(w[e]) * down);
-              else if (flip < 0.f) w[e] ^= 0x80008000u;
-            }
-            sts16(q_row + (c >> 3) * (kTile * 128) + (((c & 7) ^ (row & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
-          }
-          fence_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(L::q_ready + x));
-        }
-
-        float ref = kUnset;
-        Two sum0 = two(0.f, 0.f), sum1 = two(0.f, 0.f);
         for (int t = 0; t < n; ++t, ++done) {
           ok = mbar_wait(bar(L::s_full + x), done & 1, abort_flag, a.status, 633);
           if (__any_sync(~0u, !ok)) {
@@ -609,7 +695,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
             const Two ff = two(f, f), zero = two(0.f, 0.f);
             sum0 = fma2(sum0, ff, zero), sum1 = fma2(sum1, ff, zero);
             if (t == 0) return;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DP; c += 16) {
               float o[16];
               tmem_load(o_at + c, o);
@@ -628,6 +714,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
             // (uniform over the group: nobody writes these words before the tile's products are done)
             if ((odd[4 * vs] | odd[4 * vs + 1] | odd[4 * vs + 2] | odd[4 * vs + 3]) != 0) {
               float most = -INFINITY;
+#pragma unroll 1
               for (int c = 0; c < kTile; c += 16) {
                 float y[16];
                 tmem_load(s_at + c, y);
@@ -640,6 +727,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
                 float zero[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e) zero[e] = 0.f;
+#pragma unroll 1
                 for (int c = 0; c < DP; c += 16) tmem_store(o_at + c, zero);
               }
               tmem_store_wait();
@@ -649,6 +737,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
                 const float p = ex2(fmaf(tmem_load1(s_at + k), c2, -ref));
                 const bool sees = k <= hi && k >= lo && page >= 0 && page < a.num_pages;
                 const int64_t at = page * a.page_stride + use.h * a.head_stride + (pos - nth * a.page_size) * a.token_stride;
+#pragma unroll 1
                 for (int c = 0; c < DP; c += 16) {
                   float o[16];
                   tmem_load(o_at + c, o);
@@ -667,28 +756,40 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
               }
             }
           }
-          float s[kTile];
-          tmem_load128(s_at, s);
-          if (edge) {
+          float m[8];
 #pragma unroll
-            for (int k = 0; k < kTile; ++k)
-              if (k > hi || k < lo) s[k] = -INFINITY;
-          }
-          float m0 = max3(s[0], s[1], s[2]), m1 = max3(s[3], s[4], s[5]);
-#pragma unroll
-          for (int k = 6; k + 3 < kTile; k += 4) m0 = max3(m0, s[k], s[k + 1]), m1 = max3(m1, s[k + 2], s[k + 3]);
-          refer(fmaxf(max3(m0, s[kTile - 2], s[kTile - 1]), m1) * c2);
-          // scores to weights, 32 at a time, in the place of the scores (rounded as the product wants them;
-          // the normaliser adds them unrounded)
-          const Two cc = two(c2, c2), rr2 = two(-ref, -ref);
-#pragma unroll
+          for (int k = 0; k < 8; ++k) m[k] = -INFINITY;
+#pragma unroll 1
           for (int c = 0; c < kTile; c += 32) {
+            float s[32];
+            tmem_load32(s_at + c, s);
+            if (edge) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c + e > hi || c + e < lo) s[e] = -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 32; e += 16)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) m[k] = max3(m[k], s[e + k], s[e + k + 8]);
+          }
+          refer(max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7])) * c2);
+          const Two cc = two(c2, c2), rr2 = two(-ref, -ref);
+#pragma unroll 1
+          for (int c = 0; c < kTile; c += 32) {
+            float s[32];
+            tmem_load32(s_at + c, s);
+            if (edge) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (c + e > hi || c + e < lo) s[e] = -INFINITY;
+            }
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               float p0_, p1_, p2_, p3_;
-              apart(fma2(two(s[c + e], s[c + e + 1]), cc, rr2), p0_, p1_);
-              apart(fma2(two(s[c + e + 2], s[c + e + 3]), cc, rr2), p2_, p3_);
+              apart(fma2(two(s[e], s[e + 1]), cc, rr2), p0_, p1_);
+              apart(fma2(two(s[e + 2], s[e + 3]), cc, rr2), p2_, p3_);
               p0_ = ex2(p0_), p1_ = ex2(p1_), p2_ = ex2(p2_), p3_ = ex2(p3_);
               sum0 = add2(sum0, two(p0_, p1_)), sum1 = add2(sum1, two(p2_, p3_));
               w[e / 2] = H::pack(p0_, p1_), w[e / 2 + 1] = H::pack(p2_, p3_);
@@ -701,53 +802,50 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
           if (lane == 0) mbar_arrive(bar(L::p_ready + x));
         }
         if (!ok) break;
-
-        // ---- the item, or this worker's part of it, ends
-        ok = mbar_wait(bar(L::o_done + x), items++ & 1, abort_flag, a.status, 635);
-        if (__any_sync(~0u, !ok)) {
-          ok = false;
-          break;
-        }
-        fence_after();
-        float l0, l1, l2, l3;
-        apart(sum0, l0, l1), apart(sum1, l2, l3);
-        const float sum = (l0 + l1) + (l2 + l3);
-        const long long item_end = item_begin + use.x.tiles;
-        const int64_t place = (int64_t)(use.k.q0 + q) * a.Hq + head;
-        const bool whole = item_begin >= u_begin && item_end <= u_end;
-        const int part = item_begin >= u_begin;  // part 0 began before the worker's range
-        const size_t out_row = (size_t)(worker * 2 + part) * kItem + x * kRowsOf + row;
-        const float f = sum == 0.f ? 0.f : (Q8 ? a.v_scale[use.h] : 1.f) / sum;
-        if (there && whole && a.lse_out != nullptr) a.lse_out[place] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
-        if (there && !whole) scr.stats[out_row] = make_float2(sum == 0.f ? -INFINITY : ref, sum);
-#pragma unroll
-        for (int c = 0; c < DP; c += 32) {
-          float o[32];
-          tmem_load32(o_at + c, o);
-          if (!there) continue;
-          if (!whole) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(scr.out + out_row * DP + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-            continue;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            if (c + e >= a.D) continue;
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[j] = sum == 0.f ? 0u : Half16<BFQ>::pack(o[e + 2 * j] * f, o[e + 2 * j + 1] * f);
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + place * a.D + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-        fence_before();
-        if (!whole && part == 1 && x == 0 && row == 0)
-          scr.share[worker] = Share{use.r, use.h * use.k.blocks + use.b, use.k.q0, use.k.nq, item_begin, item_end};
       }
+      // ---- the item, or this worker's part of it, ends; the next one's queries are fetched first (the last
+      // scores of this one are done)
+      const bool was_mine = mine, was_there = there;
+      const int64_t place = (int64_t)(use.k.q0 + query) * a.Hq + head;
+      const float v_scale = Q8 ? a.v_scale[use.h] : 1.f;
+      if (!whole && part == 1 && x == 0 && row == 0)
+        scr.share[worker] = Share{use.r, use.h * use.k.blocks + use.x.b, use.k.q0, use.k.nq, item_begin, item_end};
       i += n;
-      item_begin += use.x.tiles;
-      if (i < tiles) next_item(a, use);
+      item_begin = item_end;
+      if (i < tiles) {
+        next_item(a, use);
+        mine = x == 0 || two_tiles(a, use);
+        if (mine) fetch();
+      }
+      if (!was_mine) continue;
+      ok = mbar_wait(bar(L::o_done + x), items++ & 1, abort_flag, a.status, 635);
+      if (__any_sync(~0u, !ok)) break;
+      fence_after();
+      float l0, l1, l2, l3;
+      apart(sum0, l0, l1), apart(sum1, l2, l3);
+      const float sum = (l0 + l1) + (l2 + l3), f = sum == 0.f ? 0.f : v_scale / sum;
+      const size_t out_row = (size_t)(worker * 2 + part) * kItem + x * kRowsOf + row;
+      if (was_there && whole && a.lse_out != nullptr) a.lse_out[place] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
+      if (was_there && !whole) scr.stats[out_row] = make_float2(sum == 0.f ? -INFINITY : ref, sum);
+#pragma unroll 1
+      for (int c = 0; c < DP; c += 16) {
+        float o[16];
+        tmem_load(o_at + c, o);
+        if (!was_there) continue;
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(scr.out + out_row * DP + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        } else if (c < a.D) {
+          uint32_t w[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) w[j] = sum == 0.f ? 0u : Half16<BFQ>::pack(o[2 * j] * f, o[2 * j + 1] * f);
+          uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + place * a.D + c);
+          to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+      fence_before();
     }
   }
   __syncwarp();
@@ -755,7 +853,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
   __syncthreads();
   if (warp == 1) {
     fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*reinterpret_cast<volatile uint32_t*>(smem + L::tmem)) : "memory");
   }
 }
 
