@@ -681,7 +681,7 @@ DSPARK_API dspark_status dspark_cache_append(
  *               apart, or NULL.  mask_row [N]: which one row n goes by (out of range: none); NULL:
  *               mask row n.
  * N = 0 does nothing.  Deterministic.  No workspace.
- * Limits: V <= 1048576; R <= 8192.
+ * Limits: V <= 1048576; R <= 8192; n_bias <= 1024; history_width + N below 2^29.
  * ---------------------------------------------------------------------------------- */
 DSPARK_API dspark_status dspark_adjust_logits(
     int N, int V, int R, int dtype, const void* logits, int64_t row_stride, const int32_t* tokens,

@@ -164,6 +164,8 @@ struct AppendArgs {
 };
 cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s);
 
+constexpr int kMaxBias = 1024;
+
 struct AdjustArgs {
   int N, V, R, dtype;
   const void* logits;

@@ -525,11 +525,14 @@ dspark_status dspark_adjust_logits(int N, int V, int R, int dtype, const void* l
   if (row_stride < V) return fail(DSPARK_INVALID_ARG, "row_stride %lld is below V=%d", (long long)row_stride, V);
   if (out_stride < V) return fail(DSPARK_INVALID_ARG, "out_stride %lld is below V=%d", (long long)out_stride, V);
   if (history != nullptr) {
+    if ((int64_t)history_width + N >= 1 << 29)
+      return fail(DSPARK_UNSUPPORTED_SHAPE, "history_width + N = %lld must be below 2^29", (long long)history_width + N);
     if (history_width < 0 || history_stride < history_width)
       return fail(DSPARK_INVALID_ARG, "history_stride %lld is below history_width=%d", (long long)history_stride, history_width);
     CHECK_PTR(history_len);
   }
   if (n_bias < 0) return fail(DSPARK_INVALID_ARG, "n_bias=%d is negative", n_bias);
+  if (n_bias > dspark::kMaxBias) return fail(DSPARK_UNSUPPORTED_SHAPE, "n_bias=%d exceeds %d", n_bias, dspark::kMaxBias);
   if (n_bias > 0) {
     CHECK_PTR(bias_ids);
     CHECK_PTR(bias);
