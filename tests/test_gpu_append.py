@@ -213,3 +213,18 @@ def test_streams_and_graphs(b):
     assert torch.equal(q_out, want)
     for x, y in zip(c.pools, pools):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("scale", [1e-44, 1e-38, 1e-31, 1e-29, 3.3e-3, 0.7, 1.0, 1e29, 1e31, 3e38])
+def test_scales_of_any_size(b, dtype, scale):
+    """Values divided by scales to the ends of fp32's range, as cache_write stores them: bit for bit."""
+    c = Case([400], [400], 1, 2, 64, 16, dtype, E4M3, seed=2)
+    c.scales = [torch.tensor([scale, scale * 1.0001 if scale < 1e38 else scale], device="cuda") for _ in range(2)]
+    size = torch.tensor([1.0, 1e-3, 30.0, 448.0 * scale if 1e-3 < scale < 1e3 else 1.0], device="cuda").repeat(100)[:, None, None]
+    c.v = (c.v.float() * size).to(dtype)
+    c.v[7, 0, 3], c.v[9, 1, 60], c.v[11, 0, 0], c.v[12, 0, 1] = float("inf"), float("-inf"), float("nan"), 0.0
+    c.call(b, b.rotary_rates(64), q=None)
+    d = Case([400], [400], 1, 2, 64, 16, dtype, E4M3, seed=2)
+    b.cache_write(c.k, c.v, *d.pools, _i32(d.table), _i32(d.lens), _i32(d.q_start), k_scale=c.scales[0], v_scale=c.scales[1])
+    assert torch.equal(_bits(c.pools[1]), _bits(d.pools[1]))
