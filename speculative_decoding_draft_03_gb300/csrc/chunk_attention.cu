@@ -21,8 +21,15 @@
 //   * An e4m3 cache is copied as it is; four more warps turn each tile into fp16 (which holds every e4m3
 //     value), and look at the values as warp 3 does otherwise.  bf16 query rows are scaled by powers of
 //     two into fp16's range.
+//   * An item's last scores free its queries' place: the next item's come while those are weighed, and its
+//     first product is issued behind the last one's weights (64 blocks of 512 queries: 280 us so, 370 with
+//     the queries loaded after the last weights, a row a lane).
 //   * The work is dealt out in tiles of 128 tokens that an item sees, evenly over the CTAs; items that
 //     several share are joined by a second kernel, in a fixed order.
+// What bounds it: the products of a tile of both row tiles (D = 128) keep the tensor cores busy for 2050
+// clocks; a tile takes about 3500, the rest being the hand-over from scores to weights and back, which two
+// row tiles in turn do not cover.  8192 causal queries, 32 heads over 8 of 128: 460 us, 1195 TFLOP/s; 2048 at
+// 32768 tokens: 800 us, 1330 TFLOP/s; over e4m3 the conversion comes on top (8192 causal: 542 us).
 // Every mbarrier wait is bounded; a wait that gives up reports DSPARK_TIMEOUT and the CTA winds down.
 #include <algorithm>
 
@@ -36,6 +43,7 @@ using namespace attention;
 constexpr int kRowsOf = 128;           // a row tile
 constexpr int kItem = 2 * kRowsOf;     // an item
 constexpr int kGroupThreads = 128;     // of a softmax group
+constexpr uint32_t kAbs = 0x7FFF7FFFu;  // of two 16-bit floats
 
 // ---------------------------------------------------------------------------- wrappers
 
@@ -105,6 +113,15 @@ __device__ __forceinline__ void tmem_store_u16(uint32_t at, const uint32_t* x) {
       "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]), "r"(x[10]),
       "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15])
       : "memory");
+}
+// 32 bytes, at once where they are aligned to as many.
+__device__ __forceinline__ void store32(void* p, const uint32_t* x, bool at_once) {
+  if (at_once)
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  else
+    store16(p, make_uint4(x[0], x[1], x[2], x[3])), store16(static_cast<char*>(p) + 16, make_uint4(x[4], x[5], x[6], x[7]));
 }
 struct Two {
   unsigned long long v;
@@ -192,12 +209,14 @@ struct Plan {
   static constexpr int k_raw = v + v_stages * tile;     // e4m3: [raw]
   static constexpr int v_raw = k_raw + (Q8 ? raw : 0);  // [raw]
   static constexpr int odd = v_raw + (Q8 ? raw : 0);    // [v_stages][4] words: tokens that rows add on their own
-  static constexpr int bars = odd + 16 * v_stages;
+  static constexpr int odd_told = odd + 16 * v_stages;  // [2][4]: the same, of a row tile's last tile at an edge
+  static constexpr int bars = odd_told + 32;
   // barriers
   static constexpr int k_full = 0, k_empty = k_full + k_stages, v_full = k_empty + k_stages, v_empty = v_full + v_stages,
-                       v_ok = v_empty + v_stages, s_full = v_ok + v_stages, p_ready = s_full + 2, o_done = p_ready + 2,
-                       q_ready = o_done + 2, drained = q_ready + 2, kr_full = drained + 1, kr_empty = kr_full + 1,
-                       vr_full = kr_empty + 1, vr_empty = vr_full + 1, n_bars = vr_empty + 1;
+                       v_ok = v_empty + v_stages, s_full = v_ok + v_stages, p_ready = s_full + 2, told = p_ready + 2,
+                       pv_done = told + 2, odd_done = pv_done + 2, o_done = odd_done + 2, q_ready = o_done + 2,
+                       drained = q_ready + 2, kr_full = drained + 1, kr_empty = kr_full + 1, vr_full = kr_empty + 1,
+                       vr_empty = vr_full + 1, n_bars = vr_empty + 1;
   static constexpr int scan = bars + 8 * n_bars;     // [32] long long
   static constexpr int start_off = scan + 8 * 32;    // long long
   static constexpr int start_r = start_off + 8;      // int, then head, block, tile
@@ -314,6 +333,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
   auto bar = [&](int i) { return base + L::bars + 8 * i; };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::abort_flag);
   volatile uint32_t* odd = reinterpret_cast<volatile uint32_t*>(smem + L::odd);
+  volatile uint32_t* odd_told = reinterpret_cast<volatile uint32_t*>(smem + L::odd_told);
   const long long worker = blockIdx.x, workers = gridDim.x;
   const int G = a.G;
 
@@ -326,6 +346,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(L::s_full + i), 1), mbar_init(bar(L::o_done + i), 1), mbar_init(bar(L::q_ready + i), kGroupThreads / 32);
       mbar_init(bar(L::p_ready + i), kGroupThreads / 32);
+      mbar_init(bar(L::told + i), 1), mbar_init(bar(L::pv_done + i), 1), mbar_init(bar(L::odd_done + i), kGroupThreads / 32);
     }
     mbar_init(bar(L::drained), 1);
     mbar_init(bar(L::kr_full), 1), mbar_init(bar(L::kr_empty), kGroupThreads / 32);
@@ -366,7 +387,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
   };
   // The register file, 65536 less what the launch rounds off: 384 threads of 168, or 512 of 128.
   if (warp < L::softmax_warp) {
-  fewer_registers<Q8 ? 72 : 88>();
+  fewer_registers<Q8 ? 80 : 88>();
   if (warp == 0 || warp == 2) {
     // ---- copies, of keys (warp 0) and of values (warp 2): a lane per box of a tile, its page looked up
     // one tile ahead
@@ -419,7 +440,9 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
     // 797 us so, 969 by one lane in a branch of its own, 988 with the lane chosen by its number).
     auto all = [](bool x) { return __all_sync(~0u, x) != 0; };
     Place use = stand();
-    constexpr uint32_t s_desc = idesc<BFQ && !Q8>(kTile, false, false), o_desc = idesc<BFQ && !Q8>(DP, false, true);
+    // (a negative scale turns the queries' signs)
+    const uint32_t s_desc = idesc<BFQ && !Q8>(kTile, false, false) | (a.scale < 0.f ? 1u << 13 : 0u);
+    constexpr uint32_t o_desc = idesc<BFQ && !Q8>(DP, false, true);
     // (the descriptors' lower halves; the upper one is a constant)
     const uint32_t q_first = (uint32_t)sw128(base + L::q, 16, 1024), k_first = (uint32_t)sw128(base + L::k, 16, 1024),
                    v_first = (uint32_t)sw128(base + L::v, L::panels > 1 ? kTile * 128 : 0, 1024);
@@ -447,12 +470,14 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
     }
     if (ok) commit_one(bar(L::k_empty));
     // what there is to know of a unit's products: where its values lie, whether its item ends with it, whether it
-    // has both row tiles, and whether its first product adds (the first of an item does not, unless rows have
-    // added tokens on their own)
+    // has both row tiles, whether its first product adds (the first of an item does not), and whether some of its
+    // rows see some of its tokens only
     struct Unit {
       uint32_t values, v_at, add;
-      bool ends, two, last;
+      int stage;
+      bool ends, two, last, edge;
     };
+    uint32_t odd_round = 0;  // a bit per row tile
     auto open_unit = [&](int i, bool goes_on) {  // the unit at `use`; moves on to the next
       Unit u;
       u.last = i + 1 == total;
@@ -461,9 +486,9 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
       u.values = v_first + vs * (L::tile / 16);
       u.v_at = bar(vs);
       u.add = goes_on;
-      const bool edge = !goes_on && all(at_edge(a, use.x, use.x.first + use.t * kTile));
+      u.stage = vs;
+      u.edge = all(at_edge(a, use.x, use.x.first + use.t * kTile));
       ok = ok && wait(u.v_at + 8 * (Q8 ? L::v_full : L::v_ok), v_round, 624);
-      if (edge) u.add = all((odd[4 * vs] | odd[4 * vs + 1] | odd[4 * vs + 2] | odd[4 * vs + 3]) != 0);
       if (++vs == L::v_stages) vs = 0, v_round ^= 1;
       if (!u.ends) ++use.t;
       else if (!u.last) next_item(a, use), both = all(two_tiles(a, use));
@@ -485,6 +510,18 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
           mma_ts_one(tmem + 2 * kTile + x * DP, tmem + x * kTile + 8 * kk, now.values + kk * 128, o_desc, kk > 0 ? 1u : now.add);
+        if (now.edge) {
+          const uint32_t word = lane < 4 ? odd[4 * now.stage + lane] : 0u;
+          if (lane < 4) odd_told[4 * x + lane] = word;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::told + x));
+          if (__any_sync(~0u, word != 0)) {  // the rows read the weights and add theirs before either is written again
+            commit_one(bar(L::pv_done + x));
+            ok = wait(bar(L::odd_done + x), odd_round >> x & 1, 637);
+            odd_round ^= 1u << x;
+            fence_after();
+          }
+        }
         if (now.ends) commit_one(bar(L::o_done + x));
       };
       auto next = [&](int x) {
@@ -529,15 +566,14 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
           auto piece = [&](int c) { return row + (c >> 3) * (kTile * 128) + (((c & 7) ^ (token & 7)) << 4); };
           const bool unseen = pos > use.x.last1 || (a.window > 0 && pos <= use.x.last0 - a.window);
           const bool partly = !unseen && (pos > use.x.last0 || (a.window > 0 && pos <= use.x.last1 - a.window));
-          bool strange = false;
-          if (partly)
+          uint32_t top = 0;  // the largest exponents, by halves
+          if (__any_sync(~0u, partly))
 #pragma unroll 4
             for (int c = 0; c < L::panels * 8; ++c) {
               const uint4 v = lds16(piece(c));
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) strange |= (w[e] & H::kExp) == H::kExp || ((w[e] >> 16) & H::kExp) == H::kExp;
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs), __vmaxu2(v.z & kAbs, v.w & kAbs)));
             }
+          const bool strange = partly && ((top & 0xFFFFu) >= H::kExp || (top >> 16) >= H::kExp);
           const uint32_t strangers = __ballot_sync(~0u, strange);
           if (lane == 0) odd[4 * vs + j] = strangers;
           if (unseen || strange)
@@ -557,7 +593,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
       const int ks = i % L::k_stages, vs = i % L::v_stages, p0 = use.x.first + use.t * kTile, pos = p0 + token;
       auto convert = [&](uint32_t from, uint32_t to, bool clear, bool look) {
         bool strange = false;
-#pragma unroll
+#pragma unroll 1  // (unrolled, it crowds the instruction cache: 8192 queries 570 us for 542, 65536 tokens the same)
         for (int c = 0; c < 8; ++c) {
           const uint4 x = lds16(from + token * 128 + ((c ^ (token & 7)) << 4));
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -604,89 +640,115 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
     }
   }
   } else {
-    more_registers<Q8 ? 184 : 208>();
+    more_registers<Q8 ? 176 : 208>();
     // ---- softmax: group x has row tile x; a thread, the row of its TMEM lane
     Place use = stand();
     const int x = (warp - L::softmax_warp) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + x * kTile, o_at = tmem + lanes + 2 * kTile + x * DP;
     long long item_begin = u_begin - use.t;
-    // The item's row of this thread: its query's number (of the request) and head, or none.  Its query is
-    // fetched and laid out for the products; scores in base 2 are c2 times what they give (never 0, so that
-    // what is masked stays -inf).
+    // The item's row of this thread: its query's number (of the request) and head, or none; scores in base 2 are
+    // c2 times what the products give (never 0, so that what is masked stays -inf).  The warp copies its 32 query
+    // rows to where the products read them, DP / 8 lanes a row, and says so when they have come.
     bool there;
     int query, head;
     float c2;
+    const float per_g = 1.f / (float)G;
     auto fetch = [&]() {
-      const int rr = use.x.b * kItem + x * kRowsOf + row;
-      there = rr < use.k.nq * G;
-      query = there ? rr / G : 0;
-      head = use.h * G + (there ? rr - query * G : 0);
-      const uint16_t* from = static_cast<const uint16_t*>(a.q) + (int64_t)(use.k.q0 + query) * a.q_stride_token +
-                             (int64_t)head * a.q_stride_head;
-      uint4 piece[DP / 8];
-#pragma unroll
-      for (int c = 0; c < DP / 8; ++c)
-        piece[c] = there && c * 8 < a.D ? *reinterpret_cast<const uint4*>(from + c * 8) : make_uint4(0, 0, 0, 0);
+      constexpr int kPieces = DP / 8, kRows = 32 / kPieces;  // of a row; rows at a time
+      const int warp_row = use.x.b * kItem + x * kRowsOf + (row & ~31), q0 = warp_row / G, g0 = warp_row - q0 * G;
+      auto query_of = [&](int r) { return (int)(((float)(g0 + r) + 0.5f) * per_g); };  // from q0 on (exact: below 2^8)
+      const int c = lane % kPieces, left = use.k.nq - q0;
+      const uint16_t* from = static_cast<const uint16_t*>(a.q) + (int64_t)(use.k.q0 + q0) * a.q_stride_token +
+                             (int64_t)use.h * G * a.q_stride_head + c * 8;
+#pragma unroll 4
+      for (int r = lane / kPieces; r < 32; r += kRows) {
+        const int q = query_of(r), at = (row & ~31) + r;
+        const bool real = q < left && c * 8 < a.D;
+        copy16(base + L::q + x * L::tile + at * 128 + (c >> 3) * (kTile * 128) + (((c & 7) ^ (at & 7)) << 4),
+               real ? from + q * a.q_stride_token + (g0 + r - q * G) * a.q_stride_head : a.q, real);
+      }
+      query = query_of(lane);
+      there = query < left;
+      head = use.h * G + g0 + lane - query * G;
+      query += q0;
+    };
+    auto fetched = [&]() {
+      copy_commit();
+      copy_wait<0>();
       int e2 = 0;
       if (Q8 && BFQ) {
         // fp16 operands: the row is scaled by a power of two to a maximum in [1, 2) (what falls below 2^-24 of
         // it is lost, far under the sums' rounding)
-        float top = 0.f;
-#pragma unroll
+        __syncwarp();
+        const uint32_t mine = base + L::q + x * L::tile + row * 128;
+        auto piece = [&](int c) { return mine + (c >> 3) * (kTile * 128) + (((c & 7) ^ (row & 7)) << 4); };
+        uint32_t top = 0;  // (floats without their signs are in the order of their bits)
+#pragma unroll 4
         for (int c = 0; c < DP / 8; ++c) {
-          const uint32_t w[4] = {piece[c].x, piece[c].y, piece[c].z, piece[c].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = max3(top, fabsf(Half16<true>::lo(w[e])), fabsf(Half16<true>::hi(w[e])));
+          const uint4 v = lds16(piece(c));
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs), __vmaxu2(v.z & kAbs, v.w & kAbs)));
         }
-        if (top > 0.f && top < INFINITY) e2 = min(max(ilogbf(top), -126), 126);
-      }
-      // (a negative scale turns the row's signs)
-      const float down = ldexpf(a.scale < 0.f ? -1.f : 1.f, -e2);
-      const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-      c2 = fmaxf(fabsf(a.scale) * kLog2e * (Q8 ? a.k_scale[use.h] : 1.f) * ldexpf(1.f, e2), 1e-37f);
-      const uint32_t to = base + L::q + x * L::tile + row * 128;
+        const int most = (int)(max(top & 0xFFFFu, top >> 16) >> 7);  // its exponent's bits
+        e2 = most == 0xFF ? 0 : min(max(most, 1), 253) - 127;
+        if (top == 0) e2 = 0;
+        const float down = __int_as_float((127 - e2) << 23);
+#pragma unroll 2
+        for (int c = 0; c < DP / 8; ++c) {
+          const uint4 v = lds16(piece(c));
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int c = 0; c < DP / 8; ++c) {
-        uint32_t w[4] = {piece[c].x, piece[c].y, piece[c].z, piece[c].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (Q8 && BFQ) w[e] = Half16<false>::pack(Half16<true>::lo(w[e]) * down, Half16<true>::hi(w[e]) * down);
-          else w[e] ^= flip;
+          for (int e = 0; e < 4; ++e) w[e] = Half16<false>::pack(Half16<true>::lo(w[e]) * down, Half16<true>::hi(w[e]) * down);
+          sts16(piece(c), make_uint4(w[0], w[1], w[2], w[3]));
         }
-        sts16(to + (c >> 3) * (kTile * 128) + (((c & 7) ^ (row & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
       }
+      c2 = fmaxf(fabsf(a.scale) * kLog2e * (Q8 ? a.k_scale[use.h] : 1.f) * __int_as_float((127 + e2) << 23), 1e-37f);
       fence_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::q_ready + x));
     };
-    int i = 0, done = 0, items = 0;  // tiles; tiles and items of this group
+    int i = 0, done = 0, items = 0, edges = 0, odds = 0;  // tiles; this group's tiles, items, tiles at edges, with odd values
     bool ok = true, mine = x == 0 || two_tiles(a, use);
-    if (tiles > 0 && mine) fetch();
+    if (tiles > 0 && mine) fetch(), fetched();
     while (i < tiles) {
       const int n = min(use.x.tiles - use.t, tiles - i);
-      // what the end of the item wants to know, when the next one has been opened
+      // what is asked about the item when the next one has been opened
       const long long item_end = item_begin + use.x.tiles;
       const bool whole = item_begin >= u_begin && item_end <= u_end;
       const int part = item_begin >= u_begin;  // part 0 began before the worker's range
+      const bool was_mine = mine, was_there = there, more = i + n < tiles;
+      const int r = use.r, h = use.h, last = there ? use.k.len - use.k.nq + query : -1;
+      const int64_t place = (int64_t)(use.k.q0 + query) * a.Hq + head;
+      if (!whole && part == 1 && x == 0 && row == 0)
+        scr.share[worker] = Share{r, h * use.k.blocks + use.x.b, use.k.q0, use.k.nq, item_begin, item_end};
+      item_begin = item_end;
+      // the row tile's first and last row
+      const int tile_row = use.x.b * kItem + x * kRowsOf;
+      const int last0 = use.k.len - use.k.nq + tile_row / G,
+                last1 = use.k.len - use.k.nq + min(use.k.nq - 1, (tile_row + kRowsOf - 1) / G);
+      const int begin = use.x.first + use.t * kTile;
+      const int gate_from = use.x.last0 - kTile + 2, gate_upto = a.window > 0 ? use.x.last1 - a.window : -1;
       float ref = kUnset;
       Two sum0 = two(0.f, 0.f), sum1 = two(0.f, 0.f);
-      if (mine) {
-        const int last = there ? use.k.len - use.k.nq + query : -1;
-        // the row tile's first and last row
-        const int tile_row = use.x.b * kItem + x * kRowsOf;
-        const int last0 = use.k.len - use.k.nq + tile_row / G,
-                  last1 = use.k.len - use.k.nq + min(use.k.nq - 1, (tile_row + kRowsOf - 1) / G);
-        for (int t = 0; t < n; ++t, ++done) {
-          ok = mbar_wait(bar(L::s_full + x), done & 1, abort_flag, a.status, 633);
+      for (int t = mine ? 0 : n - 1; t < n; ++t) {
+        if (was_mine) {
+          ok = mbar_wait(bar(L::s_full + x), done++ & 1, abort_flag, a.status, 633);
           if (__any_sync(~0u, !ok)) {
             ok = false;
             break;
           }
           fence_after();  // (and the tile before is in O: its product was issued before this S)
-          const int p0 = use.x.first + (use.t + t) * kTile;
-          const bool edge = p0 + kTile - 1 > last0 || (a.window > 0 && p0 <= last1 - a.window);
-          const int hi = last - p0, lo = a.window > 0 ? hi - a.window + 1 : 0;  // the columns that this row sees
+        }
+        const int p0 = begin + t * kTile;
+        // (a request's or a window's end may be an edge of the item and none of this row tile)
+        const bool gated = p0 >= gate_from || p0 <= gate_upto, leaves = t + 1 == n && more;
+        if (__builtin_expect(leaves, 0)) {  // the next item's queries are on their way from here on
+          next_item(a, use);
+          mine = x == 0 || two_tiles(a, use);
+          if (mine) fetch();
+        }
+        if (was_mine) {
+          const bool edge = __builtin_expect(gated, 0) && (p0 + kTile - 1 > last0 || (a.window > 0 && p0 <= last1 - a.window));
           // a new reference where a score passes the old one by too much
           auto refer = [&](float most) {
             if (!__any_sync(~0u, most > ref + (kSlack + H::kLift))) return;
@@ -704,57 +766,23 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
               tmem_store(o_at + c, o);
             }
           };
-          if (at_edge(a, use.x, p0)) {
-            const int vs = (i + t) % L::v_stages;
-            ok = mbar_wait(bar((Q8 ? L::v_full : L::v_ok) + vs), ((i + t) / L::v_stages) & 1, abort_flag, a.status, 634);
-            if (__any_sync(~0u, !ok)) {
-              ok = false;
-              break;
+          // what the row does not see goes out of its scores, in a pass of its own: the loops below stay short (with
+          // the selects in them, 8192 causal queries take 474 us for 460, and D = 64 452 for 419)
+          if (edge) {
+            const int hi = last - p0, lo = a.window > 0 ? hi - a.window + 1 : 0;
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 16) {
+              float s[16];
+              tmem_load(s_at + c, s);
+              // a bit for each of the columns that it does see
+              const uint32_t upto = hi - c >= 31 ? ~0u : (hi < c ? 0u : (2u << (hi - c)) - 1),
+                             before = lo <= c ? 0u : (lo - c >= 32 ? ~0u : (1u << (lo - c)) - 1), bits = upto & ~before;
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (!((bits >> e) & 1u)) s[e] = -INFINITY;
+              tmem_store(s_at + c, s);
             }
-            // (uniform over the group: nobody writes these words before the tile's products are done)
-            if ((odd[4 * vs] | odd[4 * vs + 1] | odd[4 * vs + 2] | odd[4 * vs + 3]) != 0) {
-              float most = -INFINITY;
-#pragma unroll 1
-              for (int c = 0; c < kTile; c += 16) {
-                float y[16];
-                tmem_load(s_at + c, y);
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (c + e <= hi && c + e >= lo) most = fmaxf(most, y[e]);
-              }
-              refer(most * c2);
-              if (t == 0) {
-                float zero[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) zero[e] = 0.f;
-#pragma unroll 1
-                for (int c = 0; c < DP; c += 16) tmem_store(o_at + c, zero);
-              }
-              tmem_store_wait();
-              for (int k = 0; k < kTile; ++k) {
-                if (((odd[4 * vs + (k >> 5)] >> (k & 31)) & 1u) == 0) continue;
-                const int pos = p0 + k, nth = pos / a.page_size, page = a.page_table[use.r * a.table_stride + nth];
-                const float p = ex2(fmaf(tmem_load1(s_at + k), c2, -ref));
-                const bool sees = k <= hi && k >= lo && page >= 0 && page < a.num_pages;
-                const int64_t at = page * a.page_stride + use.h * a.head_stride + (pos - nth * a.page_size) * a.token_stride;
-#pragma unroll 1
-                for (int c = 0; c < DP; c += 16) {
-                  float o[16];
-                  tmem_load(o_at + c, o);
-                  if (sees && c < a.D) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                      float v;
-                      if (Q8) v = Half16<false>::lo(e4m3_to_half2(static_cast<const uint8_t*>(a.v_pool)[at + c + e]));
-                      else v = H::lo(static_cast<const uint16_t*>(a.v_pool)[at + c + e]);
-                      o[e] = fmaf(p, v, o[e]);
-                    }
-                  }
-                  tmem_store(o_at + c, o);
-                  tmem_store_wait();
-                }
-              }
-            }
+            tmem_store_wait();
           }
           float m[8];
 #pragma unroll
@@ -763,11 +791,6 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
           for (int c = 0; c < kTile; c += 32) {
             float s[32];
             tmem_load32(s_at + c, s);
-            if (edge) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c + e > hi || c + e < lo) s[e] = -INFINITY;
-            }
 #pragma unroll
             for (int e = 0; e < 32; e += 16)
 #pragma unroll
@@ -779,11 +802,6 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
           for (int c = 0; c < kTile; c += 32) {
             float s[32];
             tmem_load32(s_at + c, s);
-            if (edge) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c + e > hi || c + e < lo) s[e] = -INFINITY;
-            }
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
@@ -800,49 +818,80 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::p_ready + x));
+          }
+        if (__builtin_expect(leaves && mine, 0)) fetched();
+        // values that are not finite, where only some rows see them, have been taken out of the product: the
+        // rows that do add them on their own, with the weights as they were told
+        if (__builtin_expect(was_mine && gated, 0)) {
+          ok = mbar_wait(bar(L::told + x), edges & 1, abort_flag, a.status, 634);
+          ++edges;
+          // (uniform over the group: these words are not written before it has told its next weights)
+          const bool some = ok && (odd_told[4 * x] | odd_told[4 * x + 1] | odd_told[4 * x + 2] | odd_told[4 * x + 3]) != 0;
+          if (some) ok = mbar_wait(bar(L::pv_done + x), odds & 1, abort_flag, a.status, 638);
+          if (__any_sync(~0u, !ok)) {
+            ok = false;
+            break;
+          }
+          if (some) {
+            ++odds;
+            fence_after();
+#pragma unroll 1
+            for (int k = 0; k < kTile; ++k) {
+              if (((odd_told[4 * x + (k >> 5)] >> (k & 31)) & 1u) == 0) continue;
+              const int pos = p0 + k, nth = pos / a.page_size, page = a.page_table[r * a.table_stride + nth];
+              const uint32_t two_weights = __float_as_uint(tmem_load1(s_at + k / 2));
+              const float p = k & 1 ? H::hi(two_weights) : H::lo(two_weights);
+              const bool sees = pos <= last && (a.window == 0 || pos > last - a.window) && page >= 0 && page < a.num_pages;
+              const int64_t at = page * a.page_stride + h * a.head_stride + (pos - nth * a.page_size) * a.token_stride;
+#pragma unroll 1
+              for (int c = 0; c < DP; c += 16) {
+                float o[16];
+                tmem_load(o_at + c, o);
+                if (sees && c < a.D) {
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    float v;
+                    if (Q8) v = Half16<false>::lo(e4m3_to_half2(static_cast<const uint8_t*>(a.v_pool)[at + c + e]));
+                    else v = H::lo(static_cast<const uint16_t*>(a.v_pool)[at + c + e]);
+                    o[e] = fmaf(p, v, o[e]);
+                  }
+                }
+                tmem_store(o_at + c, o);
+                tmem_store_wait();
+              }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(L::odd_done + x));
+          }
         }
-        if (!ok) break;
       }
-      // ---- the item, or this worker's part of it, ends; the next one's queries are fetched first (the last
-      // scores of this one are done)
-      const bool was_mine = mine, was_there = there;
-      const int64_t place = (int64_t)(use.k.q0 + query) * a.Hq + head;
-      const float v_scale = Q8 ? a.v_scale[use.h] : 1.f;
-      if (!whole && part == 1 && x == 0 && row == 0)
-        scr.share[worker] = Share{use.r, use.h * use.k.blocks + use.x.b, use.k.q0, use.k.nq, item_begin, item_end};
       i += n;
-      item_begin = item_end;
-      if (i < tiles) {
-        next_item(a, use);
-        mine = x == 0 || two_tiles(a, use);
-        if (mine) fetch();
-      }
+      if (!ok) break;
       if (!was_mine) continue;
       ok = mbar_wait(bar(L::o_done + x), items++ & 1, abort_flag, a.status, 635);
       if (__any_sync(~0u, !ok)) break;
       fence_after();
       float l0, l1, l2, l3;
       apart(sum0, l0, l1), apart(sum1, l2, l3);
-      const float sum = (l0 + l1) + (l2 + l3), f = sum == 0.f ? 0.f : v_scale / sum;
+      const float sum = (l0 + l1) + (l2 + l3), f = sum == 0.f ? 0.f : (Q8 ? a.v_scale[h] : 1.f) / sum;
       const size_t out_row = (size_t)(worker * 2 + part) * kItem + x * kRowsOf + row;
       if (was_there && whole && a.lse_out != nullptr) a.lse_out[place] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
       if (was_there && !whole) scr.stats[out_row] = make_float2(sum == 0.f ? -INFINITY : ref, sum);
+      const bool in_32 = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0;
 #pragma unroll 1
       for (int c = 0; c < DP; c += 16) {
         float o[16];
         tmem_load(o_at + c, o);
         if (!was_there) continue;
         if (!whole) {
-#pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(scr.out + out_row * DP + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          store32(scr.out + out_row * DP + c, reinterpret_cast<const uint32_t*>(o), true);
+          store32(scr.out + out_row * DP + c + 8, reinterpret_cast<const uint32_t*>(o + 8), true);
         } else if (c < a.D) {
           uint32_t w[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) w[j] = sum == 0.f ? 0u : Half16<BFQ>::pack(o[2 * j] * f, o[2 * j + 1] * f);
-          uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + place * a.D + c);
-          to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          store32(static_cast<uint16_t*>(a.out) + place * a.D + c, w, in_32);
         }
       }
       fence_before();
