@@ -9,7 +9,11 @@ choices, verify lengths and accepted counts stay there, and the block of verifie
 inside buffers of fixed size.  A request that the pool has no room for emits nothing that round, and
 goes on once pages are given back.
 
+With ``rotary`` the target's queries and keys are turned by their positions as they are appended to
+the cache, and with ``adjust`` the verified logits are penalised, biased and masked first.
+
     python examples/serving_loop.py --rounds 8
+    python examples/serving_loop.py --rounds 8 --rotary --repetition 1.2 --prompt 2000
 """
 import argparse
 import math
@@ -24,15 +28,17 @@ from speculative_decoding_draft_03_gb300 import binding as b  # noqa: E402
 from speculative_decoding_draft_03_gb300 import workloads as wl  # noqa: E402
 
 
-MAX_BLOCK = 128  # queries of a request in one attention call, at most
+MAX_BLOCK = 512  # tokens of a prompt that go through the target at once
 
 
 class ToyTarget:
     """layers x (grouped-query attention + residual) between an embedding and an unembedding."""
 
-    def __init__(self, V, dim=128, layers=2, Hq=8, Hkv=2, D=64, seed=0, device="cuda"):
+    def __init__(self, V, dim=128, layers=2, Hq=8, Hkv=2, D=64, seed=0, device="cuda", rates=None):
+        """rates (binding.rotary_rates): queries and keys are turned by their positions."""
         g = torch.Generator(device=device).manual_seed(seed)
         rnd = lambda *s: torch.randn(s, generator=g, device=device)
+        self.rates = rates
         self.V, self.dim, self.layers, self.Hq, self.Hkv, self.D = V, dim, layers, Hq, Hkv, D
         self.embed = rnd(V, dim)
         self.wq = rnd(layers, dim, Hq * D) / math.sqrt(dim) * 2
@@ -57,10 +63,22 @@ class ToyTarget:
         x = self.embed[tokens.long()]
         for layer in range(self.layers):
             q, k, v = self.qkv(layer, x)
-            cache.write(layer, k, v, q_start)
+            if self.rates is None:
+                cache.write(layer, k, v, q_start)
+            else:
+                cache.append(layer, q, k, v, q_start, self.rates, q_out=q)
             o = cache.attend(layer, q, q_start, max_q, self.D ** -0.5)["out"]
             x = x + self.out(layer, torch.nan_to_num(o))  # (rows of no request hold anything)
         return x @ self.unembed
+
+    def turned(self, x):
+        """x [T,H,D] float64 turned by the positions 0 .. T-1, rounded to bfloat16."""
+        if self.rates is None:
+            return x
+        turns = torch.arange(x.shape[0], device=x.device)[:, None] * self.rates  # (past 64 bits: whole turns)
+        a = (turns.double() * 2.0 ** -63 * math.pi)[:, None]
+        u, w = x.chunk(2, 2)
+        return torch.cat([u * a.cos() - w * a.sin(), w * a.cos() + u * a.sin()], 2).bfloat16().double()
 
     def dense(self, tokens):
         """The same for one whole sequence, without a cache, in float64 (its 16-bit roundings of
@@ -70,6 +88,7 @@ class ToyTarget:
         mask = torch.ones((T, T), dtype=torch.bool, device=x.device).tril()
         for layer in range(self.layers):
             q, k, v = (t.double() for t in self.qkv(layer, x.float()))
+            q, k = self.turned(q), self.turned(k)
             k, v = (t.repeat_interleave(self.Hq // self.Hkv, 1) for t in (k, v))
             s = torch.einsum("thd,shd->hts", q, k) * self.D ** -0.5
             p = torch.softmax(s.masked_fill(~mask, -math.inf), 2)
@@ -80,13 +99,17 @@ class ToyTarget:
 class ServingLoop:
     """R requests in R slots of a paged cache, advanced by speculative rounds."""
 
-    def __init__(self, prompts, gamma=4, page_size=16, num_pages=256, top_k=3, seed=0, cache_dtype=torch.bfloat16):
+    def __init__(self, prompts, gamma=4, page_size=16, num_pages=256, top_k=3, seed=0, cache_dtype=torch.bfloat16,
+                 rotary=False, adjust=None, block=MAX_BLOCK):
+        """rotary: with rotary positions.  adjust: dict of what adjust_logits takes for all requests alike,
+        repetition, frequency, presence (floats), bias (dict of id: what is added), mask (bool [V],
+        the ids that are allowed).  block: tokens of a prompt that go through the target at once."""
         dev = "cuda"
         self.R, self.gamma, self.top_k = len(prompts), gamma, top_k
         # sizes, step-rate table and request keys of the smallest workload; as the draft's Markov head
         # the target without its attention, W1 = embedding, W2 = unembedding, so that it is often right
         self.w = wl.make("tiny", device=dev, R=self.R, gamma=gamma)
-        self.target = ToyTarget(self.w["V"], seed=seed)
+        self.target = ToyTarget(self.w["V"], seed=seed, rates=b.rotary_rates(64) if rotary else None)
         rank, d = self.target.dim, self.w["d"]
         self.w.update(U=torch.zeros_like(self.w["U"]), W1=self.target.embed.contiguous(),
                       W2=self.target.unembed.contiguous(), rank=rank, conf_w=torch.zeros(d + rank, device=dev), conf_b=1.0)
@@ -97,15 +120,39 @@ class ServingLoop:
         self.T = self.R * (gamma + 1)  # rows of the largest verified block
         i = torch.arange(self.T, device=dev)
         self.row_index = i
-        self.prefill(prompts)
+        self.prefill(prompts, block)
+        self.adjust = None if adjust is None else self.adjustment(prompts, **adjust)
         self.rounds = 0
 
-    def prefill(self, prompts):
-        """Every token but the last goes into the cache, in blocks that one attention call takes; the
-        last is the first anchor."""
+    def adjustment(self, prompts, repetition=None, frequency=None, presence=None, bias=None, mask=None):
+        """What adjust_logits takes beside the logits and the block: the requests' tokens so far are kept
+        on the device, one row each, as long as the cache's contexts."""
+        R, V, dev = self.R, self.w["V"], "cuda"
+        i32 = dict(dtype=torch.int32, device=dev)
+        width = self.cache.page_table.shape[1] * self.cache.page_size + self.gamma + 1
+        history = torch.full((R, width), -1, **i32)
+        for r, p in enumerate(prompts):
+            history[r, :len(p)] = torch.tensor(p, **i32)
+        o = dict(history=history, prompt_len=torch.tensor([len(p) for p in prompts], **i32))
+        for name, x in (("repetition", repetition), ("frequency", frequency), ("presence", presence)):
+            if x is not None:
+                o[name] = torch.full((R,), float(x), device=dev)
+        if bias:
+            o["bias_ids"] = torch.tensor([list(bias)] * R, **i32)
+            o["bias"] = torch.tensor([list(bias.values())] * R, dtype=torch.float32, device=dev)
+        if mask is not None:
+            bits = torch.zeros((V + 31) // 32 * 32, dtype=torch.int64)
+            bits[:V] = mask.cpu()
+            words = (bits.view(-1, 32) << torch.arange(32)).sum(1)
+            o["mask"] = torch.where(words >= 2 ** 31, words - 2 ** 32, words).to(**i32)[None]
+            o["mask_row"] = torch.zeros(self.T, **i32)
+        return o
+
+    def prefill(self, prompts, block):
+        """Every token but the last goes into the cache, a block at a time; the last is the first anchor."""
         dev = "cuda"
-        for at in range(0, max(len(p) - 1 for p in prompts), MAX_BLOCK):
-            blocks = [p[at:min(at + MAX_BLOCK, len(p) - 1)] for p in prompts]
+        for at in range(0, max(len(p) - 1 for p in prompts), block):
+            blocks = [p[at:min(at + block, len(p) - 1)] for p in prompts]
             n = [len(x) for x in blocks]
             q_start = torch.tensor([sum(n[:r]) for r in range(self.R + 1)], dtype=torch.int32, device=dev)
             want = torch.tensor(n, dtype=torch.int32, device=dev)
@@ -132,11 +179,16 @@ class ServingLoop:
         block = torch.cat([self.x0[:, None], d["x"]], 1)
         before = c.seq_len.clone()
         room = c.reserve(n_new)["granted"] > 0
-        logits = self.target.forward(block[r, i], c, q_start, G1)
+        fed = block[r, i]
+        logits = self.target.forward(fed, c, q_start, G1)
+        if self.adjust is not None:  # (a request's tokens so far: its context's)
+            b.adjust_logits(logits, fed, q_start, history_len=before, out=logits, **self.adjust)
         v = b.verify_ragged(logits, q_start[:-1].contiguous(), w["U"], w["W1"], w["W2"], self.x0, d["x"], d["logq"],
                             d["lse"], ell, w["temperature"], w["req_id"], w["seed"], self.rounds)
         c.truncate(before + 1 + v["n_acc"])  # the anchor and the accepted drafts stay
         n_out, n_acc = v["n_out"] * room, v["n_acc"] * room
+        if self.adjust is not None:  # the block's tokens after the context's: as many of them as stay count
+            self.adjust["history"].scatter_(1, before.long()[:, None] + torch.arange(G1, device="cuda"), block)
         answer = torch.where(room[:, None], v["tokens"], -1)
         # row i of a request gave its token i: what was emitted keeps its row's log probability
         mine = (self.row_index < q_start[-1]) & (i < n_out[r])
@@ -157,11 +209,16 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--rounds", type=int, default=8)
     ap.add_argument("--requests", type=int, default=4)
+    ap.add_argument("--prompt", type=int, default=60, help="tokens of the longest prompt, about")
+    ap.add_argument("--rotary", action="store_true")
+    ap.add_argument("--repetition", type=float, default=None)
     a = ap.parse_args()
     g = torch.Generator().manual_seed(1)
     prompts = [torch.randint(0, 1024, (int(n),), generator=g).tolist()
-               for n in torch.randint(2, 60, (a.requests,), generator=g)]
-    loop = ServingLoop(prompts)
+               for n in torch.randint(2, max(a.prompt, 3), (a.requests,), generator=g)]
+    pages = -(-(a.prompt + a.rounds * 5 + 5) // 16) * a.requests
+    loop = ServingLoop(prompts, num_pages=max(256, pages), rotary=a.rotary,
+                       adjust=None if a.repetition is None else dict(repetition=a.repetition))
     answers = [[] for _ in prompts]
     for _ in range(a.rounds):
         o = loop.step()

@@ -212,3 +212,14 @@ def test_the_plain_forms(b):
     want[1, 1], want[1, 0], want[1, 2:] = r(z[1, 1], 2) - 0.5 - 0.5, z[1, 0] + 3, -math.inf
     want[2, 4], want[2, 8] = r(z[2, 4], 0.5) - 2.0, z[2, 8] + 4
     np.testing.assert_allclose(got, want, atol=1e-12)
+
+
+def test_limits_of_adjust_logits(b):
+    """The largest sizes that are taken, and the first that are refused."""
+    def call(N, hw, nb):
+        return b.lib.dspark_adjust_logits(N, 100, 2, 0, P[0], 100, P[1], P[2], P[3], hw, hw, P[4], P[5], P[6], P[7], P[8], nb, P[9],
+                                          P[10], P[11], 4, N, None, P[13], 100, None)
+
+    assert call(0, 50, 1024) == OK and call(0, 50, 1025) == UNSUPPORTED and "n_bias=1025" in _message(b)
+    assert call(0, (1 << 29) - 1, 3) == OK and call(0, 1 << 29, 3) == UNSUPPORTED and "2^29" in _message(b)
+    assert call(5, (1 << 29) - 5, 3) == UNSUPPORTED and call((1 << 31) - 1, (1 << 31) - 1, 3) == UNSUPPORTED
