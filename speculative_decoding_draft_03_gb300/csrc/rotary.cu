@@ -9,7 +9,9 @@
 //     heads, into shared memory; then each takes 16-byte pieces: in the half layout the same piece of
 //     both halves, in the interleaved one a piece of neighbouring pairs.
 //   * The rotation is two products and a sum in fp32; one rounding to the stored type.
-// What bounds it: device memory (each element is read and written once).
+// What bounds it: device memory, each element being read and written once.  8192 tokens of 40 heads of 128 in
+// bf16: 28.8 us, 86 % of the copy rate; 16 prompts (8.5 K tokens) appended to an e4m3 cache: 39.6 us, 79 %;
+// one token of each of 32 requests: 2.5 us, the launch.
 #include <algorithm>
 
 #include "serving.cuh"
@@ -328,7 +330,7 @@ cudaError_t launch(const RotaryArgs& a, cudaStream_t s) {
   // back: 51.5 and 51.2)
   constexpr int kThreads = sizeof(T) == 4 ? 256 : 128;
   const int tokens = std::max(1, std::min(kTokens, a.T / (4 * sm_count())));
-  const dim3 grid((unsigned)((a.T + tokens - 1) / tokens));
+  const dim3 grid((unsigned)(((int64_t)a.T + tokens - 1) / tokens));
   const size_t smem = (size_t)tokens * (a.rot / 2) * sizeof(float2);
   if (tokens == 1)  // (few tokens: what counts is one's time)
     return wide ? launch_chained(rotary_kernel<T, INTER, true, 256>, grid, dim3(256), smem, s, 1, a, tokens)
@@ -343,7 +345,7 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
   // the verified block of 32 requests: 512 threads 3.8 us, 256 4.2, 128 5.2)
   const size_t one = (size_t)(a.rot / 2) * sizeof(float2);
   if (a.T >= 8 * sm_count())
-    return launch_chained(append_kernel<T, INTER, QUANT, 128, 2>, dim3((unsigned)((a.T + 1) / 2)), dim3(128), 2 * one, s, 1, a, 2);
+    return launch_chained(append_kernel<T, INTER, QUANT, 128, 2>, dim3((unsigned)(((int64_t)a.T + 1) / 2)), dim3(128), 2 * one, s, 1, a, 2);
   return launch_chained(append_kernel<T, INTER, QUANT, 512, 1>, dim3((unsigned)a.T), dim3(512), one, s, 1, a, 1);
 }
 template <typename T, bool INTER>
