@@ -1076,9 +1076,10 @@ class PagedCache:
                             k_scale=self.k_scale, v_scale=self.v_scale, q_out=q_out, ws=self.ws, stream=stream)
 
     def attend(self, layer, q, q_start, max_q, scale, window=0, out=None, stream=None):
-        """Blocks of more than 128 queries a slot (max_q) go to chunk_attention.  The scratch is made on the first call of a stream and a size class (heads and max_q decide
-        it, the number of rows does not) and kept: calls on one stream share it in order, calls on
-        two streams never do.  Calls captured on one stream share theirs, and clear its status word:
+        """Attention of each slot's last tokens over its pages: paged_attention, or chunk_attention for
+        more than 128 queries a slot (max_q).  The scratch is made on the first call of a stream and a
+        size class (heads and max_q decide it, the number of rows does not) and kept: calls on one
+        stream share it in order, calls on two streams never do.  Calls captured on one stream share theirs, and clear its status word:
         replays of graphs that do so must not overlap."""
         T, Hq, D = q.shape
         long = max_q > MAX_BLOCK

@@ -668,13 +668,13 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
         copy16(base + L::q + x * L::tile + at * 128 + (c >> 3) * (kTile * 128) + (((c & 7) ^ (at & 7)) << 4),
                real ? from + q * a.q_stride_token + (g0 + r - q * G) * a.q_stride_head : a.q, real);
       }
+      copy_commit();
       query = query_of(lane);
       there = query < left;
       head = use.h * G + g0 + lane - query * G;
       query += q0;
     };
     auto fetched = [&]() {
-      copy_commit();
       copy_wait<0>();
       int e2 = 0;
       if (Q8 && BFQ) {
@@ -896,6 +896,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
       }
       fence_before();
     }
+    copy_wait<0>();  // (a role that gave up may have left some on their way)
   }
   __syncwarp();
   fence_before();
