@@ -44,6 +44,7 @@ constexpr int kRowsOf = 128;           // a row tile
 constexpr int kItem = 2 * kRowsOf;     // an item
 constexpr int kGroupThreads = 128;     // of a softmax group
 constexpr uint32_t kAbs = 0x7FFF7FFFu;  // of two 16-bit floats
+constexpr uint32_t kEnds = 1, kTwo = 2, kEdge = 4;  // of a tile: its item ends, has both row tiles; see at_edge
 
 // ---------------------------------------------------------------------------- wrappers
 
@@ -65,25 +66,45 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, DeviceStatus* st, int where) {
   return mbar_test(bar, parity) || wait_on(bar, parity, abort_flag, st, where);
 }
-// Products and commits by one elected lane of a warp; descriptors by their lower halves (the upper ones: rows
-// of 128 bytes in groups of eight, swizzled).  A (the weights) from tensor memory in the second.
+// Products and commits by one elected lane of a warp.  Matrices in shared memory go by their descriptors' lower
+// halves (the upper ones: rows of 128 bytes in groups of eight, swizzled).  All products of a matrix in one
+// statement: 16 columns of both operands each, one election.
 constexpr uint32_t kUpper = (1024u >> 4) | 1u << 14 | 2u << 29;
-__device__ __forceinline__ void mma_one(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-      "elect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(desc), "r"(accumulate), "n"(kUpper)
-      : "memory");
+#define BEGIN_PRODUCTS                                                                                  \
+  "{\n\t.reg .pred p, q;\n\t.reg .b32 m, n;\n\t.reg .b64 x, y;\n\telect.sync _|q, 0xffffffff;\n\t" \
+  "setp.ne.b32 p, %4, 0;\n\tmov.b32 m, %1;\n\tmov.b32 n, %2;\n\t"
+#define PRODUCT_IN_SMEM             \
+  "mov.b64 x, {m, %5};\n\tmov.b64 y, {n, %5};\n\t" \
+  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+#define PRODUCT_OF_TMEM    \
+  "mov.b64 y, {n, %5};\n\t" \
+  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [m], y, %3, p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+#define GO_ON(by_a, by_b) "add.u32 m, m, " #by_a ";\n\tadd.u32 n, n, " #by_b ";\n\t"
+#define FOUR_IN_SMEM PRODUCT_IN_SMEM GO_ON(2, 2) PRODUCT_IN_SMEM GO_ON(2, 2) PRODUCT_IN_SMEM GO_ON(2, 2) PRODUCT_IN_SMEM
+#define FOUR_OF_TMEM \
+  PRODUCT_OF_TMEM GO_ON(8, 128) PRODUCT_OF_TMEM GO_ON(8, 128) PRODUCT_OF_TMEM GO_ON(8, 128) PRODUCT_OF_TMEM
+// A panel is 64 columns, 128 rows of 128 bytes.
+template <int DP>
+__device__ __forceinline__ void product_of_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t desc) {
+  if constexpr (DP == 128)
+    asm volatile(BEGIN_PRODUCTS FOUR_IN_SMEM GO_ON(1018, 1018) FOUR_IN_SMEM "}" ::"r"(d), "r"(a), "r"(b), "r"(desc), "r"(0),
+                 "n"(kUpper)
+                 : "memory");
+  else
+    asm volatile(BEGIN_PRODUCTS FOUR_IN_SMEM "}" ::"r"(d), "r"(a), "r"(b), "r"(desc), "r"(0), "n"(kUpper) : "memory");
 }
-__device__ __forceinline__ void mma_ts_one(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %5};\n\t"
-      "elect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(desc), "r"(accumulate), "n"(kUpper)
-      : "memory");
+// A (the weights) from tensor memory, B 16 of its 128 rows at a time.
+__device__ __forceinline__ void product_of_weights(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, uint32_t accumulate) {
+  asm volatile(BEGIN_PRODUCTS FOUR_OF_TMEM GO_ON(8, 128) FOUR_OF_TMEM "}" ::"r"(d), "r"(a), "r"(b), "r"(desc), "r"(accumulate),
+               "n"(kUpper)
+               : "memory");
 }
+#undef BEGIN_PRODUCTS
+#undef PRODUCT_IN_SMEM
+#undef PRODUCT_OF_TMEM
+#undef GO_ON
+#undef FOUR_IN_SMEM
+#undef FOUR_OF_TMEM
 __device__ __forceinline__ void commit_one(uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
@@ -193,6 +214,12 @@ __device__ __forceinline__ bool at_edge(const AttentionArgs& a, const Block& x, 
   return p0 + kTile - 1 > x.last0 || (a.window > 0 && p0 <= x.last1 - a.window);
 }
 
+// (a worker's part of an item ends with the worker's last tile)
+__device__ __forceinline__ uint32_t unit_of(const AttentionArgs& a, const Place& c, bool last) {
+  return (last || c.t + 1 == c.x.tiles ? kEnds : 0u) | (two_tiles(a, c) ? kTwo : 0u) |
+         (at_edge(a, c.x, c.x.first + c.t * kTile) ? kEdge : 0u);
+}
+
 // ------------------------------------------------------------------------- shared memory
 
 template <bool Q8, int DP>
@@ -210,7 +237,8 @@ struct Plan {
   static constexpr int v_raw = k_raw + (Q8 ? raw : 0);  // [raw]
   static constexpr int odd = v_raw + (Q8 ? raw : 0);    // [v_stages][4] words: tokens that rows add on their own
   static constexpr int odd_told = odd + 16 * v_stages;  // [2][4]: the same, of a row tile's last tile at an edge
-  static constexpr int bars = odd_told + 32;
+  static constexpr int unit = odd_told + 32;  // [v_stages]: what the products have to know of the stage's tile
+  static constexpr int bars = (unit + 4 * v_stages + 7) / 8 * 8;
   // barriers
   static constexpr int k_full = 0, k_empty = k_full + k_stages, v_full = k_empty + k_stages, v_empty = v_full + v_stages,
                        v_ok = v_empty + v_stages, s_full = v_ok + v_stages, p_ready = s_full + 2, told = p_ready + 2,
@@ -334,6 +362,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::abort_flag);
   volatile uint32_t* odd = reinterpret_cast<volatile uint32_t*>(smem + L::odd);
   volatile uint32_t* odd_told = reinterpret_cast<volatile uint32_t*>(smem + L::odd_told);
+  volatile uint32_t* unit = reinterpret_cast<volatile uint32_t*>(smem + L::unit);
   const long long worker = blockIdx.x, workers = gridDim.x;
   const int G = a.G;
 
@@ -439,113 +468,85 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
     // each product, so that the descriptors are formed in uniform registers (2048 queries at 32768 tokens:
     // 797 us so, 969 by one lane in a branch of its own, 988 with the lane chosen by its number).
     auto all = [](bool x) { return __all_sync(~0u, x) != 0; };
-    Place use = stand();
     // (a negative scale turns the queries' signs)
     const uint32_t s_desc = idesc<BFQ && !Q8>(kTile, false, false) | (a.scale < 0.f ? 1u << 13 : 0u);
     constexpr uint32_t o_desc = idesc<BFQ && !Q8>(DP, false, true);
-    // (the descriptors' lower halves; the upper one is a constant)
+    // (the descriptors' lower halves)
     const uint32_t q_first = (uint32_t)sw128(base + L::q, 16, 1024), k_first = (uint32_t)sw128(base + L::k, 16, 1024),
                    v_first = (uint32_t)sw128(base + L::v, L::panels > 1 ? kTile * 128 : 0, 1024);
-    uint32_t q_round[2] = {0, 0}, p_round[2] = {0, 0};
     int ks = 0, vs = 0;
-    uint32_t k_round = 0, v_round = 0;
-    auto wait = [&](uint32_t at, uint32_t parity, int where) { return all(wait_for(at, parity, abort_flag, a.status, where)); };
+    uint32_t k_round = 0, v_round = 0, q_rounds = 0, p1_round = 0, odd_rounds = 0;  // (a bit per row tile)
+    // (after a wait that gave up the products go on over what is there, and nobody takes their results)
+    auto wait = [&](uint32_t at, uint32_t parity, int where) {
+      if (!all(mbar_test(at, parity))) wait_on(at, parity, abort_flag, a.status, where);
+    };
     auto scores = [&](int x) {
-      const uint32_t rows = q_first + x * (L::tile / 16), keys = k_first + ks * (L::tile / 16);
-#pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) {
-        const uint32_t step = kk / 4 * (kTile * 8) + kk % 4 * 2;
-        mma_one(tmem + x * kTile, rows + step, keys + step, s_desc, kk > 0);
-      }
+      product_of_rows<DP>(tmem + x * kTile, q_first + x * (L::tile / 16), k_first + ks * (L::tile / 16), s_desc);
       commit_one(bar(L::s_full + x));
     };
-    const int total = __shfl_sync(~0u, tiles, 0);
-    bool both = all(total > 0 && two_tiles(a, use));
-    bool ok = total > 0 && wait(bar(L::k_full), 0, 622);
-    for (int x = 0; ok && x < (both ? 2 : 1); ++x) {
-      ok = wait(bar(L::q_ready + x), 0, 623);
-      q_round[x] = 1;
+    auto queries = [&](int x) {
+      wait(bar(L::q_ready + x), q_rounds >> x & 1, 623);
+      q_rounds ^= 1u << x;
       fence_after();
-      if (ok) scores(x);
-    }
-    if (ok) commit_one(bar(L::k_empty));
-    // what there is to know of a unit's products: where its values lie, whether its item ends with it, whether it
-    // has both row tiles, whether its first product adds (the first of an item does not), and whether some of its
-    // rows see some of its tokens only
-    struct Unit {
-      uint32_t values, v_at, add;
-      int stage;
-      bool ends, two, last, edge;
     };
-    uint32_t odd_round = 0;  // a bit per row tile
-    auto open_unit = [&](int i, bool goes_on) {  // the unit at `use`; moves on to the next
-      Unit u;
-      u.last = i + 1 == total;
-      u.ends = all(u.last || use.t + 1 == use.x.tiles);
-      u.two = both;
-      u.values = v_first + vs * (L::tile / 16);
-      u.v_at = bar(vs);
-      u.add = goes_on;
-      u.stage = vs;
-      u.edge = all(at_edge(a, use.x, use.x.first + use.t * kTile));
-      ok = ok && wait(u.v_at + 8 * (Q8 ? L::v_full : L::v_ok), v_round, 624);
-      if (++vs == L::v_stages) vs = 0, v_round ^= 1;
-      if (!u.ends) ++use.t;
-      else if (!u.last) next_item(a, use), both = all(two_tiles(a, use));
-      return u;
-    };
-    auto open_keys = [&]() {
+    auto next_keys = [&]() {
+      commit_one(bar(L::k_empty + ks));
       if (++ks == L::k_stages) ks = 0, k_round ^= 1;
-      ok = ok && wait(bar(L::k_full + ks), k_round, 622);
     };
-    Unit now = {};
-    if (ok) now = open_unit(0, false);
-    if (ok && !now.last) open_keys();
-    for (int i = 0; ok && i < total; ++i) {
-      auto product = [&](int x) {
-        ok = wait(bar(L::p_ready + x), p_round[x], 626);
-        p_round[x] ^= 1;
-        if (!ok) return;
+    const int total = __shfl_sync(~0u, tiles, 0);
+    uint32_t now = 0;  // what there is to know of the tile
+    if (total > 0) {
+      wait(bar(L::k_full), 0, 622);
+      wait(bar(Q8 ? L::v_full : L::v_ok), 0, 624);
+      now = unit[0];
+      queries(0);
+      scores(0);
+      if (all((now & kTwo) != 0)) queries(1), scores(1);
+      next_keys();
+      if (total > 1) wait(bar(L::k_full + ks), k_round, 622);
+    }
+    uint32_t add = 0;  // does the tile's product add? (the first of an item does not)
+    for (int i = 0; i < total; ++i) {
+      const bool ends = all((now & kEnds) != 0), last = i + 1 == total;
+      const int stage = vs;
+      auto product = [&](int x, uint32_t round) {
+        wait(bar(L::p_ready + x), round, 626);
         fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_ts_one(tmem + 2 * kTile + x * DP, tmem + x * kTile + 8 * kk, now.values + kk * 128, o_desc, kk > 0 ? 1u : now.add);
-        if (now.edge) {
-          const uint32_t word = lane < 4 ? odd[4 * now.stage + lane] : 0u;
+        product_of_weights(tmem + 2 * kTile + x * DP, tmem + x * kTile, v_first + stage * (L::tile / 16), o_desc, add);
+        if (all((now & kEdge) != 0)) {
+          const uint32_t word = lane < 4 ? odd[4 * stage + lane] : 0u;
           if (lane < 4) odd_told[4 * x + lane] = word;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::told + x));
           if (__any_sync(~0u, word != 0)) {  // the rows read the weights and add theirs before either is written again
             commit_one(bar(L::pv_done + x));
-            ok = wait(bar(L::odd_done + x), odd_round >> x & 1, 637);
-            odd_round ^= 1u << x;
+            wait(bar(L::odd_done + x), odd_rounds >> x & 1, 637);
+            odd_rounds ^= 1u << x;
             fence_after();
           }
         }
-        if (now.ends) commit_one(bar(L::o_done + x));
+        if (ends) commit_one(bar(L::o_done + x));
       };
-      auto next = [&](int x) {
-        if (now.ends) {
-          ok = ok && wait(bar(L::q_ready + x), q_round[x], 623);
-          q_round[x] ^= 1;
-          fence_after();
-        }
-        if (ok) scores(x);
-      };
-      // (both: of the unit after this one; what comes after the next is looked up while the tensor cores work)
-      const bool next0 = !now.last, next1 = next0 && both;
-      product(0);
-      if (ok && next0) next(0);
-      Unit then = {};
-      if (ok && next0) then = open_unit(i + 1, !now.ends);
-      if (!ok) break;
-      if (now.two) product(1);
-      if (!ok) break;
-      commit_one(now.v_at + 8 * L::v_empty);
-      if (next1) next(1);
-      if (!ok || !next0) break;
-      commit_one(bar(L::k_empty + ks));
-      if (!then.last) open_keys();
+      product(0, i & 1);
+      uint32_t then = 0;
+      if (!last) {
+        if (ends) queries(0);
+        scores(0);
+        // the next tile's values, and what there is to know of it
+        if (++vs == L::v_stages) vs = 0, v_round ^= 1;
+        wait(bar((Q8 ? L::v_full : L::v_ok) + vs), v_round, 624);
+        then = unit[vs];
+      }
+      if (all((now & kTwo) != 0)) product(1, p1_round), p1_round ^= 1;
+      commit_one(bar(L::v_empty + stage));
+      if (last) break;
+      if (all((then & kTwo) != 0)) {
+        if (ends) queries(1);
+        scores(1);
+      }
+      next_keys();
+      if (i + 2 < total) wait(bar(L::k_full + ks), k_round, 622);
+      add = !ends;
       now = then;
     }
     // every product is done before the CTA gives its tensor memory back
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
         fence_smem();
         __syncwarp();
       }
-      if (lane == 0) mbar_arrive(bar(L::v_ok + vs));
+      if (lane == 0) unit[vs] = unit_of(a, use, i + 1 == tiles), mbar_arrive(bar(L::v_ok + vs));
       if (i + 1 < tiles && ++use.t == use.x.tiles) next_item(a, use);
     }
   } else if (Q8 && warp >= 4 && warp < 8) {
@@ -634,6 +635,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
         convert(base + L::v_raw, to, false, false);
       }
       fence_smem();
+      if (warp == 4 && lane == 0) unit[vs] = unit_of(a, use, i + 1 == tiles);
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::vr_empty)), mbar_arrive(bar(L::v_full + vs));
       if (i + 1 < tiles && ++use.t == use.x.tiles) next_item(a, use);
