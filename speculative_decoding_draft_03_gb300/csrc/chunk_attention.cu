@@ -112,14 +112,19 @@ __device__ __forceinline__ void commit_one(uint32_t bar) {
       : "memory");
 }
 #define R8(x, i) "=f"(x[i]), "=f"(x[i + 1]), "=f"(x[i + 2]), "=f"(x[i + 3]), "=f"(x[i + 4]), "=f"(x[i + 5]), "=f"(x[i + 6]), "=f"(x[i + 7])
-// 32 columns of this warp's lanes.
-__device__ __forceinline__ void tmem_load32(uint32_t at, float* x) {
+// 32 columns of this warp's lanes: begun, and awaited (the registers hold nothing between).
+__device__ __forceinline__ void tmem_begin32(uint32_t at, float* x) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
-      "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+      "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)
       : "r"(at)
       : "memory");
+}
+#undef R8
+#define R8(x, i) "+f"(x[i]), "+f"(x[i + 1]), "+f"(x[i + 2]), "+f"(x[i + 3]), "+f"(x[i + 4]), "+f"(x[i + 5]), "+f"(x[i + 6]), "+f"(x[i + 7])
+__device__ __forceinline__ void tmem_arrived32(float* x) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)::"memory");
 }
 #undef R8
 __device__ __forceinline__ float tmem_load1(uint32_t at) {
@@ -249,7 +254,8 @@ struct Plan {
   static constexpr int start_off = scan + 8 * 32;    // long long
   static constexpr int start_r = start_off + 8;      // int, then head, block, tile
   static constexpr int tmem = start_r + 16, abort_flag = tmem + 4;
-  static constexpr int total = abort_flag + 4;
+  static constexpr int places = abort_flag + 4;      // [8] of the softmax warps
+  static constexpr int total = places + 8 * sizeof(Place);
   static_assert(total <= 232448, "227 KB");
   static_assert(k + 8 * kMaxSlots <= odd, "the requests' units, before the copies begin");
 };
@@ -392,14 +398,15 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
   const Deal d = deal_tiles<L>(a, worker, workers, smem);
   fence_smem();  // (its table lay where copies will land)
   fence_before();
-  __syncthreads();
-  fence_after();
   constexpr uint32_t tmem = 0;  // (an allocation of all 512 columns begins at the first)
+  const long long u_begin = worker * d.per, u_end = min(d.total, u_begin + d.per);
   if (tid == 0) {
     scr.share[worker].r = -1;
     if (worker == 0) *scr.per = d.per;
+    *reinterpret_cast<volatile long long*>(smem + L::start_off) = u_begin;
   }
-  const long long u_begin = worker * d.per, u_end = min(d.total, u_begin + d.per);
+  __syncthreads();
+  fence_after();
   // (shared memory as the swizzle wants it, which it is without static arrays; tensor memory as said above)
   const bool aligned = (base & 1023u) == 0 && *reinterpret_cast<volatile uint32_t*>(smem + L::tmem) == tmem;
   if (!aligned && tid == 0) report_bad_input(a.status, 632);
@@ -644,11 +651,15 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
   } else {
     more_registers<Q8 ? 176 : 208>();
     // ---- softmax: group x has row tile x; a thread, the row of its TMEM lane
-    Place use = stand();
+    // (where it stands lies in shared memory, a copy a warp: it is looked at between items only, and registers are few)
+    Place& use = *reinterpret_cast<Place*>(smem + L::places + (warp - L::softmax_warp) * sizeof(Place));
+    const Place begins = stand();
+    if (lane == 0) use = begins;
+    __syncwarp();
     const int x = (warp - L::softmax_warp) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_at = tmem + lanes + x * kTile, o_at = tmem + lanes + 2 * kTile + x * DP;
-    long long item_begin = u_begin - use.t;
+    int item_begin = -use.t;  // where the item begins among the worker's tiles
     // The item's row of this thread: its query's number (of the request) and head, or none; scores in base 2 are
     // c2 times what the products give (never 0, so that what is masked stays -inf).  The warp copies its 32 query
     // rows to where the products read them, DP / 8 lanes a row, and says so when they have come.
@@ -715,14 +726,15 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
     while (i < tiles) {
       const int n = min(use.x.tiles - use.t, tiles - i);
       // what is asked about the item when the next one has been opened
-      const long long item_end = item_begin + use.x.tiles;
-      const bool whole = item_begin >= u_begin && item_end <= u_end;
-      const int part = item_begin >= u_begin;  // part 0 began before the worker's range
+      const int item_end = item_begin + use.x.tiles;
+      const bool whole = item_begin >= 0 && item_end <= tiles;
+      const int part = item_begin >= 0;  // part 0 began before the worker's range
       const bool was_mine = mine, was_there = there, more = i + n < tiles;
       const int r = use.r, h = use.h, last = there ? use.k.len - use.k.nq + query : -1;
       const int64_t place = (int64_t)(use.k.q0 + query) * a.Hq + head;
+      const long long first_unit = *reinterpret_cast<volatile long long*>(smem + L::start_off);
       if (!whole && part == 1 && x == 0 && row == 0)
-        scr.share[worker] = Share{r, h * use.k.blocks + use.x.b, use.k.q0, use.k.nq, item_begin, item_end};
+        scr.share[worker] = Share{r, h * use.k.blocks + use.x.b, use.k.q0, use.k.nq, first_unit + item_begin, first_unit + item_end};
       item_begin = item_end;
       // the row tile's first and last row
       const int tile_row = use.x.b * kItem + x * kRowsOf;
@@ -745,7 +757,11 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
         // (a request's or a window's end may be an edge of the item and none of this row tile)
         const bool gated = p0 >= gate_from || p0 <= gate_upto, leaves = t + 1 == n && more;
         if (__builtin_expect(leaves, 0)) {  // the next item's queries are on their way from here on
-          next_item(a, use);
+          Place next = use;
+          next_item(a, next);
+          __syncwarp();
+          if (lane == 0) use = next;
+          __syncwarp();
           mine = x == 0 || two_tiles(a, use);
           if (mine) fetch();
         }
@@ -789,21 +805,35 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
           float m[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) m[k] = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < kTile; c += 32) {
-            float s[32];
-            tmem_load32(s_at + c, s);
+          auto largest = [&](const float* s) {
 #pragma unroll
             for (int e = 0; e < 32; e += 16)
 #pragma unroll
               for (int k = 0; k < 8; ++k) m[k] = max3(m[k], s[e + k], s[e + k + 8]);
+          };
+          // A row's scores, all at once in registers, where there are enough; an e4m3 cache's converters leave too few
+          // of them, and its rows go by 32 columns, the next ones on their way, twice (2048 queries at 32768 tokens:
+          // 739 us at once, 766 by 32, 786 by 32 with each load awaited; 512 at 65536 over e4m3: 462, 432 and 438).
+          float s0[32], s1[32], s2[32], s3[32];
+          tmem_begin32(s_at, s0);
+          if constexpr (!Q8) {
+            tmem_begin32(s_at + 32, s1), tmem_begin32(s_at + 64, s2), tmem_begin32(s_at + 96, s3);
+            tmem_arrived32(s0), tmem_arrived32(s1), tmem_arrived32(s2), tmem_arrived32(s3);
+            largest(s0), largest(s1), largest(s2), largest(s3);
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 64) {
+              tmem_arrived32(s0);
+              tmem_begin32(s_at + c + 32, s1);
+              largest(s0);
+              tmem_arrived32(s1);
+              tmem_begin32(s_at + ((c + 64) & (kTile - 1)), s0);
+              largest(s1);
+            }
           }
           refer(max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7])) * c2);
           const Two cc = two(c2, c2), rr2 = two(-ref, -ref);
-#pragma unroll 1
-          for (int c = 0; c < kTile; c += 32) {
-            float s[32];
-            tmem_load32(s_at + c, s);
+          auto weigh = [&](const float* s, int c) {
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
@@ -815,6 +845,19 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
               w[e / 2] = H::pack(p0_, p1_), w[e / 2 + 1] = H::pack(p2_, p3_);
             }
             tmem_store_u16(s_at + c / 2, w);
+          };
+          if constexpr (!Q8) {
+            weigh(s0, 0), weigh(s1, 32), weigh(s2, 64), weigh(s3, 96);
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < kTile; c += 64) {
+              tmem_arrived32(s0);
+              tmem_begin32(s_at + c + 32, s1);
+              weigh(s0, c);
+              tmem_arrived32(s1);
+              if (c == 0) tmem_begin32(s_at + 64, s0);
+              weigh(s1, c + 32);
+            }
           }
           tmem_store_wait();
           fence_before();
