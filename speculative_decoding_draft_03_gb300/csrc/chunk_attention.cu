@@ -22,14 +22,15 @@
 //     value), and look at the values as warp 3 does otherwise.  bf16 query rows are scaled by powers of
 //     two into fp16's range.
 //   * An item's last scores free its queries' place: the next item's come while those are weighed, and its
-//     first product is issued behind the last one's weights (64 blocks of 512 queries: 280 us so, 370 with
-//     the queries loaded after the last weights, a row a lane).
+//     first product is issued behind the last one's weights (with the queries loaded after the last weights, a
+//     row a lane, 64 blocks of 512 queries took 370 us for the 285 now).
 //   * The work is dealt out in tiles of 128 tokens that an item sees, evenly over the CTAs; items that
 //     several share are joined by a second kernel, in a fixed order.
 // What bounds it: the products of a tile of both row tiles (D = 128) keep the tensor cores busy for 2050
-// clocks; a tile takes about 3500, the rest being the hand-over from scores to weights and back, which two
-// row tiles in turn do not cover.  8192 causal queries, 32 heads over 8 of 128: 460 us, 1195 TFLOP/s; 2048 at
-// 32768 tokens: 800 us, 1330 TFLOP/s; over e4m3 the conversion comes on top (8192 causal: 542 us).
+// clocks; a tile takes about 3100, the chain of one row tile: 1600 from telling the weights to seeing the next
+// scores (two waits, two matrices' products in turn with the other's), 1500 of softmax.  8192 causal queries, 32
+// heads over 8 of 128: 409 us, 1343 TFLOP/s; 2048 at 32768 tokens: 725 us, 1470 TFLOP/s; over e4m3 the
+// conversion comes on top (8192 causal: 502 us).
 // Every mbarrier wait is bounded; a wait that gives up reports DSPARK_TIMEOUT and the CTA winds down.
 #include <algorithm>
 
@@ -49,7 +50,7 @@ constexpr uint32_t kEnds = 1, kTwo = 2, kEdge = 4;  // of a tile: its item ends,
 // ---------------------------------------------------------------------------- wrappers
 
 // mbar_wait, out of line where the phase is still open: the roles' loops share the instruction cache, and a
-// dozen copies of it cost more than the calls (512 queries at 65536 tokens of an e4m3 cache: 470 us so, 580
+// dozen copies of it cost more than the calls (512 queries at 65536 tokens of an e4m3 cache took 470 us so, 580
 // inlined).
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, DeviceStatus* st, int where) {
   const long long t0 = clock64();
@@ -112,19 +113,36 @@ __device__ __forceinline__ void commit_one(uint32_t bar) {
       : "memory");
 }
 #define R8(x, i) "=f"(x[i]), "=f"(x[i + 1]), "=f"(x[i + 2]), "=f"(x[i + 3]), "=f"(x[i + 4]), "=f"(x[i + 5]), "=f"(x[i + 6]), "=f"(x[i + 7])
-// 32 columns of this warp's lanes: begun, and awaited (the registers hold nothing between).
-__device__ __forceinline__ void tmem_begin32(uint32_t at, float* x) {
+// 32 columns of this warp's lanes, and 128.
+__device__ __forceinline__ void tmem_load32(uint32_t at, float* x) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
-      "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
       : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)
       : "r"(at)
       : "memory");
 }
-#undef R8
-#define R8(x, i) "+f"(x[i]), "+f"(x[i + 1]), "+f"(x[i + 2]), "+f"(x[i + 3]), "+f"(x[i + 4]), "+f"(x[i + 5]), "+f"(x[i + 6]), "+f"(x[i + 7])
-__device__ __forceinline__ void tmem_arrived32(float* x) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)::"memory");
+__device__ __forceinline__ void tmem_load128(uint32_t at, float* x) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%128];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%129];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%64,%65,%66,%67,%68,%69,%70,%71,%72,%73,%74,%75,%76,%77,%78,%79,"
+      "%80,%81,%82,%83,%84,%85,%86,%87,%88,%89,%90,%91,%92,%93,%94,%95}, [%130];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%96,%97,%98,%99,%100,%101,%102,%103,%104,%105,%106,%107,%108,%109,%110,%111,"
+      "%112,%113,%114,%115,%116,%117,%118,%119,%120,%121,%122,%123,%124,%125,%126,%127}, [%131];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24), R8(x, 32), R8(x, 40), R8(x, 48), R8(x, 56), R8(x, 64), R8(x, 72), R8(x, 80),
+        R8(x, 88), R8(x, 96), R8(x, 104), R8(x, 112), R8(x, 120)
+      : "r"(at), "r"(at + 32), "r"(at + 64), "r"(at + 96)
+      : "memory");
 }
 #undef R8
 __device__ __forceinline__ float tmem_load1(uint32_t at) {
@@ -470,10 +488,12 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
   } else if (warp == 1) {
     // ---- products.  The tensor cores execute them in the order of their issue, so that S of the next tile
     // may follow the product that reads the weights in its place.  What happens between two products is time
-    // that the tensor cores stand still: all there is to know and to wait for is settled before the weights are
-    // awaited, and the whole warp goes along, in branches that votes make uniform, with one lane elected at
-    // each product, so that the descriptors are formed in uniform registers (2048 queries at 32768 tokens:
-    // 797 us so, 969 by one lane in a branch of its own, 988 with the lane chosen by its number).
+    // that the tensor cores stand still, and the other roles' loops leave little of the instruction cache: so
+    // what a tile needs (whether its item ends, its second row tile, an edge) is told with its values, a matrix's
+    // products are one statement, and the whole warp goes along in branches that votes make uniform, so that
+    // descriptors are formed in uniform registers (2048 queries at 32768 tokens took 797 us with an election for each
+    // product, 969 by one lane in a branch of its own, 988 with the lane chosen by its number; 8192 causal queries
+    // 461 us with this warp finding out about the tiles by itself, 447 so).
     auto all = [](bool x) { return __all_sync(~0u, x) != 0; };
     // (a negative scale turns the queries' signs)
     const uint32_t s_desc = idesc<BFQ && !Q8>(kTile, false, false) | (a.scale < 0.f ? 1u << 13 : 0u);
@@ -601,7 +621,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
       const int ks = i % L::k_stages, vs = i % L::v_stages, p0 = use.x.first + use.t * kTile, pos = p0 + token;
       auto convert = [&](uint32_t from, uint32_t to, bool clear, bool look) {
         bool strange = false;
-#pragma unroll 1  // (unrolled, it crowds the instruction cache: 8192 queries 570 us for 542, 65536 tokens the same)
+#pragma unroll 1  // (unrolled, it crowds the instruction cache: 8192 queries took 570 us for 542, 65536 tokens the same)
         for (int c = 0; c < 8; ++c) {
           const uint4 x = lds16(from + token * 128 + ((c ^ (token & 7)) << 4));
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -785,7 +805,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
             }
           };
           // what the row does not see goes out of its scores, in a pass of its own: the loops below stay short (with
-          // the selects in them, 8192 causal queries take 474 us for 460, and D = 64 452 for 419)
+          // the selects in them, 8192 causal queries took 474 us for 460, and with D = 64 452 for 419)
           if (edge) {
             const int hi = last - p0, lo = a.window > 0 ? hi - a.window + 1 : 0;
 #pragma unroll 1
@@ -811,25 +831,18 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
 #pragma unroll
               for (int k = 0; k < 8; ++k) m[k] = max3(m[k], s[e + k], s[e + k + 8]);
           };
-          // A row's scores, all at once in registers, where there are enough; an e4m3 cache's converters leave too few
-          // of them, and its rows go by 32 columns, the next ones on their way, twice (2048 queries at 32768 tokens:
-          // 739 us at once, 766 by 32, 786 by 32 with each load awaited; 512 at 65536 over e4m3: 462, 432 and 438).
-          float s0[32], s1[32], s2[32], s3[32];
-          tmem_begin32(s_at, s0);
+          // A row's scores, all at once in registers where there are enough; an e4m3 cache's converters leave too few
+          // of them, and its rows go by 32 columns, twice (2048 queries at 32768 tokens: 725 us at once, 786 by 32;
+          // 512 at 65536 over e4m3: 462 and 438).
+          constexpr int kHeld = Q8 ? 32 : kTile;
+          float s[kHeld];
           if constexpr (!Q8) {
-            tmem_begin32(s_at + 32, s1), tmem_begin32(s_at + 64, s2), tmem_begin32(s_at + 96, s3);
-            tmem_arrived32(s0), tmem_arrived32(s1), tmem_arrived32(s2), tmem_arrived32(s3);
-            largest(s0), largest(s1), largest(s2), largest(s3);
+            tmem_load128(s_at, s);
+#pragma unroll
+            for (int c = 0; c < kTile; c += 32) largest(s + c);
           } else {
 #pragma unroll 1
-            for (int c = 0; c < kTile; c += 64) {
-              tmem_arrived32(s0);
-              tmem_begin32(s_at + c + 32, s1);
-              largest(s0);
-              tmem_arrived32(s1);
-              tmem_begin32(s_at + ((c + 64) & (kTile - 1)), s0);
-              largest(s1);
-            }
+            for (int c = 0; c < kTile; c += 32) tmem_load32(s_at + c, s), largest(s);
           }
           refer(max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7])) * c2);
           const Two cc = two(c2, c2), rr2 = two(-ref, -ref);
@@ -847,23 +860,17 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
             tmem_store_u16(s_at + c / 2, w);
           };
           if constexpr (!Q8) {
-            weigh(s0, 0), weigh(s1, 32), weigh(s2, 64), weigh(s3, 96);
+#pragma unroll
+            for (int c = 0; c < kTile; c += 32) weigh(s + c, c);
           } else {
 #pragma unroll 1
-            for (int c = 0; c < kTile; c += 64) {
-              tmem_arrived32(s0);
-              tmem_begin32(s_at + c + 32, s1);
-              weigh(s0, c);
-              tmem_arrived32(s1);
-              if (c == 0) tmem_begin32(s_at + 64, s0);
-              weigh(s1, c + 32);
-            }
+            for (int c = 0; c < kTile; c += 32) tmem_load32(s_at + c, s), weigh(s, c);
           }
           tmem_store_wait();
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::p_ready + x));
-          }
+        }
         if (__builtin_expect(leaves && mine, 0)) fetched();
         // values that are not finite, where only some rows see them, have been taken out of the product: the
         // rows that do add them on their own, with the weights as they were told
