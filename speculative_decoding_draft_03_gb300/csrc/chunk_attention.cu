@@ -30,7 +30,7 @@
 // clocks; a tile takes about 3100, the chain of one row tile: 1600 from telling the weights to seeing the next
 // scores (two waits, two matrices' products in turn with the other's), 1500 of softmax.  8192 causal queries, 32
 // heads over 8 of 128: 409 us, 1343 TFLOP/s; 2048 at 32768 tokens: 725 us, 1470 TFLOP/s; over e4m3 the
-// conversion comes on top (8192 causal: 502 us).
+// conversion comes on top (8192 causal: 488 us).
 // Every mbarrier wait is bounded; a wait that gives up reports DSPARK_TIMEOUT and the CTA winds down.
 #include <algorithm>
 
@@ -113,15 +113,18 @@ __device__ __forceinline__ void commit_one(uint32_t bar) {
       : "memory");
 }
 #define R8(x, i) "=f"(x[i]), "=f"(x[i + 1]), "=f"(x[i + 2]), "=f"(x[i + 3]), "=f"(x[i + 4]), "=f"(x[i + 5]), "=f"(x[i + 6]), "=f"(x[i + 7])
-// 32 columns of this warp's lanes, and 128.
-__device__ __forceinline__ void tmem_load32(uint32_t at, float* x) {
+// 64 columns of this warp's lanes, and 128.
+__device__ __forceinline__ void tmem_load64(uint32_t at, float* x) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%65];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)
-      : "r"(at)
+      : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24), R8(x, 32), R8(x, 40), R8(x, 48), R8(x, 56)
+      : "r"(at), "r"(at + 32)
       : "memory");
 }
 __device__ __forceinline__ void tmem_load128(uint32_t at, float* x) {
@@ -832,9 +835,9 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
               for (int k = 0; k < 8; ++k) m[k] = max3(m[k], s[e + k], s[e + k + 8]);
           };
           // A row's scores, all at once in registers where there are enough; an e4m3 cache's converters leave too few
-          // of them, and its rows go by 32 columns, twice (2048 queries at 32768 tokens: 725 us at once, 786 by 32;
-          // 512 at 65536 over e4m3: 462 and 438).
-          constexpr int kHeld = Q8 ? 32 : kTile;
+          // of them, and half a row's scores are read again (2048 queries at 32768 tokens: 725 us at once, 786 by 32
+          // columns, all read twice; 512 at 65536 over e4m3: 462 with 128 held, 415 with 64, 435 with 32).
+          constexpr int kHeld = Q8 ? 64 : kTile;
           float s[kHeld];
           if constexpr (!Q8) {
             tmem_load128(s_at, s);
@@ -842,7 +845,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
             for (int c = 0; c < kTile; c += 32) largest(s + c);
           } else {
 #pragma unroll 1
-            for (int c = 0; c < kTile; c += 32) tmem_load32(s_at + c, s), largest(s);
+            for (int c = 64; c >= 0; c -= 64) tmem_load64(s_at + c, s), largest(s), largest(s + 32);
           }
           refer(max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7])) * c2);
           const Two cc = two(c2, c2), rr2 = two(-ref, -ref);
@@ -864,7 +867,10 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
             for (int c = 0; c < kTile; c += 32) weigh(s + c, c);
           } else {
 #pragma unroll 1
-            for (int c = 0; c < kTile; c += 32) tmem_load32(s_at + c, s), weigh(s, c);
+            for (int c = 0; c < kTile; c += 64) {
+              if (c > 0) tmem_load64(s_at + c, s);
+              weigh(s, c), weigh(s + 32, c + 32);
+            }
           }
           tmem_store_wait();
           fence_before();
