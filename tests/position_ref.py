@@ -65,7 +65,10 @@ def attention(q, k, v, table, lens, q_start, scale, k_scale=None, v_scale=None, 
             o, m = w @ fine, w @ fine.abs()
             for i in odd.nonzero()[:, 0].tolist():  # these reach the queries that see them alone
                 sees = seen[:, i]
+                # (the magnitude, by which weights' roundings count, is the sum of w |v| over all that is seen:
+                # such a token's finite elements are in o, and so in it too)
                 o[sees] += w[sees][..., i, None] * vv[i]
+                m[sees] += w[sees][..., i, None] * vv[i].abs()
             lse[t, heads] = torch.where(some[:, None], top, -math.inf)
             out[t, heads], mag[t, heads] = o, m
             a = torch.einsum("tgd,sd->tgs", q[t, heads].abs(), kk.abs())

@@ -364,3 +364,22 @@ def test_cache_attends_over_long_blocks(b):
         want = torch.einsum("hqk,khd->qhd", w, vv)
         mag = torch.einsum("hqk,khd->qhd", w, vv.abs())
         assert ((o["out"][t].double() - want).abs() <= 2.0 ** -8 * (mag + want.abs()) * 1.01 + 1e-6).all()
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("window", [0, 150])
+def test_many_items_with_values_that_some_do_not_see(b, dtype, cache, window):
+    """Values that are NaN in every request, near the diagonal and along the blocks, with several items of two
+    row tiles a CTA: each row has them in its sums, or not, by what it sees alone."""
+    g = torch.Generator().manual_seed(21)
+    new = torch.randint(250, 400, (24,), generator=g).tolist()
+    before = torch.randint(0, 300, (24,), generator=g).tolist()
+    c = _case([x + y for x, y in zip(new, before)], new, 16, 8, 64, 16, dtype, cache, seed=22)
+    v = c["v"].float()
+    for r in range(24):
+        for j in torch.randint(0, new[r], (3,), generator=g).tolist():
+            at, h = before[r] + j, int(torch.randint(0, 8, (1,), generator=g))
+            v[c["table"][r, at // 16], h, at % 16, h:h + 2] = math.nan
+    c["v"] = v.to(c["v"].dtype)
+    out = _check(b, c, 0.125, window)["out"].float()
+    assert torch.isnan(out).any() and torch.isfinite(out).any()
