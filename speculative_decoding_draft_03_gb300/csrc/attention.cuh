@@ -121,7 +121,7 @@ __device__ __forceinline__ Request request(const AttentionArgs& a, int r, bool r
   if (a.granted != nullptr && a.granted[r] == 0) k.len = 0;  // its queries see nothing
   if (a.window > 0) k.first = max(0, k.len - k.nq - a.window + 1) / TK * TK;
   k.chunks = max(1, (k.len - k.first + TK - 1) / TK);
-  k.blocks = (k.nq * a.G + ROWS - 1) / ROWS;
+  k.blocks = (k.nq * a.G - 1) / ROWS + 1;  // (a call's rows may reach 2^31 - 1: none may be added to them)
   return k;
 }
 
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   griddep_wait();
   const Share k = scr.share[blockIdx.x];
   if (k.r < 0) return;
-  const int G = a.G, rb = (k.nq * G + ROWS - 1) / ROWS, h = k.item / rb, row0 = (k.item - h * rb) * ROWS;
+  const int G = a.G, rb = (k.nq * G - 1) / ROWS + 1, h = k.item / rb, row0 = (k.item - h * rb) * ROWS;
   const int rows = min(ROWS, k.nq * G - row0), first = blockIdx.y * kJoinRows;
   if (first >= rows) return;
   const int w0 = blockIdx.x, parts = (int)((k.end - 1) / *scr.per) - w0 + 1;  // part p: worker w0 + p

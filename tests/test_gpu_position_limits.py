@@ -1,0 +1,50 @@
+"""The ends of what the rotary, append, long-block attention and logit-adjustment calls take: the largest
+sizes, scales and windows, and shapes at the borders of the kernels' fast paths."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import position_ref as ref
+from tests import test_gpu_chunk_attention as chunk
+from tests.test_gpu_attention import _case, _i32
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def b():
+    from speculative_decoding_draft_03_gb300 import binding
+    return binding
+
+
+def test_query_rows_up_to_the_limit(b):
+    """One request of 2^31 - 64 query rows: their count plus an item's does not fit 32 bits.  All but the last
+    128 tokens lie before the context and see nothing."""
+    T, G, D, n = (1 << 25) - 1, 64, 16, 128
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("the result takes 64 GB")
+    g = torch.Generator().manual_seed(0)
+    q = torch.randn((1, G, D), generator=g).bfloat16().cuda()
+    k, v = (torch.randn((8, 1, 16, D), generator=g).bfloat16().cuda() for _ in range(2))
+    out = torch.empty((T, G, D), dtype=torch.bfloat16, device="cuda")
+    step = 1 << 21
+    for t in range(0, T, step):
+        out[t:t + step] = 77.0
+    ws = b.workspace(b.chunk_attention_workspace_size(T, 1, G, 1, D), "cuda")
+    b.chunk_attention(q.expand(T, G, D), k, v, _i32([np.arange(8)]), _i32([n]), _i32([0, T]), 0.25, out=dict(out=out), ws=ws)
+    assert b.device_status(ws) == 0
+    for t in range(0, T - n, step):
+        assert not out[t:min(t + step, T - n)].any(), t
+    kk, vv = (x.transpose(1, 2).reshape(n, D).double() for x in (k, v))
+    s = torch.einsum("gd,sd->gs", q[0].double(), kk) * 0.25
+    j = torch.arange(n, device="cuda")
+    w = torch.softmax(s.expand(n, G, n).masked_fill(j > j[:, None, None], -math.inf), 2)
+    want, mag = w @ vv, w @ vv.abs()
+    # a half step of each weight and of the result, and fp32's sums
+    assert ((out[T - n:].double() - want).abs() <= 2.0 ** -8 * (mag + want.abs()) + 2.0 ** -16 * mag).all()
+    del out
+    torch.cuda.empty_cache()
