@@ -48,3 +48,19 @@ def test_query_rows_up_to_the_limit(b):
     assert ((out[T - n:].double() - want).abs() <= 2.0 ** -8 * (mag + want.abs()) + 2.0 ** -16 * mag).all()
     del out
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype,cache", [chunk.TYPES[0], chunk.TYPES[2]])
+@pytest.mark.parametrize("D", [128, 256])
+def test_windows_near_two_to_the_31(b, dtype, cache, D):
+    """Windows as long as tables allow, over slots with far more queries than positions: where the window of a
+    query that sees nothing would begin lies below -2^31."""
+    lens, new = [60, 100, 700], [700, 900, 300]
+    c = _case(lens, new, 2, 1, D, 256, dtype, cache, seed=31)
+    width = (1 << 23) - 2
+    c["table"] = np.pad(c["table"], ((0, 0), (0, width - c["table"].shape[1])), constant_values=-1)
+    window = width * 256 - 1
+    o, ws = chunk._run(b, c, 0.1, window, granted=_i32([0, 900, 300]))
+    assert b.device_status(ws) == 0
+    small = dict(c, table=c["table"][:, :8])
+    chunk._compare(small, o, 0.1, window, lens=[0, 100, 700])
