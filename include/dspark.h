@@ -678,8 +678,8 @@ DSPARK_API dspark_status dspark_cache_append(
  *   repetition  [R] > 0; frequency, presence [R]; each may be NULL (no such penalty).
  *   bias_ids, bias  [R, n_bias]; n_bias = 0: none.
  *   mask        mask_rows rows of bits, id v at bit v % 32 of word v / 32, rows mask_stride words
- *               apart, or NULL.  mask_row [N]: which one row n goes by (out of range: none); NULL:
- *               mask row n.
+ *               apart, or NULL (no masks; mask_row may then be given with mask_rows = 0).  mask_row
+ *               [N]: which one row n goes by (out of range: none); NULL: mask row n.
  * N = 0 does nothing.  Deterministic.  No workspace.
  * Limits: V <= 1048576; R <= 8192; n_bias <= 1024; history_width + N below 2^29.
  * ---------------------------------------------------------------------------------- */

@@ -369,6 +369,8 @@ int adjust_logits(PyObject* const* a) {
     m = rows(a[11], "mask");
     if (m.type != at::kInt || m.m < (x.m + 31) / 32)
       refuse("mask must be torch.int32 with at least " + std::to_string((x.m + 31) / 32) + " words a row");
+    if (m.n < x.n && a[12] == Py_None)  // (a mask of no rows has no address, by which the call below would know it)
+      refuse("without mask_row there is a mask row for each of the " + std::to_string(x.n) + " rows, got " + std::to_string(m.n));
   }
   const int64_t nb = R * (int64_t)b.m;
   return dspark_adjust_logits(

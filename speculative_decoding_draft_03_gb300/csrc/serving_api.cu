@@ -542,7 +542,7 @@ dspark_status dspark_adjust_logits(int N, int V, int R, int dtype, const void* l
       return fail(DSPARK_INVALID_ARG, "a mask has mask_rows=%d rows of at least %d words", mask_rows, (V + 31) / 32);
     if (mask_row == nullptr && mask_rows < N)
       return fail(DSPARK_INVALID_ARG, "without mask_row there is a mask row for each of the %d rows, got %d", N, mask_rows);
-  } else if (mask_row != nullptr) {
+  } else if (mask_row != nullptr && mask_rows != 0) {  // (a mask without rows may have no address: no row goes by it)
     return fail(DSPARK_INVALID_ARG, "mask_row goes with a mask");
   }
   if (N == 0) return DSPARK_OK;

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from tests import position_ref as ref
+from tests import test_gpu_adjust as adjust
 from tests import test_gpu_chunk_attention as chunk
 from tests.test_gpu_attention import _case, _i32
 
@@ -64,3 +65,20 @@ def test_windows_near_two_to_the_31(b, dtype, cache, D):
     assert b.device_status(ws) == 0
     small = dict(c, table=c["table"][:, :8])
     chunk._compare(small, o, 0.1, window, lens=[0, 100, 700])
+
+
+@pytest.mark.parametrize("words", [32, 40])
+def test_a_mask_without_rows(b, words):
+    """A step in which no row is under a grammar: masks of shape [0, words], every row's choice out of range."""
+    x, c = adjust._case([3, 1], [40, 3], 1000, torch.bfloat16, seed=2, biases=3)
+    d = adjust._gpu(c)
+    want = b.adjust_logits(x, **d)
+    mask = torch.zeros((0, words), dtype=torch.int32, device="cuda")
+    for row in ([-1] * 4, [0, 7, -1, 2]):
+        for out in (None, x.clone()):
+            got = b.adjust_logits(x if out is None else out, **d, mask=mask, mask_row=_i32(row), out=out)
+            assert torch.equal(got, want)
+    with pytest.raises(b.DSparkError, match="a mask row for each of the 4 rows, got 0"):
+        b.adjust_logits(x, **d, mask=mask)
+    with pytest.raises(b.DSparkError, match="at least 32 words"):
+        b.adjust_logits(x, **d, mask=mask[:, :31], mask_row=_i32([-1] * 4))
