@@ -82,3 +82,37 @@ def test_a_mask_without_rows(b, words):
         b.adjust_logits(x, **d, mask=mask)
     with pytest.raises(b.DSparkError, match="at least 32 words"):
         b.adjust_logits(x, **d, mask=mask[:, :31], mask_row=_i32([-1] * 4))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_inputs_written_just_before(b, in_place):
+    """Everything that adjust_logits reads beside the logits, written by the kernels right before it on the stream,
+    eagerly and in a graph: what it gives is what the same inputs give after a wait."""
+    x, c = adjust._case([3, 8, 1, 5], [900, 3000, 0, 2000], 20001, torch.bfloat16, seed=3, biases=20, masks=6)
+    names = [n for n in c if n != "q_start"]
+    sets = []
+    for seed in range(4):
+        d = adjust._gpu(adjust._case([3, 8, 1, 5], [900, 3000, 0, 2000], 20001, torch.bfloat16, seed=seed, biases=20, masks=6)[1])
+        sets.append(d)
+    want = [b.adjust_logits(x, **d) for d in sets]
+    torch.cuda.synchronize()
+    live = {n: t.clone() for n, t in sets[0].items()}
+    logits = x.clone()
+
+    def step(i):
+        logits.copy_(x)
+        for n in names:
+            live[n].copy_(sets[i][n])
+        return b.adjust_logits(logits, **live, out=logits if in_place else None)
+
+    graphs = []
+    for i in range(4):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, step(i)))
+    for k in range(100):
+        i = k * 7 % 4
+        got = step(i)
+        assert torch.equal(got, want[i]), k
+        graphs[i][0].replay()
+        assert torch.equal(graphs[i][1], want[i]), k
