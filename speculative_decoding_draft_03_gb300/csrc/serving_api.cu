@@ -524,9 +524,10 @@ dspark_status dspark_adjust_logits(int N, int V, int R, int dtype, const void* l
   if (!is_float_type(dtype)) return fail(DSPARK_INVALID_ARG, "bad dtype %d", dtype);
   if (row_stride < V) return fail(DSPARK_INVALID_ARG, "row_stride %lld is below V=%d", (long long)row_stride, V);
   if (out_stride < V) return fail(DSPARK_INVALID_ARG, "out_stride %lld is below V=%d", (long long)out_stride, V);
+  const int64_t entries = (history != nullptr ? history_width : 0) + (int64_t)N;  // (counted in 29 bits)
+  if (entries >= 1 << 29)
+    return fail(DSPARK_UNSUPPORTED_SHAPE, "history_width + N = %lld must be below 2^29", (long long)entries);
   if (history != nullptr) {
-    if ((int64_t)history_width + N >= 1 << 29)
-      return fail(DSPARK_UNSUPPORTED_SHAPE, "history_width + N = %lld must be below 2^29", (long long)history_width + N);
     if (history_width < 0 || history_stride < history_width)
       return fail(DSPARK_INVALID_ARG, "history_stride %lld is below history_width=%d", (long long)history_stride, history_width);
     CHECK_PTR(history_len);

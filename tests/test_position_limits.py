@@ -23,3 +23,11 @@ def test_a_mask_without_rows(b):
     assert _adjust(b, mask=None, mr=0) == OK
     assert _adjust(b, mask=None, mr=1) == INVALID
     assert _adjust(b, mask=None, mr=0, mask_row=None) == OK and _adjust(b, mr=0) == OK
+
+
+def test_tokens_alone_are_counted_in_29_bits_too(b):
+    """The limit on history_width + N holds without a history: the block's tokens are counted in the same words."""
+    for n in (1 << 29, (1 << 31) - 1):
+        assert _adjust(b, N=n, hist=None, mask=None, mr=0, mask_row=None) == UNSUPPORTED
+        assert "2^29" in b.lib.dspark_last_error_message().decode()
+    assert _adjust(b, hist=None, hw=1 << 30, mask=None, mr=0, mask_row=None) == OK  # (a width of no history)
