@@ -597,7 +597,8 @@ DSPARK_API dspark_status dspark_paged_attention_granted(
  * queries (a chunk of a prompt, a whole prompt, or both beside requests that decode).
  *
  * Arguments, results and refusals are dspark_paged_attention_granted's, but for max_q, which
- * this call does not have.  Blocks of D > 128, over pages that no multiple of 8 tokens
+ * this call does not have, and for T + window, which must be below 2^31 - 1024 (a window of
+ * max_pages * page_size tokens or more counts as none).  Blocks of D > 128, over pages that no multiple of 8 tokens
  * divides, or over pools whose entries lie on one another, are computed 16 or 32 query rows
  * at a time, much slower.
  * Workspace: dspark_chunk_attention_workspace_size() (0 for unsupported sizes).

@@ -97,10 +97,6 @@ __device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t two) {
 
 // ------------------------------------------------------------------------------- the plan
 
-// The last position before the window of a query that sees up to position `last`.  (Below 0, `last` sees
-// nothing: counted as 0, it keeps the difference within 32 bits.)
-__device__ __forceinline__ int before_window(const AttentionArgs& a, int last) { return max(last, 0) - a.window; }
-
 struct Request {
   int len, nq, q0, first;  // first: where its units begin, a multiple of TK at or before what it sees
   int chunks, blocks;      // units of a (head, ROWS query rows) item, and such items per head
@@ -123,7 +119,7 @@ __device__ __forceinline__ Request request(const AttentionArgs& a, int r, bool r
   }
   if (k.nq == 0) return k;
   if (a.granted != nullptr && a.granted[r] == 0) k.len = 0;  // its queries see nothing
-  if (a.window > 0) k.first = max(0, before_window(a, k.len - k.nq) + 1) / TK * TK;
+  if (a.window > 0) k.first = max(0, k.len - k.nq - a.window + 1) / TK * TK;
   k.chunks = max(1, (k.len - k.first + TK - 1) / TK);
   k.blocks = (k.nq * a.G - 1) / ROWS + 1;  // (a call's rows may reach 2^31 - 1: none may be added to them)
   return k;
@@ -132,7 +128,7 @@ __device__ __forceinline__ Request request(const AttentionArgs& a, int r, bool r
 // Does a query of request k see the position, or a later one?  (The first unit may begin before all
 // that they see.)
 __device__ __forceinline__ bool seen(const AttentionArgs& a, const Request& k, int pos) {
-  return a.window == 0 || pos > before_window(a, k.len - k.nq);
+  return a.window == 0 || pos > k.len - k.nq - a.window;
 }
 
 // A share that a worker leaves to the joining kernel: the item's place and its units.

@@ -209,7 +209,7 @@ __device__ __forceinline__ Block block_of(const AttentionArgs& a, const Request&
   const int i0 = row0 / a.G, i1 = min(k.nq - 1, (row0 + kItem - 1) / a.G);
   x.last0 = before + i0;
   x.last1 = before + i1;
-  x.first = a.window > 0 ? max(0, before_window(a, x.last0) + 1) / kTile * kTile : 0;
+  x.first = a.window > 0 ? max(0, x.last0 - a.window + 1) / kTile * kTile : 0;
   x.tiles = x.last1 < x.first ? 1 : (x.last1 - x.first) / kTile + 1;
   return x;
 }
@@ -237,7 +237,7 @@ __device__ __forceinline__ void next_item(const AttentionArgs& a, Place& c) {
 __device__ __forceinline__ bool two_tiles(const AttentionArgs& a, const Place& c) { return c.k.nq * a.G - c.x.b * kItem > kRowsOf; }
 // Does a row of the item not see all of the tile that begins at p0?
 __device__ __forceinline__ bool at_edge(const AttentionArgs& a, const Block& x, int p0) {
-  return p0 + kTile - 1 > x.last0 || (a.window > 0 && p0 <= before_window(a, x.last1));
+  return p0 + kTile - 1 > x.last0 || (a.window > 0 && p0 <= x.last1 - a.window);
 }
 
 // (a worker's part of an item ends with the worker's last tile)
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
     auto look_up = [&]() {
       const int pos = use.x.first + use.t * kTile + lane * box, nth = pos / a.page_size;
       slot = pos - nth * a.page_size;
-      inside = lane < boxes && pos <= use.x.last1 && (a.window == 0 || pos + box - 1 > before_window(a, use.x.last0));
+      inside = lane < boxes && pos <= use.x.last1 && (a.window == 0 || pos + box - 1 > use.x.last0 - a.window);
       page = inside ? a.page_table[use.r * a.table_stride + nth] : -1;
     };
     if (tiles > 0) look_up();
@@ -595,8 +595,8 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
           const int token = 32 * j + lane, pos = p0 + token;
           const uint32_t row = base + L::v + vs * L::tile + token * 128;
           auto piece = [&](int c) { return row + (c >> 3) * (kTile * 128) + (((c & 7) ^ (token & 7)) << 4); };
-          const bool unseen = pos > use.x.last1 || (a.window > 0 && pos <= before_window(a, use.x.last0));
-          const bool partly = !unseen && (pos > use.x.last0 || (a.window > 0 && pos <= before_window(a, use.x.last1)));
+          const bool unseen = pos > use.x.last1 || (a.window > 0 && pos <= use.x.last0 - a.window);
+          const bool partly = !unseen && (pos > use.x.last0 || (a.window > 0 && pos <= use.x.last1 - a.window));
           uint32_t top = 0;  // the largest exponents, by halves
           if (__any_sync(~0u, partly))
 #pragma unroll 4
@@ -653,8 +653,8 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
       if (i >= L::v_stages && !wait_for(bar(L::v_empty + vs), (i / L::v_stages - 1) & 1, abort_flag, a.status, 631)) break;
       const uint32_t to = base + L::v + vs * L::tile;
       if (at_edge(a, use.x, p0)) {
-        const bool unseen = pos > use.x.last1 || (a.window > 0 && pos <= before_window(a, use.x.last0));
-        const bool partly = !unseen && (pos > use.x.last0 || (a.window > 0 && pos <= before_window(a, use.x.last1)));
+        const bool unseen = pos > use.x.last1 || (a.window > 0 && pos <= use.x.last0 - a.window);
+        const bool partly = !unseen && (pos > use.x.last0 || (a.window > 0 && pos <= use.x.last1 - a.window));
         const bool strange = convert(base + L::v_raw, to, unseen, partly);
         const uint32_t strangers = __ballot_sync(~0u, strange);
         if (lane == 0) odd[4 * vs + warp - 4] = strangers;
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
       const int last0 = use.k.len - use.k.nq + tile_row / G,
                 last1 = use.k.len - use.k.nq + min(use.k.nq - 1, (tile_row + kRowsOf - 1) / G);
       const int begin = use.x.first + use.t * kTile;
-      const int gate_from = use.x.last0 - kTile + 2, gate_upto = a.window > 0 ? before_window(a, use.x.last1) : -1;
+      const int gate_from = use.x.last0 - kTile + 2, gate_upto = a.window > 0 ? use.x.last1 - a.window : -1;
       float ref = kUnset;
       Two sum0 = two(0.f, 0.f), sum1 = two(0.f, 0.f);
       for (int t = mine ? 0 : n - 1; t < n; ++t) {
@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
           if (mine) fetch();
         }
         if (was_mine) {
-          const bool edge = __builtin_expect(gated, 0) && (p0 + kTile - 1 > last0 || (a.window > 0 && p0 <= before_window(a, last1)));
+          const bool edge = __builtin_expect(gated, 0) && (p0 + kTile - 1 > last0 || (a.window > 0 && p0 <= last1 - a.window));
           // a new reference where a score passes the old one by too much
           auto refer = [&](float most) {
             if (!__any_sync(~0u, most > ref + (kSlack + H::kLift))) return;
@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
           // what the row does not see goes out of its scores, in a pass of its own: the loops below stay short (with
           // the selects in them, 8192 causal queries took 474 us for 460, and with D = 64 452 for 419)
           if (edge) {
-            const int hi = last - p0, lo = a.window > 0 ? before_window(a, last) - p0 + 1 : 0;
+            const int hi = last - p0, lo = a.window > 0 ? hi - a.window + 1 : 0;
 #pragma unroll 1
             for (int c = 0; c < kTile; c += 16) {
               float s[16];

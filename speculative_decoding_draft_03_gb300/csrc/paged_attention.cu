@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(WARPS * 32, CTAS) attention_kernel(const __gri
         if (edge) {
           const int row = row0 + 8 * nb + 2 * t4 + z;
           last = row < use.k.nq * G ? use.k.len - use.k.nq + row / G : -1;
-          if (a.window > 0) low = before_window(a, last) + 1;
+          if (a.window > 0) low = last - a.window + 1;
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i)

@@ -408,6 +408,10 @@ dspark_status dspark_chunk_attention(int T, int R, int Hq, int Hkv, int D, int n
                                      int window, void* out, float* lse_out, void* workspace, size_t ws_bytes,
                                      void* stream) {
   CHECK(check_attention(T, R, Hq, Hkv, D, num_pages, page_size, max_pages, table_stride, window, scale));
+  if (window >= (int64_t)max_pages * page_size) window = 0;  // (all that a table can hold)
+  // (a query that lies as far before its context as there are rows sees nothing: its window begins further back yet)
+  if ((int64_t)T + window >= ((int64_t)1 << 31) - 1024)
+    return fail(DSPARK_UNSUPPORTED_SHAPE, "T + window = %lld must be below 2^31 - 1024", (long long)T + window);
   CHECK(check_rows(D, dtype_q, dtype_kv, k_pool, v_pool, page_stride, head_stride, token_stride, k_scale, v_scale));
   CHECK_PTR(page_table);
   CHECK_PTR(seq_len);
@@ -425,7 +429,7 @@ dspark_status dspark_chunk_attention(int T, int R, int Hq, int Hkv, int D, int n
   a.page_stride = page_stride; a.head_stride = head_stride; a.token_stride = token_stride;
   a.page_table = page_table; a.table_stride = table_stride; a.seq_len = seq_len; a.q_start = q_start;
   a.granted = granted; a.scale = scale; a.k_scale = k_scale; a.v_scale = v_scale; a.out = out; a.lse_out = lse_out;
-  a.window = window < (int64_t)max_pages * page_size ? window : 0;  // (as above)
+  a.window = window;
   a.status = static_cast<dspark::DeviceStatus*>(workspace);
   return launched(dspark::launch_chunk_attention(a, static_cast<unsigned char*>(workspace) + 256,
                                                  static_cast<cudaStream_t>(stream)),

@@ -53,18 +53,20 @@ def test_query_rows_up_to_the_limit(b):
 
 @pytest.mark.parametrize("dtype,cache", [chunk.TYPES[0], chunk.TYPES[2]])
 @pytest.mark.parametrize("D", [128, 256])
-def test_windows_near_two_to_the_31(b, dtype, cache, D):
-    """Windows as long as tables allow, over slots with far more queries than positions: where the window of a
-    query that sees nothing would begin lies below -2^31."""
+def test_the_longest_windows(b, dtype, cache, D):
+    """Windows up to the limit with the call's rows, over slots with far more queries than positions: where the
+    window of a query that sees nothing would begin lies at the end of 32 bits."""
     lens, new = [60, 100, 700], [700, 900, 300]
     c = _case(lens, new, 2, 1, D, 256, dtype, cache, seed=31)
     width = (1 << 23) - 2
     c["table"] = np.pad(c["table"], ((0, 0), (0, width - c["table"].shape[1])), constant_values=-1)
-    window = width * 256 - 1
-    o, ws = chunk._run(b, c, 0.1, window, granted=_i32([0, 900, 300]))
+    window = (1 << 31) - 1024 - sum(new)
+    with pytest.raises(b.DSparkError, match="must be below 2\\^31 - 1024"):
+        chunk._run(b, c, 0.1, window)
+    o, ws = chunk._run(b, c, 0.1, window - 1, granted=_i32([0, 900, 300]))
     assert b.device_status(ws) == 0
     small = dict(c, table=c["table"][:, :8])
-    chunk._compare(small, o, 0.1, window, lens=[0, 100, 700])
+    chunk._compare(small, o, 0.1, window - 1, lens=[0, 100, 700])
 
 
 @pytest.mark.parametrize("words", [32, 40])
