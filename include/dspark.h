@@ -558,7 +558,8 @@ DSPARK_API dspark_status dspark_cache_compact(
  * is reported and read as zeros.
  *
  *   q        [T,Hq,D] with strides between tokens and heads; DSPARK_BF16 or DSPARK_F16.
- *   dtype_kv the type of q, or DSPARK_E4M3 with k_scale, v_scale [Hkv] (NULL otherwise).
+ *   dtype_kv the type of q, or DSPARK_E4M3 with k_scale, v_scale [Hkv] (NULL otherwise; any values:
+ *            a NaN reaches all that its head's queries see).
  *   max_q    an upper bound of every nq, 1..128; a request with more, or one whose queries
  *            do not lie within [0,T), is reported and its rows are not written.
  *   out      [T,Hq,D] of q's type, contiguous; lse_out [T,Hq] fp32 or NULL.

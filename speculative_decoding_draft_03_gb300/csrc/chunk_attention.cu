@@ -67,6 +67,15 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort_flag, DeviceStatus* st, int where) {
   return mbar_test(bar, parity) || wait_on(bar, parity, abort_flag, st, where);
 }
+// A row of fp16 queries with its signs turned, or of NaN.  (Out of line: hardly ever called.)
+__device__ __noinline__ void odd_scale(uint32_t at, int swizzle, int pieces, bool turn) {
+  const uint32_t f = turn ? 0x80008000u : 0u, n = turn ? 0u : 0x7FFF7FFFu;
+  for (int c = 0; c < pieces; ++c) {
+    const uint32_t p = at + (c >> 3) * (kTile * 128) + (((c & 7) ^ swizzle) << 4);
+    const uint4 v = lds16(p);
+    sts16(p, make_uint4((v.x ^ f) | n, (v.y ^ f) | n, (v.z ^ f) | n, (v.w ^ f) | n));
+  }
+}
 // Products and commits by one elected lane of a warp.  Matrices in shared memory go by their descriptors' lower
 // halves (the upper ones: rows of 128 bytes in groups of eight, swizzled).  All products of a matrix in one
 // statement: 16 columns of both operands each, one election.
@@ -712,33 +721,42 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
     };
     auto fetched = [&]() {
       copy_wait<0>();
-      int e2 = 0;
-      if (Q8 && BFQ) {
-        // fp16 operands: the row is scaled by a power of two to a maximum in [1, 2) (what falls below 2^-24 of
-        // it is lost, far under the sums' rounding)
+      if constexpr (Q8) {
+        float c = fabsf(a.scale) * kLog2e * a.k_scale[use.h];  // (the sign of the first is in the products)
         __syncwarp();
         const uint32_t mine = base + L::q + x * L::tile + row * 128;
         auto piece = [&](int c) { return mine + (c >> 3) * (kTile * 128) + (((c & 7) ^ (row & 7)) << 4); };
-        uint32_t top = 0;  // (floats without their signs are in the order of their bits)
+        if constexpr (BFQ) {
+          // fp16 operands: the row is scaled by a power of two to a maximum in [1, 2) (what falls below 2^-24 of
+          // it is lost, far under the sums' rounding)
+          uint32_t top = 0;  // (floats without their signs are in the order of their bits)
 #pragma unroll 4
-        for (int c = 0; c < DP / 8; ++c) {
-          const uint4 v = lds16(piece(c));
-          top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs), __vmaxu2(v.z & kAbs, v.w & kAbs)));
-        }
-        const int most = (int)(max(top & 0xFFFFu, top >> 16) >> 7);  // its exponent's bits
-        e2 = most == 0xFF ? 0 : min(max(most, 1), 253) - 127;
-        if (top == 0) e2 = 0;
-        const float down = __int_as_float((127 - e2) << 23);
+          for (int c = 0; c < DP / 8; ++c) {
+            const uint4 v = lds16(piece(c));
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & kAbs, v.y & kAbs), __vmaxu2(v.z & kAbs, v.w & kAbs)));
+          }
+          const int most = (int)(max(top & 0xFFFFu, top >> 16) >> 7);  // its exponent's bits
+          int e2 = most == 0xFF ? 0 : min(max(most, 1), 253) - 127;
+          if (top == 0) e2 = 0;
+          c *= __int_as_float((127 + e2) << 23);
+          const float down = __int_as_float((127 - e2) << 23);
 #pragma unroll 2
-        for (int c = 0; c < DP / 8; ++c) {
-          const uint4 v = lds16(piece(c));
-          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          for (int c = 0; c < DP / 8; ++c) {
+            const uint4 v = lds16(piece(c));
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = Half16<false>::pack(Half16<true>::lo(w[e]) * down, Half16<true>::hi(w[e]) * down);
-          sts16(piece(c), make_uint4(w[0], w[1], w[2], w[3]));
+            for (int e = 0; e < 4; ++e) w[e] = Half16<false>::pack(Half16<true>::lo(w[e]) * down, Half16<true>::hi(w[e]) * down);
+            sts16(piece(c), make_uint4(w[0], w[1], w[2], w[3]));
+          }
         }
+        // A k_scale below 0 turns the queries' signs, one that is no number makes them none, as masks are put into the
+        // scores and must stay -inf times c2.  (With this loop in line 512 queries at 65536 tokens took 484 us, so 420; 415
+        // without it.)
+        if (!(c >= 0.f)) odd_scale(mine, row & 7, DP / 8, c < 0.f);
+        c2 = fmaxf(fabsf(c), 0x1p-149f);
+      } else {
+        c2 = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-149f);
       }
-      c2 = fmaxf(fabsf(a.scale) * kLog2e * (Q8 ? a.k_scale[use.h] : 1.f) * __int_as_float((127 + e2) << 23), 1e-37f);
       fence_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::q_ready + x));

@@ -118,3 +118,35 @@ def test_inputs_written_just_before(b, in_place):
         assert torch.equal(got, want[i]), k
         graphs[i][0].replay()
         assert torch.equal(graphs[i][1], want[i]), k
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("scale", [0.1, -0.1])
+def test_scales_of_keys_with_signs_and_without_a_value(b, dtype, scale):
+    """An e4m3 cache whose heads' scales are positive, negative, NaN and 0, in long blocks as in short ones: signs
+    count, a NaN reaches every query that sees something and no other head."""
+    lens, new = [100, 300, 700], [150, 128, 300]  # (the first 50 queries see nothing)
+    c = _case(lens, new, 8, 4, 128, 16, dtype, E4M3, seed=14)
+    c["scales"] = (torch.tensor([0.7, -0.7, math.nan, 0.0]), c["scales"][1])
+    o, ws = chunk._run(b, c, scale)
+    assert b.device_status(ws) == 0
+    chunk._compare(c, o, scale)
+    out, lse = o["out"], o["lse"]
+    assert torch.isnan(out[50:, 4:6]).all() and torch.isnan(lse[50:, 4:6]).all()
+    assert (out[:50] == 0).all() and (lse[:50] == -math.inf).all() and torch.isfinite(out[50:, :4]).all()
+    short = _case([100, 300], [128, 100], 8, 4, 128, 16, dtype, E4M3, seed=15)
+    short["scales"] = c["scales"]
+    o, _ = chunk._run(b, short, scale)
+    ks, vs = (s.cuda() for s in short["scales"])
+    p = b.paged_attention(short["q"].cuda(), short["k"].cuda(), short["v"].cuda(), _i32(short["table"]), _i32(short["lens"]),
+                          _i32(short["q_start"]), 128, scale, k_scale=ks, v_scale=vs)
+    for a in (o, p):
+        chunk._compare(short, a, scale)
+    assert torch.equal(torch.isnan(o["out"]), torch.isnan(p["out"])) and torch.equal(torch.isnan(o["lse"]), torch.isnan(p["lse"]))
+
+
+def test_scores_of_a_scale_below_normal_products(b):
+    """Products near fp32's end, brought back by a scale below 1e-37: the scores are ordinary ones."""
+    c = _case([200, 300], [150, 129], 4, 1, 64, 16, torch.bfloat16, seed=16)
+    c["q"], c["k"] = (c["q"].float() * 1.5e18).bfloat16(), (c["k"].float() * 1.5e18).bfloat16()
+    chunk._check(b, c, scale=2e-38)
