@@ -13,7 +13,14 @@ namespace attention {
 constexpr int kTile = 128;  // tokens
 constexpr float kSlack = 8.f;
 constexpr float kUnset = -1e30f;  // the reference of a column that has seen nothing: any score passes it
+#ifdef DSPARK_TEST_WAIT_LIMIT
+// Test builds only: a short limit, and attention of long blocks with a window of kTestStallWindow copies no values,
+// so that the first wait for them gives up.
+constexpr long long kWaitCycles = DSPARK_TEST_WAIT_LIMIT;
+constexpr int kTestStallWindow = 0x5EED;
+#else
 constexpr long long kWaitCycles = 4000000000ll;  // ~2 s
+#endif
 
 // ---------------------------------------------------------------------------- wrappers
 
@@ -35,13 +42,14 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// The same, suspended for up to 262 us while the phase is open.
+// The same, suspended for up to NS ns (262 us) while the phase is open.
+template <int NS = 1 << 18>
 __device__ __forceinline__ bool mbar_sleep(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "n"(1 << 18)
+      : "r"(bar), "r"(parity), "n"(NS)
       : "memory");
   return ok != 0;
 }

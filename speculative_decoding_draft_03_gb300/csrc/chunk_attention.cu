@@ -51,10 +51,12 @@ constexpr uint32_t kEnds = 1, kTwo = 2, kEdge = 4;  // of a tile: its item ends,
 
 // mbar_wait, out of line where the phase is still open: the roles' loops share the instruction cache, and a
 // dozen copies of it cost more than the calls (512 queries at 65536 tokens of an e4m3 cache took 470 us so, 580
-// inlined).
+// inlined).  Suspended for 2 us at a time, though hardly a wait is as long: the flag is looked at in between, and the
+// warp that issues the products, which goes on over its tiles once a wait has given up, is through with a tile in
+// some 10 us (with 262 us at a time, in a millisecond; leaving its loop cost 2 % where nothing gives up).
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, DeviceStatus* st, int where) {
   const long long t0 = clock64();
-  while (!mbar_sleep(bar, parity)) {
+  while (!mbar_sleep<1 << 11>(bar, parity)) {
     if (*abort_flag) return false;
     if (clock64() - t0 > kWaitCycles) {
       *abort_flag = 1;
@@ -441,6 +443,9 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
   const bool aligned = (base & 1023u) == 0 && *reinterpret_cast<volatile uint32_t*>(smem + L::tmem) == tmem;
   if (!aligned && tid == 0) report_bad_input(a.status, 632);
   const int tiles = aligned && u_begin < u_end ? (int)(u_end - u_begin) : 0;
+#ifdef DSPARK_TEST_WAIT_LIMIT
+  const int all_tiles = tiles;
+#endif
   auto stand = [&]() {
     Place p = {};
     if (tiles > 0) {
@@ -459,6 +464,9 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
     // one tile ahead
     Place use = stand();
     const bool keys = warp == 0;
+#ifdef DSPARK_TEST_WAIT_LIMIT
+    const int tiles = !keys && a.window == kTestStallWindow ? 0 : all_tiles;
+#endif
     const int boxes = kTile / box;
     const int stages = Q8 ? 1 : (keys ? L::k_stages : L::v_stages);
     const int full = Q8 ? (keys ? L::kr_full : L::vr_full) : (keys ? L::k_full : L::v_full),
@@ -722,7 +730,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
     auto fetched = [&]() {
       copy_wait<0>();
       if constexpr (Q8) {
-        float c = fabsf(a.scale) * kLog2e * a.k_scale[use.h];  // (the sign of the first is in the products)
+        float by = fabsf(a.scale) * kLog2e * a.k_scale[use.h];  // (the sign of the first is in the products)
         __syncwarp();
         const uint32_t mine = base + L::q + x * L::tile + row * 128;
         auto piece = [&](int c) { return mine + (c >> 3) * (kTile * 128) + (((c & 7) ^ (row & 7)) << 4); };
@@ -738,7 +746,7 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
           const int most = (int)(max(top & 0xFFFFu, top >> 16) >> 7);  // its exponent's bits
           int e2 = most == 0xFF ? 0 : min(max(most, 1), 253) - 127;
           if (top == 0) e2 = 0;
-          c *= __int_as_float((127 + e2) << 23);
+          by *= __int_as_float((127 + e2) << 23);
           const float down = __int_as_float((127 - e2) << 23);
 #pragma unroll 2
           for (int c = 0; c < DP / 8; ++c) {
@@ -752,8 +760,8 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
         // A k_scale below 0 turns the queries' signs, one that is no number makes them none, as masks are put into the
         // scores and must stay -inf times c2.  (With this loop in line 512 queries at 65536 tokens took 484 us, so 420; 415
         // without it.)
-        if (!(c >= 0.f)) odd_scale(mine, row & 7, DP / 8, c < 0.f);
-        c2 = fmaxf(fabsf(c), 0x1p-149f);
+        if (!(by >= 0.f)) odd_scale(mine, row & 7, DP / 8, by < 0.f);
+        c2 = fmaxf(fabsf(by), 0x1p-149f);
       } else {
         c2 = fmaxf(fabsf(a.scale) * kLog2e, 0x1p-149f);
       }
