@@ -77,20 +77,21 @@ struct Piece<__half> {
 // x / scale, correctly rounded from the rounded reciprocal by one residual (Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor").  `lift` brings a scale below 2^-100 or above
 // 2^100, and x with it, nearer to 1, so that the reciprocal and the residual are normal numbers; what overflows
-// stays infinite.  (16 prompts appended to an e4m3 cache: 49 us with __fdiv_rn for scales out of
-// range beside it, 40 so.)
+// stays infinite, and an infinite scale leaves 0 of what is finite (its residual is taken with 0 in its place).
+// (16 prompts appended to an e4m3 cache: 49 us with __fdiv_rn for scales out of range beside it, 40 so.)
 struct Divisor {
   float scale, inverse, lift;
 };
 __device__ __forceinline__ Divisor divisor(float s) {
-  const float lift = s < 0x1p-100f ? 0x1p64f : (s > 0x1p100f ? 0x1p-64f : 1.f);
-  return {s * lift, __frcp_rn(s * lift), lift};
+  const float size = fabsf(s), lift = size < 0x1p-100f ? 0x1p64f : (size > 0x1p100f ? 0x1p-64f : 1.f);
+  return {size < INFINITY ? s * lift : (size == INFINITY ? 0.f : s), __frcp_rn(s * lift), lift};
 }
 // x / scale as e4m3, rounded to nearest even and held within +-448.
 __device__ __forceinline__ uint2 to_e4m3(float (&x)[8], const Divisor& by) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float y = x[i] * by.lift, q = y * by.inverse, r = fmaf(fmaf(-q, by.scale, y), by.inverse, q);
+    // (the residual by its negative: so a -0 stays one)
+    const float y = x[i] * by.lift, q = y * by.inverse, r = fmaf(-fmaf(q, by.scale, -y), by.inverse, q);
     x[i] = fabsf(q) < INFINITY ? r : q;
   }
   uint16_t p[4];

@@ -8,6 +8,7 @@ import torch
 
 from tests import position_ref as ref
 from tests import test_gpu_adjust as adjust
+from tests import test_gpu_append as append
 from tests import test_gpu_chunk_attention as chunk
 from tests.test_gpu_attention import _case, _i32
 
@@ -150,3 +151,24 @@ def test_scores_of_a_scale_below_normal_products(b):
     c = _case([200, 300], [150, 129], 4, 1, 64, 16, torch.bfloat16, seed=16)
     c["q"], c["k"] = (c["q"].float() * 1.5e18).bfloat16(), (c["k"].float() * 1.5e18).bfloat16()
     chunk._check(b, c, scale=2e-38)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("scale", [math.inf, -math.inf, -3e38, -1e31, -1e19, -0.7, -1e-31, -1e-44, 0.0, -0.0, math.nan])
+def test_divisions_by_any_scale(b, dtype, scale):
+    """Values stored in an e4m3 cache by cache_append as by cache_write, whatever their scales: infinite, negative, 0 and
+    NaN; bit for bit, but for the sign of a 0 that a negative scale divides."""
+    make = lambda: append.Case([300], [300], 1, 2, 64, 16, dtype, E4M3, seed=2)
+    c, d = make(), make()
+    c.scales = [torch.tensor([scale, 1.0], device="cuda") for _ in range(2)]
+    size = torch.tensor([1.0, 1e-3, 30.0], device="cuda").repeat(100)[:, None, None]
+    c.v = (c.v.float() * size).to(dtype)
+    c.v[7, :, 3], c.v[9, :, 60], c.v[11, :, 0], c.v[12, :, 1], c.v[13, :, 2] = math.inf, -math.inf, math.nan, 0.0, -0.0
+    if dtype == torch.bfloat16:
+        c.v[14:20] *= 1e36
+    c.call(b, b.rotary_rates(64), q=None)
+    b.cache_write(c.k, c.v, *d.pools, _i32(d.table), _i32(d.lens), _i32(d.q_start), k_scale=c.scales[0], v_scale=c.scales[1])
+    got, want = (append._bits(x.pools[1]).int() for x in (c, d))
+    if math.copysign(1.0, scale) < 0:  # (0 / s is -0: the quotient's -0 and the residual's +0 add up to +0, the same value)
+        got, want = (torch.where(x == 128, 0, x) for x in (got, want))
+    assert torch.equal(got, want)
