@@ -657,6 +657,17 @@ DSPARK_API dspark_status dspark_cache_append(
     const int32_t* q_start, const int32_t* granted, const float* k_scale, const float* v_scale, const int64_t* rates,
     float magnitude, void* workspace, size_t ws_bytes, void* stream);
 
+/* The same for any even rot_dim (2..D), as dspark_rotary takes it.  Where it is no multiple of 16 (of 8
+ * with interleaved pairs) a row's elements go pair by pair, some three times as slowly. */
+DSPARK_API dspark_status dspark_cache_append_any(
+    int T, int R, int Hq, int Hkv, int D, int rot_dim, int interleaved, int num_pages, int page_size, int max_pages,
+    int dtype_in, int dtype_kv, const void* q, int64_t q_stride_token, int64_t q_stride_head, const void* k,
+    const void* v, int64_t in_stride_token, int64_t in_stride_head, void* q_out, int64_t q_out_stride_token,
+    int64_t q_out_stride_head, void* k_pool, void* v_pool, int64_t page_stride, int64_t head_stride,
+    int64_t token_stride, const int32_t* page_table, int64_t table_stride, const int32_t* seq_len,
+    const int32_t* q_start, const int32_t* granted, const float* k_scale, const float* v_scale, const int64_t* rates,
+    float magnitude, void* workspace, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------------------------
  * Logits adjusted before tokens are taken from them (or verified, or given probabilities).
  *

@@ -118,6 +118,8 @@ def _load_library():
     lib.dspark_cache_append.argtypes = ([i32] * 12 + [P, i64, i64, P, P, i64, i64, P, i64, i64, P, P, i64, i64, i64, P, i64]
                                         + [P] * 5 + [P, f32, P, sz, P])
     lib.dspark_cache_append.restype = i32
+    lib.dspark_cache_append_any.argtypes = lib.dspark_cache_append.argtypes
+    lib.dspark_cache_append_any.restype = i32
     lib.dspark_adjust_logits.argtypes = ([i32] * 4 + [P, i64, P, P, P, i64, i32] + [P] * 5 + [i32, P, P, P, i64, i32, P, P,
                                                                                              i64, P])
     lib.dspark_adjust_logits.restype = i32
@@ -988,10 +990,10 @@ def rotary(x, positions, rates, interleaved=False, magnitude=1.0, inverse=False,
 
 def cache_append(q, k, v, k_pool, v_pool, page_table, seq_len, q_start, rates, interleaved=False, magnitude=1.0,
                  granted=None, k_scale=None, v_scale=None, q_out=None, ws=None, stream=None):
-    """cache_write with rotary positions on the way (dspark_cache_append): every slot's last tokens'
+    """cache_write with rotary positions on the way (dspark_cache_append_any): every slot's last tokens'
     keys k [T,Hkv,D] are turned by their position in the slot and stored with the values, and their
-    queries q [T,Hq,D] turned into q_out (made where it is not given; q itself will do).  Returns
-    q_out; None where q is."""
+    queries q [T,Hq,D] turned into q_out (made where it is not given; q itself will do).  Any even
+    number of elements may turn (2 * len(rates), up to D).  Returns q_out; None where q is."""
     _here(k, "k")
     if ws is None or (q_out is None and q is not None):
         with _made_on(stream):
@@ -1002,7 +1004,7 @@ def cache_append(q, k, v, k_pool, v_pool, page_table, seq_len, q_start, rates, i
     st = _m.cache_append(q, k, v, k_pool, v_pool, page_table, seq_len, q_start, rates, bool(interleaved), magnitude, granted,
                          k_scale, v_scale, q_out, ws, _raw_stream(stream))
     if st:
-        _check(st, "dspark_cache_append")
+        _check(st, "dspark_cache_append_any")
     return q_out
 
 

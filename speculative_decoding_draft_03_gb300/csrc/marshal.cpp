@@ -340,7 +340,7 @@ int cache_append(PyObject* const* a) {
   const Rows t = page_table(a[5]);
   const Workspace w = workspace(a[15]);
   const int rot = rotating(a[8]);
-  return dspark_cache_append(
+  return dspark_cache_append_any(
       to_int(k.T, "k"), t.n, to_int(q.heads, "Hq"), to_int(H, "Hkv"), to_int(D, "D"), rot, integer(a[9], "interleaved"),
       to_int(p.size[0], "num_pages"), to_int(p.size[2], "page_size"), t.m, cache_type(k.type), p.type, q.p, q.token, q.head, k.p,
       v.p, k.token, k.head, y.p, y.token, y.head, p.k, p.v, p.stride[0], p.stride[1], p.stride[2], static_cast<int32_t*>(t.p),

@@ -86,17 +86,21 @@ __device__ __forceinline__ Divisor divisor(float s) {
   const float size = fabsf(s), lift = size < 0x1p-100f ? 0x1p64f : (size > 0x1p100f ? 0x1p-64f : 1.f);
   return {size < INFINITY ? s * lift : (size == INFINITY ? 0.f : s), __frcp_rn(s * lift), lift};
 }
-// x / scale as e4m3, rounded to nearest even and held within +-448.
+__device__ __forceinline__ float divided(float x, const Divisor& by) {
+  // (the residual by its negative: so a -0 stays one)
+  const float y = x * by.lift, q = y * by.inverse, r = fmaf(-fmaf(q, by.scale, -y), by.inverse, q);
+  return fabsf(q) < INFINITY ? r : q;
+}
+// x / scale as e4m3, rounded to nearest even and held within +-448: two of them, and eight.
+__device__ __forceinline__ uint16_t to_e4m3(float x0, float x1, const Divisor& by) {
+  uint16_t p;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p) : "f"(divided(x1, by)), "f"(divided(x0, by)));
+  return p;
+}
 __device__ __forceinline__ uint2 to_e4m3(float (&x)[8], const Divisor& by) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // (the residual by its negative: so a -0 stays one)
-    const float y = x[i] * by.lift, q = y * by.inverse, r = fmaf(-fmaf(q, by.scale, -y), by.inverse, q);
-    x[i] = fabsf(q) < INFINITY ? r : q;
-  }
   uint16_t p[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(p[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+  for (int i = 0; i < 4; ++i) p[i] = to_e4m3(x[2 * i], x[2 * i + 1], by);
   return make_uint2(p[0] | ((uint32_t)p[1] << 16), p[2] | ((uint32_t)p[3] << 16));
 }
 
@@ -107,6 +111,13 @@ __device__ __forceinline__ float2 turn_of(int position, int64_t rate, float magn
   float s, c;
   sincospif((float)top * 0x1p-31f, &s, &c);  // half turns in [-1, 1]
   return make_float2(c * magnitude, (back ? -s : s) * magnitude);
+}
+
+// A pair turned, in place: the same roundings in every kernel here.
+__device__ __forceinline__ void turn_pair(float& p, float& q, float2 t) {
+  const float p0 = p;
+  p = fmaf(p0, t.x, -(q * t.y));
+  q = fmaf(p0, t.y, q * t.x);
 }
 
 // Where pair i's factors stand among a token's in shared memory: neighbouring pieces' pairs with the
@@ -130,21 +141,11 @@ struct Turned {
     Piece<T>::unpack(a, x);
     if (INTER) {
 #pragma unroll
-      for (int j = 0; j < PAIRS; ++j) {
-        const float2 t = f[j * pieces + u];
-        const float p = x[2 * j], q = x[2 * j + 1];
-        x[2 * j] = p * t.x - q * t.y;
-        x[2 * j + 1] = q * t.x + p * t.y;
-      }
+      for (int j = 0; j < PAIRS; ++j) turn_pair(x[2 * j], x[2 * j + 1], f[j * pieces + u]);
     } else {
       Piece<T>::unpack(b, y);
 #pragma unroll
-      for (int j = 0; j < PAIRS; ++j) {
-        const float2 t = f[j * pieces + u];
-        const float p = x[j], q = y[j];
-        x[j] = p * t.x - q * t.y;
-        y[j] = q * t.x + p * t.y;
-      }
+      for (int j = 0; j < PAIRS; ++j) turn_pair(x[j], y[j], f[j * pieces + u]);
     }
   }
 };
@@ -203,10 +204,10 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
           continue;
         }
         const int i0 = INTER ? 2 * u : u, i1 = INTER ? 2 * u + 1 : u + pairs;
-        const float2 c = factors[t * pairs + u];
-        const float p = Piece<T>::one(from + i0), q = Piece<T>::one(from + i1);
-        Piece<T>::one(to + i0, p * c.x - q * c.y);
-        Piece<T>::one(to + i1, q * c.x + p * c.y);
+        float p = Piece<T>::one(from + i0), q = Piece<T>::one(from + i1);
+        turn_pair(p, q, factors[t * pairs + u]);
+        Piece<T>::one(to + i0, p);
+        Piece<T>::one(to + i1, q);
       }
     }
   }
@@ -321,6 +322,49 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   }
 }
 
+// The same where the turned part is not whole pieces: a pair of a token's elements a thread (of the part that turns
+// its pairs, else neighbours), a token a CTA.  What bounds it: instructions, some 40 a pair.  (9.5 K tokens of 48 heads
+// of 80, 40 of them turned: 95 us, all 80 by pieces 29; with four pairs' loads together 97.)
+constexpr int kPairThreads = 256;
+template <typename T, bool INTER, bool QUANT>
+__global__ void __launch_bounds__(kPairThreads) append_pairs_kernel(const __grid_constant__ AppendArgs a) {
+  extern __shared__ float2 factors[];  // [pairs]
+  __shared__ Place place;
+  griddep_wait();
+  griddep_allow_next();
+  const int pairs = a.rot / 2, half = a.D / 2, t = blockIdx.x;
+  if (threadIdx.x == 0) place = place_token(a, t);
+  __syncthreads();
+  if (place.position < 0) return;
+  for (int i = threadIdx.x; i < pairs; i += kPairThreads) factors[i] = turn_of(place.position, a.rates[i], a.magnitude, false);
+  __syncthreads();
+  const int of_q = a.Hq * half, of_k = of_q + a.Hkv * half, all = of_k + a.Hkv * half;
+  for (int k = threadIdx.x; k < all; k += kPairThreads) {
+    const bool is_q = k < of_q, is_v = k >= of_k;
+    const int in = k - (is_q ? 0 : (is_v ? of_k : of_q)), h = in / half, u = in - h * half;
+    const bool turns = !is_v && u < pairs;
+    const int i0 = turns && !INTER ? u : 2 * u, i1 = turns && !INTER ? u + pairs : 2 * u + 1;
+    const T* from = static_cast<const T*>(is_q ? a.q : (is_v ? a.v : a.k)) + t * (is_q ? a.q_token : a.in_token) +
+                    h * (is_q ? a.q_head : a.in_head);
+    const int64_t at = is_q ? t * a.q_out_token + h * a.q_out_head : place.at + h * a.head_stride;
+    void* to = is_q ? a.q_out : (is_v ? a.v_pool : a.k_pool);
+    const T x = from[i0], y = from[i1];
+    float p = Piece<T>::one(&x), q = Piece<T>::one(&y);
+    if (turns) turn_pair(p, q, factors[u]);
+    if constexpr (QUANT) {
+      if (!is_q) {
+        const uint16_t two = to_e4m3(p, q, divisor((is_v ? a.v_scale : a.k_scale)[h]));
+        uint8_t* row = static_cast<uint8_t*>(to) + at;
+        row[i0] = (uint8_t)two, row[i1] = (uint8_t)(two >> 8);
+        continue;
+      }
+    }
+    T* row = static_cast<T*>(to) + at;
+    if (turns) Piece<T>::one(row + i0, p), Piece<T>::one(row + i1, q);
+    else row[i0] = x, row[i1] = y;  // as they are
+  }
+}
+
 template <typename T, bool INTER>
 cudaError_t launch(const RotaryArgs& a, cudaStream_t s) {
   constexpr int E = kPiece<T>;
@@ -345,6 +389,8 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
   // (16 prompts of up to 1024 tokens, e4m3: 128 threads and two tokens 40 us, 256 and four 47;
   // the verified block of 32 requests: 512 threads 3.8 us, 256 4.2, 128 5.2)
   const size_t one = (size_t)(a.rot / 2) * sizeof(float2);
+  if (a.rot % (INTER ? kPiece<T> : 2 * kPiece<T>) != 0)
+    return launch_chained(append_pairs_kernel<T, INTER, QUANT>, dim3((unsigned)a.T), dim3(kPairThreads), one, s, 1, a);
   if (a.T >= 8 * sm_count())
     return launch_chained(append_kernel<T, INTER, QUANT, 128, 2>, dim3((unsigned)(((int64_t)a.T + 1) / 2)), dim3(128), 2 * one, s, 1, a, 2);
   return launch_chained(append_kernel<T, INTER, QUANT, 512, 1>, dim3((unsigned)a.T), dim3(512), one, s, 1, a, 1);

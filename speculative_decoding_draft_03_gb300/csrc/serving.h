@@ -162,7 +162,7 @@ struct AppendArgs {
   float magnitude;
   DeviceStatus* status;
 };
-cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_cache_append(const AppendArgs& a, cudaStream_t s);  // any even rot
 
 constexpr int kMaxBias = 1024;
 

@@ -184,6 +184,54 @@ dspark_status check_turn(int D, int rot_dim, int interleaved, const int64_t* rat
   return DSPARK_OK;
 }
 
+dspark_status append(int T, int R, int Hq, int Hkv, int D, int rot_dim, int interleaved, int num_pages, int page_size,
+                     int max_pages, int dtype_in, int dtype_kv, const void* q, int64_t q_stride_token,
+                     int64_t q_stride_head, const void* k, const void* v, int64_t in_stride_token,
+                     int64_t in_stride_head, void* q_out, int64_t q_out_stride_token, int64_t q_out_stride_head,
+                     void* k_pool, void* v_pool, int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                     const int32_t* page_table, int64_t table_stride, const int32_t* seq_len, const int32_t* q_start,
+                     const int32_t* granted, const float* k_scale, const float* v_scale, const int64_t* rates,
+                     float magnitude, void* workspace, size_t ws_bytes, void* stream) {
+  CHECK(check_geometry(R, num_pages, page_size, max_pages, table_stride));
+  if (T < 0 || Hq < 0 || Hkv < 1)
+    return fail(DSPARK_INVALID_ARG, "sizes must be positive (T=%d Hq=%d Hkv=%d)", T, Hq, Hkv);
+  CHECK(check_rows(D, dtype_in, dtype_kv, k_pool, v_pool, page_stride, head_stride, token_stride, k_scale, v_scale));
+  CHECK(check_turn(D, rot_dim, interleaved, rates, magnitude));
+  if (((int64_t)Hq + 2 * (int64_t)Hkv) * D > (1 << 26))
+    return fail(DSPARK_UNSUPPORTED_SHAPE, "(Hq + 2 Hkv) * D must be at most 2^26");
+  if ((page_stride == 0 && num_pages > 1) || (head_stride == 0 && Hkv > 1) || (token_stride == 0 && page_size > 1))
+    return fail(DSPARK_INVALID_ARG, "rows of a pool that is written to must not lie on one another");
+  CHECK_PTR(page_table);
+  CHECK_PTR(seq_len);
+  CHECK_PTR(q_start);
+  CHECK(check_workspace(workspace, ws_bytes, 256));
+  if (T == 0) return DSPARK_OK;
+  CHECK_PTR(k);
+  CHECK_PTR(v);
+  CHECK(check_strided(k, in_stride_token, in_stride_head, "k"));
+  CHECK(check_strided(v, in_stride_token, in_stride_head, "v"));
+  if (Hq > 0) {
+    CHECK_PTR(q);
+    CHECK_PTR(q_out);
+    CHECK(check_strided(q, q_stride_token, q_stride_head, "q"));
+    CHECK(check_strided(q_out, q_out_stride_token, q_out_stride_head, "q_out"));
+    if ((q_out_stride_token < D && T > 1) || (q_out_stride_head < D && Hq > 1))
+      return fail(DSPARK_INVALID_ARG, "rows of q_out must not lie on one another");
+    if (q_out == q && ((T > 1 && q_out_stride_token != q_stride_token) || (Hq > 1 && q_out_stride_head != q_stride_head)))
+      return fail(DSPARK_INVALID_ARG, "queries turned in place have the strides of q");
+  }
+  dspark::AppendArgs a = {};
+  a.T = T; a.R = R; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.rot = rot_dim; a.interleaved = interleaved;
+  a.num_pages = num_pages; a.page_size = page_size; a.max_pages = max_pages; a.dtype_in = dtype_in; a.dtype_kv = dtype_kv;
+  a.q = q; a.q_token = q_stride_token; a.q_head = q_stride_head; a.k = k; a.v = v; a.in_token = in_stride_token;
+  a.in_head = in_stride_head; a.q_out = q_out; a.q_out_token = q_out_stride_token; a.q_out_head = q_out_stride_head;
+  a.k_pool = k_pool; a.v_pool = v_pool; a.page_stride = page_stride; a.head_stride = head_stride;
+  a.token_stride = token_stride; a.page_table = page_table; a.table_stride = table_stride; a.seq_len = seq_len;
+  a.q_start = q_start; a.granted = granted; a.k_scale = k_scale; a.v_scale = v_scale; a.rates = rates;
+  a.magnitude = magnitude; a.status = static_cast<dspark::DeviceStatus*>(workspace);
+  return launched(dspark::launch_cache_append(a, static_cast<cudaStream_t>(stream)), "cache_append");
+}
+
 }  // namespace
 
 extern "C" {
@@ -474,45 +522,28 @@ dspark_status dspark_cache_append(int T, int R, int Hq, int Hkv, int D, int rot_
                                   const int32_t* q_start, const int32_t* granted, const float* k_scale,
                                   const float* v_scale, const int64_t* rates, float magnitude, void* workspace,
                                   size_t ws_bytes, void* stream) {
-  CHECK(check_geometry(R, num_pages, page_size, max_pages, table_stride));
-  if (T < 0 || Hq < 0 || Hkv < 1)
-    return fail(DSPARK_INVALID_ARG, "sizes must be positive (T=%d Hq=%d Hkv=%d)", T, Hq, Hkv);
-  CHECK(check_rows(D, dtype_in, dtype_kv, k_pool, v_pool, page_stride, head_stride, token_stride, k_scale, v_scale));
-  CHECK(check_turn(D, rot_dim, interleaved, rates, magnitude));
-  if (rot_dim % 16 != 0) return fail(DSPARK_UNSUPPORTED_SHAPE, "rot_dim=%d must be a multiple of 16", rot_dim);
-  if (((int64_t)Hq + 2 * (int64_t)Hkv) * D > (1 << 26))
-    return fail(DSPARK_UNSUPPORTED_SHAPE, "(Hq + 2 Hkv) * D must be at most 2^26");
-  if ((page_stride == 0 && num_pages > 1) || (head_stride == 0 && Hkv > 1) || (token_stride == 0 && page_size > 1))
-    return fail(DSPARK_INVALID_ARG, "rows of a pool that is written to must not lie on one another");
-  CHECK_PTR(page_table);
-  CHECK_PTR(seq_len);
-  CHECK_PTR(q_start);
-  CHECK(check_workspace(workspace, ws_bytes, 256));
-  if (T == 0) return DSPARK_OK;
-  CHECK_PTR(k);
-  CHECK_PTR(v);
-  CHECK(check_strided(k, in_stride_token, in_stride_head, "k"));
-  CHECK(check_strided(v, in_stride_token, in_stride_head, "v"));
-  if (Hq > 0) {
-    CHECK_PTR(q);
-    CHECK_PTR(q_out);
-    CHECK(check_strided(q, q_stride_token, q_stride_head, "q"));
-    CHECK(check_strided(q_out, q_out_stride_token, q_out_stride_head, "q_out"));
-    if ((q_out_stride_token < D && T > 1) || (q_out_stride_head < D && Hq > 1))
-      return fail(DSPARK_INVALID_ARG, "rows of q_out must not lie on one another");
-    if (q_out == q && ((T > 1 && q_out_stride_token != q_stride_token) || (Hq > 1 && q_out_stride_head != q_stride_head)))
-      return fail(DSPARK_INVALID_ARG, "queries turned in place have the strides of q");
-  }
-  dspark::AppendArgs a = {};
-  a.T = T; a.R = R; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.rot = rot_dim; a.interleaved = interleaved;
-  a.num_pages = num_pages; a.page_size = page_size; a.max_pages = max_pages; a.dtype_in = dtype_in; a.dtype_kv = dtype_kv;
-  a.q = q; a.q_token = q_stride_token; a.q_head = q_stride_head; a.k = k; a.v = v; a.in_token = in_stride_token;
-  a.in_head = in_stride_head; a.q_out = q_out; a.q_out_token = q_out_stride_token; a.q_out_head = q_out_stride_head;
-  a.k_pool = k_pool; a.v_pool = v_pool; a.page_stride = page_stride; a.head_stride = head_stride;
-  a.token_stride = token_stride; a.page_table = page_table; a.table_stride = table_stride; a.seq_len = seq_len;
-  a.q_start = q_start; a.granted = granted; a.k_scale = k_scale; a.v_scale = v_scale; a.rates = rates;
-  a.magnitude = magnitude; a.status = static_cast<dspark::DeviceStatus*>(workspace);
-  return launched(dspark::launch_cache_append(a, static_cast<cudaStream_t>(stream)), "cache_append");
+  if (rot_dim >= 2 && rot_dim <= D && rot_dim % 2 == 0 && rot_dim % 16 != 0)
+    return fail(DSPARK_UNSUPPORTED_SHAPE, "rot_dim=%d must be a multiple of 16 (dspark_cache_append_any takes it)", rot_dim);
+  return append(T, R, Hq, Hkv, D, rot_dim, interleaved, num_pages, page_size, max_pages, dtype_in, dtype_kv, q,
+                q_stride_token, q_stride_head, k, v, in_stride_token, in_stride_head, q_out, q_out_stride_token,
+                q_out_stride_head, k_pool, v_pool, page_stride, head_stride, token_stride, page_table, table_stride,
+                seq_len, q_start, granted, k_scale, v_scale, rates, magnitude, workspace, ws_bytes, stream);
+}
+
+dspark_status dspark_cache_append_any(int T, int R, int Hq, int Hkv, int D, int rot_dim, int interleaved, int num_pages,
+                                      int page_size, int max_pages, int dtype_in, int dtype_kv, const void* q,
+                                      int64_t q_stride_token, int64_t q_stride_head, const void* k, const void* v,
+                                      int64_t in_stride_token, int64_t in_stride_head, void* q_out,
+                                      int64_t q_out_stride_token, int64_t q_out_stride_head, void* k_pool, void* v_pool,
+                                      int64_t page_stride, int64_t head_stride, int64_t token_stride,
+                                      const int32_t* page_table, int64_t table_stride, const int32_t* seq_len,
+                                      const int32_t* q_start, const int32_t* granted, const float* k_scale,
+                                      const float* v_scale, const int64_t* rates, float magnitude, void* workspace,
+                                      size_t ws_bytes, void* stream) {
+  return append(T, R, Hq, Hkv, D, rot_dim, interleaved, num_pages, page_size, max_pages, dtype_in, dtype_kv, q,
+                q_stride_token, q_stride_head, k, v, in_stride_token, in_stride_head, q_out, q_out_stride_token,
+                q_out_stride_head, k_pool, v_pool, page_stride, head_stride, token_stride, page_table, table_stride,
+                seq_len, q_start, granted, k_scale, v_scale, rates, magnitude, workspace, ws_bytes, stream);
 }
 
 dspark_status dspark_adjust_logits(int N, int V, int R, int dtype, const void* logits, int64_t row_stride,

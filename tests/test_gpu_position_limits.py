@@ -172,3 +172,75 @@ def test_divisions_by_any_scale(b, dtype, scale):
     if math.copysign(1.0, scale) < 0:  # (0 / s is -0: the quotient's -0 and the residual's +0 add up to +0, the same value)
         got, want = (torch.where(x == 128, 0, x) for x in (got, want))
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype,cache", append.TYPES)
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("Hq,H,D,rot,ps", [(1, 1, 16, 2, 1), (8, 2, 80, 40, 20), (6, 2, 80, 20, 5), (5, 1, 96, 24, 16), (64, 1, 48, 46, 8),
+                                           (12, 4, 256, 250, 64), (3, 3, 64, 8, 16)])
+def test_appends_that_turn_any_part(b, dtype, cache, interleaved, Hq, H, D, rot, ps):
+    """Parts of a row that are no whole pieces: against the 64-bit form, the two calls one after the other, and in
+    place inside a packed projection."""
+    lens, new = [1, 5, 64, 130, 7, 300], [1, 5, 3, 30, 0, 2]
+    rates = b.rotary_rates(rot)
+    how = dict(interleaved=interleaved, magnitude=1.1)
+    make = lambda: append.Case(lens, new, Hq, H, D, ps, dtype, cache, seed=D + rot)
+    c, d, e = make(), make(), make()
+    q_out = c.call(b, rates, **how)
+    c.check(b, q_out, rates, **how)
+    assert b.device_status(c.ws) == 0
+    pos = _i32(c.positions())
+    assert torch.equal(q_out, b.rotary(d.q, pos, rates, **how))
+    b.cache_write(b.rotary(d.k, pos, rates, **how), d.v, *d.pools, _i32(d.table), _i32(d.lens), _i32(d.q_start),
+                  k_scale=d.scales[0], v_scale=d.scales[1])
+    assert torch.equal(append._bits(c.pools[1]), append._bits(d.pools[1]))
+    if cache != E4M3:  # (an e4m3 cache takes the turned keys without a rounding between)
+        assert torch.equal(append._bits(c.pools[0]), append._bits(d.pools[0]))
+    packed = torch.cat([e.q, e.k, e.v], 1)
+    e.q, e.k, e.v = packed[:, :Hq], packed[:, Hq:Hq + H], packed[:, Hq + H:]
+    assert torch.equal(e.call(b, rates, q_out=e.q, **how), q_out)
+    for x, y in zip(c.pools, e.pools):
+        assert torch.equal(append._bits(x), append._bits(y))
+
+
+def test_appends_of_any_part_leave_what_is_not_theirs(b):
+    """Refused slots, rows of no slot, bad pages, elements that are not finite, a graph."""
+    rates = b.rotary_rates(20)
+    c = append.Case([40, 9, 100], [3, 2, 50], 4, 2, 80, 16, torch.bfloat16, torch.bfloat16, beyond=6)
+    q_out = torch.full_like(c.q, 9.0)
+    c.call(b, rates, q_out=q_out, granted=_i32([3, 0, 50]))
+    c.check(b, q_out, rates, skip=[1])
+    assert (q_out[3:5] == 9).all() and (q_out[55:] == 9).all() and b.device_status(c.ws) == 0
+    c = append.Case([40, 9, 100], [3, 2, 50], 4, 2, 80, 16, torch.bfloat16, torch.bfloat16)
+    c.table[1, 0] = 1 << 20
+    q_out = torch.full_like(c.q, 9.0)
+    c.call(b, rates, q_out=q_out)
+    assert b.device_status(c.ws) == 1
+    assert (q_out[3:5] == 9).all() and (q_out[:3] != 9).any() and (q_out[5:] != 9).any()
+    c = append.Case([40], [3], 1, 1, 80, 16, torch.bfloat16, torch.bfloat16)
+    c.k[1, 0, 3], c.k[1, 0, 40] = math.nan, math.inf  # of a pair, and past the part that turns
+    c.call(b, rates, q=None)
+    row = c.pools[0][c.table[0, 38 // 16], 0, 38 % 16]
+    assert torch.isnan(row).nonzero()[:, 0].tolist() == [3, 13] and torch.equal(row[20:], c.k[1, 0, 20:])
+    d = append.Case([40, 300], [30, 100], 6, 2, 80, 16, torch.float16, torch.float16)
+    want, pools = d.call(b, rates), [p.clone() for p in d.pools]
+    args, out = (_i32(d.table), _i32(d.lens), _i32(d.q_start)), torch.zeros_like(d.q)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.cache_append(d.q, d.k, d.v, *d.pools, *args, rates, ws=d.ws, q_out=out)
+    for p in d.pools:
+        p.fill_(3.0)
+    g.replay()
+    assert torch.equal(out, want) and all(torch.equal(x, y) for x, y in zip(d.pools, pools))
+
+
+def test_paged_cache_appends_any_part(b):
+    cache = b.PagedCache(2, 8, 16, 4, 1, 2, 80)
+    cache.reserve(_i32([20, 7]))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn((27, h, 80), generator=g, device="cuda").bfloat16() for h in (4, 2, 2))
+    rates = b.rotary_rates(40)
+    pos = _i32(list(range(20)) + list(range(7)))
+    assert torch.equal(cache.append(0, q, k, v, _i32([0, 20, 27]), rates), b.rotary(q, pos, rates))
+    page = cache.page_table[1, 0].item()
+    assert torch.equal(cache.k[0, page, :, :7], b.rotary(k, pos, rates)[20:].transpose(0, 1)) and cache.status() == 0

@@ -1,8 +1,10 @@
 """Host-side limits of the rotary, append, long-block attention and logit-adjustment calls: what is taken and
 refused before anything is launched."""
+import math
+
 import pytest
 
-from tests.test_serving_abi import INVALID, OK, P, UNSUPPORTED
+from tests.test_serving_abi import INVALID, OK, P, SMALL, UNSUPPORTED, _with
 
 
 @pytest.fixture(scope="module")
@@ -47,3 +49,30 @@ def test_windows_and_rows_of_long_blocks_together(b):
     for T, window in ((300, end - 301), (end - 6, 5), (300, (1 << 31) - 512), (300, (1 << 31) - 1)):  # (the last two: no window)
         assert call(T, window, q=None) == INVALID and "null pointer: q" in b.lib.dspark_last_error_message().decode(), (T, window)
     assert call(0, end - 1, q=None) == OK
+
+
+def test_cache_append_any(b):
+    """dspark_cache_append's checks, for any even part of a row."""
+    def call(T=5, R=4, Hq=4, Hkv=2, D=64, rot=20, il=0, num_pages=64, page_size=16, max_pages=8, dt=1, kv=1, qs=(256, 64),
+             ins=(128, 64), os=(256, 64), strides=(2048, 1024, 64), table_stride=8, mag=1.0, ws=256, null=(), shift=None, q_out=None,
+             name="dspark_cache_append_any"):
+        p = _with(P[:14], set(null) | ({10, 11} if kv != 3 else set()), shift)
+        return getattr(b.lib, name)(T, R, Hq, Hkv, D, rot, il, num_pages, page_size, max_pages, dt, kv, p[0], *qs, p[1], p[2], *ins,
+                                    q_out or p[3], *os, p[4], p[5], *strides, p[6], table_stride, p[7], p[8], p[9], p[10], p[11], p[12],
+                                    mag, p[13], ws, None)
+
+    none = dict(T=0, null=[0, 1, 2, 3])
+    for rot in (2, 6, 16, 20, 24, 40, 62, 64):
+        assert call(rot=rot, **none) == OK and call(rot=rot, il=1, **none) == OK, rot
+        assert call(rot=rot, name="dspark_cache_append", **none) == (UNSUPPORTED if rot % 16 else OK)
+    for rot in (0, 1, 3, 63, 66, -2):
+        assert call(rot=rot, **none) == INVALID, rot
+    assert call(T=-1) == INVALID and call(Hq=-1) == INVALID and call(Hkv=0) == INVALID and call(ws=16) == SMALL
+    for i in (0, 1, 2, 3, 4, 5, 6, 7, 8, 12, 13):
+        assert call(null=[i]) == INVALID, i
+    assert call(kv=3, null=[10]) == INVALID and call(kv=3, null=[11]) == INVALID
+    assert call(D=72) == UNSUPPORTED and call(D=272) == UNSUPPORTED
+    assert call(il=2) == INVALID and call(mag=math.nan) == INVALID and call(Hq=1 << 21, os=(1 << 27, 64)) == UNSUPPORTED
+    for kw in (dict(strides=(0, 1024, 64)), dict(qs=(250, 64)), dict(ins=(128, 60)), dict(os=(256, 4)), dict(os=(56, 64)),
+               dict(shift={0: 8}), dict(shift={4: 8}), dict(q_out=P[0], os=(512, 64))):
+        assert call(**kw) == INVALID, kw
