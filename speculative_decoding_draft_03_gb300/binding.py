@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import decimal
+import functools
 import importlib.util
 import math
 import os
@@ -913,10 +915,25 @@ def chunk_attention(q, k_pool, v_pool, page_table, seq_len, q_start, scale, k_sc
 
 # ------------------------------------------------------------------- rotary positions
 
+@functools.lru_cache(maxsize=8)
+def _pi(digits):
+    """Decimal of pi, by Machin's formula in whole numbers."""
+    one = 10 ** (digits + 10)
+
+    def arctan_of_inverse(n):
+        power = total = one // n
+        for k in range(3, 4 * digits + 40, 2):
+            power //= -n * n
+            total += power // k
+        return total
+
+    return decimal.Decimal(16 * arctan_of_inverse(5) - 4 * arctan_of_inverse(239)).scaleb(-(digits + 10))
+
+
 def rotary_rates(rot_dim, base=10000.0, scaling="none", factor=1.0, original_len=None, low=1.0, high=32.0, factors=None,
                  device="cuda") -> torch.Tensor:
     """What rotary and cache_append take as the pairs' turns per position: int64 [rot_dim/2], units of
-    2^-64 turns, computed in float64 from f_i = base^(-2i/rot_dim) radians per position and
+    2^-64 turns, from f_i = base^(-2i/rot_dim) radians per position and
 
       scaling="none"    f_i
       scaling="linear"  f_i / factor (positions interpolated)
@@ -927,7 +944,8 @@ def rotary_rates(rot_dim, base=10000.0, scaling="none", factor=1.0, original_len
       scaling="yarn"    the same with a blend linear in the pair's index (its magnitude is
                         rotary_magnitude(factor))
 
-    ``factors`` [rot_dim/2], if given, divides the result pair by pair."""
+    ``factors`` [rot_dim/2], if given, divides the result pair by pair.  Computed with 60 digits and more, so that
+    a rate is off by half a unit, and an angle at position p by 2^-64 p half turns, at most."""
     if rot_dim < 2 or rot_dim % 2:
         raise DSparkError(f"rot_dim={rot_dim} must be even and positive")
     if not (base > 0 and math.isfinite(base) and factor > 0 and math.isfinite(factor)):
@@ -935,29 +953,45 @@ def rotary_rates(rot_dim, base=10000.0, scaling="none", factor=1.0, original_len
     if scaling not in ("none", "linear", "ntk", "bands", "yarn"):
         raise DSparkError(f"scaling={scaling!r} must be none, linear, ntk, bands or yarn")
     pairs = rot_dim // 2
-    if scaling == "ntk" and rot_dim > 2:
-        base = base * factor ** (rot_dim / (rot_dim - 2))
-    f = [base ** (-2.0 * i / rot_dim) for i in range(pairs)]
-    if scaling == "linear":
-        f = [x / factor for x in f]
-    elif scaling in ("bands", "yarn"):
+    kept = None  # of each pair: 1 as it is, 0 stretched
+    if scaling in ("bands", "yarn"):
         if original_len is None or original_len <= 0 or not 0 < low < high:
             raise DSparkError(f"scaling={scaling!r} needs original_len > 0 and 0 < low < high")
-        if scaling == "bands":
-            kept = [min(1.0, max(0.0, (original_len * x / math.tau - low) / (high - low))) for x in f]
-        else:
-            if base <= 1:
-                raise DSparkError("scaling='yarn' needs base > 1")
-            index = lambda turns: rot_dim * math.log(original_len / (math.tau * turns)) / (2.0 * math.log(base))
-            first, last = max(0, math.floor(index(high))), min(rot_dim - 1, math.ceil(index(low)))
-            kept = [1.0 - min(1.0, max(0.0, (i - first) / max(last - first, 0.001))) for i in range(pairs)]
-        f = [x * (k + (1.0 - k) / factor) for x, k in zip(f, kept)]
+        if scaling == "yarn" and base <= 1:
+            raise DSparkError("scaling='yarn' needs base > 1")
     if factors is not None:
         factors = [float(x) for x in factors]
         if len(factors) != pairs or not all(x > 0 and math.isfinite(x) for x in factors):
             raise DSparkError(f"factors must hold {pairs} positive values")
-        f = [x / y for x, y in zip(f, factors)]
-    turns = [round(math.fmod(x / math.tau, 1.0) * 2.0 ** 64) % (1 << 64) for x in f]
+    # digits before the point: of the largest rate that these can make
+    digits = 60 + math.ceil(abs(math.log10(base)) + abs(math.log10(factor)) * (2 if scaling != "ntk" or rot_dim == 2 else
+                            rot_dim / (rot_dim - 2)) + max([0.0] + [abs(math.log10(x)) for x in factors or ()]))
+    context = decimal.Context(prec=digits, Emin=decimal.MIN_EMIN, Emax=decimal.MAX_EMAX)
+    with decimal.localcontext(context):
+        exact = lambda x: decimal.Decimal(float(x))
+        tau, by, b = 2 * _pi(digits), exact(factor), exact(base)
+        if scaling == "ntk" and rot_dim > 2:
+            b *= by ** (decimal.Decimal(rot_dim) / (rot_dim - 2))
+        step, f = b ** (decimal.Decimal(-2) / rot_dim), [decimal.Decimal(1)]
+        for _ in range(pairs - 1):
+            f.append(f[-1] * step)
+        clamp = lambda x: min(decimal.Decimal(1), max(decimal.Decimal(0), x))
+        if scaling == "linear":
+            f = [x / by for x in f]
+        elif scaling == "bands":
+            n, lo, span = exact(original_len) / tau, exact(low), exact(high) - exact(low)
+            kept = [clamp((n * x - lo) / span) for x in f]
+        elif scaling == "yarn":
+            index = lambda turns: rot_dim * math.log(original_len / (math.tau * turns)) / (2.0 * math.log(base))
+            first, last = max(0, math.floor(index(high))), min(rot_dim - 1, math.ceil(index(low)))
+            kept = [1 - clamp(decimal.Decimal(i - first) / max(last - first, exact(0.001))) for i in range(pairs)]
+        if kept is not None:
+            shrunk = 1 / by
+            f = [x * (k + (1 - k) * shrunk) for x, k in zip(f, kept)]
+        if factors is not None:
+            f = [x / exact(y) for x, y in zip(f, factors)]
+        units = 2 ** 64 / tau
+        turns = [round(x * units) % (1 << 64) for x in f]
     return torch.tensor([t - (1 << 64) if t >= 1 << 63 else t for t in turns], dtype=torch.int64, device=device)
 
 

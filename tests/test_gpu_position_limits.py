@@ -1,12 +1,12 @@
 """The ends of what the rotary, append, long-block attention and logit-adjustment calls take: the largest
 sizes, scales and windows, and shapes at the borders of the kernels' fast paths."""
+import decimal
 import math
 
 import numpy as np
 import pytest
 import torch
 
-from tests import position_ref as ref
 from tests import test_gpu_adjust as adjust
 from tests import test_gpu_append as append
 from tests import test_gpu_chunk_attention as chunk
@@ -244,3 +244,22 @@ def test_paged_cache_appends_any_part(b):
     assert torch.equal(cache.append(0, q, k, v, _i32([0, 20, 27]), rates), b.rotary(q, pos, rates))
     page = cache.page_table[1, 0].item()
     assert torch.equal(cache.k[0, page, :, :7], b.rotary(k, pos, rates)[20:].transpose(0, 1)) and cache.status() == 0
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_angles_at_far_positions(b, interleaved):
+    """The rotation of unit vectors at the ends of the positions' range, from the frequencies themselves in 90 digits:
+    off by the angle's 1e-7 radians, a step of the sine and cosine and their rounding."""
+    pi = decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
+    pos = [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 12345, 1999999999, 1 << 30, 100003, 1, 0]
+    x = torch.zeros((len(pos), 1, 64), device="cuda")
+    u, w = (slice(0, 64, 2), slice(1, 64, 2)) if interleaved else (slice(0, 32), slice(32, 64))
+    x[..., u] = 1.0
+    for how in (dict(), dict(scaling="linear", factor=3.0)):
+        y = b.rotary(x, _i32(pos), b.rotary_rates(64, 500000.0, **how), interleaved=interleaved).double().cpu()
+        for i, p in enumerate(pos):
+            with decimal.localcontext(decimal.Context(prec=90)):
+                f = [decimal.Decimal(500000) ** (decimal.Decimal(-k) / 32) / decimal.Decimal(how.get("factor", 1.0)) for k in range(32)]
+                a = torch.tensor([float((p * z) % (2 * pi)) for z in f], dtype=torch.float64)
+            off = torch.maximum((y[i, 0, u] - a.cos()).abs(), (y[i, 0, w] - a.sin()).abs())
+            assert (off <= 1e-7 + 2.0 ** -23 + 2.0 ** -24).all(), (p, off.max())

@@ -1,5 +1,6 @@
 """Host-side limits of the rotary, append, long-block attention and logit-adjustment calls: what is taken and
 refused before anything is launched."""
+import decimal
 import math
 
 import pytest
@@ -76,3 +77,58 @@ def test_cache_append_any(b):
     for kw in (dict(strides=(0, 1024, 64)), dict(qs=(250, 64)), dict(ins=(128, 60)), dict(os=(256, 4)), dict(os=(56, 64)),
                dict(shift={0: 8}), dict(shift={4: 8}), dict(q_out=P[0], os=(512, 64))):
         assert call(**kw) == INVALID, kw
+
+
+PI = decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
+
+
+@pytest.mark.parametrize("base", [10000.0, 500000.0, 3.7])
+@pytest.mark.parametrize("how", [dict(), dict(scaling="linear", factor=3.0), dict(factors=[1.0 + i / 7 for i in range(32)])])
+def test_rates_to_half_a_unit(b, base, how):
+    """Each rate is the whole number nearest to f 2^64 / (2 pi): with f the root of f^64 = base^-2i, which is held
+    by its bounds, (rate - 1/2)^64 <= (f 2^64 / 2 pi)^64 <= (rate + 1/2)^64."""
+    rates = [r % (1 << 64) for r in b.rotary_rates(64, base, device="cpu", **how).tolist()]
+    with decimal.localcontext(decimal.Context(prec=90)):
+        for i, r in enumerate(rates):
+            shrink = decimal.Decimal(how.get("factor", 1.0)) * decimal.Decimal(how["factors"][i] if "factors" in how else 1.0)
+            unit = 2 * PI * shrink / 2 ** 64  # radians, before what divides them
+            low, high = ((r + d) * unit for d in (decimal.Decimal("-0.50001"), decimal.Decimal("0.50001")))
+            want = 1 / decimal.Decimal(base) ** (2 * i)
+            assert low ** 64 <= want <= high ** 64, i
+
+
+def test_rates_stretched_to_half_a_unit(b):
+    """The same for a changed base, f^48 = base^-12i factor^-16i (8 elements), and for blends, by the blend's own
+    formula."""
+    turns = lambda t: [decimal.Decimal(r % (1 << 64)) for r in t.tolist()]
+    half = decimal.Decimal("0.50001")
+    with decimal.localcontext(decimal.Context(prec=90)):
+        unit = 2 * PI / 2 ** 64
+        for i, r in enumerate(turns(b.rotary_rates(8, 10000.0, "ntk", 5.0, device="cpu"))):
+            want = 1 / (decimal.Decimal(10000) ** (12 * i) * decimal.Decimal(5) ** (16 * i))
+            assert ((r - half) * unit) ** 48 <= want <= ((r + half) * unit) ** 48, i
+        f = [decimal.Decimal(10000) ** (decimal.Decimal(-i) / 32) for i in range(32)]
+        how = dict(factor=8.0, original_len=4096, low=1.0, high=32.0, device="cpu")
+        for i, r in enumerate(turns(b.rotary_rates(64, scaling="bands", **how))):
+            kept = min(decimal.Decimal(1), max(decimal.Decimal(0), (4096 * f[i] / (2 * PI) - 1) / 31))
+            assert abs(r - f[i] * (kept + (1 - kept) / 8) / unit) <= half, i
+        for i, r in enumerate(turns(b.rotary_rates(64, scaling="yarn", **how))):
+            # ln(4096 / (64 pi)) / ln(10000) 32 = 10.46 and ln(4096 / 2 pi) / ln(10000) 32 = 22.51: from 10 to 23
+            kept = 1 - min(decimal.Decimal(1), max(decimal.Decimal(0), decimal.Decimal(i - 10) / 13))
+            assert abs(r - f[i] * (kept + (1 - kept) / 8) / unit) <= half, i
+
+
+def test_rates_of_any_size(b):
+    """Bases and factors to the ends of float64's range: held modulo a turn, or 0, and no error but the binding's."""
+    for kw in (dict(base=1e300, factor=1e300, scaling="ntk"), dict(base=1e-300), dict(base=1e300), dict(factor=1e-300, scaling="linear"),
+               dict(factor=1e300, scaling="linear"), dict(factors=[1e-300] * 4), dict(base=5e-324, factor=5e-324, scaling="linear")):
+        assert b.rotary_rates(8, device="cpu", **kw).numel() == 4, kw
+    # f = 1e300^(1/2) at the third of four pairs, modulo a turn, by whole numbers of 10^-100 turns
+    got = b.rotary_rates(8, 1e-4, factors=[1.0, 1.0, 1e-60, 1.0], device="cpu")[2].item() % (1 << 64)
+    with decimal.localcontext(decimal.Context(prec=140)):
+        want = (decimal.Decimal(1e-4) ** decimal.Decimal("-0.5") / decimal.Decimal(1e-60) / (2 * PI)) % 1 * 2 ** 64
+        assert abs(want - got) <= 1
+    c = decimal.getcontext()
+    before = (c.prec, c.rounding)
+    b.rotary_rates(64, device="cpu")
+    assert (decimal.getcontext().prec, decimal.getcontext().rounding) == before
