@@ -599,9 +599,12 @@ DSPARK_API dspark_status dspark_paged_attention_granted(
  *
  * Arguments, results and refusals are dspark_paged_attention_granted's, but for max_q, which
  * this call does not have, and for T + window, which must be below 2^31 - 1024 (a window of
- * max_pages * page_size tokens or more counts as none).  Blocks of D > 128, over pages that no multiple of 8 tokens
- * divides, or over pools whose entries lie on one another, are computed 16 or 32 query rows
- * at a time, much slower.
+ * max_pages * page_size tokens or more counts as none).  Blocks of D > 128, over pages that no
+ * multiple of 8 tokens divides, or over pools whose entries lie on one another, are computed 16 or
+ * 32 query rows at a time, each over its request's whole context from the first query's window on:
+ * a prompt of n tokens is n^2 of work, with a window too, and some 40 times as long as one that the
+ * fast kernel takes (8192 tokens, 32 heads over 8 of 128: 15 ms for 0.41).  In calls of at most 128
+ * queries a request such shapes go through no more than those queries' windows.
  * Workspace: dspark_chunk_attention_workspace_size() (0 for unsupported sizes).
  * ---------------------------------------------------------------------------------- */
 DSPARK_API size_t dspark_chunk_attention_workspace_size(int T, int R, int Hq, int Hkv, int D);

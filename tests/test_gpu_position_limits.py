@@ -263,3 +263,22 @@ def test_angles_at_far_positions(b, interleaved):
                 a = torch.tensor([float((p * z) % (2 * pi)) for z in f], dtype=torch.float64)
             off = torch.maximum((y[i, 0, u] - a.cos()).abs(), (y[i, 0, w] - a.sin()).abs())
             assert (off <= 1e-7 + 2.0 ** -23 + 2.0 ** -24).all(), (p, off.max())
+
+
+@pytest.mark.parametrize("dtype,cache", chunk.TYPES)
+@pytest.mark.parametrize("window", [0, 100, 700])
+@pytest.mark.parametrize("Hq,H,D,ps", [(4, 1, 256, 64), (4, 2, 128, 20), (2, 1, 64, 5), (8, 8, 144, 12)])
+def test_long_blocks_that_go_by_rows(b, dtype, cache, window, Hq, H, D, ps):
+    """Shapes that the tensor-memory kernel does not take, over prompts of thousands of tokens, with windows, beside
+    single queries and slots with more queries than positions; values that some rows do not see among them."""
+    lens, new = [2600, 700, 1, 90, 3000, 0], [2600, 300, 1, 130, 1, 0]
+    c = _case(lens, new, Hq, H, D, ps, dtype, cache, seed=D + ps)
+    v = c["v"].float()
+    for r, j in ((0, 1000), (0, 2599), (1, 650), (4, 2990)):
+        v[c["table"][r, j // ps], 0, j % ps, 3:5] = math.nan
+    c["v"] = v.to(c["v"].dtype)
+    for r, (n, m) in enumerate(zip(lens, new)):  # (pages before every window are gone)
+        if window:
+            c["table"][r, :max(0, n - m - window + 1) // ps] = -1
+    out = chunk._check(b, c, window=window)["out"].float()
+    assert torch.isnan(out).any() and torch.isfinite(out).any()
