@@ -11,14 +11,14 @@
 //     alone to write, and without a mask it is not launched.)
 //   * Then the few ids that change.  A CTA takes a slice of the ids of one slot, for up to eight of the slot's
 //     rows: it counts the whole history's ids of its slice in shared memory (a word per id: answers, and a bit
-//     for the prompt), while the rows are still being copied; lists the ids that were counted; and adjusts
-//     them, an id a thread over all rows, with the block's tokens counted as it comes to their rows.  Large
-//     slices read the history few times.
-// (One kernel that did both slice by slice had each of its phases wait for memory on its own: 140 rows of 151936
-// bf16 logits with histories of 1 K to 8 K tokens 41 us, 34 so; 190 rows of 50257 fp32 ones with histories of up
-// to 32 K and 300 biases 86 us, 47 so.)
-// What bounds it: device memory in the first (each logit is read and written once: 16.7 of the 34 us), in the
-// second the chain from a slot's length over its history to its logits, whose lines are read for an id each.
+//     for the prompt); lists the ids that were counted; and adjusts them, an id a thread over all rows, with the
+//     block's tokens counted as it comes to their rows.  Large slices read the history few times.
+// (One kernel that did both slice by slice had each of its phases wait for memory on its own: 154 rows of 151936
+// bf16 logits with histories of 1 K to 8 K tokens 41 us, 36 so; 182 rows of 50257 fp32 ones with histories of up
+// to 32 K and 300 biases 86 us, 50 so.)
+// What bounds it: device memory in the first (each logit is read and written once: 16.7 of the 36 us), in the
+// second the chain from a slot's length over its history to its logits, whose lines are read for an id each: in
+// place without masks, where the second is alone, these cases take 20.5 and 39 us.
 #include <algorithm>
 
 #include "serving.cuh"
@@ -63,6 +63,7 @@ template <typename T>
 __global__ void __launch_bounds__(kCopyThreads) mask_kernel(const __grid_constant__ AdjustArgs a, int chunks) {
   constexpr int E = 16 / (int)sizeof(T), kPieces = kCopyThreads * kCopyAhead;  // of a CTA
   constexpr uint32_t kAll = (1u << E) - 1;
+  griddep_wait();
   griddep_allow_next();
   const int n = blockIdx.x / chunks, c = blockIdx.x - n * chunks, tid = threadIdx.x, words = (a.V + 31) / 32;
   if (n < a.q_start[0] || n >= a.q_start[a.R]) return;  // of no slot
@@ -126,10 +127,9 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
     return (int)(turn - round * slices) == mine ? (int)(round << 5 | (id & 31)) : -1;
   };
   auto id_at = [&](int at) { return ((at >> 5) * slices + mine) * 32 + (at & 31); };
-  // (All that came before the copy was complete before the copy began, so the inputs are there; only the rows have to be
-  // waited for.  Without the copy this is the first kernel of the call, and waits for what came before it.)
-  const bool alone = a.out == a.logits && a.mask == nullptr;
-  if (alone) griddep_wait();
+  // (Also before the inputs are read, though what wrote them was complete before any row was copied: what earlier grids
+  // wrote is there for a grid that has waited itself.  Counting beside the copy saved 2 us of 36, or 0.6 of 6.6.)
+  griddep_wait();
   const int q0 = min(max(a.q_start[r], 0), a.N), q1 = min(max(a.q_start[r + 1], q0), a.N);
   const int hist = a.history == nullptr ? 0 : min(max(a.history_len[r], 0), a.history_width);
   const int prompt = a.prompt_len == nullptr ? 0 : a.prompt_len[r];
@@ -148,7 +148,6 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
     if ((answer ? atomicAdd(counts + at, 1u) : atomicOr(counts + at, kPrompt)) == 0) mark(at);
   };
 
-  bool copied = alone;
   for (int first = blockIdx.z * kRows; first < q1 - q0; first += gridDim.z * kRows) {
     const int n_rows = min(kRows, q1 - q0 - first);
     __syncthreads();  // the rows before no longer read the counts
@@ -216,8 +215,6 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
       for (; bits != 0; bits &= bits - 1) list[to++] = (uint16_t)(32 * w + __ffs(bits) - 1);
     }
     __syncthreads();
-    if (!copied) griddep_wait();  // the rows are there
-    copied = true;
     // an id of a row a thread, in a loop as short as can be (unrolled over the rows it waited for instructions)
     const int per_row = listed + a.n_bias;
 #pragma unroll 1
@@ -242,8 +239,6 @@ __global__ void __launch_bounds__(kThreads) adjust_kernel(const __grid_constant_
       if ((allowed >> (id & 31)) & 1u) *y = rounded<T>(z);
     }
   }
-  griddep_wait();
-  griddep_allow_next();
 }
 
 // The slices of a slot's ids: as few as shared memory allows (each reads the slot's history), or as many as still
@@ -270,12 +265,7 @@ cudaError_t launch(const AdjustArgs& a, cudaStream_t s) {
     constexpr int kIds = kCopyThreads * kCopyAhead * (16 / (int)sizeof(T));
     const int chunks = (a.V + kIds - 1) / kIds;
     if ((long long)chunks * a.N > INT32_MAX) return cudaErrorInvalidValue;
-    // Not chained to what is before it: all that is complete, and its writes visible, when this kernel starts, and the
-    // next one, which starts after that, reads the histories while the rows are still being copied.  (154 rows of 151936
-    // bf16 logits 34.7 us; 36.5 with the next kernel waiting before its first read; 20 rows of 1024 6.8 and 7.1.)
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(chunks * a.N), cfg.blockDim = dim3(kCopyThreads), cfg.stream = s;
-    if ((e = cudaLaunchKernelEx(&cfg, mask_kernel<T>, a, chunks)) != cudaSuccess) return e;
+    if ((e = launch_chained(mask_kernel<T>, dim3(chunks * a.N), dim3(kCopyThreads), 0, s, 1, a, chunks)) != cudaSuccess) return e;
   }
   const int groups = std::max(1, std::min(4096, a.N / (a.R * kRows))), n = slices_of(a, groups);
   const uint32_t per_slices = (uint32_t)(((1ull << 32) + n - 1) / n);
