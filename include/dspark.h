@@ -627,8 +627,10 @@ DSPARK_API dspark_status dspark_chunk_attention(
  * gradient for x from the gradient for y (with the same magnitude).
  *
  *   rates     [rot_dim/2] int64: f_i as turns per position, f_i / (2 pi), in units of 2^-64
- *             (an unsigned 64-bit fraction).  The angle is then exact at every position: its
- *             error is 2^-25 half turns at most (1e-7 radians), whatever the position.
+ *             (an unsigned 64-bit fraction).  The product with the position is exact, and the
+ *             angle off by less than 1e-7 radians, whatever the position (2^-25 half turns where it
+ *             becomes a 32-bit float; 2^-32 and 2^-33 more for the product's lower half and for
+ *             rates that are off by half a unit).
  *   positions [T] int32, any value (a negative one turns back).
  *   dtype     DSPARK_F32, DSPARK_BF16 or DSPARK_F16; products and sums are fp32, rounded once.
  *   strides   (in elements) between tokens and heads; D contiguous elements a row, which

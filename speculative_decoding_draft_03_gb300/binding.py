@@ -3,8 +3,9 @@ calls, which run many times per token, the compiled ``_marshal`` module.
 
 Every step of the path runs in the library's CUDA kernels; this module checks tensor
 placement/dtypes, passes ``data_ptr()``s and the current CUDA stream, and owns the
-caller-side buffers (outputs and workspaces) through PyTorch.  If the library is
-missing this module raises at import: there is no fallback.
+caller-side buffers (outputs and workspaces) through PyTorch.  The tensors of a serving-side
+call lie on one device (a call over two is refused).  If the library is missing this module raises
+at import: there is no fallback.
 """
 from __future__ import annotations
 

@@ -23,14 +23,15 @@
 //     two into fp16's range.
 //   * An item's last scores free its queries' place: the next item's come while those are weighed, and its
 //     first product is issued behind the last one's weights (with the queries loaded after the last weights, a
-//     row a lane, 64 blocks of 512 queries took 370 us for the 285 now).
+//     row a lane, 64 blocks of 512 queries took 370 us for 290 so).
 //   * The work is dealt out in tiles of 128 tokens that an item sees, evenly over the CTAs; items that
 //     several share are joined by a second kernel, in a fixed order.
 // What bounds it: the products of a tile of both row tiles (D = 128) keep the tensor cores busy for 2050
 // clocks; a tile takes about 3100, the chain of one row tile: 1600 from telling the weights to seeing the next
 // scores (two waits, two matrices' products in turn with the other's), 1500 of softmax.  8192 causal queries, 32
-// heads over 8 of 128: 409 us, 1343 TFLOP/s; 2048 at 32768 tokens: 725 us, 1470 TFLOP/s; over e4m3 the
-// conversion comes on top (8192 causal: 488 us).
+// heads over 8 of 128: 409 us, 1343 TFLOP/s (up to 430 from run to run: it tells where the code comes to lie); 2048
+// at 32768 tokens: 716 to 737 us, 1490 to 1440 TFLOP/s; over e4m3 the conversion comes on top (8192 causal: 489 us).
+// Short items cost something beside their tiles: 64 prompts of 512, 273 us for the 99 that their bytes take.
 // Every mbarrier wait is bounded; a wait that gives up reports DSPARK_TIMEOUT and the CTA winds down.
 #include <algorithm>
 
@@ -862,7 +863,8 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
           };
           // A row's scores, all at once in registers where there are enough; an e4m3 cache's converters leave too few
           // of them, and half a row's scores are read again (2048 queries at 32768 tokens: 725 us at once, 786 by 32
-          // columns, all read twice; 512 at 65536 over e4m3: 462 with 128 held, 415 with 64, 435 with 32).
+          // columns, all read twice; 512 at 65536 over e4m3: 462 with 128 held, 415 with 64, 435 with 32).  Short items
+          // lose by it: 64 prompts of 512 take 250 us by 32 columns and 273 at once, one of 8192 445 and 410.
           constexpr int kHeld = Q8 ? 64 : kTile;
           float s[kHeld];
           if constexpr (!Q8) {
@@ -875,6 +877,10 @@ __global__ void __launch_bounds__(Plan<Q8, DP>::threads, 1)
           }
           refer(max3(max3(m[0], m[1], m[2]), max3(m[3], m[4], m[5]), fmaxf(m[6], m[7])) * c2);
           const Two cc = two(c2, c2), rr2 = two(-ref, -ref);
+          // The weights are rounded to the product's 16 bits, as the instruction wants both operands of one type; the
+          // normaliser adds them unrounded.  Each is off by half a step, 2^-8 (bf16) or 2^-11 (fp16, and over e4m3) of
+          // itself, independently: the outputs' relative error goes from the 1.6e-3 of their own rounding to bf16 to 2.1e-3
+          // (fp16 2.1e-4 to 2.9e-4).
           auto weigh = [&](const float* s, int c) {
             uint32_t w[16];
 #pragma unroll

@@ -2,9 +2,9 @@
 //
 // These calls run many times per generated token and take a few microseconds of GPU time at
 // serving's small sizes; looking at a dozen tensors from Python took longer than that.  Each
-// function here takes its arguments by position, checks the tensors (device, type, shape,
-// strides), and calls the C ABI on the given stream.  It returns the status code, or raises the
-// binding's error for a tensor that does not fit.
+// function here takes its arguments by position, checks the tensors (that all lie on one CUDA
+// device, type, shape, strides), and calls the C ABI on the given stream.  It returns the status
+// code, or raises the binding's error for a tensor that does not fit.
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <stdexcept>

@@ -9,9 +9,12 @@
 //     heads, into shared memory; then each takes 16-byte pieces: in the half layout the same piece of
 //     both halves, in the interleaved one a piece of neighbouring pairs.
 //   * The rotation is two products and a sum in fp32; one rounding to the stored type.
-// What bounds it: device memory, each element being read and written once.  8192 tokens of 40 heads of 128 in
-// bf16: 28.8 us, 86 % of the copy rate; 16 prompts (8.5 K tokens) appended to an e4m3 cache: 39.6 us, 79 %;
-// one token of each of 32 requests: 2.5 us, the launch.
+// What bounds it: device memory, each element being read and written once, where a token's rows give every thread of
+// a CTA a piece.  8192 tokens of 40 heads of 128 in bf16: 28.6 us, 86 % of the copy rate; 16 prompts (9.5 K tokens)
+// appended to an e4m3 cache: 39.7 us, 79 %; one token of each of 32 requests: 2.5 us, the launch.  With few heads most
+// of a CTA's threads stand idle: 40000 tokens of 5 heads of 128 take 26.5 us (57 %), of 2 heads 21.3 (29 %), of 1 head of
+// 64 14.1 (11 %).  Rows that are no whole pieces go an element at a time, by instructions: 8192 tokens of 40 heads of
+// 80, 20 or 40 of them turned, 98 to 104 us (15 %).
 #include <algorithm>
 
 #include "serving.cuh"
@@ -104,7 +107,9 @@ __device__ __forceinline__ uint2 to_e4m3(float (&x)[8], const Divisor& by) {
   return make_uint2(p[0] | ((uint32_t)p[1] << 16), p[2] | ((uint32_t)p[3] << 16));
 }
 
-// The cosine and sine, times the magnitude, of a position's turn; `back` turns the other way.
+// The cosine and sine, times the magnitude, of a position's turn; `back` turns the other way.  The turn goes through
+// one fp32 number, which near half a turn is off by 2^-25 half turns, as much as the result's own rounding to fp32
+// (rms error of fp32 results 3.8e-8, 3.0e-8 with exact angles): the 64-bit product's further digits are dropped.
 __device__ __forceinline__ float2 turn_of(int position, int64_t rate, float magnitude, bool back) {
   const uint64_t turns = (uint64_t)(int64_t)position * (uint64_t)rate;  // in 2^-64, modulo 1
   const int top = (int)(uint32_t)((turns + 0x80000000ull) >> 32);
@@ -374,6 +379,7 @@ cudaError_t launch(const RotaryArgs& a, cudaStream_t s) {
   // (8192 tokens of 40 heads in bf16: 28.8 us with 128 threads, 29.5 with 256; 4096 of 32 in fp32, forward and
   // back: 51.5 and 51.2)
   constexpr int kThreads = sizeof(T) == 4 ? 256 : 128;
+  // (40 heads of 128 in bf16, one token a CTA and two: 304 tokens 3.3 us and 3.5, 608 4.9 and 4.4, 1216 8.9 and 6.5)
   const int tokens = std::max(1, std::min(kTokens, a.T / (4 * sm_count())));
   const dim3 grid((unsigned)(((int64_t)a.T + tokens - 1) / tokens));
   const size_t smem = (size_t)tokens * (a.rot / 2) * sizeof(float2);
@@ -387,7 +393,9 @@ cudaError_t launch(const RotaryArgs& a, cudaStream_t s) {
 template <typename T, bool INTER, bool QUANT>
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
   // (16 prompts of up to 1024 tokens, e4m3: 128 threads and two tokens 40 us, 256 and four 47;
-  // the verified block of 32 requests: 512 threads 3.8 us, 256 4.2, 128 5.2)
+  // the verified block of 32 requests: 512 threads 3.8 us, 256 4.2, 128 5.2.  The two forms, 48 heads of 128: 608
+  // tokens 4.9 and 7.3 us, 900 7.6 and 7.9, 1216 9.1 and 9.4, 1500 11.5 and 11.1, 2000 14.2 and 12.5; into an e4m3
+  // cache 7.1 and 7.4, 8.2 and 8.2, 10.7 and 9.2, 13.3 and 12.2, 16.7 and 12.9)
   const size_t one = (size_t)(a.rot / 2) * sizeof(float2);
   if (a.rot % (INTER ? kPiece<T> : 2 * kPiece<T>) != 0)
     return launch_chained(append_pairs_kernel<T, INTER, QUANT>, dim3((unsigned)a.T), dim3(kPairThreads), one, s, 1, a);
