@@ -91,7 +91,7 @@ Rows rows(PyObject* o, const char* name) {
   const at::Tensor& t = cuda(o, name);
   if (t.dim() != 2) refuse(std::string(name) + " must be 2-D");
   const int64_t n = t.size(0), m = t.size(1);
-  if (m > 1 && t.stride(1) != 1) refuse("the rows of " + std::string(name) + " must be contiguous");
+  if (n > 0 && m > 1 && t.stride(1) != 1) refuse("the rows of " + std::string(name) + " must be contiguous");
   int64_t stride = t.stride(0);
   if (n <= 1) stride = m;  // the stride of one row means nothing
   else if (stride < m) refuse("the rows of " + std::string(name) + " overlap");

@@ -81,6 +81,9 @@ def test_a_mask_without_rows(b, words):
         for out in (None, x.clone()):
             got = b.adjust_logits(x if out is None else out, **d, mask=mask, mask_row=_i32(row), out=out)
             assert torch.equal(got, want)
+    # (a tensor of no rows may say any strides)
+    odd = torch.as_strided(torch.zeros(1, dtype=torch.int32, device="cuda"), (0, words), (0, 0))
+    assert torch.equal(b.adjust_logits(x, **d, mask=odd, mask_row=_i32([-1] * 4)), want)
     with pytest.raises(b.DSparkError, match="a mask row for each of the 4 rows, got 0"):
         b.adjust_logits(x, **d, mask=mask)
     with pytest.raises(b.DSparkError, match="at least 32 words"):
